@@ -390,6 +390,207 @@ const char *decode_attn_status_string(int code);
  * combine). */
 int decode_attn_launch_count(const decode_attn_params *p, int32_t num_splits);
 
+/* ------------------------------------------------------------------------
+ * The operators around the cache: rotary tables, the append that writes new
+ * tokens into a cache, attention over caches held in 4 bits, and attention
+ * over the pages that a cheap score selects.  They share the rules above
+ * (ownership, errors, status bits, streams, graph capture, threads).
+ * ------------------------------------------------------------------------ */
+
+/* cache types */
+#define DA_CACHE_BF16 0
+#define DA_CACHE_FP8_E4M3 1   /* as DA_FLAG_KV_FP8_E4M3 */
+#define DA_CACHE_FP4_E2M1 2   /* 4 bits per value, one E4M3 scale per 16 */
+
+/*
+ * A K/V cache of any type, under the paging and strides of a
+ * decode_attn_params (strides in elements for bf16, in bytes for the others;
+ * its k_scale / v_scale apply to FP8 and 4-bit caches).  The type here counts;
+ * DA_FLAG_KV_FP8_E4M3 in the params is ignored by the calls that take a cache.
+ *
+ * 4-bit caches.  Byte i of a (token, head), 64 in all, holds value 2i in its
+ * low nibble and 2i + 1 in its high one, each an OCP E2M1 code (sign, two
+ * exponent bits, one mantissa bit: 0, .5, 1, 1.5, 2, 3, 4, 6).  Every 16
+ * values share an E4M3 block scale: value d of token j is
+ *     k_scale * block_scale[j, d / 16] * e2m1(code).
+ * Block scales live beside the cache, 8 bytes per (token, head), the tokens
+ * of a head one behind the other: token slot of head h in page (or, for a
+ * contiguous cache, request) g is at
+ *     g * bs_stride_page + h * bs_stride_head + slot * 8  (bytes).
+ */
+typedef struct decode_attn_cache {
+  int32_t type;               /* DA_CACHE_* */
+  int32_t reserved;           /* 0 */
+  void *k;                    /* caches, 16-byte aligned */
+  void *v;
+  void *k_block_scale;        /* DA_CACHE_FP4_E2M1: 8-byte aligned; else ignored */
+  void *v_block_scale;
+  int64_t bs_stride_page;     /* bytes, positive multiples of 8 */
+  int64_t bs_stride_head;
+} decode_attn_cache;
+
+/*
+ * decode_attn() for a cache of any type: bf16 and FP8 caches run as
+ * decode_attn() runs them, 4-bit ones run their own split kernel (the same
+ * planner, partials, device planning and combine; every row count up to
+ * DECODE_ATTN_MAX_ROWS; no cluster merge, so more than one chunk always takes
+ * the workspace).  k_scale and v_scale are finite.
+ */
+int decode_attn_cached_workspace_bytes(const decode_attn_params *p,
+                                       const decode_attn_cache *c, int32_t num_splits,
+                                       size_t *bytes);
+int decode_attn_cached(const decode_attn_params *p, const decode_attn_cache *c, const void *q,
+                       const int32_t *block_table, const int32_t *seq_lens, void *out,
+                       float *lse, int32_t num_splits, void *workspace,
+                       size_t workspace_bytes, int32_t *status, void *stream);
+
+/*
+ * The cos / sin table of rotary embeddings: for the positions pos = first ..
+ * first + count - 1 and the frequencies f_i, i < num_freqs (radians per
+ * position, fp64, device memory),
+ *     table[(pos - first) * 2 num_freqs + i]             = amplitude cos(pos f_i)
+ *     table[(pos - first) * 2 num_freqs + num_freqs + i] = amplitude sin(pos f_i)
+ * in fp32, to about one ulp at every position (the angle is reduced in 64-bit
+ * fixed point).  Scalings for long contexts are the caller's choice of f and
+ * amplitude.  1 <= num_freqs <= 64, first and first + count within 0 .. 2^31.
+ * Frequencies that are not finite give NaN.
+ */
+int decode_attn_rope_table(const double *inv_freq, int32_t num_freqs, int64_t first,
+                           int64_t count, double amplitude, float *table, void *stream);
+
+/* Rotary embedding of the new tokens (decode_attn_rope_append). */
+typedef struct decode_attn_rope {
+  int32_t rotary_dim;         /* leading values of each head that are rotated: even,
+                                 0 .. 128 (0: none; the table may be NULL) */
+  int32_t interleaved;        /* pairs (2i, 2i + 1); else halves (i, i + rotary_dim / 2) */
+  int32_t table_positions;    /* rows of the table */
+  int32_t reserved;           /* 0 */
+  int64_t k_stride_batch;     /* new k [B, q_len, Hkv, D] element strides, multiples */
+  int64_t k_stride_token;     /*   of 8 */
+  int64_t k_stride_head;
+  int64_t v_stride_batch;     /* new v */
+  int64_t v_stride_token;
+  int64_t v_stride_head;
+} decode_attn_rope;
+
+/*
+ * Rotate the new tokens' q and k and write k and v into the cache, where the
+ * attention calls read them.  seq_lens counts the new tokens already: request
+ * b has n_b = new_lens[b] new tokens (q_len when new_lens is NULL), at cache
+ * positions L - n_b .. L - 1, in rows t = 0 .. n_b - 1 of q, k and v.  Rows t
+ * >= n_b are padding: their q_out rows and the cache are left as they were.
+ * The angle of a token is that of its cache position, or of positions[b *
+ * q_len + t] where given.  A pair (x1, x2) becomes
+ *     (x1 c - x2 s, x2 c + x1 s),
+ * in fp32 with every product and sum rounded, then rounded to bf16; values
+ * from rotary_dim on pass through.  From the bf16 values a cache stores
+ *     FP8:   E4M3(x * (1 / k_scale)), saturated (NaN stays NaN);
+ *     4-bit: z = x * (1 / k_scale); block scale E4M3(max |z| / 6), saturated;
+ *            code E2M1(z / block scale), ties to even, saturated; NaN is
+ *            stored as 0 and does not enter the maximum.
+ * all in fp32, so the bytes are the same wherever a token is recomputed.
+ *   p          the shapes, paging and strides of the attention calls; q_len
+ *              may be any length here; q / o strides are those of q / q_out;
+ *              scale and causal are not used; k_scale and v_scale are finite
+ *              and not 0
+ *   q, q_out   bf16; both NULL: only the cache is written.  q_out may be q.
+ *   k, v       bf16, the new tokens; both NULL: only q is rotated
+ *   table      decode_attn_rope_table() from position 0
+ *   positions  optional int32 [B, q_len]
+ *   new_lens   optional int32 [B], 0 .. q_len
+ * Status: DA_STATUS_SEQ_LEN where a length is outside [0, max_seq_len] or a
+ * new_lens entry outside [0, q_len] (clamped), DA_STATUS_SHORT_CAUSAL where L
+ * < n_b (the first n_b - L rows have no position and are skipped),
+ * DA_STATUS_BAD_PAGE where a page is out of range (that token is not written)
+ * and DA_STATUS_POSITION where a position has no row in the table (that token
+ * is not rotated or written).  Two tokens of a call that map to one slot leave either's
+ * values there.
+ */
+#define DA_STATUS_POSITION 16u
+int decode_attn_rope_append(const decode_attn_params *p, const decode_attn_cache *c,
+                            const decode_attn_rope *r, const void *q, const void *k,
+                            const void *v, const float *table, const int32_t *positions,
+                            const int32_t *new_lens, const int32_t *block_table,
+                            const int32_t *seq_lens, void *q_out, int32_t *status,
+                            void *stream);
+
+/*
+ * Digests of a paged K cache, for the selection of pages: per page and KV head
+ * the channel-wise minimum and maximum of the page's keys (those below
+ * seq_len), in 8 bits.  With amax the largest magnitude among them,
+ *     digest[page, head, 0 / 1, d] = rint(min / max * (127 / amax)),
+ *     digest_scale[page, head]     = amax / 127,
+ * in fp32 (0 where amax is 0).  Keys are the values the cache stores, without
+ * k_scale; NaN values are skipped (a channel with nothing else counts as 0)
+ * and infinities count as the largest finite bf16 value.
+ *   digest        int8 [num_pages, Hkv, 2, 128]
+ *   digest_scale  fp32 [num_pages, Hkv]
+ *   max_new       > 0: only the pages that hold tokens L - max_new .. L - 1
+ *                 of a request (a decode step); 0: every page it has
+ * Other pages' digests are left as they were.  A page that requests of a call
+ * share is digested for one of them: they should see the same tokens of it.
+ */
+int decode_attn_block_digest(const decode_attn_params *p, const decode_attn_cache *c,
+                             const int32_t *block_table, const int32_t *seq_lens,
+                             int32_t max_new, int8_t *digest, float *digest_scale,
+                             int32_t *status, void *stream);
+
+/* Which pages a query reads (decode_attn_block_select, decode_attn_sparse). */
+typedef struct decode_attn_select {
+  int32_t top_k;              /* pages per (token, kv head), 1 .. 4096 */
+  int32_t sink;               /* the first pages, always among them: >= 0 */
+  int32_t local;              /* the last pages, always among them: >= 1 */
+  int32_t reserved;           /* 0; sink + local <= top_k */
+} decode_attn_select;
+
+/*
+ * Select pages: for every request b, new token t and KV head h, out of the n =
+ * ceil(Lt / page_size) pages that the token sees (Lt = L, or L - q_len + t + 1
+ * with `causal`), the first `sink`, the last `local` and, of the others, those
+ * with the highest scores, top_k in all (all pages when n <= top_k; ties go to
+ * the lower page).  The score of a page is the largest over the query heads of
+ * the group of
+ *     ((sum_d min(q'_d, 0) min_d + max(q'_d, 0) max_d) * digest_scale) * (a / 127),
+ * with a = max |q_d| and q'_d = rint(q_d * (127 / a)): up to its 8 bits, a
+ * bound on q . k over the page's keys, each channel at its better end.  The sum is exact, the two products
+ * are fp32: the selection is the same on every run.  (NaN in q counts as 0,
+ * infinities as the largest finite bf16 value; a = 0 gives scores of 0.)
+ *   blocks     int32 [B, q_len, Hkv, top_k]: the selected pages' places in
+ *              the request, ascending, -1 behind the last; may be NULL
+ *   pages      int32 [B, q_len, Hkv, top_k]: their page ids (0 behind the
+ *              last; out-of-range entries as in decode_attn())
+ *   tokens     int32 [B, q_len, Hkv]: tokens they hold up to the last one seen
+ *   workspace  decode_attn_block_select_workspace_bytes() bytes
+ * p as for decode_attn(), paged; max_seq_len <= 2^20 pages.
+ */
+int decode_attn_block_select_workspace_bytes(const decode_attn_params *p,
+                                             const decode_attn_select *s, size_t *bytes);
+int decode_attn_block_select(const decode_attn_params *p, const decode_attn_select *s,
+                             const void *q, const int8_t *digest, const float *digest_scale,
+                             const int32_t *block_table, const int32_t *seq_lens,
+                             int32_t *blocks, int32_t *pages, int32_t *tokens,
+                             void *workspace, size_t workspace_bytes, int32_t *status,
+                             void *stream);
+
+/*
+ * Decode attention over selected pages: decode_attn_block_select(), then the
+ * attention of every (token, kv head) over its own pages, exactly as
+ * decode_attn() computes it for a request that holds those pages only.  Any
+ * cache type.  p->scale (and k_scale, where the cache has one) must be
+ * positive.  q and out hold a request's tokens at one stride: q_len == 1, B ==
+ * 1, or stride_batch == q_len * stride_token.
+ *   blocks      as above; may be NULL
+ *   workspace   decode_attn_sparse_workspace_bytes() bytes
+ */
+int decode_attn_sparse_workspace_bytes(const decode_attn_params *p, const decode_attn_cache *c,
+                                       const decode_attn_select *s, size_t *bytes);
+int decode_attn_sparse(const decode_attn_params *p, const decode_attn_cache *c,
+                       const decode_attn_select *s, const void *q, const int8_t *digest,
+                       const float *digest_scale, const int32_t *block_table,
+                       const int32_t *seq_lens, void *out, float *lse, int32_t *blocks,
+                       void *workspace, size_t workspace_bytes, int32_t *status,
+                       void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,11 +12,32 @@
 #include <mutex>
 
 #include "decode_attn.h"
+#include "internal.cuh"
 #include "kernels.cuh"
 #include "plan_rule.cuh"
 
+namespace dattn {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int check_paged(const decode_attn_params* p, bool paged) {
+  if (!paged) return DA_OK;
+  if (p->page_size <= 0 || p->page_size % kTileTokens != 0) return DA_ERR_PAGE_SIZE;
+  if (p->max_pages_per_seq < 1 || p->num_pages < 1 ||
+      p->block_table_stride < p->max_pages_per_seq ||
+      static_cast<int64_t>(p->max_seq_len) >
+          static_cast<int64_t>(p->max_pages_per_seq) * p->page_size)
+    return DA_ERR_BAD_SHAPE;
+  return DA_OK;
+}
+
+}  // namespace dattn
+
 namespace {
 
+using dattn::aligned16;
+using dattn::check_paged;
+using dattn::DecodeExt;
 using dattn::kHeadDim;
 using dattn::kTileTokens;
 
@@ -62,8 +83,6 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 int rows_of(const decode_attn_params* p) {
@@ -72,8 +91,9 @@ int rows_of(const decode_attn_params* p) {
 
 bool kv_fp8(const decode_attn_params* p) { return (p->flags & DA_FLAG_KV_FP8_E4M3) != 0; }
 
-// Shape checks shared by every entry point.
-int check_shape(const decode_attn_params* p) {
+// Shape checks shared by every entry point; rows_limit: those of the
+// attention calls, which hold a KV head's query rows in one tile.
+int check_shape(const decode_attn_params* p, bool rows_limit = true) {
   if (p == nullptr) return DA_ERR_NULL_POINTER;
   if (p->batch < 0 || p->batch > 65535 || p->q_len < 1 || p->num_q_heads < 1 ||
       p->num_kv_heads < 1 || p->num_kv_heads > 65535 || p->max_seq_len < 0 ||
@@ -84,19 +104,9 @@ int check_shape(const decode_attn_params* p) {
   if (kv_fp8(p) && (!std::isfinite(p->k_scale) || !std::isfinite(p->v_scale)))
     return DA_ERR_BAD_SHAPE;
   if (p->head_dim != DECODE_ATTN_HEAD_DIM) return DA_ERR_HEAD_DIM;
-  if (static_cast<int64_t>(p->num_q_heads / p->num_kv_heads) * p->q_len > DECODE_ATTN_MAX_ROWS)
+  if (rows_limit &&
+      static_cast<int64_t>(p->num_q_heads / p->num_kv_heads) * p->q_len > DECODE_ATTN_MAX_ROWS)
     return DA_ERR_ROWS;
-  return DA_OK;
-}
-
-int check_paged(const decode_attn_params* p, bool paged) {
-  if (!paged) return DA_OK;
-  if (p->page_size <= 0 || p->page_size % kTileTokens != 0) return DA_ERR_PAGE_SIZE;
-  if (p->max_pages_per_seq < 1 || p->num_pages < 1 ||
-      p->block_table_stride < p->max_pages_per_seq ||
-      static_cast<int64_t>(p->max_seq_len) >
-          static_cast<int64_t>(p->max_pages_per_seq) * p->page_size)
-    return DA_ERR_BAD_SHAPE;
   return DA_OK;
 }
 
@@ -146,15 +156,19 @@ int plan_for_slots(const decode_attn_params* p, const int32_t* host_seq_lens, in
   return DA_OK;
 }
 
+// Resident CTAs per SM of the split launch for this shape.
+int ctas_per_sm(const decode_attn_params* p, bool fp4) {
+  return fp4 ? dattn::fp4_ctas_per_sm(rows_of(p)) : dattn::split_ctas_per_sm(rows_of(p), kv_fp8(p));
+}
+
 // The planner on the current device: its SM count times the split launch's
 // resident CTAs per SM for this shape (occupancy of the kernel it will run).
 int plan_impl(const decode_attn_params* p, const int32_t* host_seq_lens, int32_t* num_splits,
-              int32_t* chunk_len) {
+              int32_t* chunk_len, bool fp4 = false) {
   DeviceInfo di;
   const int rc = current_device_info(&di);
   if (rc != DA_OK) return rc;
-  const int64_t slots =
-      static_cast<int64_t>(di.sm_count) * dattn::split_ctas_per_sm(rows_of(p), kv_fp8(p));
+  const int64_t slots = static_cast<int64_t>(di.sm_count) * ctas_per_sm(p, fp4);
   return plan_for_slots(p, host_seq_lens, slots, num_splits, chunk_len);
 }
 
@@ -234,8 +248,9 @@ int make_kv_map(CUtensorMap* map, const void* base, const decode_attn_params* p,
 bool stride_ok(int64_t s) { return s > 0 && s % 8 == 0 && s * 2 < (1LL << 40); }
 
 // FP8 caches: strides in bytes, multiples of 16 (the TMA stride rule)
-bool kv_stride_ok(const decode_attn_params* p, int64_t s) {
-  return kv_fp8(p) ? (s > 0 && s % 16 == 0 && s < (1LL << 40)) : stride_ok(s);
+// (so are those of 4-bit ones)
+bool kv_stride_ok(const decode_attn_params* p, int64_t s, bool fp4 = false) {
+  return kv_fp8(p) || fp4 ? (s > 0 && s % 16 == 0 && s < (1LL << 40)) : stride_ok(s);
 }
 
 // The split pass merges through thread-block clusters (no partials, no
@@ -276,19 +291,19 @@ bool device_planned(const decode_attn_params* p, int32_t num_splits) {
 }
 
 // Resident CTAs of the split launch for this shape on the current device.
-int split_slots(const decode_attn_params* p, int64_t* slots) {
+int split_slots(const decode_attn_params* p, int64_t* slots, bool fp4) {
   DeviceInfo di;
   const int rc = current_device_info(&di);
   if (rc != DA_OK) return rc;
-  *slots = static_cast<int64_t>(di.sm_count) * dattn::split_ctas_per_sm(rows_of(p), kv_fp8(p));
+  *slots = static_cast<int64_t>(di.sm_count) * ctas_per_sm(p, fp4);
   return DA_OK;
 }
 
 // Workspace of a device-planned call (offsets 256-byte aligned): plan[4],
 // pre[B + 1], items[cap] (int4), partial outputs [cap, rows, D] and partial
 // LSEs [cap, rows] (fp32).
-int list_layout(const decode_attn_params* p, ListLayout* l) {
-  int rc = split_slots(p, &l->slots);
+int list_layout(const decode_attn_params* p, ListLayout* l, bool fp4 = false) {
+  int rc = split_slots(p, &l->slots, fp4);
   if (rc != DA_OK) return rc;
   l->cap = static_cast<int64_t>(p->batch) * p->num_kv_heads + kListWaveSlack * l->slots;
   if (l->cap > 0x7fffffff) return DA_ERR_BAD_SHAPE;
@@ -331,6 +346,39 @@ dattn::PlanArgs plan_args(const decode_attn_params* p, const int32_t* seq_lens, 
 }
 
 }  // namespace
+
+namespace dattn {
+
+int workspace_bytes(const decode_attn_params* p, int32_t num_splits, const DecodeExt& ext,
+                    size_t* bytes) {
+  int rc = check_shape(p);
+  if (rc != DA_OK) return rc;
+  if (bytes == nullptr) return DA_ERR_NULL_POINTER;
+  const bool fp4 = ext.fp4 != nullptr;
+  if (!ext.per_head && device_planned(p, num_splits)) {
+    ListLayout l;
+    rc = list_layout(p, &l, fp4);
+    if (rc != DA_OK) return rc;
+    *bytes = l.total;
+    return DA_OK;
+  }
+  int32_t chunk = 0, eff = 0;
+  if (num_splits <= 0) {  // one request (or none): the host plan
+    rc = plan_impl(p, nullptr, &num_splits, &chunk, fp4);
+    if (rc != DA_OK) return rc;
+  }
+  rc = chunk_for_splits(p, num_splits, &chunk, &eff);
+  if (rc != DA_OK) return rc;
+  if (eff <= 1) {
+    *bytes = 0;
+    return DA_OK;
+  }
+  const size_t rows = static_cast<size_t>(p->batch) * p->q_len * p->num_q_heads;
+  *bytes = rows * static_cast<size_t>(eff) * (kHeadDim + 1) * sizeof(float);
+  return DA_OK;
+}
+
+}  // namespace dattn
 
 extern "C" {
 
@@ -391,30 +439,7 @@ int decode_attn_chunk_len(const decode_attn_params* p, int32_t num_splits, int32
 }
 
 int decode_attn_workspace_bytes(const decode_attn_params* p, int32_t num_splits, size_t* bytes) {
-  int rc = check_shape(p);
-  if (rc != DA_OK) return rc;
-  if (bytes == nullptr) return DA_ERR_NULL_POINTER;
-  if (device_planned(p, num_splits)) {
-    ListLayout l;
-    rc = list_layout(p, &l);
-    if (rc != DA_OK) return rc;
-    *bytes = l.total;
-    return DA_OK;
-  }
-  int32_t chunk = 0, eff = 0;
-  if (num_splits <= 0) {  // one request (or none): the host plan
-    rc = plan_impl(p, nullptr, &num_splits, &chunk);
-    if (rc != DA_OK) return rc;
-  }
-  rc = chunk_for_splits(p, num_splits, &chunk, &eff);
-  if (rc != DA_OK) return rc;
-  if (eff <= 1) {
-    *bytes = 0;
-    return DA_OK;
-  }
-  const size_t rows = static_cast<size_t>(p->batch) * p->q_len * p->num_q_heads;
-  *bytes = rows * static_cast<size_t>(eff) * (kHeadDim + 1) * sizeof(float);
-  return DA_OK;
+  return dattn::workspace_bytes(p, num_splits, DecodeExt{}, bytes);
 }
 
 int decode_attn_launch_count(const decode_attn_params* p, int32_t num_splits) {
@@ -434,15 +459,17 @@ int decode_attn_launch_count(const decode_attn_params* p, int32_t num_splits) {
 
 }  // extern "C"
 
-namespace {
+namespace dattn {
 
 // The whole path (run_combine) or the split pass alone.
 int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
                const void* v_cache, const int32_t* block_table, const int32_t* seq_lens,
                void* out, float* lse, int32_t num_splits, void* workspace,
-               size_t workspace_bytes, int32_t* status, void* stream, bool run_combine) {
+               size_t workspace_bytes, int32_t* status, void* stream, bool run_combine,
+               const DecodeExt& ext) {
   int rc = check_shape(p);
   if (rc != DA_OK) return rc;
+  const bool fp4 = ext.fp4 != nullptr;
   const bool paged = block_table != nullptr;
   rc = check_paged(p, paged);
   if (rc != DA_OK) return rc;
@@ -460,8 +487,9 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
   if (!stride_ok(p->q_stride_batch) || !stride_ok(p->q_stride_token) ||
       !stride_ok(p->q_stride_head) || !stride_ok(p->o_stride_batch) ||
       !stride_ok(p->o_stride_token) || !stride_ok(p->o_stride_head) ||
-      (!no_keys && (!kv_stride_ok(p, p->kv_stride_page) || !kv_stride_ok(p, p->kv_stride_token) ||
-                    !kv_stride_ok(p, p->kv_stride_head))))
+      (!no_keys && (!kv_stride_ok(p, p->kv_stride_page, fp4) ||
+                    !kv_stride_ok(p, p->kv_stride_token, fp4) ||
+                    !kv_stride_ok(p, p->kv_stride_head, fp4))))
     return DA_ERR_ALIGNMENT;
 
   DeviceInfo di;
@@ -469,25 +497,25 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
   if (rc != DA_OK) return rc;
   if (di.major * 10 + di.minor < 100) return DA_ERR_NO_DEVICE;
 
-  const bool listed = device_planned(p, num_splits);
+  const bool listed = !ext.per_head && device_planned(p, num_splits);
   ListLayout lay;
   int32_t chunk = 0, eff = 0;
   bool cluster_merge = false;
   if (listed) {
-    rc = list_layout(p, &lay);
+    rc = list_layout(p, &lay, fp4);
     if (rc != DA_OK) return rc;
     if (workspace == nullptr || workspace_bytes < lay.total || !aligned16(workspace))
       return DA_ERR_WORKSPACE;
   } else {
     if (num_splits <= 0) {
-      rc = plan_impl(p, nullptr, &num_splits, &chunk);
+      rc = plan_impl(p, nullptr, &num_splits, &chunk, fp4);
       if (rc != DA_OK) return rc;
     }
     rc = chunk_for_splits(p, num_splits, &chunk, &eff);
     if (rc != DA_OK) return rc;
-    cluster_merge = use_cluster_merge(p, eff);
+    cluster_merge = !fp4 && use_cluster_merge(p, eff);
     size_t need = 0;
-    decode_attn_workspace_bytes(p, num_splits, &need);
+    dattn::workspace_bytes(p, num_splits, ext, &need);
     if (!cluster_merge && need > 0 &&
         (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
       return DA_ERR_WORKSPACE;
@@ -501,7 +529,7 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
   CUtensorMap kmap, vmap;
   std::memset(&kmap, 0, sizeof(kmap));
   std::memset(&vmap, 0, sizeof(vmap));
-  if (!no_keys) {
+  if (!no_keys && !fp4) {
     rc = make_kv_map(&kmap, k_cache, p, paged, box_tokens);
     if (rc != DA_OK) return rc;
     rc = make_kv_map(&vmap, v_cache, p, paged, box_tokens);
@@ -524,7 +552,10 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
   a.part_lse = a.part_o != nullptr ? a.part_o + rows_total * eff * kHeadDim : nullptr;
   a.block_table = block_table;
   a.bt_stride = p->block_table_stride;
+  a.bt_sh = ext.per_head ? p->max_pages_per_seq : 0;
   a.seq_lens = seq_lens;
+  a.len_sb = ext.per_head ? p->num_kv_heads : 1;
+  a.len_sh = ext.per_head ? 1 : 0;
   a.status = status;
   a.batch = p->batch;
   a.q_len = p->q_len;
@@ -539,10 +570,10 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
   a.chunk_len = chunk;
   a.num_splits = eff;
   a.causal = p->causal ? 1 : 0;
-  a.scale_log2 = p->scale * (kv_fp8(p) ? p->k_scale : 1.f) * 1.4426950408889634f;
+  a.scale_log2 = p->scale * (kv_fp8(p) || fp4 ? p->k_scale : 1.f) * 1.4426950408889634f;
   a.kv_fp8 = kv_fp8(p) ? 1 : 0;
   a.test_withhold = (p->flags & DA_FLAG_TEST_WITHHOLD_COPY) != 0 ? 1 : 0;
-  a.v_scale = kv_fp8(p) ? p->v_scale : 1.f;
+  a.v_scale = kv_fp8(p) || fp4 ? p->v_scale : 1.f;
   // (no keys: no tensor map was encoded and no copy may be issued)
   a.big_box = box_tokens > kTileTokens && !no_keys ? 1 : 0;
 
@@ -562,7 +593,22 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
     if (dattn::launch_plan(plan_args(p, seq_lens, status, w, lay), st) != cudaSuccess)
       return DA_ERR_CUDA;
   }
-  if (dattn::launch_split(kmap, vmap, a, cluster_merge, st) != cudaSuccess) return DA_ERR_CUDA;
+  if (fp4) {
+    Fp4Args f;
+    f.s = a;
+    f.k = static_cast<const uint8_t*>(k_cache);
+    f.v = static_cast<const uint8_t*>(v_cache);
+    f.ks = static_cast<const uint8_t*>(ext.fp4->k_block_scale);
+    f.vs = static_cast<const uint8_t*>(ext.fp4->v_block_scale);
+    f.st_page = p->kv_stride_page;
+    f.st_token = p->kv_stride_token;
+    f.st_head = p->kv_stride_head;
+    f.sf_page = ext.fp4->bs_stride_page;
+    f.sf_head = ext.fp4->bs_stride_head;
+    if (launch_fp4(f, st) != cudaSuccess) return DA_ERR_CUDA;
+  } else if (dattn::launch_split(kmap, vmap, a, cluster_merge, st) != cudaSuccess) {
+    return DA_ERR_CUDA;
+  }
   if (run_combine && (listed || (eff > 1 && !cluster_merge))) {
     dattn::CombineArgs c = {};
     c.plan = a.plan;
@@ -582,12 +628,56 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
     c.max_seq_len = p->max_seq_len;
     c.chunk_len = chunk;
     c.num_splits = eff;
+    c.len_sb = a.len_sb;
+    c.len_sh = a.len_sh;
     if (dattn::launch_combine(c, st) != cudaSuccess) return DA_ERR_CUDA;
   }
   return DA_OK;
 }
 
-}  // namespace
+int plan_uniform(const decode_attn_params* p, const DecodeExt& ext, int32_t* num_splits,
+                 int32_t* chunk_len) {
+  return plan_impl(p, nullptr, num_splits, chunk_len, ext.fp4 != nullptr);
+}
+
+int check_device(int* sm_count) {
+  DeviceInfo di;
+  const int rc = current_device_info(&di);
+  if (rc != DA_OK) return rc;
+  if (di.major * 10 + di.minor < 100) return DA_ERR_NO_DEVICE;
+  if (sm_count != nullptr) *sm_count = di.sm_count;
+  return DA_OK;
+}
+
+int check_params(const decode_attn_params* p, bool rows_limit) { return check_shape(p, rows_limit); }
+
+int check_cache(const decode_attn_params* p, const decode_attn_cache* c, bool need_k,
+                bool need_v) {
+  const bool fp4 = c->type == DA_CACHE_FP4_E2M1;
+  if ((need_k && (c->k == nullptr || (fp4 && c->k_block_scale == nullptr))) ||
+      (need_v && (c->v == nullptr || (fp4 && c->v_block_scale == nullptr))))
+    return DA_ERR_NULL_POINTER;
+  if ((need_k && !aligned16(c->k)) || (need_v && !aligned16(c->v)) ||
+      !kv_stride_ok(p, p->kv_stride_page, fp4) || !kv_stride_ok(p, p->kv_stride_token, fp4) ||
+      !kv_stride_ok(p, p->kv_stride_head, fp4))
+    return DA_ERR_ALIGNMENT;
+  if (fp4 && ((need_k && (reinterpret_cast<uintptr_t>(c->k_block_scale) & 7u) != 0) ||
+              (need_v && (reinterpret_cast<uintptr_t>(c->v_block_scale) & 7u) != 0) ||
+              c->bs_stride_page <= 0 || c->bs_stride_head <= 0 || c->bs_stride_page % 8 != 0 ||
+              c->bs_stride_head % 8 != 0 || c->bs_stride_page >= (int64_t{1} << 40) ||
+              c->bs_stride_head >= (int64_t{1} << 40)))
+    return DA_ERR_ALIGNMENT;
+  return DA_OK;
+}
+
+decode_attn_params params_of_cache(const decode_attn_params* p, const decode_attn_cache* c) {
+  decode_attn_params r = *p;
+  r.flags &= ~static_cast<int32_t>(DA_FLAG_KV_FP8_E4M3);
+  if (c->type == DA_CACHE_FP8_E4M3) r.flags |= DA_FLAG_KV_FP8_E4M3;
+  return r;
+}
+
+}  // namespace dattn
 
 extern "C" {
 
@@ -595,7 +685,7 @@ int decode_attn(const decode_attn_params* p, const void* q, const void* k_cache,
                 const void* v_cache, const int32_t* block_table, const int32_t* seq_lens,
                 void* out, float* lse, int32_t num_splits, void* workspace,
                 size_t workspace_bytes, int32_t* status, void* stream) {
-  return run_decode(p, q, k_cache, v_cache, block_table, seq_lens, out, lse, num_splits,
+  return dattn::run_decode(p, q, k_cache, v_cache, block_table, seq_lens, out, lse, num_splits,
                     workspace, workspace_bytes, status, stream, true);
 }
 
@@ -603,7 +693,7 @@ int decode_attn_split(const decode_attn_params* p, const void* q, const void* k_
                       const void* v_cache, const int32_t* block_table, const int32_t* seq_lens,
                       void* out, float* lse, int32_t num_splits, void* workspace,
                       size_t workspace_bytes, int32_t* status, void* stream) {
-  return run_decode(p, q, k_cache, v_cache, block_table, seq_lens, out, lse, num_splits,
+  return dattn::run_decode(p, q, k_cache, v_cache, block_table, seq_lens, out, lse, num_splits,
                     workspace, workspace_bytes, status, stream, false);
 }
 
@@ -659,6 +749,8 @@ int decode_attn_combine(const decode_attn_params* p, const int32_t* seq_lens, in
   c.max_seq_len = p->max_seq_len;
   c.chunk_len = chunk_len;
   c.num_splits = num_splits;
+  c.len_sb = 1;
+  c.len_sh = 0;
   if (dattn::launch_combine(c, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return DA_ERR_CUDA;
   return DA_OK;
@@ -835,7 +927,7 @@ int decode_attn_host(const decode_attn_params* p, const void* q_host, const void
         return finish(DA_ERR_CUDA);
       q_use = w + h.q;
     }
-    rc = run_decode(p, q_use, k_cache, v_cache, bt_use, static_cast<const int32_t*>(lens_d),
+    rc = dattn::run_decode(p, q_use, k_cache, v_cache, bt_use, static_cast<const int32_t*>(lens_d),
                     const_cast<void*>(out_d), static_cast<float*>(const_cast<void*>(lse_d)),
                     num_splits, w + h.part, h.q, status_dev, stream, true);
     if (rc != DA_OK) return finish(rc);
@@ -852,7 +944,7 @@ int decode_attn_host(const decode_attn_params* p, const void* q_host, const void
                                 st) != cudaSuccess) ||
       cudaMemsetAsync(w + h.status, 0, 4, st) != cudaSuccess)
     return finish(DA_ERR_CUDA);
-  rc = run_decode(p, w + h.q, k_cache, v_cache,
+  rc = dattn::run_decode(p, w + h.q, k_cache, v_cache,
                   paged ? reinterpret_cast<const int32_t*>(w + h.bt) : nullptr,
                   reinterpret_cast<const int32_t*>(w + h.lens), w + h.out,
                   reinterpret_cast<float*>(w + h.lse), num_splits, w + h.part, h.q,

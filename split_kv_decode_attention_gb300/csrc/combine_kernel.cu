@@ -154,7 +154,9 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock, LISTED ? kBlocksPerSm - 1
     po = a.part_o + row * S * kHeadDim + lane * 4;
     ls = 1;
     os = kHeadDim;
-    L = a.seq_lens[b];
+    L = a.seq_lens[static_cast<int64_t>(b) * a.len_sb +
+                   (a.len_sh != 0 ? static_cast<int64_t>(h / (a.num_q_heads / a.num_kv_heads)) * a.len_sh
+                                  : 0)];
     n = 0;  // known after the first round trip
   }
   // one round trip for the first 32 LSEs and the first kBatch partial rows

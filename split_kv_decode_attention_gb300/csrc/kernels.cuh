@@ -49,6 +49,23 @@ struct SplitArgs {
   const int32_t* plan;
   const int32_t* pre;
   int item_slots;
+  // Lengths and block-table rows: request b, kv head h reads seq_lens[b *
+  // len_sb + h * len_sh] and the table at b * bt_stride + h * bt_sh (1, 0 and
+  // 0 where the heads of a request share them, as in every call but those over
+  // selected pages; device-planned calls use the shared form only).
+  int len_sb, len_sh;
+  int64_t bt_sh;
+};
+
+// Arguments of the 4-bit kernel: the split arguments, and the cache (byte
+// strides; the 8 block scales of a token follow those of the token before).
+struct Fp4Args {
+  SplitArgs s;
+  const uint8_t* k;
+  const uint8_t* v;
+  const uint8_t* ks;
+  const uint8_t* vs;
+  int64_t st_page, st_token, st_head, sf_page, sf_head;
 };
 
 // Arguments of the device planner kernel (plan_kernel.cu; up to 32 CTAs, each
@@ -78,6 +95,7 @@ struct CombineArgs {
   const int32_t* plan;
   const int32_t* pre;
   int num_kv_heads;
+  int len_sb, len_sh;                  // strides of seq_lens (see SplitArgs)
 };
 
 // Physical page ids of a chunk's 16-token tiles, for the TMA producer warp.
@@ -139,6 +157,11 @@ int split_ctas_per_sm(int rows, bool fp8);
 cudaError_t launch_wide(const CUtensorMap& k_map, const CUtensorMap& v_map, const SplitArgs& a,
                         cudaStream_t stream);
 int wide_ctas_per_sm();
+
+// Launch the kernel over 4-bit caches (any rows; outputs and partials as
+// launch_split without cluster merge), and its resident CTAs per SM.
+cudaError_t launch_fp4(const Fp4Args& a, cudaStream_t stream);
+int fp4_ctas_per_sm(int rows);
 
 // Launch the combine kernel (one warp per output row).
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream);

@@ -248,6 +248,16 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t four_bytes, uint32_t& l
       : "r"(four_bytes));
 }
 
+// The four bytes of a word, each two E2M1 values (the low nibble first), to
+// four f16x2.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
+
 // Sum of the two values of a packed bf16x2 (or, with f16 = true, f16x2)
 // pair, in fp32 (exact widening).  The probabilities of the P.V product are
 // rounded to 16 bits; normalising the output by the sum of those rounded

@@ -1,0 +1,457 @@
+// select_kernel.cu -- which pages of a long context each query reads.
+//
+// score_kernel: for 16 pages x the query rows of a KV head the bound
+//     sum_d min(q'_d, 0) min_d + max(q'_d, 0) max_d = [min(q', 0); max(q', 0)] . [min; max]
+// is one matrix product over 256 channels.  q' and the digests are whole
+// numbers of at most 7 bits, exact in f16, and every partial sum stays below
+// 2^22, exact in the fp32 accumulators: mma.sync computes the same integers
+// whatever its order of summation.  The digests are 1 / 16 to 1 / 256 of the
+// keys' bytes (2 x 128 of them per page); a lane loads its fragments from
+// global memory, 32 contiguous bytes of a page at a time, with no staging:
+// the channel order of a step is permuted alike in q' and digest.
+//
+// pick_kernel: per (token, KV head) the top_k of the scores.  Scores become
+// integers of the same order; forced pages the largest one.  The threshold,
+// the largest value that top_k scores reach, is found by a 4-ary search over
+// the value range (three counts per round, one barrier each), and one scan
+// writes the pages above it, and the first of those equal to it, in ascending
+// order: exact, without atomics, and independent of timing.
+
+#include "cache_kernels.cuh"
+#include "decode_attn.h"
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+namespace dattn {
+namespace {
+
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr float kBf16Max = 3.3895313892515355e38f;
+
+// tokens that new token t of a request of L tokens sees
+__device__ __forceinline__ int seen_tokens(const SelectArgs& a, int L, int t) {
+  return a.causal ? max(0, L - a.g.q_len + t + 1) : L;
+}
+
+__device__ __forceinline__ int clamp_len(const SelectArgs& a, int L) {
+  return min(max(L, 0), a.g.max_seq_len);
+}
+
+__device__ __forceinline__ uint32_t hsub2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t hmin2_0(uint32_t x) {
+  uint32_t r;
+  asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0u));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t hmax2_0(uint32_t x) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0u));
+  return r;
+}
+
+// Four signed bytes to two f16x2: byte + 128 under the exponent of 1024, less 1152.
+__device__ __forceinline__ void s8x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  constexpr uint32_t k1152 = 0x64806480u;
+  lo = hsub2(__byte_perm(u, 0x64646464u, 0x4140), k1152);
+  hi = hsub2(__byte_perm(u, 0x64646464u, 0x4342), k1152);
+}
+
+constexpr int kScoreWarps = 4;
+
+// Dynamic shared memory: q' fragments [row tiles][4 step pairs][32 lanes] of
+// 16 B, the rows' a / 127, then (several tokens) each warp's row scores
+// [rows][16 pages].
+__global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int g4 = lane >> 2;
+  const int t4 = lane & 3;
+  const int kvh = blockIdx.y;
+  const int b = blockIdx.z;
+  const int group = a.num_q_heads / a.g.num_kv_heads;
+  const int T = a.g.q_len;
+  const int rows = group * T;
+  const int tiles = (rows + 7) / 8;
+  uint4* q_frag = reinterpret_cast<uint4*>(smem);
+  float* q_scale = reinterpret_cast<float*>(smem + tiles * 2048);
+  float* row_score = q_scale + tiles * 8 + warp * tiles * 8 * 16;
+  grid_dependency_wait();
+
+  const int L = clamp_len(a, a.g.seq_lens[b]);
+  const int nb = (L + a.g.page_size - 1) / a.g.page_size;  // pages that any token sees
+  // (every page is taken: no scores are read)
+  if (nb <= a.top_k || static_cast<int>(blockIdx.x) * kScoreWarps * 16 >= nb) return;
+
+  // ---- q' of the rows, one warp per row tile
+  for (int nt = warp; nt < tiles; nt += kScoreWarps) {
+    const int r = nt * 8 + g4;
+    uint32_t w[16];
+    if (r < rows) {
+      const int t = r / group;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.q + static_cast<int64_t>(b) * a.q_sb + static_cast<int64_t>(t) * a.q_st +
+          static_cast<int64_t>(kvh * group + (r - t * group)) * a.q_sh + 32 * t4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 x = src[i];
+        w[4 * i] = x.x;
+        w[4 * i + 1] = x.y;
+        w[4 * i + 2] = x.z;
+        w[4 * i + 3] = x.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = 0u;
+    }
+    float x[32];
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float v = i & 1 ? __uint_as_float(w[i >> 1] & 0xffff0000u) : __uint_as_float(w[i >> 1] << 16);
+      x[i] = v == v ? fminf(fmaxf(v, -kBf16Max), kBf16Max) : 0.f;
+      top = fmaxf(top, fabsf(x[i]));
+    }
+    top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+    const float inv = top > 0.f ? __fdiv_rn(127.f, top) : 0.f;
+    uint32_t h[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float u = fminf(fmaxf(rintf(__fmul_rn(x[2 * i], inv)), -127.f), 127.f);
+      const float v = fminf(fmaxf(rintf(__fmul_rn(x[2 * i + 1], inv)), -127.f), 127.f);
+      h[i] = pack_f16x2(u, v);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      q_frag[(nt * 4 + i) * 32 + lane] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+    if (t4 == 0) q_scale[r] = __fdiv_rn(top, 127.f);
+  }
+  __syncthreads();
+
+  const int32_t* bt = a.g.block_table + static_cast<int64_t>(b) * a.g.bt_stride;
+  for (int tile = blockIdx.x * kScoreWarps + warp; tile * 16 < nb; tile += gridDim.x * kScoreWarps) {
+    // ---- the digests of pages tile * 16 + g4 and + 8: A fragments of 16 steps
+    uint32_t af[16][4];  // steps 0-7: minima, 8-15: maxima
+    float ds[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int col = min(tile * 16 + g4 + 8 * p, nb - 1);
+      int pg = __ldg(bt + col);
+      if (pg < 0 || pg >= a.g.num_pages) pg = 0;  // (reported by pick_kernel)
+      const int64_t at = static_cast<int64_t>(pg) * a.g.num_kv_heads + kvh;
+      ds[p] = __ldg(a.digest_scale + at);
+      const uint4* src = reinterpret_cast<const uint4*>(a.digest + at * 256 + 32 * t4);
+#pragma unroll
+      for (int mm = 0; mm < 2; ++mm) {
+        const uint4 x = __ldg(src + mm * 8), y = __ldg(src + mm * 8 + 1);
+        const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) s8x4_to_f16(w[ks], af[mm * 8 + ks][p], af[mm * 8 + ks][2 + p]);
+      }
+    }
+    float best[2] = {-INFINITY, -INFINITY};
+    for (int nt = 0; nt < tiles; ++nt) {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 q = q_frag[(nt * 4 + i) * 32 + lane];
+        mma_f16_16816(acc, af[2 * i], hmin2_0(q.x), hmin2_0(q.y));
+        mma_f16_16816(acc, af[2 * i + 1], hmin2_0(q.z), hmin2_0(q.w));
+        mma_f16_16816(acc, af[8 + 2 * i], hmax2_0(q.x), hmax2_0(q.y));
+        mma_f16_16816(acc, af[8 + 2 * i + 1], hmax2_0(q.z), hmax2_0(q.w));
+      }
+#pragma unroll
+      for (int rr = 0; rr < 2; ++rr) {
+        const int row = nt * 8 + 2 * t4 + rr;
+        if (row < rows) {
+          const float qs = q_scale[row];
+          const float u = __fmul_rn(__fmul_rn(acc[rr], ds[0]), qs);
+          const float v = __fmul_rn(__fmul_rn(acc[2 + rr], ds[1]), qs);
+          if (T == 1) {
+            best[0] = fmaxf(best[0], u);
+            best[1] = fmaxf(best[1], v);
+          } else {
+            row_score[row * 16 + g4] = u;
+            row_score[row * 16 + g4 + 8] = v;
+          }
+        }
+      }
+    }
+    if (T == 1) {
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        best[p] = fmaxf(best[p], __shfl_xor_sync(kFull, best[p], 1));
+        best[p] = fmaxf(best[p], __shfl_xor_sync(kFull, best[p], 2));
+      }
+      const int col = tile * 16 + g4 + 8 * t4;
+      if (t4 < 2 && col < nb)
+        a.scores[(static_cast<int64_t>(b) * a.g.num_kv_heads + kvh) * a.score_stride + col] =
+            t4 == 0 ? best[0] : best[1];
+    } else {
+      __syncwarp();
+      for (int i = lane; i < T * 16; i += 32) {
+        const int t = i >> 4;
+        const int col = tile * 16 + (i & 15);
+        float m = -INFINITY;
+        for (int g = 0; g < group; ++g) m = fmaxf(m, row_score[(t * group + g) * 16 + (i & 15)]);
+        if (col < nb)
+          a.scores[((static_cast<int64_t>(b) * T + t) * a.g.num_kv_heads + kvh) * a.score_stride + col] = m;
+      }
+      __syncwarp();
+    }
+  }
+}
+
+// Order-preserving integers of floats (no NaN among them); 0 is below all.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);  // (-0 counts as 0)
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+constexpr int kPer = 8;  // scores per thread and chunk
+
+// ONE: all pages fit one chunk of THREADS x kPer scores, held in registers;
+// otherwise every pass reads the chunks again (from L2).
+template <int THREADS, bool ONE>
+__global__ void __launch_bounds__(THREADS) pick_kernel(const SelectArgs a) {
+  constexpr int kWarps = THREADS / 32;
+  constexpr int kChunk = THREADS * kPer;
+  __shared__ uint32_t sh[2][3][kWarps];
+  __shared__ uint32_t scan[2][kWarps];
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = blockIdx.x;  // (b, t, kv head)
+  const int kvh = static_cast<int>(row % a.g.num_kv_heads);
+  const int64_t vb = row / a.g.num_kv_heads;
+  const int t = static_cast<int>(vb % a.g.q_len);
+  const int b = static_cast<int>(vb / a.g.q_len);
+  grid_dependency_wait();
+  const int raw = a.g.seq_lens[b];
+  const int L = clamp_len(a, raw);
+  uint32_t bad = raw != L ? DA_STATUS_SEQ_LEN : 0;
+  if (a.causal && L > 0 && L < a.g.q_len) bad |= DA_STATUS_SHORT_CAUSAL;
+  if (bad != 0 && a.g.status != nullptr && kvh == 0 && t == 0 && threadIdx.x == 0)
+    atomicOr(a.g.status, static_cast<int32_t>(bad));
+  const int Lt = seen_tokens(a, L, t);
+  const int ps = a.g.page_size;
+  const int count = (Lt + ps - 1) / ps;
+  const int K = a.top_k;
+  const int n_sel = min(count, K);
+  const int32_t* bt = a.g.block_table + static_cast<int64_t>(b) * a.g.bt_stride;
+  int32_t* pages = a.pages + row * K;
+  int32_t* blocks = a.blocks != nullptr ? a.blocks + row * K : nullptr;
+  auto put = [&](int at, int col) {
+    int pg = bt[col];
+    if (pg < 0 || pg >= a.g.num_pages) {
+      if (a.g.status != nullptr) atomicOr(a.g.status, static_cast<int32_t>(DA_STATUS_BAD_PAGE));
+      pg = 0;
+    }
+    pages[at] = pg;
+    if (blocks != nullptr) blocks[at] = col;
+  };
+  for (int i = n_sel + threadIdx.x; i < K; i += THREADS) {
+    pages[i] = 0;
+    if (blocks != nullptr) blocks[i] = -1;
+  }
+  if (threadIdx.x == 0) a.tokens[row] = count > 0 ? (n_sel - 1) * ps + (Lt - (count - 1) * ps) : 0;
+  if (count <= K) {
+    for (int i = threadIdx.x; i < count; i += THREADS) put(i, i);
+    return;
+  }
+
+  const float* sc = a.scores + row * a.score_stride;
+  const int local0 = count - a.local;  // (top_k >= sink + local, so local0 > sink here)
+  auto load = [&](int c0, uint32_t (&key)[kPer]) {
+    const int e0 = c0 + threadIdx.x * kPer;
+#pragma unroll
+    for (int v = 0; v < kPer / 4; ++v) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (e0 + 4 * v < count) x = *reinterpret_cast<const float4*>(sc + e0 + 4 * v);
+      key[4 * v] = ordered(x.x);
+      key[4 * v + 1] = ordered(x.y);
+      key[4 * v + 2] = ordered(x.z);
+      key[4 * v + 3] = ordered(x.w);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = e0 + i;
+      if (e < a.sink || e >= local0) key[i] = 0xffffffffu;
+      if (e >= count) key[i] = 0u;
+    }
+  };
+  const int chunks = ONE ? 1 : (count + kChunk - 1) / kChunk;
+  uint32_t key[kPer];
+  if constexpr (ONE) load(0, key);
+
+  // ---- the largest thr with at least K keys >= thr; all of [lo, hi] brackets it:
+  // count(>= lo) >= K always, count(>= hi + 1) < K once hi is below the maximum
+  uint32_t lo = 1, hi = 0xffffffffu;
+  bool exact = false;  // exactly K keys are >= lo
+  int round = 0;
+  while (lo < hi && !exact) {
+    // three probes in (lo, hi]
+    const uint32_t span = hi - lo;
+    uint32_t probe[3];
+    probe[0] = lo + (span >> 2) + (span < 4 ? 1 : 0);
+    probe[1] = lo + (span >> 1) + (span < 4 ? 1 : 0);
+    probe[2] = lo + (span >> 1) + (span >> 2) + (span < 4 ? 1 : 0);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) probe[i] = min(probe[i], hi);
+    uint32_t n[3] = {0, 0, 0};
+    for (int c = 0; c < chunks; ++c) {
+      if constexpr (!ONE) load(c * kChunk, key);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        n[0] += key[i] >= probe[0];
+        n[1] += key[i] >= probe[1];
+        n[2] += key[i] >= probe[2];
+      }
+    }
+    const int buf = round & 1;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const uint32_t s = __reduce_add_sync(kFull, n[i]);
+      if (lane == 0) sh[buf][i][warp] = s;
+    }
+    __syncthreads();  // (the other buffer is written next: one barrier per round)
+#pragma unroll
+    for (int i = 0; i < 3; ++i) n[i] = __reduce_add_sync(kFull, lane < kWarps ? sh[buf][i][lane] : 0u);
+    const uint32_t k = static_cast<uint32_t>(K);
+    uint32_t new_lo = lo, new_hi = hi;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      if (n[i] >= k) {
+        new_lo = max(new_lo, probe[i]);
+        if (n[i] == k) exact = true;  // (then probes above have fewer or the same)
+      } else {
+        new_hi = min(new_hi, probe[i] - 1);
+      }
+    }
+    if (exact) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (n[i] == k) new_lo = probe[i];
+    }
+    lo = new_lo;
+    hi = new_hi;
+    ++round;
+  }
+  // selected: keys above `above`, and the first `take` of those equal to it
+  const uint32_t above = exact ? lo - 1 : lo;
+
+  // ---- how many equal ones to take: K less those above
+  __syncthreads();
+  uint32_t take = 0;
+  if (!exact) {
+    uint32_t gt = 0;
+    for (int c = 0; c < chunks; ++c) {
+      if constexpr (!ONE) load(c * kChunk, key);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) gt += key[i] > above;
+    }
+    gt = __reduce_add_sync(kFull, gt);
+    if (lane == 0) sh[0][0][warp] = gt;
+    __syncthreads();
+    gt = __reduce_add_sync(kFull, lane < kWarps ? sh[0][0][lane] : 0u);
+    take = static_cast<uint32_t>(K) - gt;
+  }
+
+  // ---- one scan in page order
+  uint32_t gt0 = 0, eq0 = 0;  // in the chunks before
+  for (int c = 0; c < chunks; ++c) {
+    if constexpr (!ONE) load(c * kChunk, key);
+    uint32_t gt = 0, eq = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      gt += key[i] > above;
+      eq += take != 0 && key[i] == above;
+    }
+    uint32_t g = gt, q = eq;  // inclusive scans over the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(kFull, g, o), y = __shfl_up_sync(kFull, q, o);
+      if (lane >= o) {
+        g += x;
+        q += y;
+      }
+    }
+    if (lane == 31) {
+      scan[0][warp] = g;
+      scan[1][warp] = q;
+    }
+    __syncthreads();
+    const uint32_t wg = lane < kWarps ? scan[0][lane] : 0u, wq = lane < kWarps ? scan[1][lane] : 0u;
+    uint32_t bg = gt0 + g - gt + __reduce_add_sync(kFull, lane < warp ? wg : 0u);
+    uint32_t bq = eq0 + q - eq + __reduce_add_sync(kFull, lane < warp ? wq : 0u);
+    gt0 += __reduce_add_sync(kFull, wg);
+    eq0 += __reduce_add_sync(kFull, wq);
+    const int e0 = c * kChunk + threadIdx.x * kPer;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const bool up = key[i] > above;
+      const bool same = take != 0 && key[i] == above && bq < take;
+      if (up || same) put(static_cast<int>(bg + min(bq, take)), e0 + i);
+      bg += up;
+      bq += take != 0 && key[i] == above;
+    }
+    __syncthreads();  // (scan[] is written again)
+  }
+}
+
+template <class Kernel, class Args>
+cudaError_t launch(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const Args& a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+}  // namespace
+
+cudaError_t launch_select(const SelectArgs& a, int sm_count, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(a.g.batch) * a.g.q_len * a.g.num_kv_heads;
+  if (rows == 0) return cudaSuccess;
+  if (a.max_blocks > a.top_k) {
+    const int q_rows = a.num_q_heads / a.g.num_kv_heads * a.g.q_len;
+    const int tiles = (q_rows + 7) / 8;
+    const size_t smem = static_cast<size_t>(tiles) * 2048 + tiles * 32 +
+                        (a.g.q_len > 1 ? static_cast<size_t>(kScoreWarps) * tiles * 512 : 0);
+    if (smem > 48 * 1024) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(smem));
+      if (e != cudaSuccess) return e;
+    }
+    // a tile of 16 pages per warp, several per warp once the grid has about
+    // eight CTAs per SM (each CTA prepares q' again)
+    const int64_t full = (a.max_blocks + kScoreWarps * 16 - 1) / (kScoreWarps * 16);
+    const int64_t pairs = static_cast<int64_t>(a.g.batch) * a.g.num_kv_heads;
+    int64_t x = (8 * static_cast<int64_t>(sm_count) + pairs - 1) / pairs;
+    x = x < full ? x : full;
+    const cudaError_t e =
+        launch(score_kernel, dim3(static_cast<unsigned>(x), a.g.num_kv_heads, a.g.batch),
+               32 * kScoreWarps, smem, stream, a);
+    if (e != cudaSuccess) return e;
+  }
+  const dim3 grid(static_cast<unsigned>(rows));
+  if (a.max_blocks <= 256 * kPer) return launch(pick_kernel<256, true>, grid, 256, 0, stream, a);
+  if (a.max_blocks <= 1024 * kPer) return launch(pick_kernel<1024, true>, grid, 1024, 0, stream, a);
+  return launch(pick_kernel<1024, false>, grid, 1024, 0, stream, a);
+}
+
+}  // namespace dattn

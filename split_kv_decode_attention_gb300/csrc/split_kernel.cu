@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
     split = blockIdx.x;
     kvh = blockIdx.y;
     b = blockIdx.z;
-    L = a.seq_lens[b];  // (under the cluster merge its load overlaps the set-up)
+    L = a.seq_lens[static_cast<int64_t>(b) * a.len_sb + static_cast<int64_t>(kvh) * a.len_sh];  // (under the cluster merge its load overlaps the set-up)
     chunk = a.chunk_len;
   }
   // the request length, clamped, with its status bits (grid-planned calls)
@@ -242,7 +242,10 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
       prefetch_tensor_map(&v_map);
     }
     const uint64_t policy = l2_evict_first_policy();
-    const int32_t* bt_row = a.paged ? a.block_table + static_cast<int64_t>(b) * a.bt_stride : nullptr;
+    const int32_t* bt_row =
+        a.paged ? a.block_table + static_cast<int64_t>(b) * a.bt_stride +
+                      static_cast<int64_t>(kvh) * a.bt_sh
+                : nullptr;
     // physical page of tile (it * TPS + lane); fetched one stage ahead
     PageWindow pw{bt_row, t_begin, n_tiles, a.page_size, a.num_pages, lane, a.status, 0, 0, 0};
     if (a.paged) pw.init();

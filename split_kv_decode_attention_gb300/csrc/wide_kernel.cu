@@ -281,7 +281,8 @@ __global__ void __launch_bounds__(WCfg<F8>::kThreads, 1)
 
   int L0 = 0;  // one item per CTA: its request's clamped length
   if (!persistent) {
-    int L = a.seq_lens[blockIdx.z];
+    int L = a.seq_lens[static_cast<int64_t>(blockIdx.z) * a.len_sb +
+                       static_cast<int64_t>(blockIdx.y) * a.len_sh];
     uint32_t bad = 0;
     if (L < 0 || L > a.max_seq_len) {
       bad |= DA_STATUS_SEQ_LEN;
@@ -496,7 +497,8 @@ __global__ void __launch_bounds__(WCfg<F8>::kThreads, 1)
       // (per-item constants hoisted: the producers' instruction count per
       // stage sets the stage pace)
       const int32_t* bt_row =
-          a.paged && bx < C::kBoxes ? a.block_table + static_cast<int64_t>(it.b) * a.bt_stride
+          a.paged && bx < C::kBoxes ? a.block_table + static_cast<int64_t>(it.b) * a.bt_stride +
+                                        static_cast<int64_t>(it.kvh) * a.bt_sh
                                     : nullptr;
       const int tok_lane = it.t_begin + ti * kTileTokens;  // this lane's tile start, stage 0
       const int tile_lane_end = it.n_tiles - ti;          // stage i has data if i * kWTiles < this
@@ -1160,7 +1162,8 @@ cudaError_t launch_wide_t(const CUtensorMap& k_map, const CUtensorMap& v_map, co
   cudaError_t e = ensure_wide_attrs<F8>(&sms);
   if (e != cudaSuccess) return e;
   SplitArgs pa = a;
-  pa.persistent = a.batch <= kWMaxSchedBatch ? 1 : 0;
+  // (a length per kv head: one CTA per item, the schedule is by request)
+  pa.persistent = a.batch <= kWMaxSchedBatch && a.len_sh == 0 ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
   // persistent: one CTA per SM (at most one per possible item); otherwise one
   // CTA per item.  Device-planned calls (batch <= kWMaxSchedBatch, checked by
