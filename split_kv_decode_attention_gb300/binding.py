@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libdecode_attn.so (C ABI in include/decode_attn.h).
+"""Thin binding of libdecode_attn.so (C ABI in include/decode_attn.h): ctypes, and
+for the operators around the cache the extension native/calls.cpp.
 
 Argument marshalling only: torch tensors supply device memory and streams,
 every step of the computation runs in the library's CUDA kernels.  The names
@@ -14,6 +15,7 @@ from typing import Optional, Tuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libdecode_attn.so")
+CALLS_PATH = os.path.join(_PKG, "lib", "_calls.so")
 
 HEAD_DIM = 128
 MAX_ROWS = 128
@@ -285,9 +287,11 @@ def decode_attn(q, k_cache, v_cache, block_table, seq_lens, *, max_seq_len: int,
     import torch
 
     if k_sf is not None or v_sf is not None:
-        return _decode_attn_fp4(q, k_cache, v_cache, k_sf, v_sf, block_table, seq_lens,
-                                max_seq_len, causal, scale, num_splits, out, lse, workspace,
-                                status, stream, params, two_pass, k_scale, v_scale)
+        if params is not None:
+            raise ValueError("params cannot describe a 4-bit cache")
+        return _calls().decode_cached(q, k_cache, v_cache, k_sf, v_sf, block_table, seq_lens,
+                                      max_seq_len, causal, scale, num_splits, out, lse, workspace,
+                                      status, stream, two_pass, k_scale, v_scale)
     B, T, Hq, D = q.shape
     if out is None:
         out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=q.device)
@@ -441,165 +445,29 @@ def decode_attn_static_workspace(p: DecodeAttnParams, q, k_cache, v_cache, block
 # ---------------------------------------------------------------------------
 # The operators around the cache
 
-def _dtype(t, want, name):
-    if t.dtype not in want:
-        raise ValueError(f"{name} is {t.dtype}; expected {' or '.join(str(w) for w in want)}")
+_calls_module = None
 
 
-def _on_current_device(*tensors):
-    """Every given tensor lies on the current CUDA device (the one whose stream
-    the call takes and whose planner it asks)."""
-    import torch
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != cur:
-            raise ValueError(f"a tensor is on {t.device}, the current CUDA device is {cur}")
+def _calls():
+    """The extension lib/_calls.so (raises if it has not been built)."""
+    global _calls_module
+    if _calls_module is None:
+        import importlib.machinery
+        import importlib.util
 
-
-def _cache_args(k_cache, v_cache, k_sf, v_sf, block_table):
-    """(DecodeAttnCache, groups, tokens, kv heads) of cache tensors."""
-    import torch
-    if k_sf is not None or v_sf is not None:
-        ctype, width = DA_CACHE_FP4_E2M1, HEAD_DIM // 2
-        if k_sf is None or (v_cache is not None and v_sf is None):
-            raise ValueError("a 4-bit cache needs the block scales of K and of V")
-        _dtype(k_cache, (torch.uint8,), "k_cache")
-    elif k_cache.element_size() == 1:
-        ctype, width = DA_CACHE_FP8_E4M3, HEAD_DIM
-        _dtype(k_cache, (torch.uint8, torch.float8_e4m3fn), "k_cache")
-    else:
-        ctype, width = DA_CACHE_BF16, HEAD_DIM
-        _dtype(k_cache, (torch.bfloat16,), "k_cache")
-    if k_cache.dim() != 4 or k_cache.shape[3] != width or k_cache.stride(3) != 1:
-        raise ValueError(f"k_cache must be [groups, tokens, heads, {width}], its last dimension dense")
-    if v_cache is not None and (v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride()
-                                or v_cache.dtype != k_cache.dtype):
-        raise ValueError("k_cache and v_cache differ in shape, strides or type")
-    groups, tokens, heads, _ = k_cache.shape
-    c = DecodeAttnCache()
-    c.type = ctype
-    c.k, c.v = _ptr(k_cache), _ptr(v_cache)
-    if ctype == DA_CACHE_FP4_E2M1:
-        for t, name in ((k_sf, "k_sf"), (v_sf, "v_sf")):
-            if t is None:
-                continue
-            _dtype(t, (torch.uint8, torch.float8_e4m3fn), name)
-            if t.shape != (groups, heads, tokens, 8) or t.stride()[2:] != (8, 1):
-                raise ValueError(f"{name} must be [{groups}, {heads}, {tokens}, 8] with dense tokens")
-        if v_sf is not None and v_sf.stride() != k_sf.stride():
-            raise ValueError("k_sf and v_sf differ in strides")
-        c.k_block_scale, c.v_block_scale = _ptr(k_sf), _ptr(v_sf)
-        c.bs_stride_page, c.bs_stride_head = k_sf.stride(0), k_sf.stride(1)
-    _dtype_int(block_table, "block_table")
-    return c, groups, tokens, heads
-
-
-def _dtype_int(t, name):
-    import torch
-    if t is not None:
-        _dtype(t, (torch.int32,), name)
-        if t.dim() > 0 and t.numel() > 1 and t.stride(-1) != 1:
-            raise ValueError(f"{name} must be dense in its last dimension")
-
-
-def _cache_params(B, T, Hq, k_cache, block_table, max_seq_len, causal, scale, k_scale, v_scale,
-                  flags=0):
-    groups, tokens, heads, _ = k_cache.shape
-    p = DecodeAttnParams()
-    p.batch, p.q_len, p.num_q_heads, p.num_kv_heads, p.head_dim = B, T, Hq, heads, HEAD_DIM
-    p.max_seq_len, p.causal, p.flags = int(max_seq_len), 1 if causal else 0, flags
-    p.scale = float(scale if scale is not None else 1.0 / math.sqrt(HEAD_DIM))
-    p.kv_stride_page, p.kv_stride_token, p.kv_stride_head = k_cache.stride()[:3]
-    p.k_scale, p.v_scale = float(k_scale), float(v_scale)
-    if block_table is not None:
-        if block_table.dim() != 2 or block_table.shape[0] != B:
-            raise ValueError("block_table must be [batch, pages]")
-        p.page_size, p.num_pages = tokens, groups
-        p.max_pages_per_seq, p.block_table_stride = block_table.shape[1], block_table.stride(0)
-    elif groups != B or tokens < max_seq_len:
-        raise ValueError("a contiguous cache holds max_seq_len tokens of every request")
-    return p
-
-
-def _q_strides(p, q, out):
-    p.q_stride_batch, p.q_stride_token, p.q_stride_head = q.stride()[:3]
-    p.o_stride_batch, p.o_stride_token, p.o_stride_head = out.stride()[:3]
-
-
-def _heads_tensor(t, B, T, name):
-    import torch
-    _dtype(t, (torch.bfloat16,), name)
-    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != T or t.shape[3] != HEAD_DIM or t.stride(3) != 1:
-        raise ValueError(f"{name} must be [{B}, {T}, heads, {HEAD_DIM}], its last dimension dense")
-
-
-def _lens_tensor(t, B, name="seq_lens"):
-    _dtype_int(t, name)
-    if t.shape != (B,):
-        raise ValueError(f"{name} must be [{B}]")
-
-
-def _outputs(q, out, lse):
-    import torch
-    B, T, Hq, D = q.shape
-    if out is None:
-        out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=q.device)
-    else:
-        _heads_tensor(out, B, T, "out")
-        if out.shape[2] != Hq:
-            raise ValueError("out and q differ in heads")
-    if lse is None:
-        lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
-    else:
-        _dtype(lse, (torch.float32,), "lse")
-        if lse.shape != (B, T, Hq) or not lse.is_contiguous():
-            raise ValueError(f"lse must be dense [{B}, {T}, {Hq}]")
-    return out, lse
-
-
-def _workspace(given, need, device):
-    import torch
-    if need == 0:
-        return given
-    if given is None or given.numel() * given.element_size() < need:
-        return torch.empty((need + 15) // 16 * 4, dtype=torch.float32, device=device)
-    return given
-
-
-def _status_word(status):
-    import torch
-    if status is not None:
-        _dtype(status, (torch.int32,), "status")
-    return _ptr(status)
-
-
-def _decode_attn_fp4(q, k_cache, v_cache, k_sf, v_sf, block_table, seq_lens, max_seq_len, causal,
-                     scale, num_splits, out, lse, workspace, status, stream, params, two_pass,
-                     k_scale, v_scale):
-    B, T, Hq, _ = q.shape
-    _heads_tensor(q, B, T, "q")
-    _lens_tensor(seq_lens, B)
-    c, _, _, heads = _cache_args(k_cache, v_cache, k_sf, v_sf, block_table)
-    _on_current_device(q, k_cache, v_cache, k_sf, v_sf, block_table, seq_lens, out, lse, workspace,
-                       status)
-    out, lse = _outputs(q, out, lse)
-    p = params
-    if p is None:
-        p = _cache_params(B, T, Hq, k_cache, block_table, max_seq_len, causal, scale, k_scale,
-                          v_scale, DA_FLAG_TWO_PASS if two_pass else 0)
-        _q_strides(p, q, out)
-    num_splits = max(0, int(num_splits))
-    n = ctypes.c_size_t()
-    _check(lib().decode_attn_cached_workspace_bytes(ctypes.byref(p), ctypes.byref(c), num_splits,
-                                                    ctypes.byref(n)),
-           "decode_attn_cached_workspace_bytes")
-    workspace = _workspace(workspace, n.value, q.device)
-    _check(lib().decode_attn_cached(
-        ctypes.byref(p), ctypes.byref(c), _ptr(q), _ptr(block_table), _ptr(seq_lens), _ptr(out),
-        _ptr(lse), num_splits, _ptr(workspace), 0 if workspace is None else
-        workspace.numel() * workspace.element_size(), _status_word(status),
-        _stream_handle(stream)), "decode_attn_cached")
-    return out, lse
+        import torch  # noqa: F401  (its libraries are loaded first)
+        lib()
+        if not os.path.exists(CALLS_PATH):
+            raise RuntimeError(
+                f"{CALLS_PATH} is missing: build it with "
+                "`python -c 'import __graft_entry__ as g; g.build()'`")
+        loader = importlib.machinery.ExtensionFileLoader("_calls", CALLS_PATH)
+        module = importlib.util.module_from_spec(
+            importlib.util.spec_from_file_location("_calls", CALLS_PATH, loader=loader))
+        loader.exec_module(module)
+        module.set_error(DecodeAttnError)
+        _calls_module = module
+    return _calls_module
 
 
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[str] = None,
@@ -659,22 +527,7 @@ def rope_table(inv_freq, max_pos: int, *, amplitude: float = 1.0, first: int = 0
                stream=None):
     """fp32 [max_pos, 2 n]: amplitude * cos, then sin, of (first + row) * inv_freq,
     for inv_freq float64 [n] in device memory (rope_frequencies() gives it)."""
-    import torch
-    _dtype(inv_freq, (torch.float64,), "inv_freq")
-    if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-        raise ValueError("inv_freq must be a dense vector")
-    _on_current_device(inv_freq, out)
-    n = inv_freq.shape[0]
-    if out is None:
-        out = torch.empty((max_pos, 2 * n), dtype=torch.float32, device=inv_freq.device)
-    else:
-        _dtype(out, (torch.float32,), "out")
-        if out.shape != (max_pos, 2 * n) or not out.is_contiguous():
-            raise ValueError(f"out must be dense [{max_pos}, {2 * n}]")
-    _check(lib().decode_attn_rope_table(_ptr(inv_freq), n, int(first), int(max_pos),
-                                        float(amplitude), _ptr(out), _stream_handle(stream)),
-           "decode_attn_rope_table")
-    return out
+    return _calls().rope_table(inv_freq, max_pos, amplitude, first, out, stream)
 
 
 def rope_append(q, k, v, table, k_cache, v_cache, block_table, seq_lens, *, max_seq_len: int,
@@ -686,67 +539,9 @@ def rope_append(q, k, v, table, k_cache, v_cache, block_table, seq_lens, *, max_
     rotary_dim] (None: no rotation), `positions` int32 [B, q_len] overrides the
     cache positions as angles.  k and v None: only q is rotated; q None: only
     the caches are written.  q_out may be q."""
-    import torch
-    lead = q if q is not None else k
-    if lead is None or (k is None) != (v is None):
-        raise ValueError("q, or k and v, or all three are needed")
-    B, T = lead.shape[:2]
-    c, _, _, heads = _cache_args(k_cache, v_cache, k_sf, v_sf, block_table)
-    if c.type == DA_CACHE_FP4_E2M1 and v_sf is None:
-        raise ValueError("a 4-bit cache needs the block scales of K and of V")
-    _lens_tensor(seq_lens, B)
-    r = DecodeAttnRope()
-    if table is not None:
-        _dtype(table, (torch.float32,), "table")
-        if table.dim() != 2 or not table.is_contiguous():
-            raise ValueError("table must be dense [positions, rotary_dim]")
-        r.table_positions, r.rotary_dim = table.shape
-    r.interleaved = 1 if interleaved else 0
-    if k is not None:
-        for t, name in ((k, "k"), (v, "v")):
-            _heads_tensor(t, B, T, name)
-            if t.shape[2] != heads:
-                raise ValueError(f"{name} has {t.shape[2]} heads, the cache {heads}")
-        r.k_stride_batch, r.k_stride_token, r.k_stride_head = k.stride()[:3]
-        r.v_stride_batch, r.v_stride_token, r.v_stride_head = v.stride()[:3]
-    p = _cache_params(B, T, heads, k_cache, block_table, max_seq_len, False, 1.0, k_scale, v_scale)
-    if q is not None:
-        _heads_tensor(q, B, T, "q")
-        if q.shape[2] % heads:
-            raise ValueError(f"{q.shape[2]} query heads are no multiple of {heads}")
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        else:
-            _heads_tensor(q_out, B, T, "q_out")
-            if q_out.shape != q.shape:
-                raise ValueError("q_out and q differ in shape")
-        p.num_q_heads = q.shape[2]
-        _q_strides(p, q, q_out)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    if positions is not None:
-        _dtype_int(positions, "positions")
-        if positions.shape != (B, T) or not positions.is_contiguous():
-            raise ValueError(f"positions must be dense [{B}, {T}]")
-    if new_lens is not None:
-        _lens_tensor(new_lens, B, "new_lens")
-    _on_current_device(q, k, v, table, k_cache, v_cache, k_sf, v_sf, block_table, seq_lens, q_out,
-                       positions, new_lens, status)
-    _check(lib().decode_attn_rope_append(
-        ctypes.byref(p), ctypes.byref(c), ctypes.byref(r), _ptr(q), _ptr(k), _ptr(v), _ptr(table),
-        _ptr(positions), _ptr(new_lens), _ptr(block_table), _ptr(seq_lens), _ptr(q_out),
-        _status_word(status), _stream_handle(stream)), "decode_attn_rope_append")
-    return q_out
-
-
-def _digest_tensors(digest, digest_scale, pages, heads):
-    import torch
-    _dtype(digest, (torch.int8,), "digest")
-    _dtype(digest_scale, (torch.float32,), "digest_scale")
-    if digest.shape != (pages, heads, 2, HEAD_DIM) or not digest.is_contiguous():
-        raise ValueError(f"digest must be dense [{pages}, {heads}, 2, {HEAD_DIM}]")
-    if digest_scale.shape != (pages, heads) or not digest_scale.is_contiguous():
-        raise ValueError(f"digest_scale must be dense [{pages}, {heads}]")
+    return _calls().rope_append(q, k, v, table, k_cache, v_cache, block_table, seq_lens,
+                                max_seq_len, interleaved, positions, new_lens, k_scale, v_scale,
+                                k_sf, v_sf, q_out, status, stream)
 
 
 def block_digest(k_cache, block_table, seq_lens, digest=None, digest_scale=None, *,
@@ -755,37 +550,8 @@ def block_digest(k_cache, block_table, seq_lens, digest=None, digest_scale=None,
     [P, Hkv, 2, 128], digest_scale fp32 [P, Hkv]), allocated (zero) when not
     given.  max_new > 0 digests only the pages that hold each request's last
     max_new tokens: what a decode step has changed."""
-    import torch
-    if block_table is None:
-        raise ValueError("digests are per page: a block_table is needed")
-    B = block_table.shape[0]
-    c, pages, _, heads = _cache_args(k_cache, None, k_sf, None, block_table)
-    _lens_tensor(seq_lens, B)
-    if digest is None:
-        digest = torch.zeros((pages, heads, 2, HEAD_DIM), dtype=torch.int8, device=k_cache.device)
-    if digest_scale is None:
-        digest_scale = torch.zeros((pages, heads), dtype=torch.float32, device=k_cache.device)
-    _digest_tensors(digest, digest_scale, pages, heads)
-    p = _cache_params(B, 1, heads, k_cache, block_table, max_seq_len, False, 1.0, 1.0, 1.0)
-    _on_current_device(k_cache, k_sf, block_table, seq_lens, digest, digest_scale, status)
-    _check(lib().decode_attn_block_digest(
-        ctypes.byref(p), ctypes.byref(c), _ptr(block_table), _ptr(seq_lens), int(max_new),
-        _ptr(digest), _ptr(digest_scale), _status_word(status), _stream_handle(stream)),
-        "decode_attn_block_digest")
-    return digest, digest_scale
-
-
-def _select_args(top_k, sink, local):
-    s = DecodeAttnSelect()
-    s.top_k, s.sink, s.local = int(top_k), int(sink), int(local)
-    return s
-
-
-def _blocks_tensor(blocks, shape):
-    import torch
-    _dtype(blocks, (torch.int32,), "blocks")
-    if blocks.shape != shape or not blocks.is_contiguous():
-        raise ValueError(f"blocks must be dense {list(shape)}")
+    return _calls().block_digest(k_cache, block_table, seq_lens, digest, digest_scale, max_seq_len,
+                                 max_new, k_sf, status, stream)
 
 
 def block_select(q, digest, digest_scale, block_table, seq_lens, *, page_size: int,
@@ -794,40 +560,9 @@ def block_select(q, digest, digest_scale, block_table, seq_lens, *, page_size: i
     """The pages decode_attn_sparse() would read: (blocks int32 [B, q_len, Hkv,
     top_k], the pages' places in each request, ascending, -1 behind the last;
     pages, their ids; tokens int32 [B, q_len, Hkv], how many tokens they hold)."""
-    import torch
-    B, T, Hq, _ = q.shape
-    _heads_tensor(q, B, T, "q")
-    _dtype_int(block_table, "block_table")
-    _lens_tensor(seq_lens, B)
-    pages, heads = digest.shape[:2]
-    _digest_tensors(digest, digest_scale, pages, heads)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table must be [batch, pages]")
-    p = DecodeAttnParams()
-    p.batch, p.q_len, p.num_q_heads, p.num_kv_heads, p.head_dim = B, T, Hq, heads, HEAD_DIM
-    p.page_size, p.num_pages, p.max_seq_len = int(page_size), pages, int(max_seq_len)
-    p.max_pages_per_seq, p.block_table_stride = block_table.shape[1], block_table.stride(0)
-    p.causal, p.scale = 1 if causal else 0, 1.0
-    _q_strides(p, q, q)
-    s = _select_args(top_k, sink, local)
-    n = ctypes.c_size_t()
-    _check(lib().decode_attn_block_select_workspace_bytes(ctypes.byref(p), ctypes.byref(s),
-                                                          ctypes.byref(n)),
-           "decode_attn_block_select_workspace_bytes")
-    workspace = _workspace(workspace, n.value, q.device)
-    shape = (B, T, heads, s.top_k)
-    if blocks is None:
-        blocks = torch.empty(shape, dtype=torch.int32, device=q.device)
-    _blocks_tensor(blocks, shape)
-    ids = torch.empty(shape, dtype=torch.int32, device=q.device)
-    tokens = torch.empty(shape[:3], dtype=torch.int32, device=q.device)
-    _on_current_device(q, digest, digest_scale, block_table, seq_lens, blocks, workspace, status)
-    _check(lib().decode_attn_block_select(
-        ctypes.byref(p), ctypes.byref(s), _ptr(q), _ptr(digest), _ptr(digest_scale),
-        _ptr(block_table), _ptr(seq_lens), _ptr(blocks), _ptr(ids), _ptr(tokens), _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(),
-        _status_word(status), _stream_handle(stream)), "decode_attn_block_select")
-    return blocks, ids, tokens
+    return _calls().block_select(q, digest, digest_scale, block_table, seq_lens, page_size,
+                                 max_seq_len, top_k, sink, local, causal, blocks, workspace,
+                                 status, stream)
 
 
 def decode_attn_sparse(q, k_cache, v_cache, block_table, seq_lens, digest, digest_scale, *,
@@ -838,33 +573,6 @@ def decode_attn_sparse(q, k_cache, v_cache, block_table, seq_lens, digest, diges
     """Decode attention over the top_k pages per (token, KV head) that the digests
     of block_digest() score highest, the first `sink` and last `local` pages
     always among them: (out, lse, blocks).  Any cache type, as decode_attn()."""
-    import torch
-    B, T, Hq, _ = q.shape
-    _heads_tensor(q, B, T, "q")
-    _lens_tensor(seq_lens, B)
-    if block_table is None:
-        raise ValueError("the selection is of pages: a block_table is needed")
-    c, pages, _, heads = _cache_args(k_cache, v_cache, k_sf, v_sf, block_table)
-    _digest_tensors(digest, digest_scale, pages, heads)
-    _on_current_device(q, k_cache, v_cache, k_sf, v_sf, block_table, seq_lens, digest, digest_scale,
-                       out, lse, blocks, workspace, status)
-    out, lse = _outputs(q, out, lse)
-    p = _cache_params(B, T, Hq, k_cache, block_table, max_seq_len, causal, scale, k_scale, v_scale)
-    _q_strides(p, q, out)
-    s = _select_args(top_k, sink, local)
-    shape = (B, T, heads, s.top_k)
-    if blocks is None:
-        blocks = torch.empty(shape, dtype=torch.int32, device=q.device)
-    else:
-        _blocks_tensor(blocks, shape)
-    n = ctypes.c_size_t()
-    _check(lib().decode_attn_sparse_workspace_bytes(ctypes.byref(p), ctypes.byref(c),
-                                                    ctypes.byref(s), ctypes.byref(n)),
-           "decode_attn_sparse_workspace_bytes")
-    workspace = _workspace(workspace, n.value, q.device)
-    _check(lib().decode_attn_sparse(
-        ctypes.byref(p), ctypes.byref(c), ctypes.byref(s), _ptr(q), _ptr(digest),
-        _ptr(digest_scale), _ptr(block_table), _ptr(seq_lens), _ptr(out), _ptr(lse), _ptr(blocks),
-        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-        _status_word(status), _stream_handle(stream)), "decode_attn_sparse")
-    return out, lse, blocks
+    return _calls().sparse(q, k_cache, v_cache, block_table, seq_lens, digest, digest_scale,
+                           max_seq_len, top_k, sink, local, causal, scale, k_scale, v_scale, k_sf,
+                           v_sf, out, lse, blocks, workspace, status, stream)
