@@ -423,9 +423,9 @@ typedef struct decode_attn_cache {
   int32_t reserved;           /* 0 */
   void *k;                    /* caches, 16-byte aligned */
   void *v;
-  void *k_block_scale;        /* DA_CACHE_FP4_E2M1: 8-byte aligned; else ignored */
+  void *k_block_scale;        /* DA_CACHE_FP4_E2M1: 16-byte aligned; else ignored */
   void *v_block_scale;
-  int64_t bs_stride_page;     /* bytes, positive multiples of 8 */
+  int64_t bs_stride_page;     /* bytes, positive multiples of 16 */
   int64_t bs_stride_head;
 } decode_attn_cache;
 
@@ -434,7 +434,9 @@ typedef struct decode_attn_cache {
  * decode_attn() runs them, 4-bit ones run their own split kernel (the same
  * planner, partials, device planning and combine; every row count up to
  * DECODE_ATTN_MAX_ROWS; no cluster merge, so more than one chunk always takes
- * the workspace).  k_scale and v_scale are finite.
+ * the workspace).  Its chunks are multiples of 64 tokens, so num_splits may
+ * come out lower, and an item of a device plan may hold several KV heads.
+ * k_scale and v_scale are finite.
  */
 int decode_attn_cached_workspace_bytes(const decode_attn_params *p,
                                        const decode_attn_cache *c, int32_t num_splits,

@@ -111,8 +111,9 @@ int check_shape(const decode_attn_params* p, bool rows_limit = true) {
 }
 
 int chunk_for_splits(const decode_attn_params* p, int32_t num_splits, int32_t* chunk,
-                     int32_t* splits_eff) {
-  return dattn::plan_chunk_for_splits(p->max_seq_len, num_splits, chunk, splits_eff)
+                     int32_t* splits_eff, int unit = 0) {
+  return dattn::plan_chunk_for_splits(p->max_seq_len, num_splits, chunk, splits_eff,
+                                      unit > 0 ? dattn::kFp4Tile : dattn::kPlanTile)
              ? DA_OK
              : DA_ERR_SPLITS;
 }
@@ -121,17 +122,20 @@ int chunk_for_splits(const decode_attn_params* p, int32_t num_splits, int32_t* c
 // planner kernel): a function of the shape, the host lengths and the number
 // of CTAs the split launch keeps resident at once (SMs x CTAs per SM).
 int plan_for_slots(const decode_attn_params* p, const int32_t* host_seq_lens, int64_t slots,
-                   int32_t* num_splits, int32_t* chunk_len) {
+                   int32_t* num_splits, int32_t* chunk_len, int unit = 0) {
   dattn::PlanShape shape;
   shape.slots = slots;
   shape.batch = p->batch;
-  shape.num_kv_heads = p->num_kv_heads;
+  const int heads = unit > 0 ? p->num_kv_heads / unit : p->num_kv_heads;
+  shape.num_kv_heads = heads;
   shape.rows = rows_of(p);
   shape.max_seq_len = p->max_seq_len;
+  shape.fp4 = unit > 0 ? 1 : 0;
   bool uniform = true;
   int64_t work_tokens = 0;
   auto clamped = [&](int32_t b) {
-    return std::min<int64_t>(std::max(host_seq_lens[b], 0), p->max_seq_len);
+    return host_seq_lens != nullptr ? std::min<int64_t>(std::max(host_seq_lens[b], 0), p->max_seq_len)
+                                    : static_cast<int64_t>(p->max_seq_len);
   };
   if (host_seq_lens != nullptr) {
     for (int32_t b = 0; b < p->batch; ++b) {
@@ -139,37 +143,60 @@ int plan_for_slots(const decode_attn_params* p, const int32_t* host_seq_lens, in
       if (host_seq_lens[b] != host_seq_lens[0]) uniform = false;
     }
   }
+  if (host_seq_lens == nullptr) work_tokens = static_cast<int64_t>(p->batch) * p->max_seq_len;
   auto chunks_of = [&](int64_t c) {
     int64_t n = 0;
+    if (host_seq_lens == nullptr)  // (equal lengths)
+      return static_cast<int64_t>(p->batch) * std::max<int64_t>(1, ceil_div64(p->max_seq_len, c)) * heads;
     for (int32_t b = 0; b < p->batch; ++b) {
       const int64_t Lb = clamped(b);
       n += Lb > 0 ? ceil_div64(Lb, c) : 1;
     }
-    return n * p->num_kv_heads;
+    return n * heads;
   };
   const int64_t splits = dattn::plan_splits(shape, uniform, work_tokens, chunks_of);
   int32_t chunk = 0, eff = 0;
-  const int rc = chunk_for_splits(p, static_cast<int32_t>(splits), &chunk, &eff);
+  const int rc = chunk_for_splits(p, static_cast<int32_t>(splits), &chunk, &eff, unit);
   if (rc != DA_OK) return rc;
   *num_splits = eff;
   *chunk_len = chunk;
   return DA_OK;
 }
 
-// Resident CTAs per SM of the split launch for this shape.
-int ctas_per_sm(const decode_attn_params* p, bool fp4) {
-  return fp4 ? dattn::fp4_ctas_per_sm(rows_of(p)) : dattn::split_ctas_per_sm(rows_of(p), kv_fp8(p));
+// Resident CTAs per SM of the split launch for this shape (unit: KV heads of a
+// CTA of the 4-bit kernel, 0 for the other caches).
+int ctas_per_sm(const decode_attn_params* p, int unit) {
+  return unit > 0 ? dattn::fp4_ctas_per_sm(rows_of(p), unit)
+                  : dattn::split_ctas_per_sm(rows_of(p), kv_fp8(p));
+}
+
+// KV heads that a CTA of the 4-bit kernel takes (0: not a 4-bit cache).  More
+// heads make contiguous reads longer (64 bytes a head: 2.9, 4.8 and 7.0 TB/s
+// at 1, 2, and 4 or more), fewer make more CTAs: take the most that divide the heads
+// and still leave two 512-token items per SM when every request is at
+// max_seq_len.  Heads that choose their own pages cannot share a box.
+int unit_heads(const decode_attn_params* p, const DecodeExt& ext) {
+  if (ext.fp4 == nullptr) return 0;
+  if (ext.per_head) return 1;
+  DeviceInfo di;
+  if (current_device_info(&di) != DA_OK) return 1;
+  for (int u = dattn::fp4_warps(rows_of(p)); u > 1; u /= 2)
+    if (p->num_kv_heads % u == 0 &&
+        static_cast<int64_t>(p->batch) * (p->num_kv_heads / u) * ceil_div64(p->max_seq_len, 512) >=
+            2 * di.sm_count)
+      return u;
+  return 1;
 }
 
 // The planner on the current device: its SM count times the split launch's
 // resident CTAs per SM for this shape (occupancy of the kernel it will run).
 int plan_impl(const decode_attn_params* p, const int32_t* host_seq_lens, int32_t* num_splits,
-              int32_t* chunk_len, bool fp4 = false) {
+              int32_t* chunk_len, int unit = 0) {
   DeviceInfo di;
   const int rc = current_device_info(&di);
   if (rc != DA_OK) return rc;
-  const int64_t slots = static_cast<int64_t>(di.sm_count) * ctas_per_sm(p, fp4);
-  return plan_for_slots(p, host_seq_lens, slots, num_splits, chunk_len);
+  const int64_t slots = static_cast<int64_t>(di.sm_count) * ctas_per_sm(p, unit);
+  return plan_for_slots(p, host_seq_lens, slots, num_splits, chunk_len, unit);
 }
 
 // box_tokens: token rows per box (16; a whole stage for contiguous caches
@@ -179,14 +206,15 @@ int plan_impl(const decode_attn_params* p, const int32_t* host_seq_lens, int32_t
 struct MapKey {
   const void* base;
   cuuint64_t dims[4], strides[3];
-  cuuint32_t box;
-  int fp8;
+  cuuint32_t box[4];
+  int type, swizzle;
   bool operator==(const MapKey& o) const {
     return base == o.base && std::memcmp(dims, o.dims, sizeof(dims)) == 0 &&
-           std::memcmp(strides, o.strides, sizeof(strides)) == 0 && box == o.box && fp8 == o.fp8;
+           std::memcmp(strides, o.strides, sizeof(strides)) == 0 &&
+           std::memcmp(box, o.box, sizeof(box)) == 0 && type == o.type && swizzle == o.swizzle;
   }
 };
-constexpr int kMapCacheSize = 16;
+constexpr int kMapCacheSize = 32;
 std::mutex g_map_mu;
 struct {
   MapKey key;
@@ -195,10 +223,43 @@ struct {
 } g_map_cache[kMapCacheSize];
 int g_map_next = 0;
 
-int make_kv_map(CUtensorMap* map, const void* base, const decode_attn_params* p, bool paged,
-                int box_tokens) {
+// The encoded map of (base, layout, box), from the cache or made anew.
+int encode_map(CUtensorMap* map, const void* base, CUtensorMapDataType type, const cuuint64_t (&dims)[4],
+               const cuuint64_t (&strides)[3], const cuuint32_t (&box)[4], CUtensorMapSwizzle swizzle) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (enc == nullptr) return DA_ERR_CUDA;
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  MapKey key;
+  std::memset(&key, 0, sizeof(key));
+  key.base = base;
+  std::memcpy(key.dims, dims, sizeof(dims));
+  std::memcpy(key.strides, strides, sizeof(strides));
+  std::memcpy(key.box, box, sizeof(box));
+  key.type = type;
+  key.swizzle = swizzle;
+  {
+    std::lock_guard<std::mutex> lk(g_map_mu);
+    for (auto& e : g_map_cache)
+      if (e.valid && e.key == key) {
+        *map = e.map;
+        return DA_OK;
+      }
+  }
+  CUresult r = enc(map, type, 4, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return DA_ERR_ALIGNMENT;
+  std::lock_guard<std::mutex> lk(g_map_mu);
+  auto& e = g_map_cache[g_map_next];
+  g_map_next = (g_map_next + 1) % kMapCacheSize;
+  e.key = key;
+  e.map = *map;
+  e.valid = true;
+  return DA_OK;
+}
+
+int make_kv_map(CUtensorMap* map, const void* base, const decode_attn_params* p, bool paged,
+                int box_tokens) {
   // dims, innermost first: d (128), kv head, token-in-group, group
   //   paged: group = physical page, token-in-group = slot in page
   //   contiguous: group = request, token-in-group = token position
@@ -215,34 +276,40 @@ int make_kv_map(CUtensorMap* map, const void* base, const decode_attn_params* p,
                                  static_cast<cuuint64_t>(p->kv_stride_page) * eb};
   const cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / eb), 1,
                              static_cast<cuuint32_t>(box_tokens), 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  MapKey key;
-  std::memset(&key, 0, sizeof(key));
-  key.base = base;
-  std::memcpy(key.dims, dims, sizeof(dims));
-  std::memcpy(key.strides, strides, sizeof(strides));
-  key.box = box[2];
-  key.fp8 = kv_fp8(p) ? 1 : 0;
-  {
-    std::lock_guard<std::mutex> lk(g_map_mu);
-    for (auto& e : g_map_cache)
-      if (e.valid && e.key == key) {
-        *map = e.map;
-        return DA_OK;
-      }
+  return encode_map(map, base, kv_fp8(p) ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                    dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// 16-token halves of a box of the 4-bit kernel: whole boxes of a warp's share
+// of a stage, 64 tokens at most, that a page is a multiple of (so is a chunk).
+int fp4_box_halves(const decode_attn_params* p, bool paged, int unit) {
+  int h = 4;
+  const int stage = 2 * dattn::fp4_warps(rows_of(p)) / unit;
+  while (stage % h != 0 || (paged && p->page_size % (16 * h) != 0)) h /= 2;
+  return h;
+}
+
+// A map of a 4-bit cache: its values, or (scales) its block scales.
+int make_fp4_map(CUtensorMap* map, const void* base, const decode_attn_params* p,
+                 const decode_attn_cache* c, bool paged, int unit, bool scales) {
+  const cuuint32_t tokens = static_cast<cuuint32_t>(16 * fp4_box_halves(p, paged, unit));
+  const cuuint64_t slots = static_cast<cuuint64_t>(paged ? p->page_size : std::max(p->max_seq_len, 1));
+  const cuuint64_t groups = static_cast<cuuint64_t>(paged ? p->num_pages : std::max(p->batch, 1));
+  const cuuint64_t heads = static_cast<cuuint64_t>(p->num_kv_heads);
+  if (scales) {
+    const cuuint64_t dims[4] = {slots, heads, 1, groups};  // (a token's 8 scales: one element)
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c->bs_stride_head),
+                                   static_cast<cuuint64_t>(c->bs_stride_page),
+                                   static_cast<cuuint64_t>(c->bs_stride_page)};
+    const cuuint32_t box[4] = {tokens, static_cast<cuuint32_t>(unit), 1, 1};
+    return encode_map(map, base, CU_TENSOR_MAP_DATA_TYPE_UINT64, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
   }
-  CUresult r = enc(map, kv_fp8(p) ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                   4, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return DA_ERR_ALIGNMENT;
-  std::lock_guard<std::mutex> lk(g_map_mu);
-  auto& e = g_map_cache[g_map_next];
-  g_map_next = (g_map_next + 1) % kMapCacheSize;
-  e.key = key;
-  e.map = *map;
-  e.valid = true;
-  return DA_OK;
+  const cuuint64_t dims[4] = {kHeadDim / 2, heads, slots, groups};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p->kv_stride_head),
+                                 static_cast<cuuint64_t>(p->kv_stride_token),
+                                 static_cast<cuuint64_t>(p->kv_stride_page)};
+  const cuuint32_t box[4] = {kHeadDim / 2, static_cast<cuuint32_t>(unit), tokens, 1};
+  return encode_map(map, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 bool stride_ok(int64_t s) { return s > 0 && s % 8 == 0 && s * 2 < (1LL << 40); }
@@ -291,23 +358,24 @@ bool device_planned(const decode_attn_params* p, int32_t num_splits) {
 }
 
 // Resident CTAs of the split launch for this shape on the current device.
-int split_slots(const decode_attn_params* p, int64_t* slots, bool fp4) {
+int split_slots(const decode_attn_params* p, int64_t* slots, int unit) {
   DeviceInfo di;
   const int rc = current_device_info(&di);
   if (rc != DA_OK) return rc;
-  *slots = static_cast<int64_t>(di.sm_count) * ctas_per_sm(p, fp4);
+  *slots = static_cast<int64_t>(di.sm_count) * ctas_per_sm(p, unit);
   return DA_OK;
 }
 
 // Workspace of a device-planned call (offsets 256-byte aligned): plan[4],
 // pre[B + 1], items[cap] (int4), partial outputs [cap, rows, D] and partial
 // LSEs [cap, rows] (fp32).
-int list_layout(const decode_attn_params* p, ListLayout* l, bool fp4 = false) {
-  int rc = split_slots(p, &l->slots, fp4);
+int list_layout(const decode_attn_params* p, ListLayout* l, int unit = 0) {
+  int rc = split_slots(p, &l->slots, unit);
   if (rc != DA_OK) return rc;
-  l->cap = static_cast<int64_t>(p->batch) * p->num_kv_heads + kListWaveSlack * l->slots;
+  const int heads = unit > 0 ? unit : 1;  // KV heads of an item
+  l->cap = static_cast<int64_t>(p->batch) * (p->num_kv_heads / heads) + kListWaveSlack * l->slots;
   if (l->cap > 0x7fffffff) return DA_ERR_BAD_SHAPE;
-  const size_t rows = static_cast<size_t>(rows_of(p));
+  const size_t rows = static_cast<size_t>(rows_of(p)) * heads;
   const size_t cap = static_cast<size_t>(l->cap);
   size_t off = 0;
   l->plan = off;
@@ -326,7 +394,7 @@ int list_layout(const decode_attn_params* p, ListLayout* l, bool fp4 = false) {
 // Arguments of the planner kernel for a device-planned call whose workspace
 // starts at w.
 dattn::PlanArgs plan_args(const decode_attn_params* p, const int32_t* seq_lens, int32_t* status,
-                          uint8_t* w, const ListLayout& lay) {
+                          uint8_t* w, const ListLayout& lay, int unit = 0) {
   dattn::PlanArgs pa;
   std::memset(&pa, 0, sizeof(pa));
   pa.seq_lens = seq_lens;
@@ -337,11 +405,12 @@ dattn::PlanArgs plan_args(const decode_attn_params* p, const int32_t* seq_lens, 
   pa.slots = lay.slots;
   pa.cap = lay.cap;
   pa.batch = p->batch;
-  pa.num_kv_heads = p->num_kv_heads;
+  pa.num_kv_heads = unit > 0 ? p->num_kv_heads / unit : p->num_kv_heads;
   pa.rows = rows_of(p);
   pa.max_seq_len = p->max_seq_len;
   pa.q_len = p->q_len;
   pa.causal = p->causal ? 1 : 0;
+  pa.fp4 = unit > 0 ? 1 : 0;
   return pa;
 }
 
@@ -354,20 +423,20 @@ int workspace_bytes(const decode_attn_params* p, int32_t num_splits, const Decod
   int rc = check_shape(p);
   if (rc != DA_OK) return rc;
   if (bytes == nullptr) return DA_ERR_NULL_POINTER;
-  const bool fp4 = ext.fp4 != nullptr;
+  const int unit = unit_heads(p, ext);
   if (!ext.per_head && device_planned(p, num_splits)) {
     ListLayout l;
-    rc = list_layout(p, &l, fp4);
+    rc = list_layout(p, &l, unit);
     if (rc != DA_OK) return rc;
     *bytes = l.total;
     return DA_OK;
   }
   int32_t chunk = 0, eff = 0;
   if (num_splits <= 0) {  // one request (or none): the host plan
-    rc = plan_impl(p, nullptr, &num_splits, &chunk, fp4);
+    rc = plan_impl(p, nullptr, &num_splits, &chunk, unit);
     if (rc != DA_OK) return rc;
   }
-  rc = chunk_for_splits(p, num_splits, &chunk, &eff);
+  rc = chunk_for_splits(p, num_splits, &chunk, &eff, unit);
   if (rc != DA_OK) return rc;
   if (eff <= 1) {
     *bytes = 0;
@@ -470,6 +539,7 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
   int rc = check_shape(p);
   if (rc != DA_OK) return rc;
   const bool fp4 = ext.fp4 != nullptr;
+  const int unit = unit_heads(p, ext);
   const bool paged = block_table != nullptr;
   rc = check_paged(p, paged);
   if (rc != DA_OK) return rc;
@@ -502,16 +572,16 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
   int32_t chunk = 0, eff = 0;
   bool cluster_merge = false;
   if (listed) {
-    rc = list_layout(p, &lay, fp4);
+    rc = list_layout(p, &lay, unit);
     if (rc != DA_OK) return rc;
     if (workspace == nullptr || workspace_bytes < lay.total || !aligned16(workspace))
       return DA_ERR_WORKSPACE;
   } else {
     if (num_splits <= 0) {
-      rc = plan_impl(p, nullptr, &num_splits, &chunk, fp4);
+      rc = plan_impl(p, nullptr, &num_splits, &chunk, unit);
       if (rc != DA_OK) return rc;
     }
-    rc = chunk_for_splits(p, num_splits, &chunk, &eff);
+    rc = chunk_for_splits(p, num_splits, &chunk, &eff, unit);
     if (rc != DA_OK) return rc;
     cluster_merge = !fp4 && use_cluster_merge(p, eff);
     size_t need = 0;
@@ -529,7 +599,18 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
   CUtensorMap kmap, vmap;
   std::memset(&kmap, 0, sizeof(kmap));
   std::memset(&vmap, 0, sizeof(vmap));
-  if (!no_keys && !fp4) {
+  Fp4Maps maps4;
+  if (fp4) {
+    std::memset(&maps4, 0, sizeof(maps4));
+    if (!no_keys) {
+      const decode_attn_cache* c = ext.fp4;
+      rc = make_fp4_map(&maps4.k, c->k, p, c, paged, unit, false);
+      if (rc == DA_OK) rc = make_fp4_map(&maps4.v, c->v, p, c, paged, unit, false);
+      if (rc == DA_OK) rc = make_fp4_map(&maps4.ks, c->k_block_scale, p, c, paged, unit, true);
+      if (rc == DA_OK) rc = make_fp4_map(&maps4.vs, c->v_block_scale, p, c, paged, unit, true);
+      if (rc != DA_OK) return rc;
+    }
+  } else if (!no_keys) {
     rc = make_kv_map(&kmap, k_cache, p, paged, box_tokens);
     if (rc != DA_OK) return rc;
     rc = make_kv_map(&vmap, v_cache, p, paged, box_tokens);
@@ -553,6 +634,7 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
   a.block_table = block_table;
   a.bt_stride = p->block_table_stride;
   a.bt_sh = ext.per_head ? p->max_pages_per_seq : 0;
+  a.box_halves = fp4 ? fp4_box_halves(p, paged, unit) : 1;
   a.seq_lens = seq_lens;
   a.len_sb = ext.per_head ? p->num_kv_heads : 1;
   a.len_sh = ext.per_head ? 1 : 0;
@@ -590,22 +672,11 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
     a.part_lse = reinterpret_cast<float*>(w + lay.part_lse);
     a.chunk_len = 0;
     a.num_splits = 1;
-    if (dattn::launch_plan(plan_args(p, seq_lens, status, w, lay), st) != cudaSuccess)
+    if (dattn::launch_plan(plan_args(p, seq_lens, status, w, lay, unit), st) != cudaSuccess)
       return DA_ERR_CUDA;
   }
   if (fp4) {
-    Fp4Args f;
-    f.s = a;
-    f.k = static_cast<const uint8_t*>(k_cache);
-    f.v = static_cast<const uint8_t*>(v_cache);
-    f.ks = static_cast<const uint8_t*>(ext.fp4->k_block_scale);
-    f.vs = static_cast<const uint8_t*>(ext.fp4->v_block_scale);
-    f.st_page = p->kv_stride_page;
-    f.st_token = p->kv_stride_token;
-    f.st_head = p->kv_stride_head;
-    f.sf_page = ext.fp4->bs_stride_page;
-    f.sf_head = ext.fp4->bs_stride_head;
-    if (launch_fp4(f, st) != cudaSuccess) return DA_ERR_CUDA;
+    if (launch_fp4(maps4, a, unit, st) != cudaSuccess) return DA_ERR_CUDA;
   } else if (dattn::launch_split(kmap, vmap, a, cluster_merge, st) != cudaSuccess) {
     return DA_ERR_CUDA;
   }
@@ -630,6 +701,7 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
     c.num_splits = eff;
     c.len_sb = a.len_sb;
     c.len_sh = a.len_sh;
+    c.unit_heads = unit > 0 ? unit : 1;
     if (dattn::launch_combine(c, st) != cudaSuccess) return DA_ERR_CUDA;
   }
   return DA_OK;
@@ -637,7 +709,7 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
 
 int plan_uniform(const decode_attn_params* p, const DecodeExt& ext, int32_t* num_splits,
                  int32_t* chunk_len) {
-  return plan_impl(p, nullptr, num_splits, chunk_len, ext.fp4 != nullptr);
+  return plan_impl(p, nullptr, num_splits, chunk_len, unit_heads(p, ext));
 }
 
 int check_device(int* sm_count) {
@@ -661,10 +733,10 @@ int check_cache(const decode_attn_params* p, const decode_attn_cache* c, bool ne
       !kv_stride_ok(p, p->kv_stride_page, fp4) || !kv_stride_ok(p, p->kv_stride_token, fp4) ||
       !kv_stride_ok(p, p->kv_stride_head, fp4))
     return DA_ERR_ALIGNMENT;
-  if (fp4 && ((need_k && (reinterpret_cast<uintptr_t>(c->k_block_scale) & 7u) != 0) ||
-              (need_v && (reinterpret_cast<uintptr_t>(c->v_block_scale) & 7u) != 0) ||
-              c->bs_stride_page <= 0 || c->bs_stride_head <= 0 || c->bs_stride_page % 8 != 0 ||
-              c->bs_stride_head % 8 != 0 || c->bs_stride_page >= (int64_t{1} << 40) ||
+  if (fp4 && ((need_k && !aligned16(c->k_block_scale)) ||
+              (need_v && !aligned16(c->v_block_scale)) ||
+              c->bs_stride_page <= 0 || c->bs_stride_head <= 0 || c->bs_stride_page % 16 != 0 ||
+              c->bs_stride_head % 16 != 0 || c->bs_stride_page >= (int64_t{1} << 40) ||
               c->bs_stride_head >= (int64_t{1} << 40)))
     return DA_ERR_ALIGNMENT;
   return DA_OK;
@@ -751,6 +823,7 @@ int decode_attn_combine(const decode_attn_params* p, const int32_t* seq_lens, in
   c.num_splits = num_splits;
   c.len_sb = 1;
   c.len_sh = 0;
+  c.unit_heads = 1;
   if (dattn::launch_combine(c, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return DA_ERR_CUDA;
   return DA_OK;

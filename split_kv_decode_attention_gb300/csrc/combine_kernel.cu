@@ -134,13 +134,17 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock, LISTED ? kBlocksPerSm - 1
     const int G = a.num_q_heads / a.num_kv_heads;
     const int rows = G * a.q_len;
     const int kvh = h / G;
-    const int64_t base = static_cast<int64_t>(pb) * a.num_kv_heads + static_cast<int64_t>(kvh) * n;
+    // (an item holds unit_heads KV heads, one behind the other)
+    const int U = a.unit_heads;
+    const int unit = U == 1 ? kvh : kvh / U;
+    const int64_t base = (static_cast<int64_t>(pb) * (a.num_kv_heads / U) + static_cast<int64_t>(unit) * n) * U +
+                         (kvh - unit * U);
     const int64_t r0 = base * rows + t * G + (h - kvh * G);
     // the merge the split kernel runs in-kernel for these calls (same routine,
     // same bits): here for calls that keep the partials (DA_FLAG_TWO_PASS)
     float4 res;
     float lse_row;
-    merge_row_warp(a.part_lse + r0, rows, a.part_o + r0 * kHeadDim + lane * 4, rows * kHeadDim, n,
+    merge_row_warp(a.part_lse + r0, U * rows, a.part_o + r0 * kHeadDim + lane * 4, U * rows * kHeadDim, n,
                    dead, &res, &lse_row);
     uint16_t* orow = a.out + static_cast<int64_t>(b) * a.o_sb + static_cast<int64_t>(t) * a.o_st +
                      static_cast<int64_t>(h) * a.o_sh + lane * 4;

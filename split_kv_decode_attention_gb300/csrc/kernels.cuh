@@ -55,17 +55,14 @@ struct SplitArgs {
   // selected pages; device-planned calls use the shared form only).
   int len_sb, len_sh;
   int64_t bt_sh;
+  int box_halves;                      // 4-bit kernel: 16-token halves of a box
 };
 
-// Arguments of the 4-bit kernel: the split arguments, and the cache (byte
-// strides; the 8 block scales of a token follow those of the token before).
-struct Fp4Args {
-  SplitArgs s;
-  const uint8_t* k;
-  const uint8_t* v;
-  const uint8_t* ks;
-  const uint8_t* vs;
-  int64_t st_page, st_token, st_head, sf_page, sf_head;
+// Tensor maps of a 4-bit cache: values [d (64 B), head, slot, group] in boxes
+// of 16 box_halves tokens of a CTA's heads, 64-byte swizzle; block scales [slot
+// (8 B), head, 1, group] in boxes of the same tokens and heads.
+struct Fp4Maps {
+  CUtensorMap k, v, ks, vs;
 };
 
 // Arguments of the device planner kernel (plan_kernel.cu; up to 32 CTAs, each
@@ -79,6 +76,7 @@ struct PlanArgs {
   int64_t slots;                       // resident CTAs of the split launch
   int64_t cap;                         // item slots of the split launch
   int batch, num_kv_heads, rows, max_seq_len, q_len, causal;
+  int fp4;                             // a 4-bit cache's rule
 };
 
 struct CombineArgs {
@@ -96,6 +94,7 @@ struct CombineArgs {
   const int32_t* pre;
   int num_kv_heads;
   int len_sb, len_sh;                  // strides of seq_lens (see SplitArgs)
+  int unit_heads;                      // device-planned: KV heads of an item (1; more for 4-bit caches)
 };
 
 // Physical page ids of a chunk's 16-token tiles, for the TMA producer warp.
@@ -160,8 +159,12 @@ int wide_ctas_per_sm();
 
 // Launch the kernel over 4-bit caches (any rows; outputs and partials as
 // launch_split without cluster merge), and its resident CTAs per SM.
-cudaError_t launch_fp4(const Fp4Args& a, cudaStream_t stream);
-int fp4_ctas_per_sm(int rows);
+// A CTA takes heads_per_cta (1, 2, 4 or 8, a divisor of the KV heads) heads: items,
+// plans and partials count such units (partials hold a unit's heads one behind
+// the other).
+cudaError_t launch_fp4(const Fp4Maps& maps, const SplitArgs& a, int heads_per_cta, cudaStream_t stream);
+int fp4_ctas_per_sm(int rows, int heads_per_cta);
+int fp4_warps(int rows);  // consumer warps of a CTA: its heads divide them
 
 // Launch the combine kernel (one warp per output row).
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream);

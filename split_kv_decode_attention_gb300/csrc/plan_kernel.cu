@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const PlanArgs a)
   shape.num_kv_heads = a.num_kv_heads;
   shape.rows = a.rows;
   shape.max_seq_len = msl;
+  shape.fp4 = a.fp4;
   // The split search of the rule: the largest length in (lo, hi] whose
   // chunks reach `need`.  Up to kPlanWarpSumBatch requests each group of g
   // threads (at most kPlanSearchLens requests a thread) tests its own
@@ -207,14 +208,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const PlanArgs a)
   int32_t chunk = 0, eff = 0;
   // (the host runs this path only when max_seq_len <= 2^30, so every split
   // count gives a valid chunk)
-  plan_chunk_for_splits(msl, splits, &chunk, &eff);
+  const int tile = a.fp4 ? kFp4Tile : kPlanTile;
+  plan_chunk_for_splits(msl, splits, &chunk, &eff, tile);
   long long n_items = chunks_of(chunk);
   if (n_items > a.cap) {
-    // more items than grid slots: the smallest longer chunk (multiple of 16)
-    // that fits; hi = the whole sequence in one chunk always does
-    long long lo = chunk, hi = plan_ceil_div(msl > 1 ? msl : 1, kPlanTile) * kPlanTile;
-    while (hi - lo > kPlanTile) {
-      const long long mid = (lo + hi) / 2 / kPlanTile * kPlanTile;
+    // more items than grid slots: the smallest longer chunk (multiple of the
+    // tile) that fits; hi = the whole sequence in one chunk always does
+    long long lo = chunk, hi = plan_ceil_div(msl > 1 ? msl : 1, tile) * tile;
+    while (hi - lo > tile) {
+      const long long mid = (lo + hi) / 2 / tile * tile;
       if (chunks_of(mid) <= a.cap) hi = mid;
       else lo = mid;
     }

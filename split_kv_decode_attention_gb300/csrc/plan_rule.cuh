@@ -31,10 +31,28 @@ constexpr int kTokensPerRow = 64;
 // (GB300, 64 rows: one chunk per request 198 us against two 205 us; 128
 // rows keep two chunks, where the floor gives way to filling the SMs.)
 constexpr int kWideTokensPerRow = 256;
+// 4-bit caches: a token is 3.6 times fewer bytes than in bf16, so a chunk of the
+// same tokens is over before its set-up and merge have paid off; chunks are
+// longer and waves fewer.  Nothing merges through clusters there, so equal
+// lengths may take any number of chunks.
+#ifndef DATTN_F4_WAVES
+#define DATTN_F4_WAVES 3
+#endif
+#ifndef DATTN_F4_MIN_CHUNK
+#define DATTN_F4_MIN_CHUNK 512
+#endif
+constexpr int kFp4Waves = DATTN_F4_WAVES;
+constexpr int kFp4MinChunk = DATTN_F4_MIN_CHUNK;
+#ifndef DATTN_F4_MIN_UNIFORM
+#define DATTN_F4_MIN_UNIFORM 256
+#endif
+constexpr int kFp4MinUniform = DATTN_F4_MIN_UNIFORM;  // shortest chunk of any plan
 // Largest thread-block cluster the split kernel uses (non-portable size).
 constexpr int kMaxClusterSplits = 16;
 // Tokens per TMA box / MMA tile: chunk lengths are multiples of it.
 constexpr int kPlanTile = 16;
+// ... and of this in the 4-bit kernel, whose boxes hold up to 64 tokens.
+constexpr int kFp4Tile = 64;
 // Rows per kv head above which the tcgen05 kernel runs.
 constexpr int kPlanMaxNarrowRows = 16;
 
@@ -44,6 +62,7 @@ struct PlanShape {
   int num_kv_heads;  // Hkv
   int rows;          // query rows per kv head: (Hq / Hkv) * q_len
   int max_seq_len;   // upper bound of every length (>= 0)
+  int fp4 = 0;       // 4-bit cache (kFp4Waves, kFp4MinChunk)
 };
 
 // a / b for a >= 0, b > 0, in 32 bits when both fit: on the GPU a 64-bit
@@ -65,15 +84,16 @@ __host__ __device__ inline int64_t plan_sat_mul(int64_t a, int64_t b) {
   return a > lim / b ? lim : a * b;
 }
 
-// Chunk length for a split count: the smallest multiple of 16 that covers
+// Chunk length for a split count: the smallest multiple of `tile` that covers
 // max_seq_len in `splits` chunks; *eff = the chunks that then exist.  False
 // when splits < 1 or the chunk would exceed 2^30 tokens.
 __host__ __device__ inline bool plan_chunk_for_splits(int max_seq_len, int64_t splits,
-                                                      int32_t* chunk, int32_t* eff) {
+                                                      int32_t* chunk, int32_t* eff,
+                                                      int tile = kPlanTile) {
   if (splits < 1) return false;
   const int64_t L = max_seq_len;
   int64_t c = plan_ceil_div(L > 1 ? L : 1, splits);
-  c = plan_ceil_div(c, kPlanTile) * kPlanTile;
+  c = plan_ceil_div(c, tile) * tile;
   if (c > (int64_t{1} << 30)) return false;
   *chunk = static_cast<int32_t>(c);
   const int64_t e = plan_ceil_div(L, c);
@@ -119,22 +139,40 @@ __host__ __device__ int64_t plan_splits(const PlanShape& s, bool uniform, int64_
   const int64_t max_tiles = plan_ceil_div(msl > 1 ? msl : 1, kPlanTile);
   const int64_t pairs = static_cast<int64_t>(s.batch > 1 ? s.batch : 1) * s.num_kv_heads;
   int64_t splits = 1;
-  if (uniform) {
+  if (uniform && s.fp4) {
+    // whole waves of equal chunks: the fewest waves that fill 15/16 of the slots
+    // (or, of eight, the fullest)
+    int64_t best = 1, best_used = 0;
+    for (int64_t waves = 1; waves <= 8; ++waves) {
+      const int64_t f = plan_div(waves * s.slots, pairs);
+      if (f < 1) continue;
+      const int64_t used = plan_div(f * pairs * 16, waves * s.slots);
+      if (used > best_used) {
+        best = f;
+        best_used = used;
+      }
+      if (best_used >= 15) break;
+    }
+    splits = best;
+  } else if (uniform) {
     if (pairs < s.slots) {
       const int64_t f = plan_div(s.slots, pairs);
       splits = f < kMaxClusterSplits ? f : kMaxClusterSplits;
     }
   } else {
     const int64_t per_cta =
-        plan_ceil_div(plan_sat_mul(work_tokens, s.num_kv_heads), plan_sat_mul(kRaggedWaves, s.slots));
-    const int64_t per_row = s.rows > kPlanMaxNarrowRows ? kWideTokensPerRow : kTokensPerRow;
+        plan_ceil_div(plan_sat_mul(work_tokens, s.num_kv_heads),
+                      plan_sat_mul(s.fp4 ? kFp4Waves : kRaggedWaves, s.slots));
+    const int64_t per_row = s.rows > kPlanMaxNarrowRows && !s.fp4 ? kWideTokensPerRow : kTokensPerRow;
     const int64_t floor_rows = per_row * s.rows;
-    const int64_t min_chunk = floor_rows > kMinChunkTokens ? floor_rows : kMinChunkTokens;
+    const int64_t min_tokens = s.fp4 ? kFp4MinChunk : kMinChunkTokens;
+    const int64_t min_chunk = floor_rows > min_tokens ? floor_rows : min_tokens;
     const int64_t target = search(int64_t{kMinChunkTokens},
                                   per_cta > min_chunk ? per_cta : min_chunk, s.slots);
     splits = plan_ceil_div(msl > 1 ? msl : 1, target);
   }
-  const int64_t by_min = msl / kMinChunkTokens > 1 ? msl / kMinChunkTokens : 1;
+  const int64_t least = s.fp4 ? kFp4MinUniform : kMinChunkTokens;
+  const int64_t by_min = msl / least > 1 ? msl / least : 1;
   if (splits > by_min) splits = by_min;
   if (splits > max_tiles) splits = max_tiles;
   return splits > 1 ? splits : 1;

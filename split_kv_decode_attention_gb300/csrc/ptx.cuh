@@ -92,6 +92,15 @@ __device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity,
   return false;
 }
 
+// As mbar_wait, for waits that are short when they are needed at all: the timer
+// (a read of about a microsecond) is first looked at after 256 polls.
+__device__ __forceinline__ bool mbar_wait_lazy(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 256; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait_for(bar, parity, kWaitLimitNs);
+}
+
 // Wait for the phase with the given parity to complete; false on time-out.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   return mbar_wait_for(bar, parity, kWaitLimitNs);
@@ -375,6 +384,18 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
 
 __device__ __forceinline__ void named_barrier_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// The barrier, and whether the predicate holds for all its threads.
+__device__ __forceinline__ bool named_barrier_and(uint32_t id, uint32_t nthreads, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(nthreads), "r"(x ? 1u : 0u)
+      : "memory");
+  return r != 0;
 }
 
 }  // namespace dattn

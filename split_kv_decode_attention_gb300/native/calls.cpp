@@ -106,6 +106,12 @@ void byte_type(const at::Tensor& t, const char* name) {
     refuse(std::string(name) + " is " + c10::toString(t.scalar_type()) + "; expected uint8 or float8_e4m3fn");
 }
 
+bool same_steps(const at::Tensor& x, const at::Tensor& y) {
+  for (int64_t d = 0; d < x.dim(); ++d)
+    if (x.size(d) > 1 && x.stride(d) != y.stride(d)) return false;
+  return true;
+}
+
 void* ptr(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
 size_t bytes_of(const at::Tensor& t) {
@@ -148,6 +154,10 @@ int32_t* status_of(const at::Tensor& t) {
 }
 
 // ---- shapes
+// The stride of a dimension; one of at most one entry is never stepped along
+// and may hold anything: a multiple of every alignment stands for it.
+int64_t step(const at::Tensor& t, int64_t d) { return t.size(d) > 1 ? t.stride(d) : 4 * kD; }
+
 void int_vector(const at::Tensor& t, int64_t n, const char* name) {
   type_of(t, at::kInt, name);
   if (t.dim() != 1 || t.size(0) != n || (n > 1 && t.stride(0) != 1))
@@ -192,7 +202,7 @@ Cache cache_args(const at::Tensor& k, const at::Tensor& v, const at::Tensor& k_s
   }
   if (k.dim() != 4 || k.size(3) != width || k.stride(3) != 1)
     refuse("k_cache must be [groups, tokens, heads, " + std::to_string(width) + "], its last dimension dense");
-  if (v.defined() && (v.sizes() != k.sizes() || v.strides() != k.strides() || v.scalar_type() != k.scalar_type()))
+  if (v.defined() && (v.sizes() != k.sizes() || !same_steps(v, k) || v.scalar_type() != k.scalar_type()))
     refuse("k_cache and v_cache differ in shape, strides or type");
   r.groups = k.size(0);
   r.tokens = k.size(1);
@@ -207,11 +217,11 @@ Cache cache_args(const at::Tensor& k, const at::Tensor& v, const at::Tensor& k_s
           t->size(3) != 8 || (t->size(2) > 1 && t->stride(2) != 8) || t->stride(3) != 1)
         refuse("k_sf and v_sf must be " + dims({r.groups, r.heads, r.tokens, 8}) + " with dense tokens");
     }
-    if (v_sf.defined() && v_sf.strides() != k_sf.strides()) refuse("k_sf and v_sf differ in strides");
+    if (v_sf.defined() && !same_steps(v_sf, k_sf)) refuse("k_sf and v_sf differ in strides");
     r.c.k_block_scale = ptr(k_sf);
     r.c.v_block_scale = ptr(v_sf);
-    r.c.bs_stride_page = k_sf.stride(0);
-    r.c.bs_stride_head = k_sf.stride(1);
+    r.c.bs_stride_page = step(k_sf, 0);
+    r.c.bs_stride_head = step(k_sf, 1);
   }
   return r;
 }
@@ -231,9 +241,9 @@ decode_attn_params cache_params(int64_t B, int64_t T, int64_t Hq, const Cache& c
   p.max_seq_len = max_seq_len;
   p.causal = causal ? 1 : 0;
   p.scale = scale;
-  p.kv_stride_page = k.stride(0);
-  p.kv_stride_token = k.stride(1);
-  p.kv_stride_head = k.stride(2);
+  p.kv_stride_page = step(k, 0);
+  p.kv_stride_token = step(k, 1);
+  p.kv_stride_head = step(k, 2);
   p.k_scale = static_cast<float>(k_scale);
   p.v_scale = static_cast<float>(v_scale);
   if (bt.defined()) {
@@ -243,7 +253,7 @@ decode_attn_params cache_params(int64_t B, int64_t T, int64_t Hq, const Cache& c
     p.page_size = static_cast<int32_t>(c.tokens);
     p.num_pages = static_cast<int32_t>(c.groups);
     p.max_pages_per_seq = static_cast<int32_t>(bt.size(1));
-    p.block_table_stride = bt.stride(0);
+    p.block_table_stride = bt.size(0) > 1 ? bt.stride(0) : bt.size(1);
   } else if (c.groups != B || c.tokens < max_seq_len) {
     refuse("a contiguous cache holds max_seq_len tokens of every request");
   }
@@ -251,12 +261,12 @@ decode_attn_params cache_params(int64_t B, int64_t T, int64_t Hq, const Cache& c
 }
 
 void q_strides(decode_attn_params& p, const at::Tensor& q, const at::Tensor& out) {
-  p.q_stride_batch = q.stride(0);
-  p.q_stride_token = q.stride(1);
-  p.q_stride_head = q.stride(2);
-  p.o_stride_batch = out.stride(0);
-  p.o_stride_token = out.stride(1);
-  p.o_stride_head = out.stride(2);
+  p.q_stride_batch = step(q, 0);
+  p.q_stride_token = step(q, 1);
+  p.q_stride_head = step(q, 2);
+  p.o_stride_batch = step(out, 0);
+  p.o_stride_token = step(out, 1);
+  p.o_stride_head = step(out, 2);
 }
 
 float scale_or_default(PyObject* o) {
@@ -359,12 +369,12 @@ PyObject* rope_append(PyObject* const* a, Py_ssize_t n) {
     heads_tensor(k, B, T, "k");
     heads_tensor(v, B, T, "v");
     if (k.size(2) != c.heads || v.size(2) != c.heads) refuse("k and v must have the cache's heads");
-    r.k_stride_batch = k.stride(0);
-    r.k_stride_token = k.stride(1);
-    r.k_stride_head = k.stride(2);
-    r.v_stride_batch = v.stride(0);
-    r.v_stride_token = v.stride(1);
-    r.v_stride_head = v.stride(2);
+    r.k_stride_batch = step(k, 0);
+    r.k_stride_token = step(k, 1);
+    r.k_stride_head = step(k, 2);
+    r.v_stride_batch = step(v, 0);
+    r.v_stride_token = step(v, 1);
+    r.v_stride_head = step(v, 2);
   }
   decode_attn_params p = cache_params(B, T, c.heads, c, kc, bt, max_seq_len, false, 1.f, number(a[12]), number(a[13]));
   if (q.defined()) {

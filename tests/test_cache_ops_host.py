@@ -75,9 +75,11 @@ def test_null_descriptors(lib):
 
 def test_workspace_of_explicit_splits_needs_no_device(lib):
     n = ctypes.c_size_t()
-    p = params()
+    p = params(max_pages_per_seq=20, block_table_stride=20, max_seq_len=250)
     assert lib.decode_attn_cached_workspace_bytes(ref(p), ref(cache()), 4, ctypes.byref(n)) == 0
-    assert n.value == 2 * 8 * 4 * 129 * 4
+    assert n.value == 2 * 8 * 4 * 129 * 4        # chunks of 64 tokens
+    assert lib.decode_attn_cached_workspace_bytes(ref(p), ref(cache()), 3, ctypes.byref(n)) == 0
+    assert n.value == 2 * 8 * 2 * 129 * 4        # 84 tokens round up to 128: two chunks
     assert lib.decode_attn_cached_workspace_bytes(ref(p), ref(cache()), 1, ctypes.byref(n)) == 0
     assert n.value == 0
 
