@@ -701,6 +701,7 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
     c.num_splits = eff;
     c.len_sb = a.len_sb;
     c.len_sh = a.len_sh;
+    c.by_row = fp4 ? 1 : 0;
     c.unit_heads = unit > 0 ? unit : 1;
     if (dattn::launch_combine(c, st) != cudaSuccess) return DA_ERR_CUDA;
   }

@@ -226,6 +226,104 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock, LISTED ? kBlocksPerSm - 1
   if (lane == 0) a.lse[row] = M + logf(W);
 }
 
+// The merge for calls whose rows are few and their chunks many (4-bit caches: no
+// cluster merge, so a single row may span hundreds of chunks): a CTA per row, a
+// thread per d.  The chunks' values are loaded sixteen at a time, the first of
+// them together with the LSEs, so a row of up to 16 chunks costs two dependent
+// round trips and 16 more chunks one each.  (GB300, whole calls: 32 rows of 57
+// chunks 111 -> 105 us, 128 rows of 14 chunks 28 -> 26.7; but 16384 rows of 4
+// chunks 363 -> 386: from kRowMost rows on a warp per row is ahead.)
+constexpr int kRowThreads = kHeadDim;
+constexpr int kRowBatch = 16;
+constexpr int kRowMost = 1024;
+constexpr int kRowLses = 1024;  // weights of this many chunks are held at a time
+
+template <bool LISTED>
+__global__ void __launch_bounds__(kRowThreads) combine_row_kernel(const CombineArgs a) {
+  __shared__ float weight[kRowLses];
+  __shared__ float red[2][kRowThreads / 32];
+  constexpr uint32_t kFull = 0xffffffffu;
+  const int64_t row = blockIdx.x;
+  const int h = static_cast<int>(row % a.num_q_heads);
+  const int t = static_cast<int>((row / a.num_q_heads) % a.q_len);
+  const int b = static_cast<int>(row / (static_cast<int64_t>(a.num_q_heads) * a.q_len));
+  const int G = a.num_q_heads / a.num_kv_heads;
+  const int kvh = h / G;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  int L = a.seq_lens[static_cast<int64_t>(b) * a.len_sb + static_cast<int64_t>(kvh) * a.len_sh];
+  const int chunk = LISTED ? a.plan[0] : a.chunk_len;
+  L = L < 0 ? 0 : (L > a.max_seq_len ? a.max_seq_len : L);
+  const int n = L > 0 ? (L + chunk - 1) / chunk : 1;
+  if (n < 2) return;  // the split kernel wrote this row directly
+  int64_t r0 = row * a.num_splits, step = 1;  // partial s of the row: r0 + s * step
+  if constexpr (LISTED) {
+    // (an item holds unit_heads KV heads, one behind the other)
+    const int U = a.unit_heads;
+    const int unit = kvh / U;
+    const int64_t item = static_cast<int64_t>(a.pre[b]) * (a.num_kv_heads / U) + static_cast<int64_t>(unit) * n;
+    const int rows = G * a.q_len;
+    r0 = (item * U + (kvh - unit * U)) * rows + t * G + (h - kvh * G);
+    step = static_cast<int64_t>(U) * rows;
+  }
+  const float* pl = a.part_lse + r0;
+  const float* po = a.part_o + r0 * kHeadDim + threadIdx.x;
+  const int64_t os = step * kHeadDim;
+  const uint64_t dead = l2_evict_first_policy();  // each partial is read once
+
+  float v[kRowBatch];
+#pragma unroll
+  for (int j = 0; j < kRowBatch; ++j) v[j] = j < n ? ld_global_cg_hint1(po + j * os, dead) : 0.f;
+  float M = -INFINITY;
+  for (int s = threadIdx.x; s < n; s += kRowThreads) {
+    const float x = ld_global_cg_hint1(pl + s * step, dead);
+    if (s < kRowLses) weight[s] = x;
+    M = fmaxf(M, x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+  if (lane == 0) red[0][warp] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  uint16_t* out = a.out + static_cast<int64_t>(b) * a.o_sb + static_cast<int64_t>(t) * a.o_st +
+                  static_cast<int64_t>(h) * a.o_sh + threadIdx.x;
+  if (M == -INFINITY) {
+    *out = 0;
+    if (threadIdx.x == 0) a.lse[row] = -INFINITY;
+    return;
+  }
+  float acc = 0.f, sum = 0.f;
+  for (int s0 = 0; s0 < n; s0 += kRowLses) {
+    const int cnt = min(kRowLses, n - s0);
+    if (s0 > 0) __syncthreads();  // (the weights before are done with)
+    for (int s = threadIdx.x; s < cnt; s += kRowThreads) {
+      const float x = s0 == 0 ? weight[s] : ld_global_cg_hint1(pl + (s0 + s) * step, dead);
+      const float w = ex2((x - M) * kLog2e);
+      weight[s] = w;
+      sum += w;
+    }
+    __syncthreads();
+    for (int j0 = 0; j0 < cnt; j0 += kRowBatch) {
+      if (s0 + j0 > 0) {  // (the first batch is already in flight)
+#pragma unroll
+        for (int j = 0; j < kRowBatch; ++j)
+          v[j] = j0 + j < cnt ? ld_global_cg_hint1(po + (s0 + j0 + j) * os, dead) : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < kRowBatch; ++j)
+        if (j0 + j < cnt) acc += weight[j0 + j] * v[j];
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+  if (lane == 0) red[1][warp] = sum;
+  __syncthreads();
+  sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+  const __nv_bfloat16 o16 = __float2bfloat16_rn(acc / sum);
+  *out = *reinterpret_cast<const uint16_t*>(&o16);
+  if (threadIdx.x == 0) a.lse[row] = M + logf(sum);
+}
+
 }  // namespace
 
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream) {
@@ -241,6 +339,12 @@ cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (a.by_row && nrows <= kRowMost) {
+    cfg.gridDim = dim3(static_cast<unsigned>(nrows));
+    cfg.blockDim = dim3(kRowThreads);
+    return a.plan != nullptr ? cudaLaunchKernelEx(&cfg, combine_row_kernel<true>, a)
+                             : cudaLaunchKernelEx(&cfg, combine_row_kernel<false>, a);
+  }
   return a.plan != nullptr ? cudaLaunchKernelEx(&cfg, combine_kernel<true>, a)
                            : cudaLaunchKernelEx(&cfg, combine_kernel<false>, a);
 }

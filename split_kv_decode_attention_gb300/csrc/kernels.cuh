@@ -94,6 +94,7 @@ struct CombineArgs {
   const int32_t* pre;
   int num_kv_heads;
   int len_sb, len_sh;                  // strides of seq_lens (see SplitArgs)
+  int by_row;                          // few rows: merge with a CTA per row (4-bit caches)
   int unit_heads;                      // device-planned: KV heads of an item (1; more for 4-bit caches)
 };
 
@@ -166,7 +167,7 @@ cudaError_t launch_fp4(const Fp4Maps& maps, const SplitArgs& a, int heads_per_ct
 int fp4_ctas_per_sm(int rows, int heads_per_cta);
 int fp4_warps(int rows);  // consumer warps of a CTA: its heads divide them
 
-// Launch the combine kernel (one warp per output row).
+// Launch the combine kernel (one warp per output row, or with by_row and few rows a CTA).
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream);
 
 // Launch the device planner ahead of a device-planned split launch.
