@@ -453,7 +453,7 @@ int decode_attn_cached(const decode_attn_params *p, const decode_attn_cache *c, 
  *     table[(pos - first) * 2 num_freqs + i]             = amplitude cos(pos f_i)
  *     table[(pos - first) * 2 num_freqs + num_freqs + i] = amplitude sin(pos f_i)
  * in fp32, to about one ulp at every position (the angle is reduced in 64-bit
- * fixed point).  Scalings for long contexts are the caller's choice of f and
+ * fixed point); the table is 16-byte aligned.  Scalings for long contexts are the caller's choice of f and
  * amplitude.  1 <= num_freqs <= 64, first and first + count within 0 .. 2^31.
  * Frequencies that are not finite give NaN.
  */

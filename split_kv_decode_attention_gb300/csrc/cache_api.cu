@@ -216,7 +216,7 @@ int decode_attn_rope_table(const double* inv_freq, int32_t num_freqs, int64_t fi
     return DA_ERR_BAD_SHAPE;
   if (count == 0) return DA_OK;
   if (inv_freq == nullptr || table == nullptr) return DA_ERR_NULL_POINTER;
-  if (!aligned(inv_freq, 8) || !aligned(table, 4)) return DA_ERR_ALIGNMENT;
+  if (!aligned(inv_freq, 8) || !aligned16(table)) return DA_ERR_ALIGNMENT;
   int sms = 0;
   const int rc = dattn::check_device(&sms);
   if (rc != DA_OK) return rc;
@@ -299,6 +299,7 @@ int decode_attn_rope_append(const decode_attn_params* p, const decode_attn_cache
   a.rotary_dim = r->rotary_dim;
   a.interleaved = r->interleaved ? 1 : 0;
   a.table_positions = r->table_positions;
+  a.one = 1.f;
   a.k_inv = c->type != DA_CACHE_BF16 ? 1.f / p->k_scale : 1.f;
   a.v_inv = c->type != DA_CACHE_BF16 ? 1.f / p->v_scale : 1.f;
   return dattn::launch_append(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
@@ -326,7 +327,8 @@ int decode_attn_block_digest(const decode_attn_params* p, const decode_attn_cach
   rc = dattn::check_cache(&cp, c, true, false);
   if (rc != DA_OK) return rc;
   if (static_cast<int64_t>(max_blocks(p)) * p->num_kv_heads > 0x7fffffff) return DA_ERR_BAD_SHAPE;
-  rc = dattn::check_device(nullptr);
+  int sms = 0;
+  rc = dattn::check_device(&sms);
   if (rc != DA_OK) return rc;
   dattn::DigestArgs a;
   std::memset(&a, 0, sizeof(a));
@@ -335,8 +337,8 @@ int decode_attn_block_digest(const decode_attn_params* p, const decode_attn_cach
   a.max_new = max_new;
   a.digest = digest;
   a.digest_scale = digest_scale;
-  return dattn::launch_digest(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DA_OK
-                                                                                   : DA_ERR_CUDA;
+  return dattn::launch_digest(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DA_OK
+                                                                                        : DA_ERR_CUDA;
 }
 
 int decode_attn_block_select_workspace_bytes(const decode_attn_params* p,

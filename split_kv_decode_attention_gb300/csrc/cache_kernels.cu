@@ -18,10 +18,13 @@ constexpr uint32_t kFull = 0xffffffffu;
 // cos / sin of pos * f.  In turns the angle is pos * f / (2 pi), and only its
 // fraction counts: with F = round(2^64 frac(f / 2 pi)) as an unsigned 64-bit
 // integer, pos * F modulo 2^64 is that fraction, to pos * 2^-65 turns, by one
-// integer multiply.  The nearest quarter turn is split off exactly and the
-// remainder, at most an eighth of a turn, goes through sincospif in fp32: full
-// relative accuracy at every position, without the fp64 argument reduction
-// and sine per entry (fp64 runs at 1/64 of the fp32 rate on this GPU).
+// integer multiply; the next row of a thread is an addition away.  The nearest
+// quarter turn is split off exactly, and on the remainder x of at most pi / 4
+// the Taylor series through x^9 and x^10 are within 3e-9 and 2e-10 of sine and
+// cosine, a thirtieth of an fp32 step: full relative accuracy at every
+// position with 11 fp32 multiply-adds, where an fp64 cosine is two orders of
+// magnitude more work (fp64 runs at 1/64 of the fp32 rate on this GPU).  The
+// F of the frequencies, the only fp64 work, are made once per CTA.
 __device__ __forceinline__ uint64_t turns_fixed(double f) {
   const double kInv2PiHi = 0.15915494309189535;      // 1 / (2 pi), rounded
   const double kInv2PiLo = -9.839338337591243e-18;   // what is left of it
@@ -33,53 +36,119 @@ __device__ __forceinline__ uint64_t turns_fixed(double f) {
   return (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>(static_cast<int64_t>(rint(lo)));
 }
 
-constexpr int kTablePos = 8;  // positions per thread
+// cos and sin of phase / 2^64 turns, times amp.
+__device__ __forceinline__ void cos_sin_turns(uint64_t phase, float amp, float& c, float& s) {
+  const uint32_t hi = static_cast<uint32_t>(phase >> 32);
+  const uint32_t quarter = (hi + 0x20000000u) >> 30;
+  // the remainder, within 2^61: its high part signed, its low part not
+  const int32_t rh = static_cast<int32_t>(hi - (quarter << 30));
+  const float rest = fmaf(static_cast<float>(rh), 4294967296.f,
+                          static_cast<float>(static_cast<uint32_t>(phase)));
+  const float x = rest * 3.4061215800865545e-19f;  // 2 pi / 2^64
+  const float z = x * x;
+  const float sp = fmaf(fmaf(fmaf(fmaf(z, 1.f / 362880.f, -1.f / 5040.f), z, 1.f / 120.f), z, -1.f / 6.f), z * x, x);
+  const float cp = fmaf(fmaf(fmaf(fmaf(fmaf(z, -1.f / 3628800.f, 1.f / 40320.f), z, -1.f / 720.f), z, 1.f / 24.f), z, -0.5f), z, 1.f);
+  // a quarter turn on: (c, s) -> (-s, c)
+  const float cc = quarter & 1 ? sp : cp, ss = quarter & 1 ? cp : sp;
+  c = cc * (((quarter + 1) & 2) ? -amp : amp);
+  s = ss * ((quarter & 2) ? -amp : amp);
+}
 
-__global__ void __launch_bounds__(256)
-    rope_table_kernel(const double* inv_freq, int n, int64_t first, int64_t count, float amp,
-                      float* table) {
+constexpr int kTableThreads = 256;
+
+// V neighbouring frequencies per thread (4 where that divides their number).
+template <int V>
+__global__ void __launch_bounds__(kTableThreads)
+    rope_table_kernel(const double* inv_freq, int n, int64_t first, int64_t count, float amp, float* table) {
+  __shared__ uint64_t step[64];
   grid_dependency_wait();
-  const int per = blockDim.x / n;  // positions side by side in the block
-  const int i = threadIdx.x % n;
-  const int row = threadIdx.x / n;
+  if (threadIdx.x < n) step[threadIdx.x] = turns_fixed(inv_freq[threadIdx.x]);
+  const int cols = n / V;
+  const int per = kTableThreads / cols;  // rows side by side in the CTA
+  const int row = threadIdx.x / cols;
+  const int i = (threadIdx.x - row * cols) * V;
+  __syncthreads();
   if (row >= per) return;
-  const double f = inv_freq[i];
-  const bool ok = fabs(f) <= 1.7976931348623157e308;  // (not NaN or infinite)
-  // frequencies of 2^31 radians and more keep no fraction worth the name in
-  // fp64 terms, but stay defined: the same wrap
-  const uint64_t step = ok ? turns_fixed(f) : 0;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * per;
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * per + row; r < count; r += stride) {
-    const uint64_t phase = static_cast<uint64_t>(first + r) * step;
-    const uint32_t quarter = static_cast<uint32_t>((phase + (uint64_t{1} << 61)) >> 62);
-    const int64_t rest = static_cast<int64_t>(phase - (static_cast<uint64_t>(quarter) << 62));
-    float s, c;
-    sincospif(static_cast<float>(rest) * 0x1p-63f, &s, &c);  // rest turns / 2^64, in units of pi
-    if (quarter & 1) {
-      const float x = c;
-      c = -s;
-      s = x;
+  int64_t r = static_cast<int64_t>(blockIdx.x) * per + row;
+  uint64_t phase[V], ahead[V];
+  bool ok[V];  // (frequencies that are not finite give NaN)
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    phase[v] = static_cast<uint64_t>(first + r) * step[i + v];
+    ahead[v] = static_cast<uint64_t>(stride) * step[i + v];
+    ok[v] = fabs(inv_freq[i + v]) <= 1.7976931348623157e308;
+  }
+  float* out = table + r * 2 * n + i;
+  const int64_t ostride = stride * 2 * n;
+  for (; r < count; r += stride, out += ostride) {
+    float c[V], s[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      cos_sin_turns(phase[v], amp, c[v], s[v]);
+      if (!ok[v]) c[v] = s[v] = __int_as_float(0x7fc00000);
+      phase[v] += ahead[v];
     }
-    if (quarter & 2) {
-      c = -c;
-      s = -s;
+    if constexpr (V == 4) {
+      *reinterpret_cast<float4*>(out) = make_float4(c[0], c[1], c[2], c[3]);
+      *reinterpret_cast<float4*>(out + n) = make_float4(s[0], s[1], s[2], s[3]);
+    } else {
+      out[0] = c[0];
+      out[n] = s[0];
     }
-    if (!ok) c = s = __int_as_float(0x7fc00000);
-    float* out = table + r * 2 * n;
-    out[i] = c * amp;
-    out[n + i] = s * amp;
   }
 }
 
 // ------------------------------------------------------------------- append
 // 16 threads hold the 128 values of a (token, head), 8 each.  A CTA works on
-// one token: each thread keeps the cos / sin of its 8 values in registers for
-// all the heads it walks, so the table is read once per CTA and row of
+// one token, eight heads a pass: passes over q's heads, then k's, then v's, each
+// a pointer that steps on.  A thread keeps the cos / sin of its 8 values in
+// registers for all of them, so the table is read once per CTA and row of
 // threads, and the pair partners of the half layout come by one shuffle (a
 // thread's 8 values and their partners lie rotary_dim / 2 apart, whole threads
 // when that is a multiple of 8; other sizes read the partner from memory).
+// The first passes' rows are on their way before the token's place is known.
+// Instructions bound it as much as HBM does (at 32 + 2 x 8 heads 190 of 8
+// values each per token), so values go in pairs (mul / add.f32x2).
 constexpr int kAppendThreads = 128;
 constexpr int kRowsPerPass = kAppendThreads / 16;
+
+// Two fp32 values in a register pair.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+
+// x + y, for x a product of mul2: the assembler fuses an add.rn.f32x2 with the
+// mul.rn.f32x2 before it into one rounding (it leaves the scalar forms alone),
+// so the sum is x * one + y with a `one` that only the launch knows.
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y, uint64_t one) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(one), "l"(y));
+  return r;
+}
+
+// Two bf16 values, exactly.
+__device__ __forceinline__ uint64_t widen(uint32_t w) {
+  return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+__device__ __forceinline__ uint32_t narrow(uint64_t v) {
+  float lo, hi;
+  unpair(v, lo, hi);
+  return pack_bf16x2(lo, hi);
+}
 
 __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
   uint16_t r;
@@ -105,40 +174,55 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&x)[8]) {
 
 // The eight values of this thread (two bf16 per word) into the cache row at
 // `row` (4-bit: block scales at sf_row).  All lanes of a warp call it together.
-__device__ __forceinline__ void store_row(int type, uint8_t* row, uint8_t* sf_row, int d16,
-                                          const uint32_t (&w)[4], float inv, bool live) {
-  if (type == DA_CACHE_BF16) {
+template <int TYPE>
+__device__ __forceinline__ void store_row(uint8_t* row, uint8_t* sf_row, int d16, const uint32_t (&w)[4],
+                                          float inv, bool live) {
+  if constexpr (TYPE == DA_CACHE_BF16) {
     if (live) *reinterpret_cast<uint4*>(row + d16 * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-    return;
   }
-  float x[8];
+  [[maybe_unused]] float x[8];
+  if constexpr (TYPE != DA_CACHE_BF16) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __fmul_rn(__uint_as_float(w[i] << 16), inv);
-    x[2 * i + 1] = __fmul_rn(__uint_as_float(w[i] & 0xffff0000u), inv);
+    for (int i = 0; i < 4; ++i) unpair(mul2(widen(w[i]), pair(inv, inv)), x[2 * i], x[2 * i + 1]);
   }
-  if (type == DA_CACHE_FP8_E4M3) {
+  if constexpr (TYPE == DA_CACHE_FP8_E4M3) {
     const uint2 v = make_uint2(e4m3_pair(x[0], x[1]) | (e4m3_pair(x[2], x[3]) << 16),
                                e4m3_pair(x[4], x[5]) | (e4m3_pair(x[6], x[7]) << 16));
     if (live) *reinterpret_cast<uint2*>(row + d16 * 8) = v;
-    return;
-  }
-  float top = 0.f;
+  } else if constexpr (TYPE == DA_CACHE_FP4_E2M1) {
+    float top = 0.f, all = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));  // (NaN is passed over)
-  top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-  const uint32_t code = e4m3_pair(__fdiv_rn(top, 6.f), 0.f) & 0xffu;
-  const float sf = e4m3_value(code);
+    for (int i = 0; i < 8; ++i) {
+      top = fmaxf(top, fabsf(x[i]));  // (NaN is passed over)
+      all += x[i];
+    }
+    top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+    const uint32_t code = e4m3_pair(__fdiv_rn(top, 6.f), 0.f) & 0xffu;
+    const float sf = e4m3_value(code);
+    // x / sf, correctly rounded: a rounded reciprocal, a product, and one
+    // residual correction (Markstein 1990), three operations a value.  It needs
+    // finite quotients, so NaN becomes 0 and what lies past 8 sf, and saturates
+    // all the same, comes in; a block has such values only if its sum is not
+    // finite or its scale saturated.
+    if (!(fabsf(all) < INFINITY) || top > 6.f * 448.f) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = sf > 0.f && x[i] == x[i] ? __fdiv_rn(x[i], sf) : 0.f;
-  if (live) {
-    *reinterpret_cast<uint32_t*>(row + d16 * 4) = e2m1x8(x);
-    if ((d16 & 1) == 0) sf_row[d16 >> 1] = static_cast<uint8_t>(code);
+      for (int i = 0; i < 8; ++i) x[i] = x[i] == x[i] ? fminf(fmaxf(x[i], -8.f * sf), 8.f * sf) : 0.f;
+    }
+    const float r = sf > 0.f ? __frcp_rn(sf) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q = __fmul_rn(x[i], r);
+      x[i] = copysignf(fmaf(fmaf(-q, sf, x[i]), r, q), x[i]);  // (-0 stays -0)
+    }
+    if (live) {
+      *reinterpret_cast<uint32_t*>(row + d16 * 4) = sf > 0.f ? e2m1x8(x) : 0u;
+      if ((d16 & 1) == 0) sf_row[d16 >> 1] = static_cast<uint8_t>(code);
+    }
   }
 }
 
 // VEC: rotary_dim is a multiple of 16 (table and partners in whole vectors).
-template <bool VEC>
+template <bool VEC, int TYPE>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
   const int d16 = threadIdx.x & 15;
   const int sub = threadIdx.x >> 4;
@@ -146,7 +230,36 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
   const int token = blockIdx.x;
   const int b = token / a.g.q_len;
   const int t = token - b * a.g.q_len;
+  const int d0 = 8 * d16;
+
+  // ---- the passes of this CTA: p = blockIdx.y, + gridDim.y, ...; q's first
+  const int q_passes = (a.num_q_heads + kRowsPerPass - 1) / kRowsPerPass;
+  const int kv_passes = a.append ? (a.g.num_kv_heads + kRowsPerPass - 1) / kRowsPerPass : 0;
+  const int passes = q_passes + 2 * kv_passes;
+  const uint16_t* q0 = a.q + static_cast<int64_t>(b) * a.q_sb + static_cast<int64_t>(t) * a.q_st + d0;
+  const uint16_t* k0 = a.k + static_cast<int64_t>(b) * a.k_sb + static_cast<int64_t>(t) * a.k_st + d0;
+  const uint16_t* v0 = a.v + static_cast<int64_t>(b) * a.v_sb + static_cast<int64_t>(t) * a.v_st + d0;
+  // this thread's row in a pass (nullptr: no such head)
+  auto source = [&](int p) -> const uint16_t* {
+    if (p < q_passes) {
+      const int h = p * kRowsPerPass + sub;
+      return h < a.num_q_heads ? q0 + h * a.q_sh : nullptr;
+    }
+    p -= q_passes;
+    const bool is_v = p >= kv_passes;
+    const int h = (is_v ? p - kv_passes : p) * kRowsPerPass + sub;
+    if (p >= 2 * kv_passes || h >= a.g.num_kv_heads) return nullptr;
+    return is_v ? v0 + h * a.v_sh : k0 + h * a.k_sh;
+  };
+  auto fetch = [&](int p) {
+    const uint16_t* src = source(p);
+    return src != nullptr ? *reinterpret_cast<const uint4*>(src) : make_uint4(0u, 0u, 0u, 0u);
+  };
   grid_dependency_wait();
+  constexpr int kAhead = 3;  // passes whose rows are loaded ahead
+  uint4 next[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) next[i] = fetch(blockIdx.y + i * gridDim.y);
 
   // ---- the token's place
   uint32_t bad = 0;
@@ -185,22 +298,22 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
   const bool write = live && (bad & DA_STATUS_BAD_PAGE) == 0;
   if (!live) return;  // (the whole CTA: one token)
 
-  // ---- cos and sin of this thread's values: c[i] and the signed s[i] of value
-  // 8 d16 + i, as y = x c + partner s
+  // ---- cos and sin of this thread's values, in pairs: y = x c + partner s,
+  // with s negative for the first value of a (value, partner) pair
   const int half = a.rotary_dim >> 1;
-  const int d0 = 8 * d16;
-  float c[8], s[8];
+  uint64_t c[4], s[4];
   const float* row = a.table + static_cast<int64_t>(pos) * a.rotary_dim;
+  const bool turned = d0 < a.rotary_dim;  // (VEC: all of the thread's values or none)
   if constexpr (VEC) {
-    if (d0 < a.rotary_dim) {
+    if (turned) {
       if (a.interleaved) {
         const float4 cc = *reinterpret_cast<const float4*>(row + (d0 >> 1));
         const float4 ss = *reinterpret_cast<const float4*>(row + half + (d0 >> 1));
         const float c4[4] = {cc.x, cc.y, cc.z, cc.w}, s4[4] = {ss.x, ss.y, ss.z, ss.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          c[i] = c4[i >> 1];
-          s[i] = i & 1 ? s4[i >> 1] : -s4[i >> 1];
+        for (int i = 0; i < 4; ++i) {
+          c[i] = pair(c4[i], c4[i]);
+          s[i] = pair(-s4[i], s4[i]);
         }
       } else {
         const int f0 = d0 < half ? d0 : d0 - half;
@@ -209,122 +322,164 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
         for (int v = 0; v < 2; ++v) {
           const float4 cc = *reinterpret_cast<const float4*>(row + f0 + 4 * v);
           const float4 ss = *reinterpret_cast<const float4*>(row + half + f0 + 4 * v);
-          c[4 * v] = cc.x;
-          c[4 * v + 1] = cc.y;
-          c[4 * v + 2] = cc.z;
-          c[4 * v + 3] = cc.w;
-          s[4 * v] = sign * ss.x;
-          s[4 * v + 1] = sign * ss.y;
-          s[4 * v + 2] = sign * ss.z;
-          s[4 * v + 3] = sign * ss.w;
+          c[2 * v] = pair(cc.x, cc.y);
+          c[2 * v + 1] = pair(cc.z, cc.w);
+          s[2 * v] = pair(sign * ss.x, sign * ss.y);
+          s[2 * v + 1] = pair(sign * ss.z, sign * ss.w);
         }
       }
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int d = d0 + i;
-      const bool in = d < a.rotary_dim;
-      const int f = a.interleaved ? d >> 1 : (d < half ? d : d - half);
-      const bool second = a.interleaved ? (d & 1) != 0 : d >= half;
-      c[i] = in ? row[f] : 1.f;
-      s[i] = in ? (second ? row[half + f] : -row[half + f]) : 0.f;
+    for (int i = 0; i < 4; ++i) {
+      float cc[2], ss[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int d = d0 + 2 * i + j;
+        const bool in = d < a.rotary_dim;
+        const int f = a.interleaved ? d >> 1 : (d < half ? d : d - half);
+        const bool second = a.interleaved ? (d & 1) != 0 : d >= half;
+        cc[j] = in ? row[f] : 1.f;
+        ss[j] = in ? (second ? row[half + f] : -row[half + f]) : 0.f;
+      }
+      c[i] = pair(cc[0], cc[1]);
+      s[i] = pair(ss[0], ss[1]);
     }
   }
   // the lane that holds the partners of this thread's values (half layout)
   const int peer = (lane & 16) | ((d16 + (d0 < half ? (half >> 3) : -(half >> 3))) & 15);
 
-  // ---- the heads: q, then k, then v
-  const int rows = a.num_q_heads + (a.append ? 2 * a.g.num_kv_heads : 0);
-  const int step = kRowsPerPass * gridDim.y;
-  auto source = [&](int r) -> const uint16_t* {
-    if (r < a.num_q_heads)
-      return a.q + static_cast<int64_t>(b) * a.q_sb + static_cast<int64_t>(t) * a.q_st + r * a.q_sh;
-    r -= a.num_q_heads;
-    if (r < a.g.num_kv_heads)
-      return a.k + static_cast<int64_t>(b) * a.k_sb + static_cast<int64_t>(t) * a.k_st + r * a.k_sh;
-    r -= a.g.num_kv_heads;
-    return a.v + static_cast<int64_t>(b) * a.v_sb + static_cast<int64_t>(t) * a.v_st + r * a.v_sh;
-  };
-  const int base = blockIdx.y * kRowsPerPass + (sub & ~1);  // the warp's first row of a pass
-  uint4 next = make_uint4(0u, 0u, 0u, 0u);
-  if (base + (sub & 1) < rows) next = *reinterpret_cast<const uint4*>(source(base + (sub & 1)) + d0);
-  for (int r0 = base; r0 < rows; r0 += step) {  // (both rows of a warp together)
-    const int r = r0 + (sub & 1);
-    const bool have = r < rows;
-    const uint4 x4 = next;
-    const int rn = r + step;
-    if (rn < rows) next = *reinterpret_cast<const uint4*>(source(rn) + d0);
+  // the rotated values of a row: every product and the sum rounded, the
+  // definition, and the same bytes for a token wherever it is computed again
+  const uint64_t one = pair(a.one, a.one);
+  auto rotate = [&](const uint4& x4, const uint16_t* src, uint32_t (&y)[4]) {
     const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
-    const int kv = r - a.num_q_heads;
-    const bool is_v = kv >= a.g.num_kv_heads;
-    uint32_t p[4];
-    if constexpr (VEC) {
+    uint64_t p[4];
+    if (a.interleaved) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t o = __shfl_sync(kFull, x[i], peer);
-        p[i] = a.interleaved ? __byte_perm(x[i], 0, 0x1032) : o;
-      }
+      for (int i = 0; i < 4; ++i) p[i] = widen(__byte_perm(x[i], 0, 0x1032));
+    } else if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = widen(__shfl_sync(kFull, x[i], peer));
     } else {
-      const uint16_t* src = have ? source(r) : nullptr;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (a.interleaved) {
-          p[i] = __byte_perm(x[i], 0, 0x1032);
-          continue;
-        }
         uint32_t o[2] = {0u, 0u};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int d = d0 + 2 * i + j;
-          if (have && d < a.rotary_dim) o[j] = src[d < half ? d + half : d - half];
+          if (src != nullptr && d < a.rotary_dim) o[j] = (src - d0)[d < half ? d + half : d - half];
         }
-        p[i] = o[0] | (o[1] << 16);
+        p[i] = widen(o[0] | (o[1] << 16));
       }
       __syncwarp();  // (q_out may be q: every partner is read before any store)
     }
-    uint32_t y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float x0 = __uint_as_float(x[i] << 16), x1 = __uint_as_float(x[i] & 0xffff0000u);
-      const float p0 = __uint_as_float(p[i] << 16), p1 = __uint_as_float(p[i] & 0xffff0000u);
-      // every product and the sum rounded: the definition, and the same bytes
-      // for a token wherever it is computed again
-      const float y0 = __fadd_rn(__fmul_rn(x0, c[2 * i]), __fmul_rn(p0, s[2 * i]));
-      const float y1 = __fadd_rn(__fmul_rn(x1, c[2 * i + 1]), __fmul_rn(p1, s[2 * i + 1]));
-      const uint32_t lo = d0 + 2 * i < a.rotary_dim ? pack_bf16x2(y0, 0.f) & 0xffffu : x[i] & 0xffffu;
-      const uint32_t hi = d0 + 2 * i + 1 < a.rotary_dim ? pack_bf16x2(0.f, y1) & 0xffff0000u
-                                                        : x[i] & 0xffff0000u;
-      y[i] = is_v ? x[i] : lo | hi;
+      const uint32_t r = narrow(add2(mul2(widen(x[i]), c[i]), mul2(p[i], s[i]), one));
+      if constexpr (VEC) {
+        y[i] = turned ? r : x[i];
+      } else {
+        const int d = d0 + 2 * i;
+        y[i] = (d < a.rotary_dim ? r & 0xffffu : x[i] & 0xffffu) |
+               (d + 1 < a.rotary_dim ? r & 0xffff0000u : x[i] & 0xffff0000u);
+      }
     }
-    if (have && kv < 0)
-      *reinterpret_cast<uint4*>(a.q_out + static_cast<int64_t>(b) * a.o_sb +
-                                static_cast<int64_t>(t) * a.o_st + r * a.o_sh + d0) =
-          make_uint4(y[0], y[1], y[2], y[3]);
-    if (r0 + 1 >= a.num_q_heads && a.append) {  // (warp-uniform: one of the two rows is k or v)
-      const bool ok = have && kv >= 0 && write;
-      const int h = ok ? (is_v ? kv - a.g.num_kv_heads : kv) : 0;
-      store_row(a.c.type, (is_v ? a.c.v : a.c.k) + place + h * a.c.head,
-                (is_v ? a.c.vs : a.c.ks) + sf_place + h * a.c.sf_head, d16, y,
-                is_v ? a.v_inv : a.k_inv, ok);
+  };
+
+  uint16_t* o0 = a.q_out + static_cast<int64_t>(b) * a.o_sb + static_cast<int64_t>(t) * a.o_st + d0;
+  auto pass = [&](int p, const uint4& x) {
+    uint32_t y[4];
+    if (p < q_passes) {
+      const int h = p * kRowsPerPass + sub;
+      const bool have = h < a.num_q_heads;
+      rotate(x, have ? q0 + h * a.q_sh : nullptr, y);
+      if (have) *reinterpret_cast<uint4*>(o0 + h * a.o_sh) = make_uint4(y[0], y[1], y[2], y[3]);
+      return;
     }
+    p -= q_passes;
+    const bool is_v = p >= kv_passes;  // (uniform)
+    const int h = (is_v ? p - kv_passes : p) * kRowsPerPass + sub;
+    const bool have = h < a.g.num_kv_heads;
+    const int64_t to = place + h * a.c.head, sf_to = sf_place + h * a.c.sf_head;
+    if (is_v) {
+      y[0] = x.x;
+      y[1] = x.y;
+      y[2] = x.z;
+      y[3] = x.w;
+      store_row<TYPE>(a.c.v + to, a.c.vs + sf_to, d16, y, a.v_inv, have && write);
+    } else {
+      rotate(x, have ? k0 + h * a.k_sh : nullptr, y);
+      store_row<TYPE>(a.c.k + to, a.c.ks + sf_to, d16, y, a.k_inv, have && write);
+    }
+  };
+  for (int p = blockIdx.y; p < passes; p += kAhead * gridDim.y) {
+    uint4 now[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) now[i] = next[i];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) next[i] = fetch(p + (kAhead + i) * gridDim.y);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (p + i * static_cast<int>(gridDim.y) < passes) pass(p + i * gridDim.y, now[i]);
   }
 }
 
 // ------------------------------------------------------------------- digest
-// One warp per (page, KV head): 16 lanes hold the 128 channels, 8 each, and
-// the two half-warps take every other token; minima and maxima stay in
-// registers.  Neighbouring warps take neighbouring heads of a page, which a
-// [page, slot, head, d] cache holds side by side.
+// A warp takes a KV head's pages, about 32 KB of them (16 ragged requests of up
+// to 32K tokens in 16-token bf16 pages: one page 205 us, four 137, eight 131);
+// the warps of a CTA take neighbouring heads, which a [page, slot, head, d]
+// cache holds side by side.  A lane loads 16 bytes of a row (8, 16 or 32
+// values; 2, 4 or 8 rows per load), a batch of loads at work and the next on
+// its way, and keeps packed 16-bit minima and maxima: bf16 as it is, FP8
+// and 4-bit values exactly in f16.  The rows' partial results meet in a
+// reduce-scatter (each step sends half of what is left): 4, 12 or 28 shuffles
+// per page, after which every lane holds 8 channels of the minimum or of the
+// maximum, whatever the type.
 constexpr int kDigestWarps = 8;
+constexpr int64_t kWarpBytes = 32768;  // of keys that a warp walks, where there are enough
 constexpr float kBf16Max = 3.3895313892515355e38f;
 
+template <bool BF>
+__device__ __forceinline__ uint32_t min2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  if constexpr (BF) asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  else asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
+template <bool BF>
+__device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  if constexpr (BF) asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  else asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
 template <int TYPE>
-__global__ void __launch_bounds__(32 * kDigestWarps) digest_kernel(const DigestArgs a) {
+struct DigestCfg {
+  static constexpr bool kBf = TYPE == DA_CACHE_BF16;
+  static constexpr int kLanes = kBf ? 16 : TYPE == DA_CACHE_FP8_E4M3 ? 8 : 4;  // of a row
+  static constexpr int kRows = 32 / kLanes;                                    // per load
+  static constexpr int kWords = 128 / kLanes / 2;                              // packed values of a lane
+  // in flight (4-bit: 4, its minima and maxima fill the registers; 8 took 95 us
+  // where 4 take 72, FP8 the other way round, 90 and 75)
+  static constexpr int kLoads = TYPE == DA_CACHE_FP4_E2M1 ? 4 : 8;
+};
+
+template <int TYPE>
+__global__ void __launch_bounds__(32 * kDigestWarps) digest_kernel(const DigestArgs a, int pages_per_warp) {
+  using C = DigestCfg<TYPE>;
+  constexpr int NW = C::kWords;
   const int lane = threadIdx.x & 31;
-  const int d16 = lane & 15;
-  const int sub = lane >> 4;
-  const int64_t idx = static_cast<int64_t>(blockIdx.x) * kDigestWarps + (threadIdx.x >> 5);
+  const int l = lane % C::kLanes, rg = lane / C::kLanes;
+  const uint32_t idx = blockIdx.x * kDigestWarps + (threadIdx.x >> 5);
   const int b = blockIdx.y;
   grid_dependency_wait();
   int L = a.g.seq_lens[b];
@@ -335,96 +490,149 @@ __global__ void __launch_bounds__(32 * kDigestWarps) digest_kernel(const DigestA
   }
   const int ps = a.g.page_size;
   const int first = a.max_new > 0 ? max(0, L - a.max_new) / ps : 0;
-  const int64_t c64 = first + idx / a.g.num_kv_heads;
-  const int h = static_cast<int>(idx % a.g.num_kv_heads);
-  if (c64 * ps >= L) return;
-  const int col = static_cast<int>(c64);
-  int pg = a.g.block_table[static_cast<int64_t>(b) * a.g.bt_stride + col];
-  if (pg < 0 || pg >= a.g.num_pages) {
-    if (a.g.status != nullptr && lane == 0)
-      atomicOr(a.g.status, static_cast<int32_t>(DA_STATUS_BAD_PAGE));
-    return;  // (nothing is digested for a page that does not exist)
-  }
-  const int held = min(ps, L - col * ps);
-  const uint8_t* base = a.c.k + pg * a.c.page + h * a.c.head;
-  const uint8_t* sfb = TYPE == DA_CACHE_FP4_E2M1 ? a.c.ks + pg * a.c.sf_page + h * a.c.sf_head : nullptr;
-  float lo[8], hi[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo[i] = INFINITY;
-    hi[i] = -INFINITY;
-  }
-  constexpr int kBatch = 8;  // 16 tokens in flight per warp
-  for (int j0 = sub; j0 < held; j0 += 2 * kBatch) {
-    uint4 x[kBatch];
-    uint32_t sf[kBatch];
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int tok = min(j0 + 2 * j, held - 1);  // (the last token again: no effect)
-      const uint8_t* p = base + static_cast<int64_t>(tok) * a.c.token;
-      if constexpr (TYPE == DA_CACHE_BF16) {
-        x[j] = __ldg(reinterpret_cast<const uint4*>(p + d16 * 16));
-      } else if constexpr (TYPE == DA_CACHE_FP8_E4M3) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p + d16 * 8));
-        x[j].x = v.x;
-        x[j].y = v.y;
-      } else {
-        x[j].x = __ldg(reinterpret_cast<const uint32_t*>(p + d16 * 4));
-        sf[j] = __ldg(sfb + static_cast<int64_t>(tok) * 8 + (d16 >> 1));
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      float v[8];
-      if constexpr (TYPE == DA_CACHE_BF16) {
-        const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          v[i] = i & 1 ? __uint_as_float(w[i >> 1] & 0xffff0000u) : __uint_as_float(w[i >> 1] << 16);
-      } else if constexpr (TYPE == DA_CACHE_FP8_E4M3) {
-        uint32_t w[4];
-        e4m3x4_to_f16x4(x[j].x, w[0], w[1]);
-        e4m3x4_to_f16x4(x[j].y, w[2], w[3]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i & 1 ? packed_hi(w[i >> 1], true) : packed_lo(w[i >> 1], true);
-      } else {
-        uint32_t w[4];
-        e2m1x8_to_f16(x[j].x, w);
-        const float s = e4m3_value(sf[j]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          v[i] = (i & 1 ? packed_hi(w[i >> 1], true) : packed_lo(w[i >> 1], true)) * s;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {  // (fminf / fmaxf pass over NaN)
-        lo[i] = fminf(lo[i], v[i]);
-        hi[i] = fmaxf(hi[i], v[i]);
-      }
+  const int cols = (L + ps - 1) / ps;                       // pages of the request
+  const uint32_t group = idx / a.g.num_kv_heads;
+  const int h = static_cast<int>(idx - group * a.g.num_kv_heads);
+  const int64_t col0 = first + static_cast<int64_t>(group) * pages_per_warp;
+  if (col0 >= cols) return;
+  const int n = min(pages_per_warp, cols - static_cast<int>(col0));
+  // the warp's page ids, lane i the i-th (-1: does not exist, not digested)
+  int id = -1;
+  if (lane < n) {
+    id = a.g.block_table[static_cast<int64_t>(b) * a.g.bt_stride + col0 + lane];
+    if (id < 0 || id >= a.g.num_pages) {
+      if (a.g.status != nullptr) atomicOr(a.g.status, static_cast<int32_t>(DA_STATUS_BAD_PAGE));
+      id = -1;
     }
   }
-  float top = 0.f;
+  constexpr int kTokens = C::kLoads * C::kRows;             // of a batch
+  const int parts = (ps + kTokens - 1) / kTokens;           // batches of a page
+  const uint8_t* kbase = a.c.k + static_cast<int64_t>(h) * a.c.head + l * 16;
+  const uint8_t* sbase = TYPE == DA_CACHE_FP4_E2M1 ? a.c.ks + static_cast<int64_t>(h) * a.c.sf_head + 2 * l : nullptr;
+  auto held = [&](int page) { return min(ps, L - (static_cast<int>(col0) + page) * ps); };  // tokens of a page
+
+  uint4 x[C::kLoads];
+  uint32_t sf[TYPE == DA_CACHE_FP4_E2M1 ? C::kLoads : 1];
+  auto load = [&](int page, int part) {
+    const int pg = __shfl_sync(kFull, id, page);
+    const int last = held(page) - 1;
+    const uint8_t* p = kbase + static_cast<int64_t>(max(pg, 0)) * a.c.page;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo[i] = fminf(lo[i], __shfl_xor_sync(kFull, lo[i], 16));
-    hi[i] = fmaxf(hi[i], __shfl_xor_sync(kFull, hi[i], 16));
-    const bool none = lo[i] > hi[i];  // (nothing but NaN)
-    lo[i] = none ? 0.f : fminf(fmaxf(lo[i], -kBf16Max), kBf16Max);
-    hi[i] = none ? 0.f : fminf(fmaxf(hi[i], -kBf16Max), kBf16Max);
-    top = fmaxf(top, fmaxf(fabsf(lo[i]), fabsf(hi[i])));
+    for (int j = 0; j < C::kLoads; ++j) {
+      const int row = part * kTokens + j * C::kRows;
+      if (row > last || pg < 0) continue;                   // (uniform)
+      const int tok = min(row + rg, last);                  // (the last token again: no effect)
+      x[j] = __ldg(reinterpret_cast<const uint4*>(p + static_cast<int64_t>(tok) * a.c.token));
+      if constexpr (TYPE == DA_CACHE_FP4_E2M1)
+        sf[j] = __ldg(reinterpret_cast<const uint16_t*>(sbase + static_cast<int64_t>(pg) * a.c.sf_page +
+                                                        static_cast<int64_t>(tok) * 8));
+    }
+  };
+  load(0, 0);
+  uint32_t v[2 * NW];                                       // minima, then maxima
+  for (int page = 0; page < n; ++page) {
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      v[i] = C::kBf ? 0x7f807f80u : 0x7c007c00u;            // + infinity
+      v[NW + i] = C::kBf ? 0xff80ff80u : 0xfc00fc00u;
+    }
+    const int tokens = held(page);
+    for (int part = 0; part < parts; ++part) {
+      uint4 y[C::kLoads];
+      uint32_t ys[TYPE == DA_CACHE_FP4_E2M1 ? C::kLoads : 1];
+#pragma unroll
+      for (int j = 0; j < C::kLoads; ++j) {
+        y[j] = x[j];
+        if constexpr (TYPE == DA_CACHE_FP4_E2M1) ys[j] = sf[j];
+      }
+      if (part + 1 < parts) load(page, part + 1);
+      else if (page + 1 < n) load(page + 1, 0);
+#pragma unroll
+      for (int j = 0; j < C::kLoads; ++j) {
+        if (part * kTokens + j * C::kRows >= tokens) break;  // (uniform)
+        const uint32_t w[4] = {y[j].x, y[j].y, y[j].z, y[j].w};
+        uint32_t u[NW];
+        if constexpr (TYPE == DA_CACHE_BF16) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) u[i] = w[i];
+        } else if constexpr (TYPE == DA_CACHE_FP8_E4M3) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e4m3x4_to_f16x4(w[i], u[2 * i], u[2 * i + 1]);
+        } else {
+          const uint32_t s2 = e4m3x2_to_f16x2(ys[j]);       // the lane's two block scales
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t c4[4];
+            e2m1x8_to_f16(w[i], c4);
+            const uint32_t s = __byte_perm(s2, 0, i < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) u[4 * i + q] = mul_f16x2(c4[q], s);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {                      // (NaN is passed over)
+          v[i] = min2<C::kBf>(v[i], u[i]);
+          v[NW + i] = max2<C::kBf>(v[NW + i], u[i]);
+        }
+      }
+    }
+    const int pg = __shfl_sync(kFull, id, page);
+    if (pg < 0) continue;
+    // ---- the row groups meet: step by step a lane keeps half of its words (by
+    // its lane bit: the minima or the maxima first) and takes the other's
+#pragma unroll
+    for (int m = 16, left = 2 * NW; m >= C::kLanes; m >>= 1) {
+      left >>= 1;
+      const bool up = (lane & m) != 0;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        if (i >= left) break;
+        const uint32_t mine = up ? v[left + i] : v[i], give = up ? v[i] : v[left + i];
+        const uint32_t got = __shfl_xor_sync(kFull, give, m);
+        v[i] = (lane & 16) != 0 ? max2<C::kBf>(mine, got) : min2<C::kBf>(mine, got);
+      }
+    }
+    // now v[0 .. 3]: 8 channels from d0 on, of the minimum (lanes 0-15) or maximum
+    float f[8];
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (C::kBf) {
+        f[2 * i] = __uint_as_float(v[i] << 16);
+        f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+      } else {
+        f[2 * i] = packed_lo(v[i], true);
+        f[2 * i + 1] = packed_hi(v[i], true);
+      }
+      odd |= isinf(f[2 * i]) || isinf(f[2 * i + 1]);
+    }
+    if (__any_sync(kFull, odd)) {
+      // infinite keys, or channels with nothing but NaN (minimum above maximum)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float other = __shfl_xor_sync(kFull, f[i], 16);
+        const bool none = (lane & 16) != 0 ? f[i] < other : f[i] > other;
+        f[i] = none ? 0.f : fminf(fmaxf(f[i], -kBf16Max), kBf16Max);
+      }
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
+    top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));  // (not negative: bits in order)
+    const float inv = top > 0.f ? __fdiv_rn(127.f, top) : 0.f;
+    uint32_t q[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = min(max(__float2int_rn(__fmul_rn(f[i], inv)), -127), 127);
+      q[i >> 2] |= (static_cast<uint32_t>(c) & 0xffu) << (8 * (i & 3));
+    }
+    int d0 = l * 2 * NW;
+    if constexpr (C::kRows >= 4) d0 += (lane & 8) != 0 ? NW : 0;
+    if constexpr (C::kRows >= 8) d0 += (lane & 4) != 0 ? NW / 2 : 0;
+    const int64_t at = static_cast<int64_t>(pg) * a.g.num_kv_heads + h;
+    *reinterpret_cast<uint2*>(a.digest + at * 256 + ((lane & 16) != 0 ? 128 : 0) + d0) = make_uint2(q[0], q[1]);
+    if (lane == 0) a.digest_scale[at] = __fdiv_rn(top, 127.f);
   }
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-  const float inv = top > 0.f ? __fdiv_rn(127.f, top) : 0.f;
-  // half-warp 0 writes the minima, 1 the maxima
-  uint32_t w[2] = {0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int q = min(max(__float2int_rn(__fmul_rn(sub == 0 ? lo[i] : hi[i], inv)), -127), 127);
-    w[i >> 2] |= (static_cast<uint32_t>(q) & 0xffu) << (8 * (i & 3));
-  }
-  const int64_t at = static_cast<int64_t>(pg) * a.g.num_kv_heads + h;
-  *reinterpret_cast<uint2*>(a.digest + at * 256 + sub * 128 + d16 * 8) = make_uint2(w[0], w[1]);
-  if (lane == 0) a.digest_scale[at] = __fdiv_rn(top, 127.f);
 }
 
 template <class Kernel, class... Args>
@@ -447,42 +655,61 @@ cudaError_t launch(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStrea
 cudaError_t launch_rope_table(const double* inv_freq, int num_freqs, int64_t first, int64_t count,
                               double amplitude, float* table, int sm_count, cudaStream_t stream) {
   if (count == 0) return cudaSuccess;
-  const int per = 256 / num_freqs;
-  const int64_t blocks = (count + static_cast<int64_t>(per) * kTablePos - 1) / (per * kTablePos);
+  const bool wide = num_freqs % 4 == 0;  // (and the table 16-byte aligned: the rows are then, too)
+  const int per = kTableThreads / (wide ? num_freqs / 4 : num_freqs);
+  // a few rows per thread at most while the CTAs fit the GPU once
+  const int64_t blocks = (count + per - 1) / per;
   const int64_t most = static_cast<int64_t>(sm_count) * 8;
-  return launch(rope_table_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), 256, 0,
-                stream, inv_freq, num_freqs, first, count, static_cast<float>(amplitude), table);
+  const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most));
+  const float amp = static_cast<float>(amplitude);
+  return wide ? launch(rope_table_kernel<4>, grid, kTableThreads, 0, stream, inv_freq, num_freqs, first, count, amp, table)
+              : launch(rope_table_kernel<1>, grid, kTableThreads, 0, stream, inv_freq, num_freqs, first, count, amp, table);
+}
+
+template <bool VEC>
+static cudaError_t launch_append_vec(const AppendArgs& a, dim3 grid, cudaStream_t stream) {
+  switch (a.c.type) {
+    case DA_CACHE_BF16: return launch(append_kernel<VEC, DA_CACHE_BF16>, grid, kAppendThreads, 0, stream, a);
+    case DA_CACHE_FP8_E4M3: return launch(append_kernel<VEC, DA_CACHE_FP8_E4M3>, grid, kAppendThreads, 0, stream, a);
+    default: return launch(append_kernel<VEC, DA_CACHE_FP4_E2M1>, grid, kAppendThreads, 0, stream, a);
+  }
 }
 
 cudaError_t launch_append(const AppendArgs& a, int sm_count, cudaStream_t stream) {
-  const int rows = a.num_q_heads + (a.append ? 2 * a.g.num_kv_heads : 0);
   const int64_t tokens = static_cast<int64_t>(a.g.batch) * a.g.q_len;
-  if (rows == 0 || tokens == 0) return cudaSuccess;
-  // few tokens: spread a token's heads over CTAs until about four per SM exist
-  const int64_t passes = (rows + kRowsPerPass - 1) / kRowsPerPass;
+  const int64_t passes = (a.num_q_heads + kRowsPerPass - 1) / kRowsPerPass +
+                         (a.append ? 2 * ((a.g.num_kv_heads + kRowsPerPass - 1) / kRowsPerPass) : 0);
+  if (passes == 0 || tokens == 0) return cudaSuccess;
+  // few tokens: spread a token's passes over CTAs until about four per SM exist
   const int64_t want = (4 * static_cast<int64_t>(sm_count) + tokens - 1) / tokens;
-  const unsigned split = static_cast<unsigned>(want < passes ? want : passes);
-  const dim3 grid(static_cast<unsigned>(tokens), split);
-  return a.rotary_dim % 16 == 0 ? launch(append_kernel<true>, grid, kAppendThreads, 0, stream, a)
-                                : launch(append_kernel<false>, grid, kAppendThreads, 0, stream, a);
+  const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>(want < passes ? want : passes));
+  return a.rotary_dim % 16 == 0 ? launch_append_vec<true>(a, grid, stream)
+                                : launch_append_vec<false>(a, grid, stream);
 }
 
-cudaError_t launch_digest(const DigestArgs& a, cudaStream_t stream) {
+cudaError_t launch_digest(const DigestArgs& a, int sm_count, cudaStream_t stream) {
   int64_t cols = (static_cast<int64_t>(a.g.max_seq_len) + a.g.page_size - 1) / a.g.page_size;
   if (a.max_new > 0) {
     const int64_t touched = (static_cast<int64_t>(a.max_new) + a.g.page_size - 2) / a.g.page_size + 1;
     if (touched < cols) cols = touched;
   }
   if (cols == 0 || a.g.batch == 0) return cudaSuccess;
-  const dim3 grid(static_cast<unsigned>((cols * a.g.num_kv_heads + kDigestWarps - 1) / kDigestWarps),
+  // few pages, as in a decode step: one per warp, for latency
+  const int64_t row = a.c.type == DA_CACHE_BF16 ? 256 : a.c.type == DA_CACHE_FP8_E4M3 ? 128 : 72;
+  const int64_t pairs = cols * a.g.num_kv_heads * a.g.batch;
+  int64_t per = kWarpBytes / (row * a.g.page_size);
+  if (per > pairs / (16 * static_cast<int64_t>(sm_count))) per = pairs / (16 * static_cast<int64_t>(sm_count));
+  per = per < 1 ? 1 : per > 32 ? 32 : per;
+  const int64_t units = (cols + per - 1) / per * a.g.num_kv_heads;
+  const dim3 grid(static_cast<unsigned>((units + kDigestWarps - 1) / kDigestWarps),
                   static_cast<unsigned>(a.g.batch));
   switch (a.c.type) {
     case DA_CACHE_BF16:
-      return launch(digest_kernel<DA_CACHE_BF16>, grid, 32 * kDigestWarps, 0, stream, a);
+      return launch(digest_kernel<DA_CACHE_BF16>, grid, 32 * kDigestWarps, 0, stream, a, static_cast<int>(per));
     case DA_CACHE_FP8_E4M3:
-      return launch(digest_kernel<DA_CACHE_FP8_E4M3>, grid, 32 * kDigestWarps, 0, stream, a);
+      return launch(digest_kernel<DA_CACHE_FP8_E4M3>, grid, 32 * kDigestWarps, 0, stream, a, static_cast<int>(per));
     default:
-      return launch(digest_kernel<DA_CACHE_FP4_E2M1>, grid, 32 * kDigestWarps, 0, stream, a);
+      return launch(digest_kernel<DA_CACHE_FP4_E2M1>, grid, 32 * kDigestWarps, 0, stream, a, static_cast<int>(per));
   }
 }
 

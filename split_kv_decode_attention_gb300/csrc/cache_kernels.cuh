@@ -46,6 +46,7 @@ struct AppendArgs {
   int append;           // k and v are given
   int rotary_dim, interleaved, table_positions;
   float k_inv, v_inv;   // 1 / k_scale, 1 / v_scale
+  float one;            // 1
 };
 cudaError_t launch_append(const AppendArgs& a, int sm_count, cudaStream_t stream);
 
@@ -56,7 +57,7 @@ struct DigestArgs {
   int8_t* digest;
   float* digest_scale;
 };
-cudaError_t launch_digest(const DigestArgs& a, cudaStream_t stream);
+cudaError_t launch_digest(const DigestArgs& a, int sm_count, cudaStream_t stream);
 
 struct SelectArgs {
   PagingView g;
