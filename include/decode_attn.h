@@ -433,9 +433,10 @@ typedef struct decode_attn_cache {
  * decode_attn() for a cache of any type: bf16 and FP8 caches run as
  * decode_attn() runs them, 4-bit ones run their own split kernel (the same
  * planner, partials, device planning and combine; every row count up to
- * DECODE_ATTN_MAX_ROWS; no cluster merge, so more than one chunk always takes
- * the workspace).  Its chunks are multiples of 64 tokens, so num_splits may
- * come out lower, and an item of a device plan may hold several KV heads.
+ * DECODE_ATTN_MAX_ROWS; clusters where the call is short and has at most 32
+ * rows per kv head, and the workspace is then 0 bytes).  Its chunks are
+ * multiples of 64 tokens, so num_splits may come out lower, and an item of a
+ * device plan may hold several KV heads.
  * k_scale and v_scale are finite.
  */
 int decode_attn_cached_workspace_bytes(const decode_attn_params *p,

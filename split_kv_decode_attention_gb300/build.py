@@ -78,7 +78,7 @@ def _compile_calls(obj: str) -> str:
 def _link_calls(obj: str, torch_lib: str) -> None:
     tmp = CALLS_PATH + f".tmp{os.getpid()}"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", torch_lib, "-ltorch_python", "-ltorch",
-           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L", LIB_DIR, "-ldecode_attn", "-Wl,-rpath,$ORIGIN"]
+           "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L", LIB_DIR, "-ldecode_attn", "-Wl,-rpath,$ORIGIN"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"linking _calls.so failed:\n{res.stdout}\n{res.stderr}")

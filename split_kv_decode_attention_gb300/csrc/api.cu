@@ -206,15 +206,14 @@ int plan_impl(const decode_attn_params* p, const int32_t* host_seq_lens, int32_t
 struct MapKey {
   const void* base;
   cuuint64_t dims[4], strides[3];
-  cuuint32_t box[4];
-  int type, swizzle;
+  cuuint32_t box;
+  int fp8;
   bool operator==(const MapKey& o) const {
     return base == o.base && std::memcmp(dims, o.dims, sizeof(dims)) == 0 &&
-           std::memcmp(strides, o.strides, sizeof(strides)) == 0 &&
-           std::memcmp(box, o.box, sizeof(box)) == 0 && type == o.type && swizzle == o.swizzle;
+           std::memcmp(strides, o.strides, sizeof(strides)) == 0 && box == o.box && fp8 == o.fp8;
   }
 };
-constexpr int kMapCacheSize = 32;
+constexpr int kMapCacheSize = 16;
 std::mutex g_map_mu;
 struct {
   MapKey key;
@@ -223,39 +222,15 @@ struct {
 } g_map_cache[kMapCacheSize];
 int g_map_next = 0;
 
-// The encoded map of (base, layout, box), from the cache or made anew.
 int encode_map(CUtensorMap* map, const void* base, CUtensorMapDataType type, const cuuint64_t (&dims)[4],
                const cuuint64_t (&strides)[3], const cuuint32_t (&box)[4], CUtensorMapSwizzle swizzle) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (enc == nullptr) return DA_ERR_CUDA;
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  MapKey key;
-  std::memset(&key, 0, sizeof(key));
-  key.base = base;
-  std::memcpy(key.dims, dims, sizeof(dims));
-  std::memcpy(key.strides, strides, sizeof(strides));
-  std::memcpy(key.box, box, sizeof(box));
-  key.type = type;
-  key.swizzle = swizzle;
-  {
-    std::lock_guard<std::mutex> lk(g_map_mu);
-    for (auto& e : g_map_cache)
-      if (e.valid && e.key == key) {
-        *map = e.map;
-        return DA_OK;
-      }
-  }
-  CUresult r = enc(map, type, 4, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return DA_ERR_ALIGNMENT;
-  std::lock_guard<std::mutex> lk(g_map_mu);
-  auto& e = g_map_cache[g_map_next];
-  g_map_next = (g_map_next + 1) % kMapCacheSize;
-  e.key = key;
-  e.map = *map;
-  e.valid = true;
-  return DA_OK;
+  return enc(map, type, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? DA_OK
+             : DA_ERR_ALIGNMENT;
 }
 
 int make_kv_map(CUtensorMap* map, const void* base, const decode_attn_params* p, bool paged,
@@ -276,8 +251,32 @@ int make_kv_map(CUtensorMap* map, const void* base, const decode_attn_params* p,
                                  static_cast<cuuint64_t>(p->kv_stride_page) * eb};
   const cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / eb), 1,
                              static_cast<cuuint32_t>(box_tokens), 1};
-  return encode_map(map, base, kv_fp8(p) ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                    dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  MapKey key;
+  std::memset(&key, 0, sizeof(key));
+  key.base = base;
+  std::memcpy(key.dims, dims, sizeof(dims));
+  std::memcpy(key.strides, strides, sizeof(strides));
+  key.box = box[2];
+  key.fp8 = kv_fp8(p) ? 1 : 0;
+  {
+    std::lock_guard<std::mutex> lk(g_map_mu);
+    for (auto& e : g_map_cache)
+      if (e.valid && e.key == key) {
+        *map = e.map;
+        return DA_OK;
+      }
+  }
+  const int rc =
+      encode_map(map, base, kv_fp8(p) ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                 dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (rc != DA_OK) return rc;
+  std::lock_guard<std::mutex> lk(g_map_mu);
+  auto& e = g_map_cache[g_map_next];
+  g_map_next = (g_map_next + 1) % kMapCacheSize;
+  e.key = key;
+  e.map = *map;
+  e.valid = true;
+  return DA_OK;
 }
 
 // 16-token halves of a box of the 4-bit kernel: whole boxes of a warp's share
@@ -289,7 +288,8 @@ int fp4_box_halves(const decode_attn_params* p, bool paged, int unit) {
   return h;
 }
 
-// A map of a 4-bit cache: its values, or (scales) its block scales.
+// A map of a 4-bit cache: its values, or (scales) its block scales.  (Encoded
+// for every call: 36 ns.)
 int make_fp4_map(CUtensorMap* map, const void* base, const decode_attn_params* p,
                  const decode_attn_cache* c, bool paged, int unit, bool scales) {
   const cuuint32_t tokens = static_cast<cuuint32_t>(16 * fp4_box_halves(p, paged, unit));
@@ -323,8 +323,12 @@ bool kv_stride_ok(const decode_attn_params* p, int64_t s, bool fp4 = false) {
 // The split pass merges through thread-block clusters (no partials, no
 // combine) when allowed by the flags and when the splits_eff CTAs of every
 // (request, kv head) form a supported cluster and all clusters fit at once.
-bool use_cluster_merge(const decode_attn_params* p, int32_t splits_eff) {
+bool use_cluster_merge(const decode_attn_params* p, int32_t splits_eff, int unit = 0) {
   if ((p->flags & DA_FLAG_TWO_PASS) != 0 || splits_eff < 2 || p->batch < 1) return false;
+  if (unit > 0)  // (4-bit caches: CTAs of one head, and one group of rows)
+    return unit == 1 && rows_of(p) <= dattn::kFp4MaxRows &&
+           dattn::fp4_cluster_merge_fits(rows_of(p), splits_eff,
+                                         static_cast<int64_t>(p->batch) * p->num_kv_heads);
   return dattn::split_cluster_merge_fits(rows_of(p), kv_fp8(p), splits_eff,
                                          static_cast<int64_t>(p->batch) * p->num_kv_heads);
 }
@@ -438,7 +442,7 @@ int workspace_bytes(const decode_attn_params* p, int32_t num_splits, const Decod
   }
   rc = chunk_for_splits(p, num_splits, &chunk, &eff, unit);
   if (rc != DA_OK) return rc;
-  if (eff <= 1) {
+  if (eff <= 1 || (unit > 0 && use_cluster_merge(p, eff, unit))) {
     *bytes = 0;
     return DA_OK;
   }
@@ -583,7 +587,7 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
     }
     rc = chunk_for_splits(p, num_splits, &chunk, &eff, unit);
     if (rc != DA_OK) return rc;
-    cluster_merge = !fp4 && use_cluster_merge(p, eff);
+    cluster_merge = use_cluster_merge(p, eff, unit);
     size_t need = 0;
     dattn::workspace_bytes(p, num_splits, ext, &need);
     if (!cluster_merge && need > 0 &&
@@ -676,7 +680,7 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
       return DA_ERR_CUDA;
   }
   if (fp4) {
-    if (launch_fp4(maps4, a, unit, st) != cudaSuccess) return DA_ERR_CUDA;
+    if (launch_fp4(maps4, a, unit, cluster_merge, st) != cudaSuccess) return DA_ERR_CUDA;
   } else if (dattn::launch_split(kmap, vmap, a, cluster_merge, st) != cudaSuccess) {
     return DA_ERR_CUDA;
   }

@@ -14,6 +14,7 @@ constexpr int kHeadDim = 128;
 constexpr int kTileTokens = 16;        // tokens per TMA box / per MMA tile
 constexpr int kMaxRows = 128;          // GQA group x q_len rows per CTA
 constexpr int kMaxNarrowRows = 16;     // above this: the tcgen05 kernel
+constexpr int kFp4MaxRows = 32;        // 4-bit kernel: rows of a CTA at most
 constexpr int kWideMaxPlannedBatch = 1024;  // tcgen05 kernel: device-planned calls up to this batch
 
 // Arguments of the split kernel (one CTA per (chunk, kv head, request)).
@@ -163,7 +164,11 @@ int wide_ctas_per_sm();
 // A CTA takes heads_per_cta (1, 2, 4 or 8, a divisor of the KV heads) heads: items,
 // plans and partials count such units (partials hold a unit's heads one behind
 // the other).
-cudaError_t launch_fp4(const Fp4Maps& maps, const SplitArgs& a, int heads_per_cta, cudaStream_t stream);
+// cluster_merge (one head per CTA): the chunks of a head are a cluster and
+// write the final output.
+cudaError_t launch_fp4(const Fp4Maps& maps, const SplitArgs& a, int heads_per_cta, bool cluster_merge,
+                       cudaStream_t stream);
+bool fp4_cluster_merge_fits(int rows, int num_splits, int64_t num_clusters);
 int fp4_ctas_per_sm(int rows, int heads_per_cta);
 int fp4_warps(int rows);  // consumer warps of a CTA: its heads divide them
 

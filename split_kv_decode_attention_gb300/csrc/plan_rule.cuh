@@ -47,6 +47,7 @@ constexpr int kFp4MinChunk = DATTN_F4_MIN_CHUNK;
 #define DATTN_F4_MIN_UNIFORM 256
 #endif
 constexpr int kFp4MinUniform = DATTN_F4_MIN_UNIFORM;  // shortest chunk of any plan
+constexpr int kFp4ClusterChunk = 512;                 // longest chunk that clusters are preferred for
 // Largest thread-block cluster the split kernel uses (non-portable size).
 constexpr int kMaxClusterSplits = 16;
 // Tokens per TMA box / MMA tile: chunk lengths are multiples of it.
@@ -154,6 +155,9 @@ __host__ __device__ int64_t plan_splits(const PlanShape& s, bool uniform, int64_
       if (best_used >= 15) break;
     }
     splits = best;
+    // short: as many chunks as a cluster may have, which then needs no partials
+    if (msl <= int64_t{kMaxClusterSplits} * kFp4ClusterChunk && splits > kMaxClusterSplits)
+      splits = kMaxClusterSplits;
   } else if (uniform) {
     if (pairs < s.slots) {
       const int64_t f = plan_div(s.slots, pairs);

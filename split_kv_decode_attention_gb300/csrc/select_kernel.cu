@@ -8,14 +8,19 @@
 // whatever its order of summation.  The digests are 1 / 16 to 1 / 256 of the
 // keys' bytes (2 x 128 of them per page); a lane loads its fragments from
 // global memory, 32 contiguous bytes of a page at a time, with no staging:
-// the channel order of a step is permuted alike in q' and digest.
+// the channel order of a step is permuted alike in q' and digest.  The loads of
+// a warp's next 16 pages, and the page ids of those after, are in flight while
+// it multiplies.
 //
 // pick_kernel: per (token, KV head) the top_k of the scores.  Scores become
 // integers of the same order; forced pages the largest one.  The threshold,
 // the largest value that top_k scores reach, is found by a 4-ary search over
-// the value range (three counts per round, one barrier each), and one scan
-// writes the pages above it, and the first of those equal to it, in ascending
-// order: exact, without atomics, and independent of timing.
+// the range of the scores (three counts per round, packed into one warp sum,
+// and one barrier), and one scan lists the pages above it, and the first of
+// those equal to it, in ascending order: exact, without atomics, and
+// independent of timing.  It is all latency, and the page ids of the list are
+// looked up side by side at the end (one after the other by the threads that
+// found them, they were most of 15 us).
 
 #include "cache_kernels.cuh"
 #include "decode_attn.h"
@@ -67,14 +72,16 @@ constexpr int kScoreWarps = 4;
 
 // Dynamic shared memory: q' fragments [row tiles][4 step pairs][32 lanes] of
 // 16 B, the rows' a / 127, then (several tokens) each warp's row scores
-// [rows][16 pages].
+// [rows][16 pages].  NT: an upper bound of the row tiles.
+template <int NT>
 __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int g4 = lane >> 2;
   const int t4 = lane & 3;
-  const int kvh = blockIdx.y;
+  // (heads fastest: the digests of a page's heads lie side by side, and are read at the same time)
+  const int kvh = blockIdx.x;
   const int b = blockIdx.z;
   const int group = a.num_q_heads / a.g.num_kv_heads;
   const int T = a.g.q_len;
@@ -83,12 +90,44 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectArg
   uint4* q_frag = reinterpret_cast<uint4*>(smem);
   float* q_scale = reinterpret_cast<float*>(smem + tiles * 2048);
   float* row_score = q_scale + tiles * 8 + warp * tiles * 8 * 16;
+  allow_dependent_launch();  // (whatever follows waits for this grid all the same)
   grid_dependency_wait();
 
   const int L = clamp_len(a, a.g.seq_lens[b]);
   const int nb = (L + a.g.page_size - 1) / a.g.page_size;  // pages that any token sees
   // (every page is taken: no scores are read)
-  if (nb <= a.top_k || static_cast<int>(blockIdx.x) * kScoreWarps * 16 >= nb) return;
+  if (nb <= a.top_k || static_cast<int>(blockIdx.y) * kScoreWarps * 16 >= nb) return;
+
+  // ---- the digests of pages tile * 16 + g4 and + 8, minima then maxima, as
+  // loaded; and the page ids of the tile after
+  const int32_t* bt = a.g.block_table + static_cast<int64_t>(b) * a.g.bt_stride;
+  const int tile_step = gridDim.y * kScoreWarps;
+  int tile = blockIdx.y * kScoreWarps + warp;
+  auto ids = [&](int t, int (&pg)[2]) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) pg[p] = __ldg(bt + min(t * 16 + g4 + 8 * p, nb - 1));
+  };
+  int pg[2];
+  uint4 raw[2][4];
+  float ds[2];
+  auto load = [&]() {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int id = pg[p] < 0 || pg[p] >= a.g.num_pages ? 0 : pg[p];  // (reported by pick_kernel)
+      const int64_t at = static_cast<int64_t>(id) * a.g.num_kv_heads + kvh;
+      ds[p] = __ldg(a.digest_scale + at);
+      const uint4* src = reinterpret_cast<const uint4*>(a.digest + at * 256 + 32 * t4);
+      raw[p][0] = __ldg(src);
+      raw[p][1] = __ldg(src + 1);
+      raw[p][2] = __ldg(src + 8);
+      raw[p][3] = __ldg(src + 9);
+    }
+  };
+  if (tile * 16 < nb) {
+    ids(tile, pg);
+    load();
+    ids(tile + tile_step, pg);
+  }
 
   // ---- q' of the rows, one warp per row tile
   for (int nt = warp; nt < tiles; nt += kScoreWarps) {
@@ -136,45 +175,56 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectArg
   }
   __syncthreads();
 
-  const int32_t* bt = a.g.block_table + static_cast<int64_t>(b) * a.g.bt_stride;
-  for (int tile = blockIdx.x * kScoreWarps + warp; tile * 16 < nb; tile += gridDim.x * kScoreWarps) {
-    // ---- the digests of pages tile * 16 + g4 and + 8: A fragments of 16 steps
-    uint32_t af[16][4];  // steps 0-7: minima, 8-15: maxima
-    float ds[2];
+  for (; tile * 16 < nb; tile += tile_step) {
+    uint32_t w[2][16];
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const int col = min(tile * 16 + g4 + 8 * p, nb - 1);
-      int pg = __ldg(bt + col);
-      if (pg < 0 || pg >= a.g.num_pages) pg = 0;  // (reported by pick_kernel)
-      const int64_t at = static_cast<int64_t>(pg) * a.g.num_kv_heads + kvh;
-      ds[p] = __ldg(a.digest_scale + at);
-      const uint4* src = reinterpret_cast<const uint4*>(a.digest + at * 256 + 32 * t4);
+    for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int mm = 0; mm < 2; ++mm) {
-        const uint4 x = __ldg(src + mm * 8), y = __ldg(src + mm * 8 + 1);
-        const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      for (int i = 0; i < 4; ++i) {
+        w[p][4 * i] = raw[p][i].x;
+        w[p][4 * i + 1] = raw[p][i].y;
+        w[p][4 * i + 2] = raw[p][i].z;
+        w[p][4 * i + 3] = raw[p][i].w;
+      }
+    const float ds0 = ds[0], ds1 = ds[1];
+    if ((tile + tile_step) * 16 < nb) {
+      load();
+      ids(tile + 2 * tile_step, pg);
+    }
+    float acc[NT][4];
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) s8x4_to_f16(w[ks], af[mm * 8 + ks][p], af[mm * 8 + ks][2 + p]);
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // step pairs: channels 32 t4 + 8 i ..
+      uint32_t af[4][4];           // minima of the two steps, maxima of the two
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          s8x4_to_f16(w[p][(k >> 1) * 8 + 2 * i + (k & 1)], af[k][p], af[k][2 + p]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (nt < tiles) {
+          const uint4 q = q_frag[(nt * 4 + i) * 32 + lane];
+          mma_f16_16816(acc[nt], af[0], hmin2_0(q.x), hmin2_0(q.y));
+          mma_f16_16816(acc[nt], af[1], hmin2_0(q.z), hmin2_0(q.w));
+          mma_f16_16816(acc[nt], af[2], hmax2_0(q.x), hmax2_0(q.y));
+          mma_f16_16816(acc[nt], af[3], hmax2_0(q.z), hmax2_0(q.w));
+        }
       }
     }
     float best[2] = {-INFINITY, -INFINITY};
-    for (int nt = 0; nt < tiles; ++nt) {
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 q = q_frag[(nt * 4 + i) * 32 + lane];
-        mma_f16_16816(acc, af[2 * i], hmin2_0(q.x), hmin2_0(q.y));
-        mma_f16_16816(acc, af[2 * i + 1], hmin2_0(q.z), hmin2_0(q.w));
-        mma_f16_16816(acc, af[8 + 2 * i], hmax2_0(q.x), hmax2_0(q.y));
-        mma_f16_16816(acc, af[8 + 2 * i + 1], hmax2_0(q.z), hmax2_0(q.w));
-      }
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) {
         const int row = nt * 8 + 2 * t4 + rr;
         if (row < rows) {
           const float qs = q_scale[row];
-          const float u = __fmul_rn(__fmul_rn(acc[rr], ds[0]), qs);
-          const float v = __fmul_rn(__fmul_rn(acc[2 + rr], ds[1]), qs);
+          const float u = __fmul_rn(__fmul_rn(acc[nt][rr], ds0), qs);
+          const float v = __fmul_rn(__fmul_rn(acc[nt][2 + rr], ds1), qs);
           if (T == 1) {
             best[0] = fmaxf(best[0], u);
             best[1] = fmaxf(best[1], v);
@@ -184,7 +234,6 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectArg
           }
         }
       }
-    }
     if (T == 1) {
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
@@ -216,16 +265,18 @@ __device__ __forceinline__ uint32_t ordered(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-constexpr int kPer = 8;  // scores per thread and chunk
+constexpr int kMaxTopK = 4096;
 
 // ONE: all pages fit one chunk of THREADS x kPer scores, held in registers;
 // otherwise every pass reads the chunks again (from L2).
-template <int THREADS, bool ONE>
+template <int THREADS, int kPer, bool ONE>
 __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectArgs a) {
   constexpr int kWarps = THREADS / 32;
   constexpr int kChunk = THREADS * kPer;
-  __shared__ uint32_t sh[2][3][kWarps];
+  __shared__ uint32_t sh[2][kWarps];
+  __shared__ uint32_t sh3[2][kWarps];
   __shared__ uint32_t scan[2][kWarps];
+  __shared__ int list[kMaxTopK];           // the selected pages' places
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int64_t row = blockIdx.x;  // (b, t, kv head)
@@ -233,6 +284,8 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectArgs a) {
   const int64_t vb = row / a.g.num_kv_heads;
   const int t = static_cast<int>(vb % a.g.q_len);
   const int b = static_cast<int>(vb / a.g.q_len);
+  // (no early launch of what follows: the attention's CTAs would settle around
+  // this grid's and stay unevenly spread, 52 -> 73 us on 8 requests x 3 tokens)
   grid_dependency_wait();
   const int raw = a.g.seq_lens[b];
   const int L = clamp_len(a, raw);
@@ -291,9 +344,31 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectArgs a) {
   uint32_t key[kPer];
   if constexpr (ONE) load(0, key);
 
-  // ---- the largest thr with at least K keys >= thr; all of [lo, hi] brackets it:
-  // count(>= lo) >= K always, count(>= hi + 1) < K once hi is below the maximum
-  uint32_t lo = 1, hi = 0xffffffffu;
+  // ---- the range of the keys that are not forced: they are more than K less
+  // the forced ones, so the threshold lies in it (or at the forced ones' value,
+  // where they are K)
+  uint32_t least = 0xffffffffu, most = 0;
+  for (int c = 0; c < chunks; ++c) {
+    if constexpr (!ONE) load(c * kChunk, key);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (key[i] != 0u) least = min(least, key[i]);
+      if (key[i] != 0xffffffffu) most = max(most, key[i]);
+    }
+  }
+  least = __reduce_min_sync(kFull, least);
+  most = __reduce_max_sync(kFull, most);
+  if (lane == 0) {
+    scan[0][warp] = least;
+    scan[1][warp] = most;
+  }
+  __syncthreads();
+  least = __reduce_min_sync(kFull, lane < kWarps ? scan[0][lane] : 0xffffffffu);
+  most = __reduce_max_sync(kFull, lane < kWarps ? scan[1][lane] : 0u);
+
+  // ---- the largest thr with at least K keys >= thr, in [lo, hi]: count(>= lo)
+  // >= K always, and count(>= x) < K for every x in (hi, 0xffffffff]
+  uint32_t lo = least, hi = a.sink + a.local >= K ? 0xffffffffu : most;
   bool exact = false;  // exactly K keys are >= lo
   int round = 0;
   while (lo < hi && !exact) {
@@ -305,25 +380,45 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectArgs a) {
     probe[2] = lo + (span >> 1) + (span >> 2) + (span < 4 ? 1 : 0);
 #pragma unroll
     for (int i = 0; i < 3; ++i) probe[i] = min(probe[i], hi);
-    uint32_t n[3] = {0, 0, 0};
-    for (int c = 0; c < chunks; ++c) {
-      if constexpr (!ONE) load(c * kChunk, key);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        n[0] += key[i] >= probe[0];
-        n[1] += key[i] >= probe[1];
-        n[2] += key[i] >= probe[2];
-      }
-    }
     const int buf = round & 1;
+    uint32_t n[3];
+    if constexpr (ONE) {
+      // counts of a warp are at most 32 x kPer: three fields of ten bits
+      static_assert(kPer < 32, "ten bits");
+      uint32_t c = 0;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const uint32_t s = __reduce_add_sync(kFull, n[i]);
-      if (lane == 0) sh[buf][i][warp] = s;
+      for (int i = 0; i < kPer; ++i)
+        c += (key[i] >= probe[0]) + ((key[i] >= probe[1]) << 10) + ((key[i] >= probe[2]) << 20);
+      c = __reduce_add_sync(kFull, c);
+      if (lane == 0) sh[buf][warp] = c;
+      __syncthreads();  // (the other buffer is written next: one barrier per round)
+      c = lane < kWarps ? sh[buf][lane] : 0u;
+      const uint32_t two = __reduce_add_sync(kFull, (c & 0x3ffu) | ((c & 0xffc00u) << 6));
+      n[0] = two & 0xffffu;
+      n[1] = two >> 16;
+      n[2] = __reduce_add_sync(kFull, c >> 20);
+    } else {
+      n[0] = n[1] = n[2] = 0;
+      for (int c = 0; c < chunks; ++c) {
+        load(c * kChunk, key);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          n[0] += key[i] >= probe[0];
+          n[1] += key[i] >= probe[1];
+          n[2] += key[i] >= probe[2];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const uint32_t x = __reduce_add_sync(kFull, n[i]);
+        if (lane == 0) (i < 2 ? sh : sh3)[i & 1][warp] = x;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        n[i] = __reduce_add_sync(kFull, lane < kWarps ? (i < 2 ? sh : sh3)[i & 1][lane] : 0u);
+      __syncthreads();
     }
-    __syncthreads();  // (the other buffer is written next: one barrier per round)
-#pragma unroll
-    for (int i = 0; i < 3; ++i) n[i] = __reduce_add_sync(kFull, lane < kWarps ? sh[buf][i][lane] : 0u);
     const uint32_t k = static_cast<uint32_t>(K);
     uint32_t new_lo = lo, new_hi = hi;
 #pragma unroll
@@ -358,9 +453,9 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectArgs a) {
       for (int i = 0; i < kPer; ++i) gt += key[i] > above;
     }
     gt = __reduce_add_sync(kFull, gt);
-    if (lane == 0) sh[0][0][warp] = gt;
+    if (lane == 0) sh[0][warp] = gt;
     __syncthreads();
-    gt = __reduce_add_sync(kFull, lane < kWarps ? sh[0][0][lane] : 0u);
+    gt = __reduce_add_sync(kFull, lane < kWarps ? sh[0][lane] : 0u);
     take = static_cast<uint32_t>(K) - gt;
   }
 
@@ -398,12 +493,13 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectArgs a) {
     for (int i = 0; i < kPer; ++i) {
       const bool up = key[i] > above;
       const bool same = take != 0 && key[i] == above && bq < take;
-      if (up || same) put(static_cast<int>(bg + min(bq, take)), e0 + i);
+      if (up || same) list[bg + min(bq, take)] = e0 + i;
       bg += up;
       bq += take != 0 && key[i] == above;
     }
-    __syncthreads();  // (scan[] is written again)
+    __syncthreads();  // (scan[] is written again; the list is complete)
   }
+  for (int i = threadIdx.x; i < K; i += THREADS) put(i, list[i]);
 }
 
 template <class Kernel, class Args>
@@ -431,10 +527,10 @@ cudaError_t launch_select(const SelectArgs& a, int sm_count, cudaStream_t stream
     const int tiles = (q_rows + 7) / 8;
     const size_t smem = static_cast<size_t>(tiles) * 2048 + tiles * 32 +
                         (a.g.q_len > 1 ? static_cast<size_t>(kScoreWarps) * tiles * 512 : 0);
+    auto* kernel = tiles == 1 ? score_kernel<1> : tiles <= 4 ? score_kernel<4> : score_kernel<16>;
     if (smem > 48 * 1024) {
       const cudaError_t e =
-          cudaFuncSetAttribute(score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(smem));
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
       if (e != cudaSuccess) return e;
     }
     // a tile of 16 pages per warp, several per warp once the grid has about
@@ -444,14 +540,15 @@ cudaError_t launch_select(const SelectArgs& a, int sm_count, cudaStream_t stream
     int64_t x = (8 * static_cast<int64_t>(sm_count) + pairs - 1) / pairs;
     x = x < full ? x : full;
     const cudaError_t e =
-        launch(score_kernel, dim3(static_cast<unsigned>(x), a.g.num_kv_heads, a.g.batch),
+        launch(kernel, dim3(a.g.num_kv_heads, static_cast<unsigned>(x), a.g.batch),
                32 * kScoreWarps, smem, stream, a);
     if (e != cudaSuccess) return e;
   }
   const dim3 grid(static_cast<unsigned>(rows));
-  if (a.max_blocks <= 256 * kPer) return launch(pick_kernel<256, true>, grid, 256, 0, stream, a);
-  if (a.max_blocks <= 1024 * kPer) return launch(pick_kernel<1024, true>, grid, 1024, 0, stream, a);
-  return launch(pick_kernel<1024, false>, grid, 1024, 0, stream, a);
+  if (a.max_blocks <= 2048) return launch(pick_kernel<256, 8, true>, grid, 256, 0, stream, a);
+  if (a.max_blocks <= 4096) return launch(pick_kernel<256, 16, true>, grid, 256, 0, stream, a);
+  if (a.max_blocks <= 8192) return launch(pick_kernel<512, 16, true>, grid, 512, 0, stream, a);
+  return launch(pick_kernel<1024, 8, false>, grid, 1024, 0, stream, a);
 }
 
 }  // namespace dattn

@@ -12,6 +12,8 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -131,19 +133,35 @@ void on_current_device(std::initializer_list<const at::Tensor*> ts) {
   }
 }
 
-void* stream_of(PyObject* o) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
-  if (PyLong_Check(o)) {
-    void* p = PyLong_AsVoidPtr(o);
-    if (PyErr_Occurred()) throw python_error();
-    return p;
+// The stream of a call.  What the call allocates belongs to the current stream;
+// on another one the allocator is told, so that the memory is not handed out
+// again before the call is done with it.
+struct Stream {
+  void* raw;
+  bool foreign;
+
+  void uses(const at::Tensor& t) const {
+    if (foreign && t.defined() && t.numel() > 0)
+      c10::cuda::CUDACachingAllocator::recordStream(
+          t.storage().data_ptr(),
+          c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(raw), t.device().index()));
   }
-  PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
-  if (h == nullptr) throw python_error();
-  void* p = PyLong_AsVoidPtr(h);
-  Py_DECREF(h);
+};
+
+Stream stream_of(PyObject* o) {
+  void* current = c10::cuda::getCurrentCUDAStream().stream();
+  if (o == Py_None) return {current, false};
+  void* p = nullptr;
+  if (PyLong_Check(o)) {
+    p = PyLong_AsVoidPtr(o);
+  } else {
+    PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
+    if (h == nullptr) throw python_error();
+    p = PyLong_AsVoidPtr(h);
+    Py_DECREF(h);
+  }
   if (PyErr_Occurred()) throw python_error();
-  return p;
+  return {p, p != current};
 }
 
 int32_t* status_of(const at::Tensor& t) {
@@ -273,8 +291,9 @@ float scale_or_default(PyObject* o) {
   return o == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(kD))) : static_cast<float>(number(o));
 }
 
+// (a CUDA tensor by then: on_current_device has looked)
 at::Tensor empty_like_device(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
-  return at::empty(shape, like.options().dtype(type));
+  return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
 
 at::Tensor out_or_new(const at::Tensor& out, const at::Tensor& q) {
@@ -330,9 +349,11 @@ PyObject* rope_table(PyObject* const* a, Py_ssize_t n) {
   on_current_device({&f, &out});
   if (out.defined()) dense(out, at::kFloat, {rows, 2 * nf}, "out");
   else out = empty_like_device({rows, 2 * nf}, at::kFloat, f);
+  const Stream stream = stream_of(a[5]);
   check(decode_attn_rope_table(static_cast<const double*>(ptr(f)), static_cast<int32_t>(std::min<int64_t>(nf, 1 << 20)),
-                               first, rows, amplitude, static_cast<float*>(ptr(out)), stream_of(a[5])),
+                               first, rows, amplitude, static_cast<float*>(ptr(out)), stream.raw),
         "decode_attn_rope_table");
+  stream.uses(out);
   return give(out);
 }
 
@@ -395,11 +416,13 @@ PyObject* rope_append(PyObject* const* a, Py_ssize_t n) {
     if (!q_out.defined()) q_out = empty_like_device(q.sizes(), at::kBFloat16, q);
     q_strides(p, q, q_out);
   }
+  const Stream stream = stream_of(a[18]);
   check(decode_attn_rope_append(&p, &c.c, &r, ptr(q), ptr(k), ptr(v), static_cast<const float*>(ptr(table)),
                                 static_cast<const int32_t*>(ptr(pos)), static_cast<const int32_t*>(ptr(new_lens)),
                                 static_cast<const int32_t*>(ptr(bt)), static_cast<const int32_t*>(ptr(lens)),
-                                ptr(q_out), status_of(status), stream_of(a[18])),
+                                ptr(q_out), status_of(status), stream.raw),
         "decode_attn_rope_append");
+  stream.uses(q_out);
   if (!q.defined()) Py_RETURN_NONE;
   return give(q_out);
 }
@@ -426,10 +449,13 @@ PyObject* block_digest(PyObject* const* a, Py_ssize_t n) {
   if (!digest.defined()) digest = at::zeros({c.groups, c.heads, 2, kD}, kc.options().dtype(at::kChar));
   if (!scale.defined()) scale = at::zeros({c.groups, c.heads}, kc.options().dtype(at::kFloat));
   digest_tensors(digest, scale, c.groups, c.heads);
+  const Stream stream = stream_of(a[9]);
   check(decode_attn_block_digest(&p, &c.c, static_cast<const int32_t*>(ptr(bt)), static_cast<const int32_t*>(ptr(lens)),
                                  integer32(a[6], "max_new"), static_cast<int8_t*>(ptr(digest)),
-                                 static_cast<float*>(ptr(scale)), status_of(status), stream_of(a[9])),
+                                 static_cast<float*>(ptr(scale)), status_of(status), stream.raw),
         "decode_attn_block_digest");
+  stream.uses(digest);
+  stream.uses(scale);
   return give({digest, scale});
 }
 
@@ -458,10 +484,14 @@ PyObject* decode_cached(PyObject* const* a, Py_ssize_t n) {
   size_t need = 0;
   check(decode_attn_cached_workspace_bytes(&p, &c.c, splits, &need), "decode_attn_cached_workspace_bytes");
   const at::Tensor ws = workspace_or_new(given, need, q);
+  const Stream stream = stream_of(a[15]);
   check(decode_attn_cached(&p, &c.c, ptr(q), static_cast<const int32_t*>(ptr(bt)),
                            static_cast<const int32_t*>(ptr(lens)), ptr(out), static_cast<float*>(ptr(lse)), splits,
-                           ptr(ws), bytes_of(ws), status_of(status), stream_of(a[15])),
+                           ptr(ws), bytes_of(ws), status_of(status), stream.raw),
         "decode_attn_cached");
+  stream.uses(out);
+  stream.uses(lse);
+  stream.uses(ws);
   return give({out, lse});
 }
 
@@ -499,12 +529,17 @@ PyObject* sparse(PyObject* const* a, Py_ssize_t n) {
   size_t need = 0;
   check(decode_attn_sparse_workspace_bytes(&p, &c.c, &s, &need), "decode_attn_sparse_workspace_bytes");
   const at::Tensor ws = workspace_or_new(given, need, q);
+  const Stream stream = stream_of(a[22]);
   check(decode_attn_sparse(&p, &c.c, &s, ptr(q), static_cast<const int8_t*>(ptr(digest)),
                            static_cast<const float*>(ptr(dscale)), static_cast<const int32_t*>(ptr(bt)),
                            static_cast<const int32_t*>(ptr(lens)), ptr(out), static_cast<float*>(ptr(lse)),
                            static_cast<int32_t*>(ptr(blocks)), ptr(ws), bytes_of(ws), status_of(status),
-                           stream_of(a[22])),
+                           stream.raw),
         "decode_attn_sparse");
+  stream.uses(out);
+  stream.uses(lse);
+  stream.uses(blocks);
+  stream.uses(ws);
   return give({out, lse, blocks});
 }
 
@@ -543,12 +578,17 @@ PyObject* block_select(PyObject* const* a, Py_ssize_t n) {
   size_t need = 0;
   check(decode_attn_block_select_workspace_bytes(&p, &s, &need), "decode_attn_block_select_workspace_bytes");
   const at::Tensor ws = workspace_or_new(given, need, q);
+  const Stream stream = stream_of(a[14]);
   check(decode_attn_block_select(&p, &s, ptr(q), static_cast<const int8_t*>(ptr(digest)),
                                  static_cast<const float*>(ptr(dscale)), static_cast<const int32_t*>(ptr(bt)),
                                  static_cast<const int32_t*>(ptr(lens)), static_cast<int32_t*>(ptr(blocks)),
                                  static_cast<int32_t*>(ptr(pages)), static_cast<int32_t*>(ptr(tokens)), ptr(ws),
-                                 bytes_of(ws), status_of(status), stream_of(a[14])),
+                                 bytes_of(ws), status_of(status), stream.raw),
         "decode_attn_block_select");
+  stream.uses(blocks);
+  stream.uses(pages);
+  stream.uses(tokens);
+  stream.uses(ws);
   return give({blocks, pages, tokens});
 }
 
