@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(kTableThreads)
 // thread's 8 values and their partners lie rotary_dim / 2 apart, whole threads
 // when that is a multiple of 8; other sizes read the partner from memory).
 // The first passes' rows are on their way before the token's place is known.
-// Instructions bound it as much as HBM does (at 32 + 2 x 8 heads 190 of 8
-// values each per token), so values go in pairs (mul / add.f32x2).
+// Instructions bound it as much as HBM does, so values go in pairs (mul /
+// add.f32x2).
 constexpr int kAppendThreads = 128;
 constexpr int kRowsPerPass = kAppendThreads / 16;
 

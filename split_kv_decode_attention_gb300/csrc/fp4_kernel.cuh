@@ -47,7 +47,7 @@
 // CM (HG = 1, calls of few and short chunks): the chunks of a head are a
 // thread-block cluster and merge through distributed shared memory, so the
 // call is one launch and writes no partials (one request of 4096 tokens, 32 / 8
-// heads: two launches 7.7 us on the device, one 6.1).
+// heads: 11 us replayed either way, but 7 and not 10 us of the host's time).
 // Slots behind a sequence may hold anything: their scores are masked and
 // their value scales replaced by zero.  More query rows than a CTA holds run
 // as groups in the grid's y.
@@ -67,32 +67,14 @@ constexpr float kPShift = 6.f;   // P is about 2^6 at the maximum when m moves
 constexpr float kPTop = 15.f;    // m moves when P would pass 2^15
 constexpr int kWarpKeys = 32;    // keys of a warp per stage
 
-#ifndef DATTN_F4_STAGES
-#define DATTN_F4_STAGES 3
-#endif
+// Ring stages: 2 lose 10%, 4 and 5 cost the shared memory of a CTA and gain nothing.
+constexpr int kRingStages = 3;
 // Consumer warps, resident CTAs per SM and registers of a consumer thread in
 // the 8-, 16- and 32-row variants.  A CTA is its consumers and a warpgroup for
 // the producer, which hands its registers over: (consumers x regs + 128 x
 // kProducerRegs) must not exceed the threads x the launch's registers, 65536 /
 // (CTAs x threads) rounded down to 8.
-#ifndef DATTN_F4_W1
-#define DATTN_F4_W1 4
-#define DATTN_F4_C1 3
-#define DATTN_F4_R1 128
-#endif
-#ifndef DATTN_F4_W2
-#define DATTN_F4_W2 8
-#define DATTN_F4_C2 1
-#define DATTN_F4_R2 232
-#endif
-#ifndef DATTN_F4_W4
-#define DATTN_F4_W4 8
-#define DATTN_F4_C4 1
-#define DATTN_F4_R4 232
-#endif
-constexpr int kShape[3][3] = {{DATTN_F4_W1, DATTN_F4_C1, DATTN_F4_R1},
-                              {DATTN_F4_W2, DATTN_F4_C2, DATTN_F4_R2},
-                              {DATTN_F4_W4, DATTN_F4_C4, DATTN_F4_R4}};
+constexpr int kShape[3][3] = {{4, 3, 128}, {8, 1, 232}, {8, 1, 232}};
 constexpr int kProducerRegs = 32;
 
 // NT: tiles of 8 query rows; HG: KV heads of a CTA.
@@ -106,10 +88,10 @@ struct Fp4Cfg {
   static_assert(kWarps % 4 == 0 && 32 * kWarps * kRegs + 128 * kProducerRegs <= kThreads * kLaunchRegs,
                 "the register split would wait forever");
   static constexpr int kShares = kWarps / HG;               // warps of a head
-  static_assert(kShares * HG == kWarps, "whole shares");
+  static_assert(kShares * HG == kWarps && (kShares & (kShares - 1)) == 0, "whole shares");
   static constexpr int kHalves = 2 * kShares;               // 16-token halves of a stage
   static constexpr int kStepTokens = 16 * kHalves;
-  static constexpr int kStages = DATTN_F4_STAGES;
+  static constexpr int kStages = kRingStages;
   static constexpr int kRows = 8 * NT;
   // a stage: its tokens of K ([token][HG heads][64 B]), of V, then their block
   // scales (per box: [HG heads][tokens of the box][8 B])
@@ -324,8 +306,9 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
       auto place = [&](int h0) {
 #pragma unroll
         for (int h = 0; h < kGroup; ++h) {
-          pg[h] = __shfl_sync(kFull, win.cur_pg, (first - win.base + h0 + h) & 31);
-          sl[h] = __shfl_sync(kFull, win.cur_sl, (first - win.base + h0 + h) & 31);
+          const int src = (first - win.base + h0 + h) & 31;
+          pg[h] = __shfl_sync(kFull, win.cur_pg, src);
+          sl[h] = __shfl_sync(kFull, win.cur_sl, src);
         }
       };
       place(0);
@@ -534,20 +517,6 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
       }
     }
 
-    // ---- V and its scales into registers: the stage is then free
-    uint2 v[2][4];
-    uint32_t vs[2][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[h][j] = lds64(st + ((j & 1) ? v_off1 : v_off0) + h * C::kHalfKv + (j >> 1) * kKeys8);
-        vs[h][j] = lds_u8(st + ((j & 1) ? vs_off1 : vs_off0) + h * sf_half + (j >> 1) * 64);
-        // slots behind the sequence may hold anything: 0 x NaN is NaN
-        if constexpr (!FULL)
-          if (tok0 + 16 * h + ((j & 1) ? vkey1 : vkey0) + 8 * (j >> 1) >= t_end) vs[h][j] = 0u;
-      }
-
     // ---- online softmax over the step (base 2)
     bool move = false;
 #pragma unroll
@@ -607,18 +576,27 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
       }
     }
 
-    release();
-
     // ---- O^T[128 d x 8 NT rows] += V^T . P^T
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t s01 = e4m3x2_to_f16x2(__byte_perm(vs[h][0], vs[h][1], 0x0040));
-      const uint32_t s23 = e4m3x2_to_f16x2(__byte_perm(vs[h][2], vs[h][3], 0x0040));
+      uint2 v[4];
+      uint32_t vs[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = lds64(st + ((j & 1) ? v_off1 : v_off0) + h * C::kHalfKv + (j >> 1) * kKeys8);
+        vs[j] = lds_u8(st + ((j & 1) ? vs_off1 : vs_off0) + h * sf_half + (j >> 1) * 64);
+        // slots behind the sequence may hold anything: 0 x NaN is NaN
+        if constexpr (!FULL)
+          if (tok0 + 16 * h + ((j & 1) ? vkey1 : vkey0) + 8 * (j >> 1) >= t_end) vs[j] = 0u;
+      }
+      if (h == 1) release();
+      const uint32_t s01 = e4m3x2_to_f16x2(__byte_perm(vs[0], vs[1], 0x0040));
+      const uint32_t s23 = e4m3x2_to_f16x2(__byte_perm(vs[2], vs[3], 0x0040));
 #pragma unroll
       for (int half = 0; half < 2; ++half) {  // bytes 0-3, 4-7 of the block: mt 0-3, 4-7
         uint32_t x[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = half ? v[h][j].y : v[h][j].x;
+        for (int j = 0; j < 4; ++j) x[j] = half ? v[j].y : v[j].x;
         constexpr uint32_t kLow = 0x0f0f0f0fu;
         // low nibbles (d even) of two keys side by side, then high ones (d odd)
         uint32_t e01[4], o01[4], e23[4], o23[4];

@@ -35,19 +35,16 @@ constexpr int kWideTokensPerRow = 256;
 // same tokens is over before its set-up and merge have paid off; chunks are
 // longer and waves fewer.  Nothing merges through clusters there, so equal
 // lengths may take any number of chunks.
-#ifndef DATTN_F4_WAVES
-#define DATTN_F4_WAVES 3
-#endif
-#ifndef DATTN_F4_MIN_CHUNK
-#define DATTN_F4_MIN_CHUNK 512
-#endif
-constexpr int kFp4Waves = DATTN_F4_WAVES;
-constexpr int kFp4MinChunk = DATTN_F4_MIN_CHUNK;
-#ifndef DATTN_F4_MIN_UNIFORM
-#define DATTN_F4_MIN_UNIFORM 256
-#endif
-constexpr int kFp4MinUniform = DATTN_F4_MIN_UNIFORM;  // shortest chunk of any plan
+// (64 ragged requests of up to 32K: 2 waves 272 us, 3 255, 4 255, 8 274.)
+constexpr int kFp4Waves = 3;
+constexpr int kFp4MinChunk = 512;
+constexpr int kFp4MinUniform = 256;                   // shortest chunk of any plan
 constexpr int kFp4ClusterChunk = 512;                 // longest chunk that clusters are preferred for
+constexpr int kFp4StartTokens = 512;                  // a chunk's set-up, in tokens of its loop
+// Lists of selected pages are short and their calls latency: chunks may be too.
+// (64 tokens and not 256: 2 requests x 512 tokens 19.9 -> 16.7 us, one of 1024
+// 31 -> 26.6)
+constexpr int kListMinChunk = 64;
 // Largest thread-block cluster the split kernel uses (non-portable size).
 constexpr int kMaxClusterSplits = 16;
 // Tokens per TMA box / MMA tile: chunk lengths are multiples of it.
@@ -64,6 +61,7 @@ struct PlanShape {
   int rows;          // query rows per kv head: (Hq / Hkv) * q_len
   int max_seq_len;   // upper bound of every length (>= 0)
   int fp4 = 0;       // 4-bit cache (kFp4Waves, kFp4MinChunk)
+  int listed = 0;    // keys from lists of selected pages (kListMinChunk)
 };
 
 // a / b for a >= 0, b > 0, in 32 bits when both fit: on the GPU a 64-bit
@@ -141,18 +139,19 @@ __host__ __device__ int64_t plan_splits(const PlanShape& s, bool uniform, int64_
   const int64_t pairs = static_cast<int64_t>(s.batch > 1 ? s.batch : 1) * s.num_kv_heads;
   int64_t splits = 1;
   if (uniform && s.fp4) {
-    // whole waves of equal chunks: the fewest waves that fill 15/16 of the slots
-    // (or, of eight, the fullest)
-    int64_t best = 1, best_used = 0;
-    for (int64_t waves = 1; waves <= 8; ++waves) {
-      const int64_t f = plan_div(waves * s.slots, pairs);
+    // equal chunks: of the counts that fill one wave, two, ... the one with the
+    // least of waves x (chunk + start-up), partials charged where there are any
+    int64_t best = 1, best_cost = 0;
+    for (int64_t waves = 0; waves <= 8; ++waves) {
+      int64_t f = waves == 0 ? 1 : plan_div(waves * s.slots, pairs);  // (0: no split at all)
       if (f < 1) continue;
-      const int64_t used = plan_div(f * pairs * 16, waves * s.slots);
-      if (used > best_used) {
+      if (f > max_tiles) f = max_tiles;
+      const int64_t cost = plan_ceil_div(f * pairs, s.slots) * (plan_ceil_div(msl > 1 ? msl : 1, f) + kFp4StartTokens) +
+                           (f > 1 ? kFp4StartTokens / 2 : 0);
+      if (best_cost == 0 || cost < best_cost) {
         best = f;
-        best_used = used;
+        best_cost = cost;
       }
-      if (best_used >= 15) break;
     }
     splits = best;
     // short: as many chunks as a cluster may have, which then needs no partials
@@ -175,7 +174,7 @@ __host__ __device__ int64_t plan_splits(const PlanShape& s, bool uniform, int64_
                                   per_cta > min_chunk ? per_cta : min_chunk, s.slots);
     splits = plan_ceil_div(msl > 1 ? msl : 1, target);
   }
-  const int64_t least = s.fp4 ? kFp4MinUniform : kMinChunkTokens;
+  const int64_t least = s.listed ? kListMinChunk : s.fp4 ? kFp4MinUniform : kMinChunkTokens;
   const int64_t by_min = msl / least > 1 ? msl / least : 1;
   if (splits > by_min) splits = by_min;
   if (splits > max_tiles) splits = max_tiles;

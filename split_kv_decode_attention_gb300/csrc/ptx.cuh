@@ -386,16 +386,4 @@ __device__ __forceinline__ void named_barrier_sync(uint32_t id, uint32_t nthread
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
-// The barrier, and whether the predicate holds for all its threads.
-__device__ __forceinline__ bool named_barrier_and(uint32_t id, uint32_t nthreads, bool x) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
-      "barrier.cta.red.and.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(nthreads), "r"(x ? 1u : 0u)
-      : "memory");
-  return r != 0;
-}
-
 }  // namespace dattn

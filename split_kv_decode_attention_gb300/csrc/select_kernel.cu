@@ -69,6 +69,7 @@ __device__ __forceinline__ void s8x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& 
 }
 
 constexpr int kScoreWarps = 4;
+constexpr int kScoreCtas = 8;  // per SM (2 to 8 within 2% of each other, 12 to 32 up to 15% slower)
 
 // Dynamic shared memory: q' fragments [row tiles][4 step pairs][32 lanes] of
 // 16 B, the rows' a / 127, then (several tokens) each warp's row scores
@@ -533,11 +534,11 @@ cudaError_t launch_select(const SelectArgs& a, int sm_count, cudaStream_t stream
           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
       if (e != cudaSuccess) return e;
     }
-    // a tile of 16 pages per warp, several per warp once the grid has about
-    // eight CTAs per SM (each CTA prepares q' again)
+    // a tile of 16 pages per warp, several per warp once the grid has
+    // kScoreCtas CTAs per SM (each CTA prepares q' again)
     const int64_t full = (a.max_blocks + kScoreWarps * 16 - 1) / (kScoreWarps * 16);
     const int64_t pairs = static_cast<int64_t>(a.g.batch) * a.g.num_kv_heads;
-    int64_t x = (8 * static_cast<int64_t>(sm_count) + pairs - 1) / pairs;
+    int64_t x = (kScoreCtas * static_cast<int64_t>(sm_count) + pairs - 1) / pairs;
     x = x < full ? x : full;
     const cudaError_t e =
         launch(kernel, dim3(a.g.num_kv_heads, static_cast<unsigned>(x), a.g.batch),
