@@ -454,8 +454,8 @@ int decode_attn_cached(const decode_attn_params *p, const decode_attn_cache *c, 
  *     table[(pos - first) * 2 num_freqs + i]             = amplitude cos(pos f_i)
  *     table[(pos - first) * 2 num_freqs + num_freqs + i] = amplitude sin(pos f_i)
  * in fp32, to about one ulp at every position (the angle is reduced in 64-bit
- * fixed point); the table is 16-byte aligned.  Scalings for long contexts are the caller's choice of f and
- * amplitude.  1 <= num_freqs <= 64, first and first + count within 0 .. 2^31.
+ * fixed point); the table is 16-byte aligned.  Scalings for long contexts are
+ * the caller's choice of f and amplitude.  1 <= num_freqs <= 64, first and first + count within 0 .. 2^31.
  * Frequencies that are not finite give NaN.
  */
 int decode_attn_rope_table(const double *inv_freq, int32_t num_freqs, int64_t first,
@@ -494,8 +494,8 @@ typedef struct decode_attn_rope {
  * all in fp32, so the bytes are the same wherever a token is recomputed.
  *   p          the shapes, paging and strides of the attention calls; q_len
  *              may be any length here; q / o strides are those of q / q_out;
- *              scale and causal are not used; k_scale and v_scale are finite
- *              and not 0
+ *              scale and causal are not used; k_scale and v_scale and their
+ *              reciprocals are finite
  *   q, q_out   bf16; both NULL: only the cache is written.  q_out may be q.
  *   k, v       bf16, the new tokens; both NULL: only q is rotated
  *   table      decode_attn_rope_table() from position 0
@@ -506,8 +506,8 @@ typedef struct decode_attn_rope {
  * < n_b (the first n_b - L rows have no position and are skipped),
  * DA_STATUS_BAD_PAGE where a page is out of range (that token is not written)
  * and DA_STATUS_POSITION where a position has no row in the table (that token
- * is not rotated or written).  Two tokens of a call that map to one slot leave either's
- * values there.
+ * is not rotated or written).  Two tokens of a call that map to one slot leave
+ * either's values there.
  */
 #define DA_STATUS_POSITION 16u
 int decode_attn_rope_append(const decode_attn_params *p, const decode_attn_cache *c,
@@ -555,8 +555,9 @@ typedef struct decode_attn_select {
  * the group of
  *     ((sum_d min(q'_d, 0) min_d + max(q'_d, 0) max_d) * digest_scale) * (a / 127),
  * with a = max |q_d| and q'_d = rint(q_d * (127 / a)): up to its 8 bits, a
- * bound on q . k over the page's keys, each channel at its better end.  The sum is exact, the two products
- * are fp32: the selection is the same on every run.  (NaN in q counts as 0,
+ * bound on q . k over the page's keys, each channel at its better end.  The
+ * sum is exact, the two products are fp32: the selection is the same on every
+ * run.  (NaN in q counts as 0,
  * infinities as the largest finite bf16 value; a = 0 gives scores of 0.)
  *   blocks     int32 [B, q_len, Hkv, top_k]: the selected pages' places in
  *              the request, ascending, -1 behind the last; may be NULL

@@ -243,7 +243,7 @@ int decode_attn_rope_append(const decode_attn_params* p, const decode_attn_cache
   if (r->rotary_dim < 0 || r->rotary_dim > DECODE_ATTN_HEAD_DIM || r->rotary_dim % 2 != 0 ||
       r->table_positions < 0 || r->reserved != 0 ||
       static_cast<int64_t>(p->batch) * p->q_len > 0x7fffffff ||
-      (c->type != DA_CACHE_BF16 && (p->k_scale == 0.f || p->v_scale == 0.f)))
+      (c->type != DA_CACHE_BF16 && (!std::isfinite(1.f / p->k_scale) || !std::isfinite(1.f / p->v_scale))))
     return DA_ERR_BAD_SHAPE;
   if (p->batch == 0) return DA_OK;
   const bool rotate = q != nullptr, append = k != nullptr;

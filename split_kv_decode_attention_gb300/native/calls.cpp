@@ -16,6 +16,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -25,6 +26,7 @@
 #include <cstdint>
 #include <cstring>
 #include <initializer_list>
+#include <optional>
 #include <string>
 
 #include "decode_attn.h"
@@ -134,36 +136,43 @@ void on_current_device(std::initializer_list<const at::Tensor*> ts) {
   }
 }
 
-// The stream of a call.  What the call allocates belongs to the current stream;
-// on another one the allocator is told, so that the memory is not handed out
-// again before the call is done with it.
-struct Stream {
+// The stream of a call.  Where it is not the current one, it is made current
+// until the call returns: what the call allocates then comes from that stream's
+// memory (a block that the current stream has freed may still be in use there),
+// and the allocator is told that the results are read on the caller's.
+class Stream {
+ public:
+  explicit Stream(PyObject* o) {
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream();
+    raw = current.stream();
+    if (o == Py_None) return;
+    void* p = nullptr;
+    if (PyLong_Check(o)) {
+      p = PyLong_AsVoidPtr(o);
+    } else {
+      PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
+      if (h == nullptr) throw python_error();
+      p = PyLong_AsVoidPtr(h);
+      Py_DECREF(h);
+    }
+    if (PyErr_Occurred()) throw python_error();
+    if (p == raw) return;
+    raw = p;
+    caller_ = current;
+    guard_.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(p), current.device_index()));
+  }
+
+  // (a tensor that the call allocated and hands out)
+  void returns(const at::Tensor& t) const {
+    if (caller_ && t.numel() > 0) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), *caller_);
+  }
+
   void* raw;
-  bool foreign;
 
-  void uses(const at::Tensor& t) const {
-    if (foreign && t.defined() && t.numel() > 0)
-      c10::cuda::CUDACachingAllocator::recordStream(
-          t.storage().data_ptr(),
-          c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(raw), t.device().index()));
-  }
+ private:
+  std::optional<c10::cuda::CUDAStream> caller_;
+  std::optional<c10::cuda::CUDAStreamGuard> guard_;
 };
-
-Stream stream_of(PyObject* o) {
-  void* current = c10::cuda::getCurrentCUDAStream().stream();
-  if (o == Py_None) return {current, false};
-  void* p = nullptr;
-  if (PyLong_Check(o)) {
-    p = PyLong_AsVoidPtr(o);
-  } else {
-    PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
-    if (h == nullptr) throw python_error();
-    p = PyLong_AsVoidPtr(h);
-    Py_DECREF(h);
-  }
-  if (PyErr_Occurred()) throw python_error();
-  return {p, p != current};
-}
 
 int32_t* status_of(const at::Tensor& t) {
   if (!t.defined()) return nullptr;
@@ -297,15 +306,21 @@ at::Tensor empty_like_device(at::IntArrayRef shape, at::ScalarType type, const a
   return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
 
-at::Tensor out_or_new(const at::Tensor& out, const at::Tensor& q) {
-  if (!out.defined()) return empty_like_device(q.sizes(), at::kBFloat16, q);
+at::Tensor new_result(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like, const Stream& stream) {
+  at::Tensor t = empty_like_device(shape, type, like);
+  stream.returns(t);
+  return t;
+}
+
+at::Tensor out_or_new(const at::Tensor& out, const at::Tensor& q, const Stream& stream) {
+  if (!out.defined()) return new_result(q.sizes(), at::kBFloat16, q, stream);
   heads_tensor(out, q.size(0), q.size(1), "out");
   if (out.size(2) != q.size(2)) refuse("out and q differ in heads");
   return out;
 }
 
-at::Tensor lse_or_new(const at::Tensor& lse, const at::Tensor& q) {
-  if (!lse.defined()) return empty_like_device({q.size(0), q.size(1), q.size(2)}, at::kFloat, q);
+at::Tensor lse_or_new(const at::Tensor& lse, const at::Tensor& q, const Stream& stream) {
+  if (!lse.defined()) return new_result({q.size(0), q.size(1), q.size(2)}, at::kFloat, q, stream);
   dense(lse, at::kFloat, {q.size(0), q.size(1), q.size(2)}, "lse");
   return lse;
 }
@@ -348,13 +363,15 @@ PyObject* rope_table(PyObject* const* a, Py_ssize_t n) {
   at::Tensor out = tensor(a[4], "out");
   if (rows < 0) refuse("max_pos is negative");
   on_current_device({&f, &out});
-  if (out.defined()) dense(out, at::kFloat, {rows, 2 * nf}, "out");
-  else out = empty_like_device({rows, 2 * nf}, at::kFloat, f);
-  const Stream stream = stream_of(a[5]);
+  const Stream stream(a[5]);
+  if (out.defined()) {
+    dense(out, at::kFloat, {rows, 2 * nf}, "out");
+  } else {
+    out = new_result({rows, 2 * nf}, at::kFloat, f, stream);
+  }
   check(decode_attn_rope_table(static_cast<const double*>(ptr(f)), static_cast<int32_t>(std::min<int64_t>(nf, 1 << 20)),
                                first, rows, amplitude, static_cast<float*>(ptr(out)), stream.raw),
         "decode_attn_rope_table");
-  stream.uses(out);
   return give(out);
 }
 
@@ -413,17 +430,16 @@ PyObject* rope_append(PyObject* const* a, Py_ssize_t n) {
   if (pos.defined()) dense(pos, at::kInt, {B, T}, "positions");
   if (new_lens.defined()) int_vector(new_lens, B, "new_lens");
   on_current_device({&q, &k, &v, &table, &kc, &vc, &bt, &lens, &pos, &new_lens, &k_sf, &v_sf, &q_out, &status});
+  const Stream stream(a[18]);
   if (q.defined()) {
-    if (!q_out.defined()) q_out = empty_like_device(q.sizes(), at::kBFloat16, q);
+    if (!q_out.defined()) q_out = new_result(q.sizes(), at::kBFloat16, q, stream);
     q_strides(p, q, q_out);
   }
-  const Stream stream = stream_of(a[18]);
   check(decode_attn_rope_append(&p, &c.c, &r, ptr(q), ptr(k), ptr(v), static_cast<const float*>(ptr(table)),
                                 static_cast<const int32_t*>(ptr(pos)), static_cast<const int32_t*>(ptr(new_lens)),
                                 static_cast<const int32_t*>(ptr(bt)), static_cast<const int32_t*>(ptr(lens)),
                                 ptr(q_out), status_of(status), stream.raw),
         "decode_attn_rope_append");
-  stream.uses(q_out);
   if (!q.defined()) Py_RETURN_NONE;
   return give(q_out);
 }
@@ -447,16 +463,20 @@ PyObject* block_digest(PyObject* const* a, Py_ssize_t n) {
   decode_attn_params p =
       cache_params(B, 1, c.heads, c, kc, bt, integer32(a[5], "max_seq_len"), false, 1.f, 1.0, 1.0);
   on_current_device({&kc, &bt, &lens, &digest, &scale, &k_sf, &status});
-  if (!digest.defined()) digest = at::zeros({c.groups, c.heads, 2, kD}, kc.options().dtype(at::kChar));
-  if (!scale.defined()) scale = at::zeros({c.groups, c.heads}, kc.options().dtype(at::kFloat));
+  const Stream stream(a[9]);
+  if (!digest.defined()) {
+    digest = at::zeros({c.groups, c.heads, 2, kD}, kc.options().dtype(at::kChar));
+    stream.returns(digest);
+  }
+  if (!scale.defined()) {
+    scale = at::zeros({c.groups, c.heads}, kc.options().dtype(at::kFloat));
+    stream.returns(scale);
+  }
   digest_tensors(digest, scale, c.groups, c.heads);
-  const Stream stream = stream_of(a[9]);
   check(decode_attn_block_digest(&p, &c.c, static_cast<const int32_t*>(ptr(bt)), static_cast<const int32_t*>(ptr(lens)),
                                  integer32(a[6], "max_new"), static_cast<int8_t*>(ptr(digest)),
                                  static_cast<float*>(ptr(scale)), status_of(status), stream.raw),
         "decode_attn_block_digest");
-  stream.uses(digest);
-  stream.uses(scale);
   return give({digest, scale});
 }
 
@@ -479,20 +499,17 @@ PyObject* decode_cached(PyObject* const* a, Py_ssize_t n) {
                                       scale_or_default(a[9]), number(a[17]), number(a[18]));
   p.flags = truth(a[16]) ? DA_FLAG_TWO_PASS : 0;
   on_current_device({&q, &kc, &vc, &k_sf, &v_sf, &bt, &lens, &given, &status, &out0, &lse0});
-  const at::Tensor out = out_or_new(out0, q), lse = lse_or_new(lse0, q);
+  const Stream stream(a[15]);
+  const at::Tensor out = out_or_new(out0, q, stream), lse = lse_or_new(lse0, q, stream);
   q_strides(p, q, out);
   const int32_t splits = std::max<int32_t>(0, integer32(a[10], "num_splits"));
   size_t need = 0;
   check(decode_attn_cached_workspace_bytes(&p, &c.c, splits, &need), "decode_attn_cached_workspace_bytes");
   const at::Tensor ws = workspace_or_new(given, need, q);
-  const Stream stream = stream_of(a[15]);
   check(decode_attn_cached(&p, &c.c, ptr(q), static_cast<const int32_t*>(ptr(bt)),
                            static_cast<const int32_t*>(ptr(lens)), ptr(out), static_cast<float*>(ptr(lse)), splits,
                            ptr(ws), bytes_of(ws), status_of(status), stream.raw),
         "decode_attn_cached");
-  stream.uses(out);
-  stream.uses(lse);
-  stream.uses(ws);
   return give({out, lse});
 }
 
@@ -523,24 +540,20 @@ PyObject* sparse(PyObject* const* a, Py_ssize_t n) {
   s.local = integer32(a[10], "local");
   if (s.top_k < 1) refuse("top_k must be at least 1");
   on_current_device({&q, &kc, &vc, &k_sf, &v_sf, &bt, &lens, &digest, &dscale, &given, &status, &out0, &lse0, &blocks});
-  const at::Tensor out = out_or_new(out0, q), lse = lse_or_new(lse0, q);
+  const Stream stream(a[22]);
+  const at::Tensor out = out_or_new(out0, q, stream), lse = lse_or_new(lse0, q, stream);
   q_strides(p, q, out);
   if (blocks.defined()) dense(blocks, at::kInt, {B, T, c.heads, s.top_k}, "blocks");
-  else blocks = empty_like_device({B, T, c.heads, s.top_k}, at::kInt, q);
+  else blocks = new_result({B, T, c.heads, s.top_k}, at::kInt, q, stream);
   size_t need = 0;
   check(decode_attn_sparse_workspace_bytes(&p, &c.c, &s, &need), "decode_attn_sparse_workspace_bytes");
   const at::Tensor ws = workspace_or_new(given, need, q);
-  const Stream stream = stream_of(a[22]);
   check(decode_attn_sparse(&p, &c.c, &s, ptr(q), static_cast<const int8_t*>(ptr(digest)),
                            static_cast<const float*>(ptr(dscale)), static_cast<const int32_t*>(ptr(bt)),
                            static_cast<const int32_t*>(ptr(lens)), ptr(out), static_cast<float*>(ptr(lse)),
                            static_cast<int32_t*>(ptr(blocks)), ptr(ws), bytes_of(ws), status_of(status),
                            stream.raw),
         "decode_attn_sparse");
-  stream.uses(out);
-  stream.uses(lse);
-  stream.uses(blocks);
-  stream.uses(ws);
   return give({out, lse, blocks});
 }
 
@@ -572,24 +585,20 @@ PyObject* block_select(PyObject* const* a, Py_ssize_t n) {
   s.local = integer32(a[9], "local");
   if (s.top_k < 1) refuse("top_k must be at least 1");
   on_current_device({&q, &digest, &dscale, &bt, &lens, &blocks, &given, &status});
+  const Stream stream(a[14]);
   if (blocks.defined()) dense(blocks, at::kInt, {B, T, c.heads, s.top_k}, "blocks");
-  else blocks = empty_like_device({B, T, c.heads, s.top_k}, at::kInt, q);
-  const at::Tensor pages = empty_like_device({B, T, c.heads, s.top_k}, at::kInt, q);
-  const at::Tensor tokens = empty_like_device({B, T, c.heads}, at::kInt, q);
+  else blocks = new_result({B, T, c.heads, s.top_k}, at::kInt, q, stream);
+  const at::Tensor pages = new_result({B, T, c.heads, s.top_k}, at::kInt, q, stream);
+  const at::Tensor tokens = new_result({B, T, c.heads}, at::kInt, q, stream);
   size_t need = 0;
   check(decode_attn_block_select_workspace_bytes(&p, &s, &need), "decode_attn_block_select_workspace_bytes");
   const at::Tensor ws = workspace_or_new(given, need, q);
-  const Stream stream = stream_of(a[14]);
   check(decode_attn_block_select(&p, &s, ptr(q), static_cast<const int8_t*>(ptr(digest)),
                                  static_cast<const float*>(ptr(dscale)), static_cast<const int32_t*>(ptr(bt)),
                                  static_cast<const int32_t*>(ptr(lens)), static_cast<int32_t*>(ptr(blocks)),
                                  static_cast<int32_t*>(ptr(pages)), static_cast<int32_t*>(ptr(tokens)), ptr(ws),
                                  bytes_of(ws), status_of(status), stream.raw),
         "decode_attn_block_select");
-  stream.uses(blocks);
-  stream.uses(pages);
-  stream.uses(tokens);
-  stream.uses(ws);
   return give({blocks, pages, tokens});
 }
 

@@ -114,7 +114,7 @@ def append(lib, p=None, c=None, r=None, q=A, k=A, v=A, table=A, positions=None, 
     (dict(r=rope(v_stride_batch=0)), -6), (dict(table=None), -1), (dict(table=A + 4), -6), (dict(lens=None), -1),
     (dict(q=None), -1), (dict(q_out=None), -1), (dict(v=None), -1), (dict(k=None), -1),
     (dict(q=None, q_out=None, k=None, v=None), -1), (dict(k=A + 8), -6), (dict(positions=A + 2), -6),
-    (dict(p=params(k_scale=0.0)), -2), (dict(p=params(v_scale=math.nan)), -2), (dict(c=cache(v=0)), -1),
+    (dict(p=params(k_scale=0.0)), -2), (dict(p=params(v_scale=math.nan)), -2), (dict(p=params(v_scale=1e-39)), -2), (dict(c=cache(v=0)), -1),
     (dict(p=params(q_stride_token=4)), -6), (dict(p=params(max_seq_len=65)), -2), (dict(p=params(q_len=0)), -2)])
 def test_append_refusals(lib, kw, code):
     assert append(lib, **kw) == code

@@ -443,6 +443,81 @@ def test_fp4_attention_poisoned_slots(da, splits):
         assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
 
 
+def longer(pc, max_len):
+    """The same requests under a larger max_seq_len: a wider block table, -1 behind
+    the pages that exist."""
+    wide = torch.full((len(pc.lens), -(-max_len // pc.page)), -1, dtype=torch.int32)
+    for b, n in enumerate(pc.lens):
+        wide[b, :-(-n // pc.page)] = pc.bt[b, :-(-n // pc.page)]
+    pc.bt, pc.max_len = wide, max_len
+    return pc
+
+
+@pytest.mark.parametrize("splits", [0, 128])
+@pytest.mark.parametrize("heads", [2, 4, 8, 12])
+@pytest.mark.parametrize("G,T,page", [(1, 1, 16), (8, 1, 64), (16, 1, 16), (8, 4, 48), (8, 9, 32)])
+def test_fp4_attention_heads_that_share_boxes(da, heads, G, T, page, splits):
+    """Calls with work enough for CTAs of two, four and eight KV heads."""
+    pc = longer(Paged("fp4", [700, 33, 0, 1500, 16], heads, page, 170 + heads, std=1.5), 65280).gpu()
+    q = bf16(gen(171), 5, T, heads * G, D, std=2.0)
+    out, lse = da.decode_attn(q.cuda(), pc.dk, pc.dv, pc.dbt, pc.dlens, max_seq_len=pc.max_len, causal=T > 1,
+                              num_splits=splits, **pc.scales())
+    check_attention(pc, q, out, lse, T > 1, 1 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("splits", [0, 1])
+def test_fp4_attention_many_requests_in_a_contiguous_cache(da, splits):
+    lens = [(37 * i) % 257 for i in range(320)]
+    pc = Paged("fp4", lens, 2, 0, 172).gpu()
+    q = bf16(gen(173), 320, 1, 8, D, std=2.0)
+    out, lse = da.decode_attn(q.cuda(), pc.dk, pc.dv, None, pc.dlens, max_seq_len=pc.max_len, num_splits=splits,
+                              **pc.scales())
+    check_attention(pc, q, out, lse, False, 1 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("G", [1, 20])
+def test_fp4_attention_more_requests_than_a_planner_holds(da, G):
+    lens = [(13 * i) % 41 for i in range(1100)]
+    pc = Paged("fp4", lens, 1, 16, 174).gpu()
+    q = bf16(gen(175), 1100, 1, G, D, std=2.0)
+    out, lse = da.decode_attn(q.cuda(), pc.dk, pc.dv, pc.dbt, pc.dlens, max_seq_len=pc.max_len, **pc.scales())
+    check_attention(pc, q, out, lse, False, 1 / math.sqrt(D))
+
+
+def test_fp4_attention_poisoned_slots_of_shared_boxes(da):
+    pc = longer(Paged("fp4", [1, 17, 140, 0, 63], 8, 48, 176), 65280).gpu()
+    q = bf16(gen(177), 5, 1, 16, D).cuda()
+    clean = da.decode_attn(q, pc.dk, pc.dv, pc.dbt, pc.dlens, max_seq_len=pc.max_len, **pc.scales())
+    live = torch.zeros(pc.k.shape[:2], dtype=torch.bool)
+    for b, n in enumerate(pc.lens):
+        for j in range(n):
+            live[int(pc.bt[b, j // 48]), j % 48] = True
+    dead = (~live).cuda()
+    for c, sf in ((pc.dk, pc.dk_sf), (pc.dv, pc.dv_sf)):
+        c[dead] = 0xFF
+        sf.permute(0, 2, 1, 3)[dead] = 0x7F
+    out, lse = da.decode_attn(q, pc.dk, pc.dv, pc.dbt, pc.dlens, max_seq_len=pc.max_len, **pc.scales())
+    assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
+
+
+def test_fp4_attention_one_launch_and_two(da):
+    """The cluster merge and the merge of partials agree with the reference, into
+    tensors that the caller gives."""
+    pc = Paged("fp4", [2000, 1111], 2, 16, 178).gpu()
+    q = bf16(gen(179), 2, 1, 8, D, std=2.0)
+    out = torch.full((2, 1, 8, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((2, 1, 8), 7.0, device="cuda")
+    for two in (False, True):
+        ws = torch.full((1 << 22,), 0xFF, dtype=torch.uint8, device="cuda")
+        got = da.decode_attn(q.cuda(), pc.dk, pc.dv, pc.dbt, pc.dlens, max_seq_len=2000, num_splits=4, out=out, lse=lse,
+                             workspace=ws, two_pass=two, **pc.scales())
+        assert got[0].data_ptr() == out.data_ptr() and got[1].data_ptr() == lse.data_ptr()
+        assert bool((ws != 0xFF).any()) == two
+        check_attention(pc, q, out, lse, False, 1 / math.sqrt(D))
+        out.fill_(7.0)
+        lse.fill_(7.0)
+
+
 def test_fp4_attention_bad_pages_and_lengths(da):
     pc = Paged("fp4", [40, 20], 2, 16, 82).gpu()
     q = bf16(gen(83), 2, 1, 4, D).cuda()
@@ -755,3 +830,96 @@ def test_empty_batches(da):
     dg, ds = da.block_digest(k, bt, lens, max_seq_len=32, k_sf=sf)
     out, lse, blocks = da.decode_attn_sparse(q, k, k, bt, lens, dg, ds, max_seq_len=32, top_k=2, k_sf=sf, v_sf=sf)
     assert blocks.shape == (0, 1, 2, 2)
+
+
+def test_calls_on_a_stream_that_is_not_the_current_one(da):
+    """What a call allocates and clears is ordered with the call's stream, however
+    busy the current one is."""
+    pc = Paged("fp4", [900, 450, 33], 4, 16, 162).gpu()
+    q, new = bf16(gen(163), 3, 1, 16, D).cuda(), bf16(gen(164), 3, 1, 4, D).cuda()
+    f = da.rope_frequencies(D)[0].cuda()
+    kw = dict(max_seq_len=900)
+
+    def run(stream):
+        tab = da.rope_table(f, 1000, stream=stream)
+        turned = da.rope_append(q, new, new, tab, pc.dk, pc.dv, pc.dbt, pc.dlens, stream=stream, **kw, **pc.scales())
+        dg, ds = da.block_digest(pc.dk, pc.dbt, pc.dlens, k_sf=pc.dk_sf, stream=stream, **kw)
+        dense = da.decode_attn(turned, pc.dk, pc.dv, pc.dbt, pc.dlens, stream=stream, **kw, **pc.scales())
+        some = da.decode_attn_sparse(turned, pc.dk, pc.dv, pc.dbt, pc.dlens, dg, ds, top_k=5, stream=stream, **kw,
+                                     **pc.scales())
+        picked = da.block_select(turned, dg, ds, pc.dbt, pc.dlens, page_size=16, top_k=5, stream=stream, **kw)
+        return [tab, turned, dg, ds, *dense, *some, picked[0], picked[2]]
+
+    want = run(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        before = torch.cuda.current_stream()
+        torch.cuda._sleep(100_000_000)
+        got = run(stream)
+        assert torch.cuda.current_stream() == before
+        side.synchronize()
+        with torch.cuda.stream(side):
+            copies = [t.clone() for t in got]
+        side.synchronize()
+        torch.cuda.synchronize()
+        for a, b, c in zip(want, copies, got):
+            assert torch.equal(a, b) and torch.equal(a, c)
+
+
+def test_two_graphs_that_share_a_workspace(da):
+    """Captured calls leave nothing in a workspace that another call needs."""
+    pc = longer(Paged("fp4", [3000, 1500, 700], 4, 16, 165), 8192).gpu()
+    q = bf16(gen(166), 3, 1, 16, D).cuda()
+    dg, ds = da.block_digest(pc.dk, pc.dbt, pc.dlens, max_seq_len=8192, k_sf=pc.dk_sf)
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")
+    kw = dict(max_seq_len=8192, workspace=ws)
+
+    def dense():
+        return da.decode_attn(q, pc.dk, pc.dv, pc.dbt, pc.dlens, **kw, **pc.scales())
+
+    def some():
+        return da.decode_attn_sparse(q, pc.dk, pc.dv, pc.dbt, pc.dlens, dg, ds, top_k=20, **kw, **pc.scales())
+
+    want = [[t.clone() for t in f()] for f in (dense, some)]
+    graphs, outs = [], []
+    for f in (dense, some):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(f())
+        graphs.append(g)
+    for order in ((0, 1), (1, 0), (0, 0), (1, 1)):
+        for t in (*outs[0], *outs[1]):
+            t.zero_()
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in order:
+            for a, b in zip(outs[i], want[i]):
+                assert torch.equal(a, b)
+    # lengths that change between replays
+    pc.lens = [2999, 1, 0]
+    pc.dlens.copy_(torch.tensor(pc.lens, dtype=torch.int32))
+    for g in graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    check_attention(pc, q.cpu(), *outs[0], False, 1 / math.sqrt(D))
+    assert torch.equal(outs[1][2].cpu(), reference_blocks(pc, q.cpu(), dg.cpu(), ds.cpu(), 20, 1, 1, False))
+
+
+def test_sparse_into_given_tensors(da):
+    pc = Paged("bf16", [900, 450], 2, 16, 167).gpu()
+    q = bf16(gen(168), 2, 2, 8, D).cuda()
+    dg, ds = da.block_digest(pc.dk, pc.dbt, pc.dlens, max_seq_len=900)
+    kw = dict(max_seq_len=900, top_k=7, causal=True)
+    want = da.decode_attn_sparse(q, pc.dk, pc.dv, pc.dbt, pc.dlens, dg, ds, **kw)
+    wide = torch.zeros(2, 2, 12, D, dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(2, 2, 8, device="cuda")
+    blocks = torch.zeros(2, 2, 2, 7, dtype=torch.int32, device="cuda")
+    ws = torch.full((1 << 22,), 0xFF, dtype=torch.uint8, device="cuda")
+    got = da.decode_attn_sparse(q, pc.dk, pc.dv, pc.dbt, pc.dlens, dg, ds, out=wide[:, :, 2:10], lse=lse, blocks=blocks,
+                                workspace=ws, **kw)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert got[2].data_ptr() == blocks.data_ptr() and bool((ws != 0xFF).any())
+    assert not bool(wide[:, :, :2].any()) and not bool(wide[:, :, 10:].any())
