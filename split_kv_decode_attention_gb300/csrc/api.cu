@@ -164,11 +164,15 @@ int plan_for_slots(const decode_attn_params* p, const int32_t* host_seq_lens, in
   return DA_OK;
 }
 
+// 4-bit caches of calls with more query rows per KV head than the 4-bit kernel
+// holds go to the tcgen05 kernel.
+bool wide4(const decode_attn_params* p) { return rows_of(p) > dattn::kFp4MaxRows; }
+
 // Resident CTAs per SM of the split launch for this shape (unit: KV heads of a
 // CTA of the 4-bit kernel, 0 for the other caches).
 int ctas_per_sm(const decode_attn_params* p, int unit) {
-  return unit > 0 ? dattn::fp4_ctas_per_sm(rows_of(p), unit)
-                  : dattn::split_ctas_per_sm(rows_of(p), kv_fp8(p));
+  return unit > 0 && !wide4(p) ? dattn::fp4_ctas_per_sm(rows_of(p), unit)
+                               : dattn::split_ctas_per_sm(rows_of(p), kv_fp8(p));
 }
 
 // KV heads that a CTA of the 4-bit kernel takes (0: not a 4-bit cache).  More
@@ -178,7 +182,7 @@ int ctas_per_sm(const decode_attn_params* p, int unit) {
 // max_seq_len.  Heads that choose their own pages cannot share a box.
 int unit_heads(const decode_attn_params* p, const DecodeExt& ext) {
   if (ext.fp4 == nullptr) return 0;
-  if (ext.per_head) return 1;
+  if (ext.per_head || wide4(p)) return 1;
   DeviceInfo di;
   if (current_device_info(&di) != DA_OK) return 1;
   for (int u = 8; u > 1; u /= 2)
@@ -284,7 +288,7 @@ int make_kv_map(CUtensorMap* map, const void* base, const decode_attn_params* p,
 // of a stage, 64 tokens at most, that a page is a multiple of (so is a chunk).
 int fp4_box_halves(const decode_attn_params* p, bool paged, int unit) {
   int h = 4;
-  const int stage = 2 * dattn::fp4_warps(rows_of(p)) / unit;
+  const int stage = wide4(p) ? 4 : 2 * dattn::fp4_warps(rows_of(p)) / unit;
   while (stage % h != 0 || (paged && p->page_size % (16 * h) != 0)) h /= 2;
   return h;
 }
@@ -326,8 +330,8 @@ bool kv_stride_ok(const decode_attn_params* p, int64_t s, bool fp4 = false) {
 // (request, kv head) form a supported cluster and all clusters fit at once.
 bool use_cluster_merge(const decode_attn_params* p, int32_t splits_eff, int unit = 0) {
   if ((p->flags & DA_FLAG_TWO_PASS) != 0 || splits_eff < 2 || p->batch < 1) return false;
-  if (unit > 0)  // (4-bit caches: CTAs of one head, and one group of rows)
-    return unit == 1 && rows_of(p) <= dattn::kFp4MaxRows &&
+  if (unit > 0)  // (4-bit caches: CTAs of one head)
+    return unit == 1 && !wide4(p) &&
            dattn::fp4_cluster_merge_fits(rows_of(p), splits_eff,
                                          static_cast<int64_t>(p->batch) * p->num_kv_heads);
   return dattn::split_cluster_merge_fits(rows_of(p), kv_fp8(p), splits_eff,
@@ -382,7 +386,7 @@ int list_layout(const decode_attn_params* p, ListLayout* l, int unit = 0) {
   if (rc != DA_OK) return rc;
   const int heads = unit > 0 ? unit : 1;  // KV heads of an item
   l->cap = static_cast<int64_t>(p->batch) * (p->num_kv_heads / heads) +
-           (unit > 0 ? kFp4WaveSlack : kListWaveSlack) * l->slots;
+           (unit > 0 && !wide4(p) ? kFp4WaveSlack : kListWaveSlack) * l->slots;
   if (l->cap > 0x7fffffff) return DA_ERR_BAD_SHAPE;
   const size_t rows = static_cast<size_t>(rows_of(p)) * heads;
   const size_t cap = static_cast<size_t>(l->cap);
@@ -685,7 +689,8 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
       return DA_ERR_CUDA;
   }
   if (fp4) {
-    if (launch_fp4(maps4, a, unit, cluster_merge, st) != cudaSuccess) return DA_ERR_CUDA;
+    if ((wide4(p) ? launch_wide_fp4(maps4, a, st) : launch_fp4(maps4, a, unit, cluster_merge, st)) != cudaSuccess)
+      return DA_ERR_CUDA;
   } else if (dattn::launch_split(kmap, vmap, a, cluster_merge, st) != cudaSuccess) {
     return DA_ERR_CUDA;
   }

@@ -456,12 +456,6 @@ __device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
-  return r;
-}
-
 template <int TYPE>
 struct DigestCfg {
   static constexpr bool kBf = TYPE == DA_CACHE_BF16;

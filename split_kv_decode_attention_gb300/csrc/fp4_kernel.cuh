@@ -49,8 +49,8 @@
 // call is one launch and writes no partials (one request of 4096 tokens, 32 / 8
 // heads: 11 us replayed either way, but 7 and not 10 us of the host's time).
 // Slots behind a sequence may hold anything: their scores are masked and
-// their value scales replaced by zero.  More query rows than a CTA holds run
-// as groups in the grid's y.
+// their value scales replaced by zero.  More than 32 query
+// rows per KV head run on the tcgen05 kernel.
 #pragma once
 
 #include <type_traits>
@@ -221,12 +221,10 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
   }
   grid_dependency_wait();
 
-  // ---- this CTA's work item: (chunk, KV head group, request), row group
-  int split, unit, b, L, chunk, rgroup;
-  const int groups = (a.rows + C::kRows - 1) / C::kRows;
+  // ---- this CTA's work item: (chunk, KV head group, request)
+  int split, unit, b, L, chunk;
   const bool listed = a.items != nullptr;
   if (listed) {
-    rgroup = blockIdx.y;
     const int n_items = a.plan[1];
     const int4 itm = a.items[blockIdx.x];
     chunk = a.plan[0];
@@ -237,8 +235,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
     L = itm.w;
   } else {
     split = blockIdx.x;
-    unit = blockIdx.y / groups;
-    rgroup = blockIdx.y - unit * groups;
+    unit = blockIdx.y;
     b = blockIdx.z;
     // (a length per head only with HG = 1)
     L = a.seq_lens[static_cast<int64_t>(b) * a.len_sb + static_cast<int64_t>(unit) * a.len_sh];
@@ -260,8 +257,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
   const int hh = warp % HG;                              // this (consumer) warp's head of the group
   const int share = warp / HG;                           // and its share of the head's keys
   const int kvh = unit * HG + hh;
-  const int row0 = rgroup * C::kRows;                    // first row of the group
-  const int rows = min(C::kRows, a.rows - row0);
+  const int rows = a.rows;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -362,11 +358,11 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     if (C::kQSmem && nt % C::kShares != share) continue;  // one warp of the head prepares each row tile
-    const int r = row0 + nt * 8 + g4;
+    const int r = nt * 8 + g4;
     uint4 x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (nt * 8 + g4 < rows) {
+    if (r < rows) {
       const int t = r / a.group;
       const uint16_t* qr = a.q + static_cast<int64_t>(b) * a.q_sb + static_cast<int64_t>(t) * a.q_st +
                            static_cast<int64_t>(kvh * a.group + (r - t * a.group)) * a.q_sh + 32 * t4;
@@ -427,7 +423,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
       else e = __shfl_sync(kFull, q_e, (2 * t4 + rr) * 4);
       rs[nt][rr] = ldexpf(a.scale_log2, e);
       int lm = t_end;
-      if (a.causal && row < rows) lm = min(lm, L - a.q_len + 1 + (row0 + row) / a.group);
+      if (a.causal && row < rows) lm = min(lm, L - a.q_len + 1 + row / a.group);
       lim[nt][rr] = lm;
       lim_all = min(lim_all, lm);
     }
@@ -655,11 +651,11 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
   const int S = a.num_splits;
   // where a row of this head goes: its (token, head), and its partial's index
   auto place = [&](int row, int head, int& t) {
-    t = (row0 + row) / a.group;
-    return (unit * HG + head) * a.group + (row0 + row - t * a.group);
+    t = row / a.group;
+    return (unit * HG + head) * a.group + (row - t * a.group);
   };
   auto part_index = [&](int row, int head, int t, int h) {
-    return listed ? (static_cast<int64_t>(blockIdx.x) * HG + head) * a.rows + row0 + row
+    return listed ? (static_cast<int64_t>(blockIdx.x) * HG + head) * a.rows + row
                   : ((static_cast<int64_t>(b) * a.q_len + t) * a.num_q_heads + h) * S + split;
   };
   auto put_lse = [&](int row, int head, float m2, float sum) {
@@ -848,10 +844,9 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
 template <int NT, int HG, bool CM = false>
 cudaError_t launch_one(const Fp4Maps& maps, const SplitArgs& a, cudaStream_t stream) {
   using C = Fp4Cfg<NT, HG>;
-  const int groups = (a.rows + C::kRows - 1) / C::kRows;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = a.items != nullptr ? dim3(static_cast<unsigned>(a.item_slots), groups)
-                                   : dim3(a.num_splits, a.num_kv_heads / HG * groups, a.batch);
+  cfg.gridDim = a.items != nullptr ? dim3(static_cast<unsigned>(a.item_slots))
+                                   : dim3(a.num_splits, a.num_kv_heads / HG, a.batch);
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;

@@ -157,6 +157,7 @@ int split_ctas_per_sm(int rows, bool fp8);
 // outputs and partials as launch_split without cluster merge).
 cudaError_t launch_wide(const CUtensorMap& k_map, const CUtensorMap& v_map, const SplitArgs& a,
                         cudaStream_t stream);
+cudaError_t launch_wide_fp4(const Fp4Maps& maps, const SplitArgs& a, cudaStream_t stream);
 int wide_ctas_per_sm();
 
 // Launch the kernel over 4-bit caches (any rows; outputs and partials as

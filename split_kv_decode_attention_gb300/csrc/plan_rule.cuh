@@ -36,6 +36,7 @@ constexpr int kWideTokensPerRow = 256;
 // longer and waves fewer.  Nothing merges through clusters there, so equal
 // lengths may take any number of chunks.
 // (64 ragged requests of up to 32K: 2 waves 272 us, 3 255, 4 255, 8 274.)
+constexpr int kFp4PlanRows = 32;
 constexpr int kFp4Waves = 3;
 constexpr int kFp4MinChunk = 512;
 constexpr int kFp4MinUniform = 256;                   // shortest chunk of any plan
@@ -137,6 +138,7 @@ __host__ __device__ int64_t plan_splits(const PlanShape& s, bool uniform, int64_
   const int64_t msl = s.max_seq_len;
   const int64_t max_tiles = plan_ceil_div(msl > 1 ? msl : 1, kPlanTile);
   const int64_t pairs = static_cast<int64_t>(s.batch > 1 ? s.batch : 1) * s.num_kv_heads;
+  const bool narrow4 = s.fp4 && s.rows <= kFp4PlanRows;  // (the others: the tcgen05 kernel's items)
   int64_t splits = 1;
   if (uniform && s.fp4) {
     // equal chunks: of the counts that fill one wave, two, ... the one with the
@@ -155,7 +157,7 @@ __host__ __device__ int64_t plan_splits(const PlanShape& s, bool uniform, int64_
     }
     splits = best;
     // short: as many chunks as a cluster may have, which then needs no partials
-    if (msl <= int64_t{kMaxClusterSplits} * kFp4ClusterChunk && splits > kMaxClusterSplits)
+    if (narrow4 && msl <= int64_t{kMaxClusterSplits} * kFp4ClusterChunk && splits > kMaxClusterSplits)
       splits = kMaxClusterSplits;
   } else if (uniform) {
     if (pairs < s.slots) {
@@ -165,10 +167,10 @@ __host__ __device__ int64_t plan_splits(const PlanShape& s, bool uniform, int64_
   } else {
     const int64_t per_cta =
         plan_ceil_div(plan_sat_mul(work_tokens, s.num_kv_heads),
-                      plan_sat_mul(s.fp4 ? kFp4Waves : kRaggedWaves, s.slots));
-    const int64_t per_row = s.rows > kPlanMaxNarrowRows && !s.fp4 ? kWideTokensPerRow : kTokensPerRow;
+                      plan_sat_mul(narrow4 ? kFp4Waves : kRaggedWaves, s.slots));
+    const int64_t per_row = s.rows > kPlanMaxNarrowRows && !narrow4 ? kWideTokensPerRow : kTokensPerRow;
     const int64_t floor_rows = per_row * s.rows;
-    const int64_t min_tokens = s.fp4 ? kFp4MinChunk : kMinChunkTokens;
+    const int64_t min_tokens = narrow4 ? kFp4MinChunk : kMinChunkTokens;
     const int64_t min_chunk = floor_rows > min_tokens ? floor_rows : min_tokens;
     const int64_t target = search(int64_t{kMinChunkTokens},
                                   per_cta > min_chunk ? per_cta : min_chunk, s.slots);

@@ -267,6 +267,12 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&r)[4]) {
       : "r"(w));
 }
 
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
 // Sum of the two values of a packed bf16x2 (or, with f16 = true, f16x2)
 // pair, in fp32 (exact widening).  The probabilities of the P.V product are
 // rounded to 16 bits; normalising the output by the sum of those rounded

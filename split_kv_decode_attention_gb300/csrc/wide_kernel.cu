@@ -93,6 +93,10 @@ constexpr int kWTiles = kWTok / kTileTokens; // 16-token page tiles per stage
 constexpr int kWHalf = kWTok * 128;          // [64 tokens][64 d] 16-bit = 8 KB
 constexpr int kWStageBytes = 4 * kWHalf;     // operand stage: K halves, then V halves
 constexpr int kWF8Tile = kTileTokens * 128;  // one FP8 tile (K or V): 16 rows of 128 bytes
+constexpr int kWF4Tile = kTileTokens * 64;   // one 4-bit tile: 16 rows of 64 bytes
+constexpr int kWF4Scales = kTileTokens * 8;  // and its block scales
+constexpr int kWF4Stages = 6;
+constexpr float kWF4Shift = 6.f;             // 4-bit: P is about 2^6 at the row's maximum
 // Requests whose schedule tables fit in shared memory (else one item per
 // CTA), and up to which the partial chunks are sorted by length.
 constexpr int kWMaxSchedBatch = kWideMaxPlannedBatch;
@@ -120,17 +124,22 @@ static_assert(kWStatFloats * 4 <= kWStatBytes, "statistics buffer");
 // TMA copies issued by one warp are serialised (~130-240 cycles per box), and
 // the time to issue a stage counts against its ring slot, so all producer
 // warps share each stage's boxes.
-template <bool F8>
+// KV: the cache's type (DA_CACHE_*).  F8 stands for either widened type.
+template <int KV>
 struct WCfg {
+  static constexpr bool F8 = KV != DA_CACHE_BF16;
+  static constexpr bool F4 = KV == DA_CACHE_FP4_E2M1;
   static constexpr int kProducers = F8 ? DATTN_WIDE_F8_PRODUCERS : DATTN_WIDE_PRODUCERS;
   static constexpr int kConverters = F8 ? DATTN_WIDE_F8_CONVERTERS : 0;
   static constexpr int kProducerWarp = 8;
   static constexpr int kConverterWarp = kProducerWarp + kProducers;
   static constexpr int kMmaWarp = kConverterWarp + kConverters;
   static constexpr int kThreads = 32 * (kMmaWarp + 1);
-  static constexpr int kStages = F8 ? DATTN_WIDE_F8_STAGES : DATTN_WIDE_STAGES;  // TMA ring
-  static constexpr int kLoadBytes = F8 ? 2 * kWTiles * kWF8Tile : kWStageBytes;
-  static constexpr int kBoxes = F8 ? 2 * kWTiles : 4 * kWTiles;  // 2 KB boxes per stage
+  static constexpr int kStages = F4 ? kWF4Stages : F8 ? DATTN_WIDE_F8_STAGES : DATTN_WIDE_STAGES;  // TMA ring
+  static constexpr int kLoadBytes = F4 ? 2 * kWTiles * (kWF4Tile + kWF4Scales) : F8 ? 2 * kWTiles * kWF8Tile : kWStageBytes;
+  // boxes per 16-token tile, of 2 KB each (4-bit: K, V and both block scales)
+  static constexpr int kPerTile = F8 && !F4 ? 2 : 4;
+  static constexpr int kBoxes = kPerTile * kWTiles;
   // where the MMAs read K and V: the TMA ring itself (bf16: the two halves of
   // each 32 KB stage), or the FP8 variant's widened K and V rings
   static constexpr int kOpK = F8 ? DATTN_WIDE_F8_OPK : kStages;
@@ -253,17 +262,26 @@ __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+// The maps of a cache.
+template <int KV>
+struct WMaps {
+  CUtensorMap k, v;
+};
+template <>
+struct WMaps<DA_CACHE_FP4_E2M1> : Fp4Maps {};
+
 // Tile j of an item goes to softmax group g = j & 1 (warps 4g..4g+3): its
 // scores land in TMEM buffer S[g], its probabilities in TMEM buffer P[g], and
 // P.V accumulates into O[g]; the two groups alternate, so one group's softmax
 // overlaps the other's, and their (m, l, O) merge exactly at the end.  Phases
 // of the ring and of each group's barriers run on across items.
 // KS: key split for items of at most 64 query rows (see the file comment).
-template <bool F8, bool KS>
-__global__ void __launch_bounds__(WCfg<F8>::kThreads, 1)
-    wide_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-                const SplitArgs a) {
-  using C = WCfg<F8>;
+template <int KV, bool KS>
+__global__ void __launch_bounds__(WCfg<KV>::kThreads, 1)
+    wide_kernel(const __grid_constant__ WMaps<KV> maps, const SplitArgs a) {
+  using C = WCfg<KV>;
+  constexpr bool F8 = C::F8;  // widened to f16
+  constexpr bool F4 = C::F4;
   constexpr uint32_t kFull = 0xffffffffu;
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -437,19 +455,31 @@ __global__ void __launch_bounds__(WCfg<F8>::kThreads, 1)
   if (warp >= C::kProducerWarp && warp < C::kConverterWarp) {
     const int pw_idx = warp - C::kProducerWarp;
     if (lane == 0 && pw_idx == 0 && a.max_seq_len > 0) {
-      prefetch_tensor_map(&k_map);
-      prefetch_tensor_map(&v_map);
+      prefetch_tensor_map(&maps.k);
+      prefetch_tensor_map(&maps.v);
+      if constexpr (F4) {
+        prefetch_tensor_map(&maps.ks);
+        prefetch_tensor_map(&maps.vs);
+      }
     }
     const uint64_t policy = l2_evict_first_policy();
     const uint32_t q_stage = smem_base + C::kOffQ;
     // this lane's box of every stage
-    constexpr int kPerTile = F8 ? 2 : 4;
+    constexpr int kPerTile = C::kPerTile;
     const int bx = lane * C::kProducers + pw_idx;
     const int ti = bx / kPerTile;
     const int half = F8 ? 0 : (bx & 1);
     const bool is_v = F8 ? (bx & 1) != 0 : (bx & 2) != 0;
-    const int box_off = F8 ? C::kOffLoad + (is_v ? kWTiles * kWF8Tile : 0) + ti * kWF8Tile
-                           : C::kOffLoad + (is_v ? 2 * kWHalf : 0) + half * kWHalf + ti * 2048;
+    const bool is_sf = F4 && (bx & 2) != 0;  // 4-bit: block scales
+    const int box_off =
+        F4 ? C::kOffLoad + (is_sf ? 2 * kWTiles * kWF4Tile : 0) +
+                 ((is_v ? kWTiles : 0) + ti) * (is_sf ? kWF4Scales : kWF4Tile)
+        : F8 ? C::kOffLoad + (is_v ? kWTiles * kWF8Tile : 0) + ti * kWF8Tile
+             : C::kOffLoad + (is_v ? 2 * kWHalf : 0) + half * kWHalf + ti * 2048;
+    // 4-bit: a box holds box_halves tiles of a page; the lane of the first issues it
+    const bool issues = bx < C::kBoxes && (!F4 || (ti & (a.box_halves - 1)) == 0);
+    const uint32_t lane_bytes =
+        F4 ? (issues ? static_cast<uint32_t>(a.box_halves * (is_sf ? kWF4Scales : kWF4Tile)) : 0u) : 2048u;
     int gs = 0;       // stages of all previous items
     int last_g = -1;  // the last stage this warp issued
     bool ok = true;
@@ -509,12 +539,17 @@ __global__ void __launch_bounds__(WCfg<F8>::kThreads, 1)
       };
       // boxes of this warp in a full stage, and in the item's last one
       const int last_boxes = (it.n_tiles - (it.n_iters - 1) * kWTiles) * kPerTile;
-      const uint32_t full_bytes =
-          static_cast<uint32_t>((C::kBoxes - pw_idx + C::kProducers - 1) / C::kProducers) * 2048u;
-      const uint32_t last_bytes =
-          static_cast<uint32_t>(last_boxes > pw_idx
-                                    ? (last_boxes - pw_idx + C::kProducers - 1) / C::kProducers
-                                    : 0) * 2048u;
+      uint32_t full_bytes, last_bytes;
+      if constexpr (F4) {
+        full_bytes = __reduce_add_sync(kFull, lane_bytes);
+        last_bytes = __reduce_add_sync(kFull, bx < last_boxes ? lane_bytes : 0u);
+      } else {
+        full_bytes =
+            static_cast<uint32_t>((C::kBoxes - pw_idx + C::kProducers - 1) / C::kProducers) * 2048u;
+        last_bytes = static_cast<uint32_t>(last_boxes > pw_idx
+                                               ? (last_boxes - pw_idx + C::kProducers - 1) / C::kProducers
+                                               : 0) * 2048u;
+      }
       int s = gs % C::kStages;         // ring slot and its use count, advanced per stage
       int use = gs / C::kStages;
       int pg_next = page_of(0);
@@ -533,7 +568,7 @@ __global__ void __launch_bounds__(WCfg<F8>::kThreads, 1)
         const bool skip = withhold && gs + i == 0;
         if (lane == 0 && !skip) mbar_arrive_expect_tx(&full_bar[s], last ? last_bytes : full_bytes);
         __syncwarp();
-        if (bx < boxes && !skip) {
+        if (bx < boxes && (!F4 || issues) && !skip) {
           if (a.paged && static_cast<unsigned>(pg) >= static_cast<unsigned>(a.num_pages)) {
             if (a.status != nullptr) atomicOr(a.status, static_cast<int32_t>(DA_STATUS_BAD_PAGE));
             pg = 0;
@@ -541,8 +576,15 @@ __global__ void __launch_bounds__(WCfg<F8>::kThreads, 1)
           const int tok = tok_lane + i * kWTok;
           const int grp = a.paged ? pg : it.b;
           const int tin = a.paged ? (ps_pow2 ? tok & (ps - 1) : tok % ps) : tok;
-          tma_load_4d(smem + box_off + s * C::kLoadBytes, is_v ? &v_map : &k_map, &full_bar[s],
-                      half * 64, it.kvh, tin, grp, policy);
+          uint8_t* dst = smem + box_off + s * C::kLoadBytes;
+          if constexpr (F4) {
+            if (is_sf)
+              tma_load_4d(dst, is_v ? &maps.vs : &maps.ks, &full_bar[s], tin, it.kvh, 0, grp, policy);
+            else
+              tma_load_4d(dst, is_v ? &maps.v : &maps.k, &full_bar[s], 0, it.kvh, tin, grp, policy);
+          } else {
+            tma_load_4d(dst, is_v ? &maps.v : &maps.k, &full_bar[s], half * 64, it.kvh, tin, grp, policy);
+          }
         }
         __syncwarp();
         last_g = gs + i;
@@ -591,6 +633,42 @@ __global__ void __launch_bounds__(WCfg<F8>::kThreads, 1)
     const int src_off = ctin * 128 + ((cc ^ cj) << 4);
     const int dst_off = (cc >> 2) * kWHalf + ctin * 128;
     const int st_lo = (c0 ^ cj) << 4, st_hi = ((c0 + 1) ^ cj) << 4;
+    // 4-bit stages: 16 bytes of a row are 32 values d = 32 c .., two whole scale
+    // blocks, and become 16-byte chunks 4 (c & 1) .. + 3 of d-half c / 2.  A
+    // thread takes chunk fc of rows frow and frow + 32 of K and of V; loads
+    // (64-byte swizzle: slot c ^ (row / 2 & 3)) and stores of eight rows hit
+    // all bank groups.
+    const int fc = (ct >> 3) & 3, frow = (ct >> 5) * 8 + cj;
+    auto widen4 = [&](const uint8_t* src, uint8_t* dst_k, uint8_t* dst_v, int tok0, int t_end) {
+      uint4 raw[4];
+      uint32_t sf[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int row = (u >> 1) * kWTok + frow + 32 * (u & 1);  // (V's rows follow K's)
+        raw[u] = *reinterpret_cast<const uint4*>(src + row * 64 + ((fc ^ ((cj >> 1) & 3)) << 4));
+        sf[u] = *reinterpret_cast<const uint16_t*>(src + 2 * kWTiles * kWF4Tile + row * 8 + 2 * fc);
+      }
+      const int v_rows = t_end - tok0;  // V rows at or past this are zeroed
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int row = frow + 32 * (u & 1);
+        uint8_t* dst = (u >= 2 ? dst_v : dst_k) + (fc >> 1) * kWHalf + row * 128;
+        const uint32_t s2 = e4m3x2_to_f16x2(sf[u]);
+        const uint32_t words[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+        const bool zero = u >= 2 && row >= v_rows;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t x[4];
+          e2m1x8_to_f16(words[i], x);
+          const uint32_t s = __byte_perm(s2, 0, i < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) x[q] = zero ? 0u : mul_f16x2(x[q], s);
+          *reinterpret_cast<uint4*>(dst + (((4 * (fc & 1) + i) ^ cj) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
     auto widen = [&](const uint8_t* src, uint8_t* dst_k, uint8_t* dst_v, int tok0, int t_end) {
       uint4 raw[8];
 #pragma unroll
@@ -627,8 +705,11 @@ __global__ void __launch_bounds__(WCfg<F8>::kThreads, 1)
         if (ok && gs >= C::kOpV)
           ok = __all_sync(kFull, mbar_wait(&convv_empty[ov_slot], ((gs / C::kOpV) - 1) & 1)) != 0;
         if (!ok) break;
-        widen(smem + C::kOffLoad + s * C::kLoadBytes, smem + C::kOffOpK + ok_slot * C::kKSlotBytes,
-              smem + C::kOffOpV + ov_slot * C::kVSlotBytes, it.t_begin + i * kWTok, it.t_end);
+        uint8_t* src = smem + C::kOffLoad + s * C::kLoadBytes;
+        uint8_t* dst_k = smem + C::kOffOpK + ok_slot * C::kKSlotBytes;
+        uint8_t* dst_v = smem + C::kOffOpV + ov_slot * C::kVSlotBytes;
+        if constexpr (F4) widen4(src, dst_k, dst_v, it.t_begin + i * kWTok, it.t_end);
+        else widen(src, dst_k, dst_v, it.t_begin + i * kWTok, it.t_end);
         if (lane == 0) {
           mbar_arrive(&convk_full[ok_slot]);
           mbar_arrive(&convv_full[ov_slot]);
@@ -780,7 +861,10 @@ __global__ void __launch_bounds__(WCfg<F8>::kThreads, 1)
     // the A operand of S = Q.K^T, d pairs packed in 64 columns (group 0: one
     // row per thread).  FP8: straight from global memory, all 16 chunks of the
     // row in flight at once, widened to f16 (the products run in f16).
-    if (!C::kQStaged && grp == 0) {
+    // 4-bit: both groups read it, since a row is scaled by the power of two that
+    // brings its largest value to [2^14, 2^15) and the scores are scaled back.
+    float row_scale = a.scale_log2;
+    if (!C::kQStaged && (F4 || grp == 0)) {
       if (ok) {
         uint4 v[16];
         if (row < a.rows) {
@@ -794,20 +878,44 @@ __global__ void __launch_bounds__(WCfg<F8>::kThreads, 1)
 #pragma unroll
           for (int ch = 0; ch < 16; ++ch) v[ch] = make_uint4(0, 0, 0, 0);
         }
+        float f1 = 1.f, f2 = 1.f;
+        if constexpr (F4) {
+          uint32_t top = 0;  // the largest magnitude's bits (bf16 orders like integers)
 #pragma unroll
-        for (int qc = 0; qc < 4; ++qc) {  // 32 d = 16 columns per step
-          uint32_t w[16];
+          for (int ch = 0; ch < 16; ++ch) {
+            const uint32_t w[4] = {v[ch].x, v[ch].y, v[ch].z, v[ch].w};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint4 x = v[qc * 4 + c];
-            w[4 * c] = bf16x2_to_f16x2(x.x);
-            w[4 * c + 1] = bf16x2_to_f16x2(x.y);
-            w[4 * c + 2] = bf16x2_to_f16x2(x.z);
-            w[4 * c + 3] = bf16x2_to_f16x2(x.w);
+            for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
           }
-          tmem_st16(lane_base + kWColQ + qc * 16, w);
+          // (rows of zeros, or with infinities or NaN, as they are)
+          const int e = top > 0 && top < 0x7f80u ? max(static_cast<int>(top >> 7), 1) - 127 - 14 : 0;
+          // times 2^-e, in two factors since -e may exceed an exponent's range
+          f1 = __uint_as_float(static_cast<uint32_t>(127 - e / 2) << 23);
+          f2 = __uint_as_float(static_cast<uint32_t>(127 - (e - e / 2)) << 23);
+          row_scale = ldexpf(a.scale_log2, e);
         }
-        tmem_wait_st();
+        auto f16 = [&](uint32_t x) {
+          if constexpr (F4)
+            return pack_f16x2(__uint_as_float(x << 16) * f1 * f2, __uint_as_float(x & 0xffff0000u) * f1 * f2);
+          else
+            return bf16x2_to_f16x2(x);
+        };
+        if (grp == 0) {
+#pragma unroll
+          for (int qc = 0; qc < 4; ++qc) {  // 32 d = 16 columns per step
+            uint32_t w[16];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint4 x = v[qc * 4 + c];
+              w[4 * c] = f16(x.x);
+              w[4 * c + 1] = f16(x.y);
+              w[4 * c + 2] = f16(x.z);
+              w[4 * c + 3] = f16(x.w);
+            }
+            tmem_st16(lane_base + kWColQ + qc * 16, w);
+          }
+          tmem_wait_st();
+        }
       }
     }
     // (or from the staging buffer the producers filled)
@@ -885,8 +993,9 @@ __global__ void __launch_bounds__(WCfg<F8>::kThreads, 1)
       // any other scale scales them here (s_fma = 1).
       const int tile0 = it.t_begin + j * kWTok;
       const int tok0 = tile0 + kh * kKeys;  // this thread's first key
-      const bool raw = a.scale_log2 > 0.f;
-      const float s_fma = raw ? a.scale_log2 : 1.f;
+      const float sc = F4 ? row_scale : a.scale_log2;
+      const bool raw = sc > 0.f;
+      const float s_fma = raw ? sc : 1.f;
       float mt = -INFINITY;
       if (raw) {
         if (tok0 + kKeys <= lim) {
@@ -900,12 +1009,12 @@ __global__ void __launch_bounds__(WCfg<F8>::kThreads, 1)
             mt = fmax3(mt, x[i], x[i + 1]);
           }
         }
-        mt *= a.scale_log2;
+        mt *= sc;
       } else {
 #pragma unroll
         for (int i = 0; i < kKeys; i += 2) {
-          x[i] = tok0 + i < lim ? x[i] * a.scale_log2 : -INFINITY;
-          x[i + 1] = tok0 + i + 1 < lim ? x[i + 1] * a.scale_log2 : -INFINITY;
+          x[i] = tok0 + i < lim ? x[i] * sc : -INFINITY;
+          x[i + 1] = tok0 + i + 1 < lim ? x[i + 1] * sc : -INFINITY;
           mt = fmax3(mt, x[i], x[i + 1]);
         }
       }
@@ -918,7 +1027,8 @@ __global__ void __launch_bounds__(WCfg<F8>::kThreads, 1)
       uint32_t pk[kKeys / 2];
       float2 ps = make_float2(0.f, 0.f), qs = make_float2(0.f, 0.f);
       const float2 s2 = make_float2(s_fma, s_fma);
-      const float2 nm2 = make_float2(-mref, -mref);
+      const float nm = F4 ? kWF4Shift - mref : -mref;
+      const float2 nm2 = make_float2(nm, nm);
 #pragma unroll
       for (int i = 0; i < kKeys; i += 2) {
         const float2 e = __ffma2_rn(make_float2(x[i], x[i + 1]), s2, nm2);
@@ -1114,7 +1224,7 @@ __global__ void __launch_bounds__(WCfg<F8>::kThreads, 1)
       }
     }
     if (grp == 0 && kh == 0 && row < a.rows) {
-      const float lse = Lt > 0.f ? (Mu + log2f(Lt)) * kLn2w : -INFINITY;
+      const float lse = Lt > 0.f ? (Mu - (F4 ? kWF4Shift : 0.f) + log2f(Lt)) * kLn2w : -INFINITY;
       if (direct)
         a.lse[prow] = lse;
       else
@@ -1130,36 +1240,35 @@ __global__ void __launch_bounds__(WCfg<F8>::kThreads, 1)
 }
 
 std::mutex g_wide_mu;
-bool g_wide_attr[2][64];
+bool g_wide_attr[3][64];
 int g_wide_sms[64];
 
-template <bool F8>
+template <int KV>
 cudaError_t ensure_wide_attrs(int* sms) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lk(g_wide_mu);
-  if (!g_wide_attr[F8][dev]) {
-    e = cudaFuncSetAttribute(wide_kernel<F8, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             WCfg<F8>::kSmemBytes);
+  if (!g_wide_attr[KV][dev]) {
+    e = cudaFuncSetAttribute(wide_kernel<KV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             WCfg<KV>::kSmemBytes);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(wide_kernel<F8, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             WCfg<F8>::kSmemBytes);
+    e = cudaFuncSetAttribute(wide_kernel<KV, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             WCfg<KV>::kSmemBytes);
     if (e != cudaSuccess) return e;
     e = cudaDeviceGetAttribute(&g_wide_sms[dev], cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    g_wide_attr[F8][dev] = true;
+    g_wide_attr[KV][dev] = true;
   }
   if (sms != nullptr) *sms = g_wide_sms[dev];
   return cudaSuccess;
 }
 
-template <bool F8>
-cudaError_t launch_wide_t(const CUtensorMap& k_map, const CUtensorMap& v_map, const SplitArgs& a,
-                          cudaStream_t stream) {
+template <int KV>
+cudaError_t launch_wide_t(const WMaps<KV>& maps, const SplitArgs& a, cudaStream_t stream) {
   int sms = 0;
-  cudaError_t e = ensure_wide_attrs<F8>(&sms);
+  cudaError_t e = ensure_wide_attrs<KV>(&sms);
   if (e != cudaSuccess) return e;
   SplitArgs pa = a;
   // (a length per kv head: one CTA per item, the schedule is by request)
@@ -1174,8 +1283,8 @@ cudaError_t launch_wide_t(const CUtensorMap& k_map, const CUtensorMap& v_map, co
                                : static_cast<int64_t>(a.num_splits) * a.num_kv_heads * a.batch;
   cfg.gridDim = pa.persistent ? dim3(static_cast<unsigned>(std::min<int64_t>(sms, items)))
                               : dim3(a.num_splits, a.num_kv_heads, a.batch);
-  cfg.blockDim = dim3(WCfg<F8>::kThreads);
-  cfg.dynamicSmemBytes = WCfg<F8>::kSmemBytes;
+  cfg.blockDim = dim3(WCfg<KV>::kThreads);
+  cfg.dynamicSmemBytes = WCfg<KV>::kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1183,30 +1292,35 @@ cudaError_t launch_wide_t(const CUtensorMap& k_map, const CUtensorMap& v_map, co
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   // up to 64 query rows: the key-split form
-  return a.rows <= kWRows / 2 ? cudaLaunchKernelEx(&cfg, wide_kernel<F8, true>, k_map, v_map, pa)
-                              : cudaLaunchKernelEx(&cfg, wide_kernel<F8, false>, k_map, v_map, pa);
+  return a.rows <= kWRows / 2 ? cudaLaunchKernelEx(&cfg, wide_kernel<KV, true>, maps, pa)
+                              : cudaLaunchKernelEx(&cfg, wide_kernel<KV, false>, maps, pa);
 }
 
 }  // namespace
 
 cudaError_t launch_wide(const CUtensorMap& k_map, const CUtensorMap& v_map, const SplitArgs& a,
                         cudaStream_t stream) {
-  return a.kv_fp8 ? launch_wide_t<true>(k_map, v_map, a, stream)
-                  : launch_wide_t<false>(k_map, v_map, a, stream);
+  return a.kv_fp8 ? launch_wide_t<DA_CACHE_FP8_E4M3>({k_map, v_map}, a, stream)
+                  : launch_wide_t<DA_CACHE_BF16>({k_map, v_map}, a, stream);
+}
+
+cudaError_t launch_wide_fp4(const Fp4Maps& maps, const SplitArgs& a, cudaStream_t stream) {
+  return launch_wide_t<DA_CACHE_FP4_E2M1>({maps}, a, stream);
 }
 
 int wide_ctas_per_sm() {
   static int cached[64];  // per device, queried once
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-  if (ensure_wide_attrs<false>(nullptr) != cudaSuccess) return 1;
+  if (ensure_wide_attrs<DA_CACHE_BF16>(nullptr) != cudaSuccess) return 1;
   {
     std::lock_guard<std::mutex> lk(g_wide_mu);
     if (cached[dev] > 0) return cached[dev];
   }
   int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, wide_kernel<false, false>, WCfg<false>::kThreads,
-                                                    WCfg<false>::kSmemBytes) != cudaSuccess ||
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, wide_kernel<DA_CACHE_BF16, false>,
+                                                    WCfg<DA_CACHE_BF16>::kThreads,
+                                                    WCfg<DA_CACHE_BF16>::kSmemBytes) != cudaSuccess ||
       n < 1)
     return 1;
   std::lock_guard<std::mutex> lk(g_wide_mu);
