@@ -3,14 +3,15 @@
 // score_kernel: for 16 pages x the query rows of a KV head the bound
 //     sum_d min(q'_d, 0) min_d + max(q'_d, 0) max_d = [min(q', 0); max(q', 0)] . [min; max]
 // is one matrix product over 256 channels.  q' and the digests are whole
-// numbers of at most 7 bits, exact in f16, and every partial sum stays below
-// 2^22, exact in the fp32 accumulators: mma.sync computes the same integers
-// whatever its order of summation.  The digests are 1 / 16 to 1 / 256 of the
-// keys' bytes (2 x 128 of them per page); a lane loads its fragments from
-// global memory, 32 contiguous bytes of a page at a time, with no staging:
-// the channel order of a step is permuted alike in q' and digest.  The loads of
-// a warp's next 16 pages, and the page ids of those after, are in flight while
-// it multiplies.
+// numbers of at most 7 and 8 bits, exact in f16, and every partial sum stays
+// below 2^22 units, exact in the fp32 accumulators: mma.sync computes the same
+// integers whatever its order of summation.  The digests are 1 / 16 to 1 / 256
+// of the keys' bytes (2 x 128 of them per page).  The lanes of a page copy 64
+// contiguous bytes at a time into a ring in shared memory, a tile of 16 pages
+// ahead, from which each thread takes its own bytes as fragments: the channel
+// order of a step is permuted alike in q' and digest.  (72 MB of digests in
+// 20.4 us: 3.5 TB/s, 5 us of them launch and the chain length - page id - digest;
+// wider loads, deeper rings and the heads of a page in one CTA change nothing.)
 //
 // pick_kernel: per (token, KV head) the top_k of the scores.  Scores become
 // integers of the same order; forced pages the largest one.  The threshold,
@@ -18,9 +19,10 @@
 // the range of the scores (three counts per round, packed into one warp sum,
 // and one barrier), and one scan lists the pages above it, and the first of
 // those equal to it, in ascending order: exact, without atomics, and
-// independent of timing.  It is all latency, and the page ids of the list are
-// looked up side by side at the end (one after the other by the threads that
-// found them, they were most of 15 us).
+// independent of timing.  It is all latency: scores are loaded before
+// the length is known (rows of up to 8192 pages), and so are the page ids (up
+// to 2048); otherwise the ids of the list are looked up side by side at the end
+// (one after the other by the threads that found them, they were most of 15 us).
 
 #include "cache_kernels.cuh"
 #include "decode_attn.h"
@@ -42,12 +44,6 @@ __device__ __forceinline__ int clamp_len(const SelectArgs& a, int L) {
   return min(max(L, 0), a.g.max_seq_len);
 }
 
-__device__ __forceinline__ uint32_t hsub2(uint32_t x, uint32_t y) {
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
-  return r;
-}
-
 __device__ __forceinline__ uint32_t hmin2_0(uint32_t x) {
   uint32_t r;
   asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0u));
@@ -60,20 +56,45 @@ __device__ __forceinline__ uint32_t hmax2_0(uint32_t x) {
   return r;
 }
 
-// Four signed bytes to two f16x2: byte + 128 under the exponent of 1024, less 1152.
+// Four signed bytes x to two f16x2 of x + 128 in units of 2^-24: the byte as the
+// mantissa of a subnormal number, exact, and no arithmetic.  A row's products
+// then come out 128 sum(q') too high, which is taken off at the end.
 __device__ __forceinline__ void s8x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   const uint32_t u = w ^ 0x80808080u;
-  constexpr uint32_t k1152 = 0x64806480u;
-  lo = hsub2(__byte_perm(u, 0x64646464u, 0x4140), k1152);
-  hi = hsub2(__byte_perm(u, 0x64646464u, 0x4342), k1152);
+  lo = __byte_perm(u, 0u, 0x4140);
+  hi = __byte_perm(u, 0u, 0x4342);
+}
+constexpr float kUnits = 16777216.f;
+
+// 16 (4) bytes to shared memory, past L1 (asynchronously; each thread waits for its own)
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 constexpr int kScoreWarps = 4;
-constexpr int kScoreCtas = 8;  // per SM (2 to 8 within 2% of each other, 12 to 32 up to 15% slower)
+// Tiles of a warp's ring (72 MB of digests, 32 ragged requests: 2 tiles 20.4 us,
+// 3 22.4, 4 26.7; registers in the place of a ring 21.1)
+constexpr int kScoreStages = 2;
+constexpr int kScoreStageBytes = 8 * 32 * 16 + 2 * 32 * 4;  // a tile's digests and scales
+constexpr int kScoreCtas = 4;  // per SM (2 to 8 within 6% of each other, 12 to 32 up to 15% slower)
 
 // Dynamic shared memory: q' fragments [row tiles][4 step pairs][32 lanes] of
-// 16 B, the rows' a / 127, then (several tokens) each warp's row scores
-// [rows][16 pages].  NT: an upper bound of the row tiles.
+// 16 B, the rows' a / 127 and 128 sum(q'), then (several tokens) each warp's row
+// scores [rows][16 pages], then each warp's ring of tiles, in which a thread
+// keeps the very bytes that it reads again ([8][32 lanes] of 16 B, [2][32] of
+// 4 B).  NT: an upper bound of the row tiles; a single one is
+// prepared by every warp for itself, in registers.
 template <int NT>
 __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -89,8 +110,8 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectArg
   const int rows = group * T;
   const int tiles = (rows + 7) / 8;
   uint4* q_frag = reinterpret_cast<uint4*>(smem);
-  float* q_scale = reinterpret_cast<float*>(smem + tiles * 2048);
-  float* row_score = q_scale + tiles * 8 + warp * tiles * 8 * 16;
+  float2* q_scale = reinterpret_cast<float2*>(smem + tiles * 2048);
+  float* row_score = reinterpret_cast<float*>(q_scale + tiles * 8) + warp * tiles * 8 * 16;
   allow_dependent_launch();  // (whatever follows waits for this grid all the same)
   grid_dependency_wait();
 
@@ -100,48 +121,56 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectArg
   if (nb <= a.top_k || static_cast<int>(blockIdx.y) * kScoreWarps * 16 >= nb) return;
 
   // ---- the digests of pages tile * 16 + g4 and + 8, minima then maxima, as
-  // loaded; and the page ids of the tile after
+  // loaded, kScoreStages - 1 tiles ahead; and the page ids of the tile after
   const int32_t* bt = a.g.block_table + static_cast<int64_t>(b) * a.g.bt_stride;
   const int tile_step = gridDim.y * kScoreWarps;
   int tile = blockIdx.y * kScoreWarps + warp;
+  const uint8_t* ring =
+      smem + tiles * (2048 + 64) + (T > 1 ? kScoreWarps * tiles * 512 : 0) + warp * kScoreStages * kScoreStageBytes;
+  const uint32_t ring_at = smem_addr(ring) + lane * 16;
+  const uint32_t ring_scale = smem_addr(ring) + 4096 + lane * 4;
   auto ids = [&](int t, int (&pg)[2]) {
 #pragma unroll
     for (int p = 0; p < 2; ++p) pg[p] = __ldg(bt + min(t * 16 + g4 + 8 * p, nb - 1));
   };
-  int pg[2];
-  uint4 raw[2][4];
-  float ds[2];
-  auto load = [&]() {
+  auto load = [&](int slot, const int (&pg)[2]) {
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       const int id = pg[p] < 0 || pg[p] >= a.g.num_pages ? 0 : pg[p];  // (reported by pick_kernel)
       const int64_t at = static_cast<int64_t>(id) * a.g.num_kv_heads + kvh;
-      ds[p] = __ldg(a.digest_scale + at);
-      const uint4* src = reinterpret_cast<const uint4*>(a.digest + at * 256 + 32 * t4);
-      raw[p][0] = __ldg(src);
-      raw[p][1] = __ldg(src + 1);
-      raw[p][2] = __ldg(src + 8);
-      raw[p][3] = __ldg(src + 9);
+      const int8_t* src = a.digest + at * 256 + 16 * t4;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) copy16(ring_at + slot * kScoreStageBytes + (p * 4 + i) * 512, src + 64 * i);
+      copy4(ring_scale + slot * kScoreStageBytes + p * 128, a.digest_scale + at);
     }
   };
+  int pg[2];
   if (tile * 16 < nb) {
-    ids(tile, pg);
-    load();
-    ids(tile + tile_step, pg);
+    int first[kScoreStages - 1][2];
+#pragma unroll
+    for (int i = 0; i < kScoreStages - 1; ++i) ids(tile + i * tile_step, first[i]);
+    ids(tile + (kScoreStages - 1) * tile_step, pg);
+#pragma unroll
+    for (int i = 0; i < kScoreStages - 1; ++i) {
+      if ((tile + i * tile_step) * 16 < nb) load(i, first[i]);
+      copies_end();
+    }
   }
 
-  // ---- q' of the rows, one warp per row tile
-  for (int nt = warp; nt < tiles; nt += kScoreWarps) {
+  // ---- q' of the rows, one warp per row tile (or the only one, by each warp)
+  uint4 q_own[NT == 1 ? 4 : 1];
+  float2 own_scale[NT == 1 ? 2 : 1];  // of rows 2 t4 and 2 t4 + 1
+  for (int nt = NT == 1 ? 0 : warp; nt < tiles; nt += kScoreWarps) {
     const int r = nt * 8 + g4;
     uint32_t w[16];
     if (r < rows) {
       const int t = r / group;
       const uint4* src = reinterpret_cast<const uint4*>(
           a.q + static_cast<int64_t>(b) * a.q_sb + static_cast<int64_t>(t) * a.q_st +
-          static_cast<int64_t>(kvh * group + (r - t * group)) * a.q_sh + 32 * t4);
+          static_cast<int64_t>(kvh * group + (r - t * group)) * a.q_sh + 16 * t4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint4 x = src[i];
+        const uint4 x = src[(i & 1) + 8 * (i >> 1)];
         w[4 * i] = x.x;
         w[4 * i + 1] = x.y;
         w[4 * i + 2] = x.z;
@@ -163,42 +192,64 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectArg
     top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
     const float inv = top > 0.f ? __fdiv_rn(127.f, top) : 0.f;
     uint32_t h[16];
+    float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float u = fminf(fmaxf(rintf(__fmul_rn(x[2 * i], inv)), -127.f), 127.f);
       const float v = fminf(fmaxf(rintf(__fmul_rn(x[2 * i + 1], inv)), -127.f), 127.f);
       h[i] = pack_f16x2(u, v);
+      sum += u + v;
     }
+    sum += __shfl_xor_sync(kFull, sum, 1);
+    sum += __shfl_xor_sync(kFull, sum, 2);
+    const float2 qs = make_float2(__fdiv_rn(top, 127.f), 128.f * sum);
+    if constexpr (NT == 1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      q_frag[(nt * 4 + i) * 32 + lane] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
-    if (t4 == 0) q_scale[r] = __fdiv_rn(top, 127.f);
+      for (int i = 0; i < 4; ++i) q_own[i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+#pragma unroll
+      for (int rr = 0; rr < 2; ++rr) {
+        own_scale[rr].x = __shfl_sync(kFull, qs.x, (2 * t4 + rr) * 4);
+        own_scale[rr].y = __shfl_sync(kFull, qs.y, (2 * t4 + rr) * 4);
+      }
+      break;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        q_frag[(nt * 4 + i) * 32 + lane] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+      if (t4 == 0) q_scale[r] = qs;
+    }
   }
-  __syncthreads();
+  if constexpr (NT > 1) __syncthreads();
 
+  int slot = 0;
   for (; tile * 16 < nb; tile += tile_step) {
+    copies_wait<kScoreStages - 2>();
     uint32_t w[2][16];
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        w[p][4 * i] = raw[p][i].x;
-        w[p][4 * i + 1] = raw[p][i].y;
-        w[p][4 * i + 2] = raw[p][i].z;
-        w[p][4 * i + 3] = raw[p][i].w;
+        const uint4 raw =
+            *reinterpret_cast<const uint4*>(ring + slot * kScoreStageBytes + (p * 4 + i) * 512 + lane * 16);
+        w[p][4 * i] = raw.x;
+        w[p][4 * i + 1] = raw.y;
+        w[p][4 * i + 2] = raw.z;
+        w[p][4 * i + 3] = raw.w;
       }
-    const float ds0 = ds[0], ds1 = ds[1];
-    if ((tile + tile_step) * 16 < nb) {
-      load();
-      ids(tile + 2 * tile_step, pg);
-    }
+    const float* ds = reinterpret_cast<const float*>(ring + slot * kScoreStageBytes + 4096) + lane;
+    const float ds0 = ds[0], ds1 = ds[32];
+    // (the slot before this one was read a step ago)
+    if ((tile + (kScoreStages - 1) * tile_step) * 16 < nb) load(slot == 0 ? kScoreStages - 1 : slot - 1, pg);
+    copies_end();
+    ids(tile + kScoreStages * tile_step, pg);
+    slot = slot + 1 == kScoreStages ? 0 : slot + 1;
     float acc[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {  // step pairs: channels 32 t4 + 8 i ..
+    for (int i = 0; i < 4; ++i) {  // step pairs: channels 64 (i / 2) + 16 t4 + 8 (i % 2) ..
       uint32_t af[4][4];           // minima of the two steps, maxima of the two
 #pragma unroll
       for (int k = 0; k < 4; ++k)
@@ -208,7 +259,9 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectArg
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if (nt < tiles) {
-          const uint4 q = q_frag[(nt * 4 + i) * 32 + lane];
+          uint4 q;
+          if constexpr (NT == 1) q = q_own[i];
+          else q = q_frag[(nt * 4 + i) * 32 + lane];
           mma_f16_16816(acc[nt], af[0], hmin2_0(q.x), hmin2_0(q.y));
           mma_f16_16816(acc[nt], af[1], hmin2_0(q.z), hmin2_0(q.w));
           mma_f16_16816(acc[nt], af[2], hmax2_0(q.x), hmax2_0(q.y));
@@ -223,9 +276,11 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectArg
       for (int rr = 0; rr < 2; ++rr) {
         const int row = nt * 8 + 2 * t4 + rr;
         if (row < rows) {
-          const float qs = q_scale[row];
-          const float u = __fmul_rn(__fmul_rn(acc[nt][rr], ds0), qs);
-          const float v = __fmul_rn(__fmul_rn(acc[nt][2 + rr], ds1), qs);
+          float2 qs;
+          if constexpr (NT == 1) qs = own_scale[rr];
+          else qs = q_scale[row];
+          const float u = __fmul_rn(__fmul_rn(fmaf(acc[nt][rr], kUnits, -qs.y), ds0), qs.x);
+          const float v = __fmul_rn(__fmul_rn(fmaf(acc[nt][2 + rr], kUnits, -qs.y), ds1), qs.x);
           if (T == 1) {
             best[0] = fmaxf(best[0], u);
             best[1] = fmaxf(best[1], v);
@@ -277,7 +332,8 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectArgs a) {
   __shared__ uint32_t sh[2][kWarps];
   __shared__ uint32_t sh3[2][kWarps];
   __shared__ uint32_t scan[2][kWarps];
-  __shared__ int list[kMaxTopK];           // the selected pages' places
+  constexpr bool kIds = ONE && kPer <= 8;    // page ids in registers, too (16 of them cost more than the look-up)
+  __shared__ int list[kIds ? 1 : kMaxTopK];  // else the selected pages' places
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int64_t row = blockIdx.x;  // (b, t, kv head)
@@ -288,6 +344,24 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectArgs a) {
   // (no early launch of what follows: the attention's CTAs would settle around
   // this grid's and stay unevenly spread, 52 -> 73 us on 8 requests x 3 tokens)
   grid_dependency_wait();
+  const int K = a.top_k;
+  const int32_t* bt = a.g.block_table + static_cast<int64_t>(b) * a.g.bt_stride;
+  const float* sc = a.scores + row * a.score_stride;
+  // ONE: this thread's scores and page ids are on their way before the length is known
+  const int e_first = threadIdx.x * kPer;
+  float4 x_all[ONE ? kPer / 4 : 1];
+  int ids[kIds ? kPer : 1];
+  if constexpr (ONE) {
+#pragma unroll
+    for (int v = 0; v < kPer / 4; ++v) {
+      x_all[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (a.max_blocks > K && e_first + 4 * v < a.max_blocks) x_all[v] = *reinterpret_cast<const float4*>(sc + e_first + 4 * v);
+    }
+  }
+  if constexpr (kIds) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) ids[i] = a.max_blocks > K && e_first + i < a.max_blocks ? __ldg(bt + e_first + i) : 0;
+  }
   const int raw = a.g.seq_lens[b];
   const int L = clamp_len(a, raw);
   uint32_t bad = raw != L ? DA_STATUS_SEQ_LEN : 0;
@@ -297,13 +371,10 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectArgs a) {
   const int Lt = seen_tokens(a, L, t);
   const int ps = a.g.page_size;
   const int count = (Lt + ps - 1) / ps;
-  const int K = a.top_k;
   const int n_sel = min(count, K);
-  const int32_t* bt = a.g.block_table + static_cast<int64_t>(b) * a.g.bt_stride;
   int32_t* pages = a.pages + row * K;
   int32_t* blocks = a.blocks != nullptr ? a.blocks + row * K : nullptr;
-  auto put = [&](int at, int col) {
-    int pg = bt[col];
+  auto put = [&](int at, int col, int pg) {
     if (pg < 0 || pg >= a.g.num_pages) {
       if (a.g.status != nullptr) atomicOr(a.g.status, static_cast<int32_t>(DA_STATUS_BAD_PAGE));
       pg = 0;
@@ -317,18 +388,18 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectArgs a) {
   }
   if (threadIdx.x == 0) a.tokens[row] = count > 0 ? (n_sel - 1) * ps + (Lt - (count - 1) * ps) : 0;
   if (count <= K) {
-    for (int i = threadIdx.x; i < count; i += THREADS) put(i, i);
+    for (int i = threadIdx.x; i < count; i += THREADS) put(i, i, bt[i]);
     return;
   }
 
-  const float* sc = a.scores + row * a.score_stride;
   const int local0 = count - a.local;  // (top_k >= sink + local, so local0 > sink here)
   auto load = [&](int c0, uint32_t (&key)[kPer]) {
     const int e0 = c0 + threadIdx.x * kPer;
 #pragma unroll
     for (int v = 0; v < kPer / 4; ++v) {
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (e0 + 4 * v < count) x = *reinterpret_cast<const float4*>(sc + e0 + 4 * v);
+      if constexpr (ONE) x = x_all[v];
+      else if (e0 + 4 * v < count) x = *reinterpret_cast<const float4*>(sc + e0 + 4 * v);
       key[4 * v] = ordered(x.x);
       key[4 * v + 1] = ordered(x.y);
       key[4 * v + 2] = ordered(x.z);
@@ -494,13 +565,18 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectArgs a) {
     for (int i = 0; i < kPer; ++i) {
       const bool up = key[i] > above;
       const bool same = take != 0 && key[i] == above && bq < take;
-      if (up || same) list[bg + min(bq, take)] = e0 + i;
+      if (up || same) {
+        const int at = static_cast<int>(bg + min(bq, take));
+        if constexpr (kIds) put(at, e0 + i, ids[i]);
+        else list[at] = e0 + i;
+      }
       bg += up;
       bq += take != 0 && key[i] == above;
     }
-    __syncthreads();  // (scan[] is written again; the list is complete)
+    if constexpr (!kIds) __syncthreads();  // (scan[] is written again; the list is complete)
   }
-  for (int i = threadIdx.x; i < K; i += THREADS) put(i, list[i]);
+  if constexpr (!kIds)
+    for (int i = threadIdx.x; i < K; i += THREADS) put(i, list[i], bt[list[i]]);
 }
 
 template <class Kernel, class Args>
@@ -526,8 +602,9 @@ cudaError_t launch_select(const SelectArgs& a, int sm_count, cudaStream_t stream
   if (a.max_blocks > a.top_k) {
     const int q_rows = a.num_q_heads / a.g.num_kv_heads * a.g.q_len;
     const int tiles = (q_rows + 7) / 8;
-    const size_t smem = static_cast<size_t>(tiles) * 2048 + tiles * 32 +
-                        (a.g.q_len > 1 ? static_cast<size_t>(kScoreWarps) * tiles * 512 : 0);
+    const size_t smem = static_cast<size_t>(tiles) * 2048 + tiles * 64 +
+                        (a.g.q_len > 1 ? static_cast<size_t>(kScoreWarps) * tiles * 512 : 0) +
+                        kScoreWarps * kScoreStages * kScoreStageBytes;
     auto* kernel = tiles == 1 ? score_kernel<1> : tiles <= 4 ? score_kernel<4> : score_kernel<16>;
     if (smem > 48 * 1024) {
       const cudaError_t e =
