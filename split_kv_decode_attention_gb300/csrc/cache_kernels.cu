@@ -104,9 +104,10 @@ __global__ void __launch_bounds__(kTableThreads)
 // one token, eight heads a pass: passes over q's heads, then k's, then v's, each
 // a pointer that steps on.  A thread keeps the cos / sin of its 8 values in
 // registers for all of them, so the table is read once per CTA and row of
-// threads, and the pair partners of the half layout come by one shuffle (a
+// threads, and the pair partners of the half layout come by shuffles (a
 // thread's 8 values and their partners lie rotary_dim / 2 apart, whole threads
-// when that is a multiple of 8; other sizes read the partner from memory).
+// when that is a multiple of 8, halves of them when it is one of 4; other sizes
+// read the partner from memory).
 // The first passes' rows are on their way before the token's place is known.
 // Instructions bound it as much as HBM does, so values go in pairs (mul /
 // add.f32x2).
@@ -221,9 +222,13 @@ __device__ __forceinline__ void store_row(uint8_t* row, uint8_t* sf_row, int d16
   }
 }
 
-// VEC: rotary_dim is a multiple of 16 (table and partners in whole vectors).
-template <bool VEC, int TYPE>
+// ALIGN: the largest of 16, 8 and 2 that divides rotary_dim.  At 16 partners
+// are whole threads' values; at 8 (72, say) halves of two threads' values, and
+// table rows whole vectors all the same; else both are read value by value
+// (8192 tokens, 32 / 8 heads, FP8, rotary_dim 72: 70 us that way, 40 in halves).
+template <int ALIGN, int TYPE>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
+  constexpr bool VEC = ALIGN >= 8;
   const int d16 = threadIdx.x & 15;
   const int sub = threadIdx.x >> 4;
   const int lane = threadIdx.x & 31;
@@ -316,12 +321,13 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
           s[i] = pair(-s4[i], s4[i]);
         }
       } else {
-        const int f0 = d0 < half ? d0 : d0 - half;
-        const float sign = d0 < half ? -1.f : 1.f;
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const float4 cc = *reinterpret_cast<const float4*>(row + f0 + 4 * v);
-          const float4 ss = *reinterpret_cast<const float4*>(row + half + f0 + 4 * v);
+        for (int v = 0; v < 2; ++v) {  // (half a multiple of 4: four values are on one side)
+          const int d = d0 + 4 * v;
+          const int f0 = d < half ? d : d - half;
+          const float sign = d < half ? -1.f : 1.f;
+          const float4 cc = *reinterpret_cast<const float4*>(row + f0);
+          const float4 ss = *reinterpret_cast<const float4*>(row + half + f0);
           c[2 * v] = pair(cc.x, cc.y);
           c[2 * v + 1] = pair(cc.z, cc.w);
           s[2 * v] = pair(sign * ss.x, sign * ss.y);
@@ -346,8 +352,14 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
       s[i] = pair(ss[0], ss[1]);
     }
   }
-  // the lane that holds the partners of this thread's values (half layout)
-  const int peer = (lane & 16) | ((d16 + (d0 < half ? (half >> 3) : -(half >> 3))) & 15);
+  // the lanes that hold the partners of this thread's first and last four values
+  // (half layout; ALIGN 8: in the other half of their words)
+  int peer[2];
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    const int d = d0 + 4 * v;
+    peer[v] = (lane & 16) | (((d < half ? d + half : d - half) >> 3) & 15);
+  }
 
   // the rotated values of a row: every product and the sum rounded, the
   // definition, and the same bytes for a token wherever it is computed again
@@ -360,7 +372,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
       for (int i = 0; i < 4; ++i) p[i] = widen(__byte_perm(x[i], 0, 0x1032));
     } else if constexpr (VEC) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = widen(__shfl_sync(kFull, x[i], peer));
+      for (int i = 0; i < 4; ++i) p[i] = widen(__shfl_sync(kFull, x[ALIGN == 8 ? (i + 2) & 3 : i], peer[i >> 1]));
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -660,12 +672,12 @@ cudaError_t launch_rope_table(const double* inv_freq, int num_freqs, int64_t fir
               : launch(rope_table_kernel<1>, grid, kTableThreads, 0, stream, inv_freq, num_freqs, first, count, amp, table);
 }
 
-template <bool VEC>
-static cudaError_t launch_append_vec(const AppendArgs& a, dim3 grid, cudaStream_t stream) {
+template <int ALIGN>
+static cudaError_t launch_append_type(const AppendArgs& a, dim3 grid, cudaStream_t stream) {
   switch (a.c.type) {
-    case DA_CACHE_BF16: return launch(append_kernel<VEC, DA_CACHE_BF16>, grid, kAppendThreads, 0, stream, a);
-    case DA_CACHE_FP8_E4M3: return launch(append_kernel<VEC, DA_CACHE_FP8_E4M3>, grid, kAppendThreads, 0, stream, a);
-    default: return launch(append_kernel<VEC, DA_CACHE_FP4_E2M1>, grid, kAppendThreads, 0, stream, a);
+    case DA_CACHE_BF16: return launch(append_kernel<ALIGN, DA_CACHE_BF16>, grid, kAppendThreads, 0, stream, a);
+    case DA_CACHE_FP8_E4M3: return launch(append_kernel<ALIGN, DA_CACHE_FP8_E4M3>, grid, kAppendThreads, 0, stream, a);
+    default: return launch(append_kernel<ALIGN, DA_CACHE_FP4_E2M1>, grid, kAppendThreads, 0, stream, a);
   }
 }
 
@@ -677,8 +689,9 @@ cudaError_t launch_append(const AppendArgs& a, int sm_count, cudaStream_t stream
   // few tokens: spread a token's passes over CTAs until about four per SM exist
   const int64_t want = (4 * static_cast<int64_t>(sm_count) + tokens - 1) / tokens;
   const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>(want < passes ? want : passes));
-  return a.rotary_dim % 16 == 0 ? launch_append_vec<true>(a, grid, stream)
-                                : launch_append_vec<false>(a, grid, stream);
+  return a.rotary_dim % 16 == 0  ? launch_append_type<16>(a, grid, stream)
+         : a.rotary_dim % 8 == 0 ? launch_append_type<8>(a, grid, stream)
+                                 : launch_append_type<2>(a, grid, stream);
 }
 
 cudaError_t launch_digest(const DigestArgs& a, int sm_count, cudaStream_t stream) {

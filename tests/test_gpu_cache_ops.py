@@ -196,7 +196,7 @@ def check_append(da, kind, page, lens, T, hq, hkv, rot, interleaved, seed, new_l
 
 
 @pytest.mark.parametrize("interleaved", [False, True], ids=["halves", "pairs"])
-@pytest.mark.parametrize("rot", [0, 2, 16, 24, 72, 96, 128])
+@pytest.mark.parametrize("rot", [0, 2, 8, 16, 20, 24, 72, 96, 120, 126, 128])
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
 def test_append_one_token(da, kind, rot, interleaved):
     assert check_append(da, kind, 16, [1, 17, 40, 16], 1, 4, 2, rot, interleaved, 5) == 0
@@ -211,7 +211,7 @@ def test_append_shapes(da, kind, page, hq, hkv, T, lens):
     assert check_append(da, kind, page, lens, T, hq, hkv, 128, True, 12 + T, fused=False) == 0
 
 
-@pytest.mark.parametrize("rot", [24, 128])
+@pytest.mark.parametrize("rot", [20, 24, 128])
 @pytest.mark.parametrize("kind", ["bf16", "fp4"])
 def test_append_in_place(da, kind, rot):
     assert check_append(da, kind, 16, [20, 33], 3, 6, 2, rot, False, 21, in_place=True) == 0
