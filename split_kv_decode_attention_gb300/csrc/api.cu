@@ -212,10 +212,10 @@ struct MapKey {
   const void* base;
   cuuint64_t dims[4], strides[3];
   cuuint32_t box;
-  int fp8;
+  int fp8, own_pages;
   bool operator==(const MapKey& o) const {
     return base == o.base && std::memcmp(dims, o.dims, sizeof(dims)) == 0 &&
-           std::memcmp(strides, o.strides, sizeof(strides)) == 0 && box == o.box && fp8 == o.fp8;
+           std::memcmp(strides, o.strides, sizeof(strides)) == 0 && box == o.box && fp8 == o.fp8 && own_pages == o.own_pages;
   }
 };
 constexpr int kMapCacheSize = 16;
@@ -228,18 +228,29 @@ struct {
 int g_map_next = 0;
 
 int encode_map(CUtensorMap* map, const void* base, CUtensorMapDataType type, const cuuint64_t (&dims)[4],
-               const cuuint64_t (&strides)[3], const cuuint32_t (&box)[4], CUtensorMapSwizzle swizzle) {
+               const cuuint64_t (&strides)[3], const cuuint32_t (&box)[4], CUtensorMapSwizzle swizzle,
+               CUtensorMapL2promotion promotion) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (enc == nullptr) return DA_ERR_CUDA;
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(map, type, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             swizzle, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? DA_OK
              : DA_ERR_ALIGNMENT;
 }
 
+// What L2 fetches beyond a box's rows is the neighbouring heads', which other
+// CTAs are about to read -- unless every head reads pages of its own: then no
+// more than a row (32 requests x 64 selected pages, FP8: 194 MB read for 134
+// with 256-byte fetches, and 38 us for 31).
+CUtensorMapL2promotion promotion_of(bool own_pages, int row_bytes) {
+  return !own_pages || row_bytes >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+         : row_bytes >= 128             ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                        : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
+}
+
 int make_kv_map(CUtensorMap* map, const void* base, const decode_attn_params* p, bool paged,
-                int box_tokens) {
+                int box_tokens, bool own_pages) {
   // dims, innermost first: d (128), kv head, token-in-group, group
   //   paged: group = physical page, token-in-group = slot in page
   //   contiguous: group = request, token-in-group = token position
@@ -263,6 +274,7 @@ int make_kv_map(CUtensorMap* map, const void* base, const decode_attn_params* p,
   std::memcpy(key.strides, strides, sizeof(strides));
   key.box = box[2];
   key.fp8 = kv_fp8(p) ? 1 : 0;
+  key.own_pages = own_pages ? 1 : 0;
   {
     std::lock_guard<std::mutex> lk(g_map_mu);
     for (auto& e : g_map_cache)
@@ -273,7 +285,7 @@ int make_kv_map(CUtensorMap* map, const void* base, const decode_attn_params* p,
   }
   const int rc =
       encode_map(map, base, kv_fp8(p) ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                 dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+                 dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, promotion_of(own_pages, kHeadDim * static_cast<int>(eb)));
   if (rc != DA_OK) return rc;
   std::lock_guard<std::mutex> lk(g_map_mu);
   auto& e = g_map_cache[g_map_next];
@@ -296,7 +308,7 @@ int fp4_box_halves(const decode_attn_params* p, bool paged, int unit) {
 // A map of a 4-bit cache: its values, or (scales) its block scales.  (Encoded
 // for every call: 36 ns.)
 int make_fp4_map(CUtensorMap* map, const void* base, const decode_attn_params* p,
-                 const decode_attn_cache* c, bool paged, int unit, bool scales) {
+                 const decode_attn_cache* c, bool paged, int unit, bool scales, bool own_pages) {
   const cuuint32_t tokens = static_cast<cuuint32_t>(16 * fp4_box_halves(p, paged, unit));
   const cuuint64_t slots = static_cast<cuuint64_t>(paged ? p->page_size : std::max(p->max_seq_len, 1));
   const cuuint64_t groups = static_cast<cuuint64_t>(paged ? p->num_pages : std::max(p->batch, 1));
@@ -307,14 +319,16 @@ int make_fp4_map(CUtensorMap* map, const void* base, const decode_attn_params* p
                                    static_cast<cuuint64_t>(c->bs_stride_page),
                                    static_cast<cuuint64_t>(c->bs_stride_page)};
     const cuuint32_t box[4] = {tokens, static_cast<cuuint32_t>(unit), 1, 1};
-    return encode_map(map, base, CU_TENSOR_MAP_DATA_TYPE_UINT64, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+    return encode_map(map, base, CU_TENSOR_MAP_DATA_TYPE_UINT64, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE,
+                      promotion_of(own_pages, static_cast<int>(8 * tokens)));
   }
   const cuuint64_t dims[4] = {kHeadDim / 2, heads, slots, groups};
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p->kv_stride_head),
                                  static_cast<cuuint64_t>(p->kv_stride_token),
                                  static_cast<cuuint64_t>(p->kv_stride_page)};
   const cuuint32_t box[4] = {kHeadDim / 2, static_cast<cuuint32_t>(unit), tokens, 1};
-  return encode_map(map, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B);
+  return encode_map(map, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B,
+                    promotion_of(own_pages, kHeadDim / 2));
 }
 
 bool stride_ok(int64_t s) { return s > 0 && s % 8 == 0 && s * 2 < (1LL << 40); }
@@ -617,16 +631,16 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
     std::memset(&maps4, 0, sizeof(maps4));
     if (!no_keys) {
       const decode_attn_cache* c = ext.fp4;
-      rc = make_fp4_map(&maps4.k, c->k, p, c, paged, unit, false);
-      if (rc == DA_OK) rc = make_fp4_map(&maps4.v, c->v, p, c, paged, unit, false);
-      if (rc == DA_OK) rc = make_fp4_map(&maps4.ks, c->k_block_scale, p, c, paged, unit, true);
-      if (rc == DA_OK) rc = make_fp4_map(&maps4.vs, c->v_block_scale, p, c, paged, unit, true);
+      rc = make_fp4_map(&maps4.k, c->k, p, c, paged, unit, false, ext.per_head);
+      if (rc == DA_OK) rc = make_fp4_map(&maps4.v, c->v, p, c, paged, unit, false, ext.per_head);
+      if (rc == DA_OK) rc = make_fp4_map(&maps4.ks, c->k_block_scale, p, c, paged, unit, true, ext.per_head);
+      if (rc == DA_OK) rc = make_fp4_map(&maps4.vs, c->v_block_scale, p, c, paged, unit, true, ext.per_head);
       if (rc != DA_OK) return rc;
     }
   } else if (!no_keys) {
-    rc = make_kv_map(&kmap, k_cache, p, paged, box_tokens);
+    rc = make_kv_map(&kmap, k_cache, p, paged, box_tokens, ext.per_head);
     if (rc != DA_OK) return rc;
-    rc = make_kv_map(&vmap, v_cache, p, paged, box_tokens);
+    rc = make_kv_map(&vmap, v_cache, p, paged, box_tokens, ext.per_head);
     if (rc != DA_OK) return rc;
   }
 

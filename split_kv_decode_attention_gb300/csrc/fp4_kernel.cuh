@@ -49,8 +49,16 @@
 // call is one launch and writes no partials (one request of 4096 tokens, 32 / 8
 // heads: 11 us replayed either way, but 7 and not 10 us of the host's time).
 // Slots behind a sequence may hold anything: their scores are masked and
-// their value scales replaced by zero.  More than 32 query
-// rows per KV head run on the tcgen05 kernel.
+// their value scales replaced by zero.  More than 32 query rows per KV head run
+// on the tcgen05 kernel.
+//
+// GB300, whole calls: 64 ragged requests of up to 32K tokens, 4 rows per head:
+// 254 us, 5.4 TB/s, 0.80 of a copy's rate.  32 requests of up to 16K, 16 rows:
+// 96 us, 3.5 TB/s, 0.52: there two consumer warps per scheduler (their 64
+// accumulators and the widened operands fill the registers) issue 0.5
+// instructions per cycle, the ALU and the tensor pipe each 39 % busy.  Twelve
+// consumer warps, CTAs that stay and take item after item, V loaded before the
+// softmax, and two to five stages were built and are slower or no faster.
 #pragma once
 
 #include <type_traits>

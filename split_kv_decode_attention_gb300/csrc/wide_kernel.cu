@@ -108,7 +108,7 @@ constexpr int kWStatBytes = 3200;
 constexpr int kWSchedInts = 4 * kWMaxSchedBatch + 4;
 static_assert(kWStatFloats * 4 <= kWStatBytes, "statistics buffer");
 
-// Warp roles and shared-memory layout of the two variants.
+// Warp roles and shared-memory layout of the variants.
 //   bf16 caches: warps 0-7 softmax, 8..12 TMA producers, 13 MMA; the TMA ring
 //     holds the MMA operands directly (5 stages of 32 KB).
 //   FP8 caches: warps 0-7 softmax, 8..10 TMA producers, 11..14 converters,
@@ -118,7 +118,19 @@ static_assert(kWStatFloats * 4 <= kWStatBytes, "statistics buffer");
 //     kind::f16 must be 16-bit).  A K slot is released as soon as its S =
 //     Q.K^T completes, a V slot only after its P.V, so the two rings hold
 //     each half only as long as it is needed.
-// Shared memory: TMA ring, K and V operand rings (FP8 only), Q staging (bf16
+//   4-bit caches (33..128 rows; fp4_kernel.cuh takes fewer): the FP8 variant's
+//     roles and operand rings over a ring of 6 stages of 9 KB: per 16 tokens a
+//     box of K, of V (64 bytes a token, 64-byte swizzle) and of both block
+//     scales, or one box for up to 64 tokens of a page.  A converter thread
+//     turns 16 bytes and two block scales into 32 f16 values (one cvt per byte,
+//     one multiply per two values).  The query rows are scaled by powers of two
+//     into f16's range, the scores back; P is 2^6 at a row's maximum, so that
+//     f16 keeps weights down to 2^-30 of it.  A 64-key tile takes 0.84 us of an
+//     SM as in the FP8 variant (tensor pipe 31 %, ALU 52 % busy, 1.3 TB/s; 16
+//     requests of 4 to 16K tokens, 8 heads: 64 rows 151 us, 128 rows 160 us,
+//     where groups of 32 rows on the warp-level kernel took 203 and 353).
+//     Two producers are 4 % slower, four 8 %, a third K slot changes nothing.
+// Shared memory: TMA ring, K and V operand rings (FP8 and 4-bit), Q staging (bf16
 // only: [128 rows][16 chunks of 16 B], chunk c of row r at c ^ (r & 15)), the
 // groups' merge statistics (two buffers), schedule tables, barriers.
 // TMA copies issued by one warp are serialised (~130-240 cycles per box), and
@@ -606,8 +618,8 @@ __global__ void __launch_bounds__(WCfg<KV>::kThreads, 1)
     return;
   }
 
-  // ======================================================= FP8 converters
-  // Widen each landed FP8 stage: its K tiles into the next K slot and its V
+  // ============================================== converters (FP8 and 4-bit)
+  // Widen each landed stage.  FP8: its K tiles into the next K slot and its V
   // tiles into the next V slot, each an f16 operand ([2 d-halves][64 tokens]
   // [64 d], 128-byte swizzle): 16-byte chunk c of FP8 row t (d = 16c ..
   // 16c+15) becomes 8-d chunks 2c and 2c+1 of d-half c / 4.  Each 8-lane
