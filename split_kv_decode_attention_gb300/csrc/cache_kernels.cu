@@ -229,7 +229,7 @@ __device__ __forceinline__ void store_row(uint8_t* row, uint8_t* sf_row, int d16
 // ALIGN: the largest of 16, 8 and 2 that divides rotary_dim.  At 16 partners
 // are whole threads' values; at 8 (72, say) halves of two threads' values, and
 // table rows whole vectors all the same; else both are read value by value
-// (8192 tokens, 32 / 8 heads, FP8, rotary_dim 72: 70 us that way, 40 in halves).
+// (8192 tokens, 32 / 8 heads, FP8, rotary_dim 72: 70 us that way, 41 in halves).
 template <int ALIGN, int TYPE>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
   constexpr bool VEC = ALIGN >= 8;
@@ -326,12 +326,12 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
         }
       } else {
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {  // (half a multiple of 4: four values are on one side)
-          const int d = d0 + 4 * v;
-          const int f0 = d < half ? d : d - half;
-          const float sign = d < half ? -1.f : 1.f;
-          const float4 cc = *reinterpret_cast<const float4*>(row + f0);
-          const float4 ss = *reinterpret_cast<const float4*>(row + half + f0);
+        for (int v = 0; v < 2; ++v) {  // (half a multiple of 4: four values are on one side; of 8: eight)
+          const bool first = (ALIGN == 8 ? d0 + 4 * v : d0) < half;
+          const int f0 = first ? d0 : d0 - half;
+          const float sign = first ? -1.f : 1.f;
+          const float4 cc = *reinterpret_cast<const float4*>(row + f0 + 4 * v);
+          const float4 ss = *reinterpret_cast<const float4*>(row + half + f0 + 4 * v);
           c[2 * v] = pair(cc.x, cc.y);
           c[2 * v + 1] = pair(cc.z, cc.w);
           s[2 * v] = pair(sign * ss.x, sign * ss.y);
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
   int peer[2];
 #pragma unroll
   for (int v = 0; v < 2; ++v) {
-    const int d = d0 + 4 * v;
+    const int d = ALIGN == 8 ? d0 + 4 * v : d0;
     peer[v] = (lane & 16) | (((d < half ? d + half : d - half) >> 3) & 15);
   }
 
