@@ -4,6 +4,8 @@
 // selection scores.  All of them stream their data once and are bound by HBM
 // at size and by launch latency in a decode step.
 
+#include <type_traits>
+
 #include "cache_kernels.cuh"
 #include "decode_attn.h"
 #include "kernels.cuh"
@@ -446,12 +448,12 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
 // to 32K tokens in 16-token bf16 pages: one page 205 us, four 137, eight 131);
 // the warps of a CTA take neighbouring heads, which a [page, slot, head, d]
 // cache holds side by side.  A lane loads 16 bytes of a row (8, 16 or 32
-// values; 2, 4 or 8 rows per load), a batch of loads at work and the next on
-// its way, and keeps packed 16-bit minima and maxima: bf16 as it is, FP8
-// and 4-bit values exactly in f16.  The rows' partial results meet in a
-// reduce-scatter (each step sends half of what is left): 4, 12 or 28 shuffles
-// per page, after which every lane holds 8 channels of the minimum or of the
-// maximum, whatever the type.  (16 ragged requests, 774 MB of bf16 keys: 126.8
+// values; 2, 4 or 8 rows per load; 8 bytes of FP8 and 4-bit pages of 16 tokens),
+// a batch of loads at work and the next on its way, and keeps packed 16-bit
+// minima and maxima: bf16 as it is, FP8 and 4-bit values exactly in f16.  The
+// rows' partial results meet in a reduce-scatter (each step sends half of what
+// is left): 4, 12 or 28 shuffles per page, after which every lane holds 8
+// channels of the minimum or of the maximum, whatever the type.  (16 ragged requests, 774 MB of bf16 keys: 126.8
 // us, 6.1 TB/s, 0.91 of a copy's rate; 4-bit keys, 50 requests of 3 to 8K tokens
 // in 32-token pages: 38 us, 2.2 TB/s, bound by the instructions of a page's end.)
 constexpr int kDigestWarps = 8;
@@ -474,20 +476,24 @@ __device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
   return r;
 }
 
-template <int TYPE>
+// SHORT: batches of 16 tokens and 8 bytes a lane, for 16-token pages (16 ragged
+// requests of up to 32K tokens: FP8 121 -> 99 us, 4-bit 144 -> 116; 48-token
+// pages are the same either way, 64-token ones 7 % faster with 16 bytes).
+template <int TYPE, bool SHORT>
 struct DigestCfg {
   static constexpr bool kBf = TYPE == DA_CACHE_BF16;
-  static constexpr int kLanes = kBf ? 16 : TYPE == DA_CACHE_FP8_E4M3 ? 8 : 4;  // of a row
-  static constexpr int kRows = 32 / kLanes;                                    // per load
-  static constexpr int kWords = 128 / kLanes / 2;                              // packed values of a lane
+  using Vec = std::conditional_t<kBf || !SHORT, uint4, uint2>;  // of a row, per lane
+  static constexpr int kLanes = (TYPE == DA_CACHE_FP4_E2M1 ? 64 : kBf ? 256 : 128) / sizeof(Vec);  // of a row
+  static constexpr int kRows = 32 / kLanes;                             // per load
+  static constexpr int kWords = 128 / kLanes / 2;                       // packed values of a lane
   // in flight (4-bit: 4, its minima and maxima fill the registers; 8 took 95 us
   // where 4 take 72, FP8 the other way round, 90 and 75)
   static constexpr int kLoads = TYPE == DA_CACHE_FP4_E2M1 ? 4 : 8;
 };
 
-template <int TYPE>
+template <int TYPE, bool SHORT>
 __global__ void __launch_bounds__(32 * kDigestWarps) digest_kernel(const DigestArgs a, int pages_per_warp) {
-  using C = DigestCfg<TYPE>;
+  using C = DigestCfg<TYPE, SHORT>;
   constexpr int NW = C::kWords;
   const int lane = threadIdx.x & 31;
   const int l = lane % C::kLanes, rg = lane / C::kLanes;
@@ -519,11 +525,12 @@ __global__ void __launch_bounds__(32 * kDigestWarps) digest_kernel(const DigestA
   }
   constexpr int kTokens = C::kLoads * C::kRows;             // of a batch
   const int parts = (ps + kTokens - 1) / kTokens;           // batches of a page
-  const uint8_t* kbase = a.c.k + static_cast<int64_t>(h) * a.c.head + l * 16;
-  const uint8_t* sbase = TYPE == DA_CACHE_FP4_E2M1 ? a.c.ks + static_cast<int64_t>(h) * a.c.sf_head + 2 * l : nullptr;
+  using Vec = typename C::Vec;
+  const uint8_t* kbase = a.c.k + static_cast<int64_t>(h) * a.c.head + l * sizeof(Vec);
+  const uint8_t* sbase = TYPE == DA_CACHE_FP4_E2M1 ? a.c.ks + static_cast<int64_t>(h) * a.c.sf_head + l * (SHORT ? 1 : 2) : nullptr;
   auto held = [&](int page) { return min(ps, L - (static_cast<int>(col0) + page) * ps); };  // tokens of a page
 
-  uint4 x[C::kLoads];
+  Vec x[C::kLoads];
   uint32_t sf[TYPE == DA_CACHE_FP4_E2M1 ? C::kLoads : 1];
   auto load = [&](int page, int part) {
     const int pg = __shfl_sync(kFull, id, page);
@@ -534,10 +541,13 @@ __global__ void __launch_bounds__(32 * kDigestWarps) digest_kernel(const DigestA
       const int row = part * kTokens + j * C::kRows;
       if (row > last || pg < 0) continue;                   // (uniform)
       const int tok = min(row + rg, last);                  // (the last token again: no effect)
-      x[j] = __ldg(reinterpret_cast<const uint4*>(p + static_cast<int64_t>(tok) * a.c.token));
+      x[j] = __ldg(reinterpret_cast<const Vec*>(p + static_cast<int64_t>(tok) * a.c.token));
       if constexpr (TYPE == DA_CACHE_FP4_E2M1)
-        sf[j] = __ldg(reinterpret_cast<const uint16_t*>(sbase + static_cast<int64_t>(pg) * a.c.sf_page +
-                                                        static_cast<int64_t>(tok) * 8));
+      {
+        const uint8_t* src = sbase + static_cast<int64_t>(pg) * a.c.sf_page + static_cast<int64_t>(tok) * 8;
+        if constexpr (SHORT) sf[j] = __ldg(src);
+        else sf[j] = __ldg(reinterpret_cast<const uint16_t*>(src));
+      }
     }
   };
   load(0, 0);
@@ -550,7 +560,7 @@ __global__ void __launch_bounds__(32 * kDigestWarps) digest_kernel(const DigestA
     }
     const int tokens = held(page);
     for (int part = 0; part < parts; ++part) {
-      uint4 y[C::kLoads];
+      Vec y[C::kLoads];
       uint32_t ys[TYPE == DA_CACHE_FP4_E2M1 ? C::kLoads : 1];
 #pragma unroll
       for (int j = 0; j < C::kLoads; ++j) {
@@ -562,18 +572,25 @@ __global__ void __launch_bounds__(32 * kDigestWarps) digest_kernel(const DigestA
 #pragma unroll
       for (int j = 0; j < C::kLoads; ++j) {
         if (part * kTokens + j * C::kRows >= tokens) break;  // (uniform)
-        const uint32_t w[4] = {y[j].x, y[j].y, y[j].z, y[j].w};
+        constexpr int kVec = sizeof(Vec) / 4;
+        uint32_t w[kVec];
+        w[0] = y[j].x;
+        w[1] = y[j].y;
+        if constexpr (kVec == 4) {
+          w[2] = y[j].z;
+          w[3] = y[j].w;
+        }
         uint32_t u[NW];
         if constexpr (TYPE == DA_CACHE_BF16) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) u[i] = w[i];
         } else if constexpr (TYPE == DA_CACHE_FP8_E4M3) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) e4m3x4_to_f16x4(w[i], u[2 * i], u[2 * i + 1]);
+          for (int i = 0; i < kVec; ++i) e4m3x4_to_f16x4(w[i], u[2 * i], u[2 * i + 1]);
         } else {
-          const uint32_t s2 = e4m3x2_to_f16x2(ys[j]);       // the lane's two block scales
+          const uint32_t s2 = e4m3x2_to_f16x2(ys[j]);       // the lane's block scales
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < kVec; ++i) {
             uint32_t c4[4];
             e2m1x8_to_f16(w[i], c4);
             const uint32_t s = __byte_perm(s2, 0, i < 2 ? 0x1010 : 0x3232);
@@ -716,13 +733,14 @@ cudaError_t launch_digest(const DigestArgs& a, int sm_count, cudaStream_t stream
   const int64_t units = (cols + per - 1) / per * a.g.num_kv_heads;
   const dim3 grid(static_cast<unsigned>((units + kDigestWarps - 1) / kDigestWarps),
                   static_cast<unsigned>(a.g.batch));
+  const bool half = a.g.page_size < 32;  // (16-token batches)
+  auto run = [&](auto* kernel) { return launch(kernel, grid, 32 * kDigestWarps, 0, stream, a, static_cast<int>(per)); };
   switch (a.c.type) {
-    case DA_CACHE_BF16:
-      return launch(digest_kernel<DA_CACHE_BF16>, grid, 32 * kDigestWarps, 0, stream, a, static_cast<int>(per));
+    case DA_CACHE_BF16: return run(digest_kernel<DA_CACHE_BF16, false>);
     case DA_CACHE_FP8_E4M3:
-      return launch(digest_kernel<DA_CACHE_FP8_E4M3>, grid, 32 * kDigestWarps, 0, stream, a, static_cast<int>(per));
+      return half ? run(digest_kernel<DA_CACHE_FP8_E4M3, true>) : run(digest_kernel<DA_CACHE_FP8_E4M3, false>);
     default:
-      return launch(digest_kernel<DA_CACHE_FP4_E2M1>, grid, 32 * kDigestWarps, 0, stream, a, static_cast<int>(per));
+      return half ? run(digest_kernel<DA_CACHE_FP4_E2M1, true>) : run(digest_kernel<DA_CACHE_FP4_E2M1, false>);
   }
 }
 
