@@ -14,7 +14,10 @@
  * exact attention softmax(QK^T/sqrt(d))V ("Capstone FlashAttention", §1.1),
  * over the keys j < L = seq_lens[b]; with `causal`, token t (at position
  * L - q_len + t) only sees keys j <= L - q_len + t.  A row with no visible key
- * gives out = 0 and lse = -inf.
+ * gives out = 0 and lse = -inf.  (So does one whose scores are all -inf, which
+ * takes infinite entries or products past fp32.)  A row that meets NaN, in its
+ * query or in a key that it sees, or an infinite score of +inf, gives NaN and a
+ * NaN lse, whatever the number of chunks; other rows are not affected.
  *
  * How.  The KV sequence of each (request, kv head) is cut into chunks of
  * `chunk_len` tokens that run on different SMs; each chunk keeps a running

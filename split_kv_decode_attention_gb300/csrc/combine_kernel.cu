@@ -8,8 +8,9 @@
 //     M = max_s lse_s,  w_s = exp(lse_s - M),
 //     out = sum_s w_s O_s / sum_s w_s,   lse = M + ln(sum_s w_s).
 // One warp per row: lane i owns d = 4i..4i+3, so each partial row is one
-// coalesced 512-byte read.  Empty chunks (lse -inf) weigh nothing; a row with
-// no finite lse gives out = 0, lse = -inf.
+// coalesced 512-byte read.  Empty chunks (lse -inf) weigh nothing; a row whose
+// LSEs are all -inf gives out = 0, lse = -inf.  A NaN among them makes the
+// maximum, and with it the whole row and its LSE, NaN.
 
 #include "decode_attn.h"
 #include "kernels.cuh"
@@ -22,8 +23,8 @@ namespace {
 // 4i..4i+3): partial s of the row has its LSE at pl[s * ls] and its output
 // slice at po[s * os] (po already offset by 4 * lane).  The grid-planned path
 // below follows the same order of operations, so both give the same bits.  Returns the merged, normalised slice of this
-// lane and (every lane) the merged LSE; a row with no finite LSE gives 0 and
-// -inf.  Loads go through L2 only (other CTAs of the same kernel may have
+// lane and (every lane) the merged LSE; a row whose LSEs are all -inf gives 0
+// and -inf.  Loads go through L2 only (other CTAs of the same kernel may have
 // written the partials) with `policy` (each partial is read once).
 __device__ __forceinline__ void merge_row_warp(const float* pl, int ls, const float* po, int os,
                                                int n, uint64_t policy, float4* res, float* lse) {
@@ -41,12 +42,12 @@ __device__ __forceinline__ void merge_row_warp(const float* pl, int ls, const fl
                  : make_float4(0.f, 0.f, 0.f, 0.f);
   float M = lse0;
   for (int s = lane + 32; s < n; s += 32)
-    M = fmaxf(M, ld_global_cg_hint1(pl + static_cast<int64_t>(s) * ls, policy));
-  M = fmaxf(M, __shfl_xor_sync(kFull, M, 16));
-  M = fmaxf(M, __shfl_xor_sync(kFull, M, 8));
-  M = fmaxf(M, __shfl_xor_sync(kFull, M, 4));
-  M = fmaxf(M, __shfl_xor_sync(kFull, M, 2));
-  M = fmaxf(M, __shfl_xor_sync(kFull, M, 1));
+    M = fmax_nan(M, ld_global_cg_hint1(pl + static_cast<int64_t>(s) * ls, policy));
+  M = fmax_nan(M, __shfl_xor_sync(kFull, M, 16));
+  M = fmax_nan(M, __shfl_xor_sync(kFull, M, 8));
+  M = fmax_nan(M, __shfl_xor_sync(kFull, M, 4));
+  M = fmax_nan(M, __shfl_xor_sync(kFull, M, 2));
+  M = fmax_nan(M, __shfl_xor_sync(kFull, M, 1));
   if (M == -INFINITY) {
     *res = make_float4(0.f, 0.f, 0.f, 0.f);
     *lse = -INFINITY;
@@ -182,12 +183,12 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock, LISTED ? kBlocksPerSm - 1
                    static_cast<int64_t>(h) * a.o_sh + lane * 4;
   // splits in groups of 32: lane j holds lse of split s0 + j
   float M = lane < n ? lse0 : -INFINITY;
-  for (int s = lane + 32; s < n; s += 32) M = fmaxf(M, ld_global_hint1(pl + static_cast<int64_t>(s) * ls, dead));
-  M = fmaxf(M, __shfl_xor_sync(kFull, M, 16));
-  M = fmaxf(M, __shfl_xor_sync(kFull, M, 8));
-  M = fmaxf(M, __shfl_xor_sync(kFull, M, 4));
-  M = fmaxf(M, __shfl_xor_sync(kFull, M, 2));
-  M = fmaxf(M, __shfl_xor_sync(kFull, M, 1));
+  for (int s = lane + 32; s < n; s += 32) M = fmax_nan(M, ld_global_hint1(pl + static_cast<int64_t>(s) * ls, dead));
+  M = fmax_nan(M, __shfl_xor_sync(kFull, M, 16));
+  M = fmax_nan(M, __shfl_xor_sync(kFull, M, 8));
+  M = fmax_nan(M, __shfl_xor_sync(kFull, M, 4));
+  M = fmax_nan(M, __shfl_xor_sync(kFull, M, 2));
+  M = fmax_nan(M, __shfl_xor_sync(kFull, M, 1));
   if (M == -INFINITY) {
     *reinterpret_cast<uint2*>(orow) = make_uint2(0u, 0u);
     if (lane == 0) a.lse[row] = -INFINITY;
@@ -278,13 +279,13 @@ __global__ void __launch_bounds__(kRowThreads) combine_row_kernel(const CombineA
   for (int s = threadIdx.x; s < n; s += kRowThreads) {
     const float x = ld_global_cg_hint1(pl + s * step, dead);
     if (s < kRowLses) weight[s] = x;
-    M = fmaxf(M, x);
+    M = fmax_nan(M, x);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+  for (int o = 16; o > 0; o >>= 1) M = fmax_nan(M, __shfl_xor_sync(kFull, M, o));
   if (lane == 0) red[0][warp] = M;
   __syncthreads();
-  M = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  M = fmax_nan(fmax_nan(red[0][0], red[0][1]), fmax_nan(red[0][2], red[0][3]));
   uint16_t* out = a.out + static_cast<int64_t>(b) * a.o_sb + static_cast<int64_t>(t) * a.o_st +
                   static_cast<int64_t>(h) * a.o_sh + threadIdx.x;
   if (M == -INFINITY) {

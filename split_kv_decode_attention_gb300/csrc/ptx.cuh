@@ -311,6 +311,15 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return r;
 }
 
+// The larger of two values, NaN if either is (fmaxf passes NaN over): the
+// maximum of the LSEs that a merge joins, so that a chunk whose sums are NaN
+// does not count as one without keys.
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // bf16x2 -> f16x2; exact for magnitudes in f16's normal range [2^-14, 65504].
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v) {
   return pack_f16x2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));

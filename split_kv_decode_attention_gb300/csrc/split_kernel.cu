@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
 #pragma unroll
       for (int w = 0; w < TPS; ++w)
         Qs += stat_q[w * C::kRows + row] * ex2(stat_m[w * C::kRows + row] - Mu);
-      const float f = (Qs > 0.f ? ex2(m[nt][rr] - Mu) / Qs : 0.f) * (F8 ? a.v_scale : 1.f);
+      const float f = (Qs == 0.f ? 0.f : ex2(m[nt][rr] - Mu) / Qs) * (F8 ? a.v_scale : 1.f);
       // accumulator rows g4 / g4 + 8 of output tile mt hold d = 16mt + g4 /
       // + 8 (bf16 path) or d = 16mt + 2g4 / + 1 (FP8 path)
       float* dst = red + (warp * C::kRows + row) * C::kRedStride + (F8 ? 2 * g4 : g4);
@@ -689,7 +689,7 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
 #pragma unroll
     for (int w = 0; w < TPS; ++w)
       Ls += stat_l[w * C::kRows + row] * ex2(stat_m[w * C::kRows + row] - Mu);
-    return Ls > 0.f ? (Mu + log2f(Ls)) * kLn2 : -INFINITY;
+    return Ls == 0.f ? -INFINITY : (Mu + log2f(Ls)) * kLn2;  // (NaN stays NaN)
   };
   // the merged (row, d..d+3) of the CTA's output: the warps' scaled rows summed
   auto merged = [&](int row, int d) {
@@ -731,7 +731,7 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
       const int row = u >> 5;
       const int d = (u & 31) * 4;
       float M = -INFINITY;
-      for (int r = 0; r < S; ++r) M = fmaxf(M, inbox_l[r * slots + slot]);
+      for (int r = 0; r < S; ++r) M = fmax_nan(M, inbox_l[r * slots + slot]);
       float4 acc4 = make_float4(0.f, 0.f, 0.f, 0.f);
       float W = 0.f;
       if (M != -INFINITY) {
@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
           acc4.w += w * x.w;
         }
       }
-      const float inv = W > 0.f ? 1.f / W : 0.f;
+      const float inv = W == 0.f ? 0.f : 1.f / W;
       const int t = row / a.group;
       const int h = kvh * a.group + (row - t * a.group);
       *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(b) * a.o_sb +
@@ -755,7 +755,7 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
                      pack_bf16x2(acc4.z * inv, acc4.w * inv));
       if (d == 0) {
         const int64_t prow = (static_cast<int64_t>(b) * a.q_len + t) * a.num_q_heads + h;
-        a.lse[prow] = W > 0.f ? M + logf(W) : -INFINITY;
+        a.lse[prow] = W == 0.f ? -INFINITY : M + logf(W);
       }
     }
     return;
@@ -795,7 +795,7 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
                      : make_float4(0.f, 0.f, 0.f, 0.f);
       float M = -INFINITY;
 #pragma unroll
-      for (int r = 0; r < kPeers; ++r) M = fmaxf(M, lr[r]);
+      for (int r = 0; r < kPeers; ++r) M = fmax_nan(M, lr[r]);
       float4 acc4 = make_float4(0.f, 0.f, 0.f, 0.f);
       float W = 0.f;
       if (M != -INFINITY) {
@@ -821,7 +821,7 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
           }
         }
       }
-      const float inv = W > 0.f ? 1.f / W : 0.f;
+      const float inv = W == 0.f ? 0.f : 1.f / W;
       const int t = row / a.group;
       const int h = kvh * a.group + (row - t * a.group);
       *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(b) * a.o_sb +
@@ -831,7 +831,7 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
                      pack_bf16x2(acc4.z * inv, acc4.w * inv));
       if (d == 0) {
         const int64_t prow = (static_cast<int64_t>(b) * a.q_len + t) * a.num_q_heads + h;
-        a.lse[prow] = W > 0.f ? M + logf(W) : -INFINITY;
+        a.lse[prow] = W == 0.f ? -INFINITY : M + logf(W);
       }
     }
     cluster_sync();  // no CTA leaves while another may still read its smem

@@ -1172,7 +1172,7 @@ __global__ void __launch_bounds__(WCfg<KV>::kThreads, 1)
       Lt += pl0 * pf0 + pl1 * pf1;
       Qt += pq0 * pf0 + pq1 * pf1;
     }
-    const float inv = (Qt > 0.f ? 1.f / Qt : 0.f) * (F8 ? a.v_scale : 1.f);
+    const float inv = (Qt == 0.f ? 0.f : 1.f / Qt) * (F8 ? a.v_scale : 1.f);  // (NaN stays NaN)
     const bool have0 = ok && n_iters > 0;  // O[0] / O[1] were written
     const bool have1 = ok && n_iters > 1;
     const bool direct = it.nsplit == 1;
@@ -1236,7 +1236,7 @@ __global__ void __launch_bounds__(WCfg<KV>::kThreads, 1)
       }
     }
     if (grp == 0 && kh == 0 && row < a.rows) {
-      const float lse = Lt > 0.f ? (Mu - (F4 ? kWF4Shift : 0.f) + log2f(Lt)) * kLn2w : -INFINITY;
+      const float lse = Lt == 0.f ? -INFINITY : (Mu - (F4 ? kWF4Shift : 0.f) + log2f(Lt)) * kLn2w;
       if (direct)
         a.lse[prow] = lse;
       else
