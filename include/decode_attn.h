@@ -526,7 +526,8 @@ int decode_attn_rope_append(const decode_attn_params *p, const decode_attn_cache
  * seq_len), in 8 bits.  With amax the largest magnitude among them,
  *     digest[page, head, 0 / 1, d] = rint(min / max * (127 / amax)),
  *     digest_scale[page, head]     = amax / 127,
- * in fp32 (0 where amax is 0).  Keys are the values the cache stores, without
+ * in fp32 (0 where amax is 0; below 3.8e-37, where 127 / amax overflows, zeros
+ * stay 0 and the others become 127 of their sign).  Keys are the values the cache stores, without
  * k_scale; NaN values are skipped (a channel with nothing else counts as 0)
  * and infinities count as the largest finite bf16 value.
  *   digest        int8 [num_pages, Hkv, 2, 128]
@@ -561,7 +562,9 @@ typedef struct decode_attn_select {
  * bound on q . k over the page's keys, each channel at its better end.  The
  * sum is exact, the two products are fp32: the selection is the same on every
  * run.  (NaN in q counts as 0,
- * infinities as the largest finite bf16 value; a = 0 gives scores of 0.)
+ * infinities as the largest finite bf16 value; a = 0 gives scores of 0; where
+ * 127 / a overflows, below a = 3.8e-37, zeros stay 0 and the others become 127
+ * of their sign.)
  *   blocks     int32 [B, q_len, Hkv, top_k]: the selected pages' places in
  *              the request, ascending, -1 behind the last; may be NULL
  *   pages      int32 [B, q_len, Hkv, top_k]: their page ids (0 behind the

@@ -191,7 +191,12 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectArg
     }
     top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
     top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-    const float inv = top > 0.f ? __fdiv_rn(127.f, top) : 0.f;
+    float inv = top > 0.f ? __fdiv_rn(127.f, top) : 0.f;
+    if (inv == INFINITY) {  // (top below 3.8e-37: zeros stay zero, 0 x infinity is NaN)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = x[i] == 0.f ? 0.f : copysignf(127.f, x[i]);
+      inv = 1.f;
+    }
     uint32_t h[16];
     float sum = 0.f;
 #pragma unroll
