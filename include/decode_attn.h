@@ -456,8 +456,10 @@ int decode_attn_cached(const decode_attn_params *p, const decode_attn_cache *c, 
  * position, fp64, device memory),
  *     table[(pos - first) * 2 num_freqs + i]             = amplitude cos(pos f_i)
  *     table[(pos - first) * 2 num_freqs + num_freqs + i] = amplitude sin(pos f_i)
- * in fp32, to about one ulp at every position (the angle is reduced in 64-bit
- * fixed point); the table is 16-byte aligned.  Scalings for long contexts are
+ * in fp32, within 2^-21 of an entry's own size plus what the angle is off: it is
+ * reduced in 64-bit fixed point, to pos * 2^-65 + 2^-56 turns (1e-9 radians at
+ * the last position; entries near a zero crossing are small, but not exact to
+ * their own last bits).  The table is 16-byte aligned.  Scalings for long contexts are
  * the caller's choice of f and amplitude.  1 <= num_freqs <= 64, first and first + count within 0 .. 2^31.
  * Frequencies that are not finite give NaN.
  */

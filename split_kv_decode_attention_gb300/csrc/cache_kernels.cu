@@ -23,21 +23,25 @@ constexpr uint32_t kFull = 0xffffffffu;
 // integer multiply; the next row of a thread is an addition away.  The nearest
 // quarter turn is split off exactly, and on the remainder x of at most pi / 4
 // the Taylor series through x^9 and x^10 are within 3e-9 and 2e-10 of sine and
-// cosine, a twentieth of an fp32 rounding: full relative accuracy at every
-// position with 11 fp32 multiply-adds, where an fp64 cosine is two orders of
-// magnitude more work (fp64 runs at 1/64 of the fp32 rate on this GPU).  The
+// cosine, a twentieth of an fp32 rounding.  With the roundings of x and of the
+// series an entry is within 6.5 x 2^-24 of itself, plus what the angle is off:
+// pos * 2^-65 turns, and 2^-57 where a zero crossing leaves only the low word,
+// which fp32 rounds.  That takes 11 fp32 multiply-adds, where an fp64 cosine is two
+// orders of magnitude more work (fp64 runs at 1/64 of the fp32 rate on this GPU).  The
 // F of the frequencies, the only fp64 work, are made once per CTA.  (131072
 // positions x 128: 14.4 us, 4.7 TB/s written, 0.70 of a copy's rate; the integer
 // and polynomial work keeps the ALU 61 % busy.)
 __device__ __forceinline__ uint64_t turns_fixed(double f) {
   const double kInv2PiHi = 0.15915494309189535;      // 1 / (2 pi), rounded
   const double kInv2PiLo = -9.839338337591243e-18;   // what is left of it
-  const double p = f * kInv2PiHi;
-  const double e = fma(f, kInv2PiHi, -p) + f * kInv2PiLo;
-  const double frac = p - floor(p);                  // exact
+  const double m = fabs(f);
+  const double p = m * kInv2PiHi;
+  const double e = fma(m, kInv2PiHi, -p) + m * kInv2PiLo;
+  const double frac = p - floor(p);                  // exact (of a negative p it would round)
   const double hi = floor(frac * 4294967296.0);
   const double lo = (frac * 4294967296.0 - hi) * 4294967296.0 + e * 18446744073709551616.0;
-  return (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>(static_cast<int64_t>(rint(lo)));
+  const uint64_t turns = (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>(static_cast<int64_t>(rint(lo)));
+  return f < 0.0 ? 0 - turns : turns;
 }
 
 // cos and sin of phase / 2^64 turns, times amp.
