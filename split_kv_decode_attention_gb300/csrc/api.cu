@@ -118,6 +118,8 @@ int chunk_for_splits(const decode_attn_params* p, int32_t num_splits, int32_t* c
              : DA_ERR_SPLITS;
 }
 
+bool use_cluster_merge(const decode_attn_params* p, int32_t splits_eff, int unit = 0);
+
 // The planner proper (the rule of plan_rule.cuh, shared with the device
 // planner kernel): a function of the shape, the host lengths and the number
 // of CTAs the split launch keeps resident at once (SMs x CTAs per SM).
@@ -132,6 +134,7 @@ int plan_for_slots(const decode_attn_params* p, const int32_t* host_seq_lens, in
   shape.max_seq_len = p->max_seq_len;
   shape.fp4 = unit > 0 ? 1 : 0;
   shape.listed = per_head ? 1 : 0;
+  shape.clusters = unit > 0 && use_cluster_merge(p, dattn::kMaxClusterSplits, unit) ? 1 : 0;
   bool uniform = true;
   int64_t work_tokens = 0;
   auto clamped = [&](int32_t b) {
@@ -342,7 +345,7 @@ bool kv_stride_ok(const decode_attn_params* p, int64_t s, bool fp4 = false) {
 // The split pass merges through thread-block clusters (no partials, no
 // combine) when allowed by the flags and when the splits_eff CTAs of every
 // (request, kv head) form a supported cluster and all clusters fit at once.
-bool use_cluster_merge(const decode_attn_params* p, int32_t splits_eff, int unit = 0) {
+bool use_cluster_merge(const decode_attn_params* p, int32_t splits_eff, int unit) {
   if ((p->flags & DA_FLAG_TWO_PASS) != 0 || splits_eff < 2 || p->batch < 1) return false;
   if (unit > 0)  // (4-bit caches: CTAs of one head)
     return unit == 1 && !wide4(p) &&
