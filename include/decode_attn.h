@@ -537,7 +537,9 @@ int decode_attn_rope_append(const decode_attn_params *p, const decode_attn_cache
  *   max_new       > 0: only the pages that hold tokens L - max_new .. L - 1
  *                 of a request (a decode step); 0: every page it has
  * Other pages' digests are left as they were.  A page that requests of a call
- * share is digested for one of them: they should see the same tokens of it.
+ * share is digested once for each of them, at the same time: they have to see
+ * the same tokens of it (whole pages of a common prefix do), else its entry may
+ * be made of both.
  */
 int decode_attn_block_digest(const decode_attn_params *p, const decode_attn_cache *c,
                              const int32_t *block_table, const int32_t *seq_lens,

@@ -227,8 +227,9 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock, LISTED ? kBlocksPerSm - 1
   if (lane == 0) a.lse[row] = M + logf(W);
 }
 
-// The merge for calls whose rows are few and their chunks many (4-bit caches: no
-// cluster merge, so a single row may span hundreds of chunks): a CTA per row, a
+// The merge for calls whose rows are few and their chunks many (4-bit caches:
+// only short calls planned on the host merge through clusters, so a single row
+// may span hundreds of chunks): a CTA per row, a
 // thread per d.  The chunks' values are loaded sixteen at a time, the first of
 // them together with the LSEs, so a row of up to 16 chunks costs two dependent
 // round trips and 16 more chunks one each.  (GB300, whole calls: 32 rows of 57

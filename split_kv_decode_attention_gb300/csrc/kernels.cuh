@@ -160,8 +160,9 @@ cudaError_t launch_wide(const CUtensorMap& k_map, const CUtensorMap& v_map, cons
 cudaError_t launch_wide_fp4(const Fp4Maps& maps, const SplitArgs& a, cudaStream_t stream);
 int wide_ctas_per_sm();
 
-// Launch the kernel over 4-bit caches (any rows; outputs and partials as
-// launch_split without cluster merge), and its resident CTAs per SM.
+// Launch the kernel over 4-bit caches (up to kFp4MaxRows rows, launch_wide_fp4
+// takes more; outputs and partials as launch_split without cluster merge), and
+// its resident CTAs per SM.
 // A CTA takes heads_per_cta (1, 2, 4 or 8, a divisor of the KV heads) heads: items,
 // plans and partials count such units (partials hold a unit's heads one behind
 // the other).
