@@ -17,7 +17,8 @@
  * gives out = 0 and lse = -inf.  (So does one whose scores are all -inf, which
  * takes infinite entries or products past fp32.)  A row that meets NaN, in its
  * query or in a key that it sees, or an infinite score of +inf, gives NaN and a
- * NaN lse, whatever the number of chunks; other rows are not affected.
+ * NaN lse, whatever the number of chunks; other rows are not affected.  (Over
+ * FP8 caches |q| above 65504 counts as infinite.)
  *
  * How.  The KV sequence of each (request, kv head) is cut into chunks of
  * `chunk_len` tokens that run on different SMs; each chunk keeps a running

@@ -29,7 +29,7 @@ constexpr uint32_t kFull = 0xffffffffu;
 // which fp32 rounds.  That takes 11 fp32 multiply-adds, where an fp64 cosine is two
 // orders of magnitude more work (fp64 runs at 1/64 of the fp32 rate on this GPU).  The
 // F of the frequencies, the only fp64 work, are made once per CTA.  (131072
-// positions x 128: 14.4 us, 4.7 TB/s written, 0.70 of a copy's rate; the integer
+// positions x 128: 14.6 us, 4.6 TB/s written, 0.69 of a copy's rate; the integer
 // and polynomial work keeps the ALU 61 % busy.)
 __device__ __forceinline__ uint64_t turns_fixed(double f) {
   const double kInv2PiHi = 0.15915494309189535;      // 1 / (2 pi), rounded
