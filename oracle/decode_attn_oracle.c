@@ -283,8 +283,8 @@ int oracle_decode_attn(int batch, int q_len, int num_q_heads, int num_kv_heads,
  * Combine of normalised partial results (fp64).
  *   part_out [nrows, nsplit, D], part_lse [nrows, nsplit]
  *   nvalid   optional per-row count of leading splits to use (NULL: all)
- * Splits whose lse is -inf carry no weight; a row with no finite lse gives
- * out = 0, lse = -inf.
+ * Splits whose lse is -inf carry no weight; a row with no other gives out = 0,
+ * lse = -inf, and one with a NaN lse is NaN.
  */
 int oracle_merge_partials(int64_t nrows, int nsplit, int head_dim,
                           const double *part_out, const double *part_lse,
@@ -297,7 +297,7 @@ int oracle_merge_partials(int64_t nrows, int nsplit, int head_dim,
     double *o = out + r * head_dim;
     double M = -INFINITY;
     for (int s = 0; s < n; ++s)
-      if (pl[s] > M) M = pl[s];
+      if (isnan(pl[s]) || pl[s] > M) M = pl[s];  /* (nothing is above NaN) */
     for (int d = 0; d < head_dim; ++d) o[d] = 0.0;
     if (M == -INFINITY) { lse[r] = -INFINITY; continue; }
     double W = 0.0;
