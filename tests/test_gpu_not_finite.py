@@ -189,3 +189,28 @@ def test_merge_alone(da, S):
         # bf16 rounding 2^-8; weights and sums in fp32, exponentials to 2^-21
         assert bool(((out[1, 0, h] - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -18).all())
         assert abs(float(lse[1, 0, h]) - float(torch.logsumexp(part_l[1, 0, h, :2].double(), 0))) <= 2.0 ** -18
+
+
+@pytest.mark.parametrize("plan", list(PLANS))
+@pytest.mark.parametrize("G", [4, 16, 24, 40])
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
+def test_scores_that_are_all_minus_infinity(da, kind, G, plan):
+    """They weigh nothing: 0 and -inf, as where there are no keys, in every merge."""
+    pc = Paged(kind, [700, 333], 2, 16, 360 + G)
+    if kind == "bf16":
+        pc.k[..., 5] = -1.0
+    elif kind == "fp8":
+        pc.k[..., 5] = 0xB8                      # -1
+    else:
+        pc.k[..., 2] = (pc.k[..., 2] & 0x0F) | 0xA0
+        pc.k_sf[..., 0] = 0x38
+    pc.gpu()
+    q = bf16(gen(361), 2, 1, 2 * G, D)
+    q[0, 0, 1, 5] = q[1, 0, G, 5] = math.inf
+    out, lse = attend(da, pc, q, *PLANS[plan])
+    bad = torch.zeros(q.shape[:3], dtype=torch.bool)
+    for b, h in ((0, 1), (1, G)):
+        assert not bool(out[b, 0, h].any()) and float(lse[b, 0, h]) == -math.inf
+        bad[b, 0, h] = True
+        out[b, 0, h], lse[b, 0, h] = math.nan, math.nan      # (the others are checked as above)
+    check(pc, q, out, lse, bad)
