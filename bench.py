@@ -58,8 +58,8 @@ PROFILE_DIR = os.path.join(ROOT, "profiles")
 # and the sources its machine code depends on (a committed ncu summary is
 # trusted only while their hash matches)
 KERNEL_SOURCES = {
-    "split_kv_kernel": ["split_kernel.cu", "ptx.cuh", "kernels.cuh"],
-    "wide_kernel": ["wide_kernel.cu", "tcgen05.cuh", "ptx.cuh", "kernels.cuh"],
+    "split_kv_kernel": ["split_kernel.cu", "split_kernel.cuh", "rows.cuh", "ptx.cuh", "kernels.cuh"],
+    "wide_kernel": ["wide_kernel.cu", "wide_kernel.cuh", "rows.cuh", "tcgen05.cuh", "ptx.cuh", "kernels.cuh"],
 }
 NARROW_MAX_ROWS = 16
 

@@ -606,6 +606,135 @@ int decode_attn_sparse(const decode_attn_params *p, const decode_attn_cache *c,
                        void *workspace, size_t workspace_bytes, int32_t *status,
                        void *stream);
 
+/* ------------------------------------------------------------------------
+ * Trees of drafted tokens, cross attention, and reading a cache back.
+ *
+ * A speculative step that verifies a tree of drafts instead of one chain:
+ * decode_attn_tree_mask() from each draft's parent, rope_append() at the
+ * positions it gives, decode_attn_tree() instead of decode_attn(), and, once
+ * the accepted path is known, decode_attn_cache_keep() for each cache.
+ * ------------------------------------------------------------------------ */
+
+#define DECODE_ATTN_MAX_TREE 1024  /* new tokens of a request in a tree */
+#define DA_STATUS_TREE 32u         /* a parent that is no earlier token, or kept tokens
+                                      that do not rise */
+
+/*
+ * Masks of trees.  Request b's new tokens are the last n_b = new_lens[b] (or
+ * q_len) of its seq_lens[b] tokens; parents[b * q_len + t] is the new token
+ * before token t on its path, -1 where that is the sequence before the tree (a
+ * request may have several such roots).
+ *   parents    int32 [B, q_len], each -1 or an earlier token, parents[t] < t
+ *   mask       uint32 [B, q_len, ceil(q_len / 32)]: bit i % 32 of word i / 32 of
+ *              row t is set for t itself and the tokens on its path
+ *   positions  int32 [B, q_len], or NULL: L - n_b + the number of tokens on t's
+ *              path before it (what rope_append() takes)
+ * Rows t >= n_b get zeros.  Status: DA_STATUS_TREE for a parent that is not
+ * allowed (taken as -1), DA_STATUS_SEQ_LEN for a length outside [0, max_seq_len]
+ * or [0, q_len] (clamped), DA_STATUS_SHORT_CAUSAL where L < n_b.
+ * 1 <= q_len <= DECODE_ATTN_MAX_TREE.
+ */
+int decode_attn_tree_mask(int32_t batch, int32_t q_len, int32_t max_seq_len,
+                          const int32_t *parents, const int32_t *new_lens,
+                          const int32_t *seq_lens, uint32_t *mask, int32_t *positions,
+                          int32_t *status, void *stream);
+
+/*
+ * Decode attention of a tree's tokens: as decode_attn_cached(), where new token
+ * t of request b (n_b = new_lens[b], or q_len, of them, the last of its L) sees
+ *     the keys j < L - n_b, and key L - n_b + i where bit i of its row is set.
+ * Rows t >= n_b are padding: their q is not used, out = 0 and lse = -inf.  So
+ * for a row that sees no key.  What a hidden key holds does not matter, NaN
+ * included; the values of the new tokens have to be finite, though, since a
+ * hidden one enters the product with weight 0.
+ *   mask                uint32 rows as decode_attn_tree_mask() writes them (any
+ *                       other pattern of bits is as good), 4-byte aligned
+ *   mask_stride_batch   words from a request's rows to the next one's; 0: one
+ *                       mask for all
+ * p->causal is not used, nor is DA_FLAG_TEST_WITHHOLD_COPY above
+ * DECODE_ATTN_MAX_ROWS.  (Hq / Hkv) * q_len may exceed DECODE_ATTN_MAX_ROWS;
+ * Hq / Hkv may not, nor q_len DECODE_ATTN_MAX_TREE.  Above that many rows the
+ * workspace also holds, for FP8 and 4-bit caches, the batch's keys and values in
+ * bf16 (B * max_seq_len * Hkv * 512 bytes).
+ * Status as decode_attn(); DA_STATUS_SHORT_CAUSAL where L < n_b (the first
+ * n_b - L new tokens then have no key).
+ */
+int decode_attn_tree_workspace_bytes(const decode_attn_params *p, const decode_attn_cache *c,
+                                     int32_t num_splits, size_t *bytes);
+int decode_attn_tree(const decode_attn_params *p, const decode_attn_cache *c, const void *q,
+                     const uint32_t *mask, int64_t mask_stride_batch, const int32_t *new_lens,
+                     const int32_t *block_table, const int32_t *seq_lens, void *out,
+                     float *lse, int32_t num_splits, void *workspace, size_t workspace_bytes,
+                     int32_t *status, void *stream);
+
+/*
+ * Cross attention: as decode_attn_cached(), every row over all seq_lens[b] keys
+ * (an encoder's states, of a length of their own), for any q_len: one new token
+ * or a whole prompt.  Request b has q_lens[b] tokens (q_len when NULL); rows
+ * behind them are padding: their q is not used, out = 0 and lse = -inf.
+ * p->causal is not used.  Rows, workspace and status as decode_attn_tree(), but
+ * q_len has no limit of its own ((Hq / Hkv) * q_len < 2^31).
+ */
+int decode_attn_cross_workspace_bytes(const decode_attn_params *p, const decode_attn_cache *c,
+                                      int32_t num_splits, size_t *bytes);
+int decode_attn_cross(const decode_attn_params *p, const decode_attn_cache *c, const void *q,
+                      const int32_t *q_lens, const int32_t *block_table,
+                      const int32_t *seq_lens, void *out, float *lse, int32_t num_splits,
+                      void *workspace, size_t workspace_bytes, int32_t *status, void *stream);
+
+/*
+ * Keep some of the new tokens: of request b's n_b = new_lens[b] (or p->q_len)
+ * new tokens, the last of its seq_lens[b], the counts[b] tokens keep[b][0],
+ * keep[b][1], .. (rising) become its first new tokens, in K, V and the block
+ * scales:
+ *     token L - n_b + i  <-  token L - n_b + keep[b][i],   i < counts[b],
+ * and out_lens[b] = L - n_b + counts[b].  The bytes are moved as they are (a
+ * key keeps the rotation it was appended with).
+ *   keep      int32 [B, max_keep], 0 <= max_keep <= p->q_len
+ *   out_lens  int32 [B], or NULL; not seq_lens itself
+ * p->q_len <= DECODE_ATTN_MAX_TREE; of *p the shapes, paging and cache strides
+ * are used.  Pages that hold new tokens belong to one request of the call.
+ * Status: DA_STATUS_TREE where an entry does not rise or is no new token (it and
+ * those behind it are dropped) or a count is outside [0, min(max_keep, n_b)]
+ * (clamped), DA_STATUS_BAD_PAGE (that token is not moved), DA_STATUS_SEQ_LEN and
+ * DA_STATUS_SHORT_CAUSAL (tokens before position 0 are not moved) as above.
+ */
+int decode_attn_cache_keep(const decode_attn_params *p, const decode_attn_cache *c,
+                           const int32_t *keep, int32_t max_keep, const int32_t *counts,
+                           const int32_t *new_lens, const int32_t *block_table,
+                           const int32_t *seq_lens, int32_t *out_lens, int32_t *status,
+                           void *stream);
+
+/* Where decode_attn_cache_read() writes. */
+typedef struct decode_attn_read {
+  int32_t max_tokens;         /* tokens of a request at most, >= 0 */
+  int32_t reserved;           /* 0 */
+  int64_t rows;               /* with offsets: rows of the outputs; else not used */
+  int64_t stride_batch;       /* element strides of both outputs, multiples of 8; */
+  int64_t stride_token;       /*   stride_batch is not used with offsets */
+  int64_t stride_head;
+} decode_attn_read;
+
+/*
+ * Read a cache back: tokens starts[b] (0 when NULL) .. seq_lens[b] - 1 of every
+ * request, at most max_tokens of them, as bf16,
+ *     k_scale * K  and  v_scale * V   (4-bit: scale * (block_scale * e2m1)),
+ * the product with the cache's scale rounded once to fp32 and once to bf16;
+ * bf16 caches are copied.  NaN stays NaN.
+ *   k_out, v_out  bf16, 16-byte aligned: [B, max_tokens, Hkv, 128], token
+ *                 starts[b] + i in row i of request b; or, with offsets, [rows,
+ *                 Hkv, 128], in row offsets[b] + i.  v_out may be NULL (with
+ *                 c->v then unused).
+ * Rows that no token goes to are left as they were.  Status: DA_STATUS_SEQ_LEN
+ * where a length or a start is out of range (clamped) or a row of offsets is
+ * (not written), DA_STATUS_BAD_PAGE as in decode_attn().
+ */
+int decode_attn_cache_read(const decode_attn_params *p, const decode_attn_cache *c,
+                           const decode_attn_read *r, const int32_t *starts,
+                           const int32_t *offsets, const int32_t *block_table,
+                           const int32_t *seq_lens, void *k_out, void *v_out,
+                           int32_t *status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -19,6 +19,7 @@ CALLS_PATH = os.path.join(_PKG, "lib", "_calls.so")
 
 HEAD_DIM = 128
 MAX_ROWS = 128
+MAX_TREE = 1024
 TOKEN_TILE = 16
 
 DA_OK = 0
@@ -27,6 +28,7 @@ DA_STATUS_SEQ_LEN = 2
 DA_STATUS_SHORT_CAUSAL = 4
 DA_STATUS_TIMEOUT = 8
 DA_STATUS_POSITION = 16
+DA_STATUS_TREE = 32
 DA_CACHE_BF16 = 0
 DA_CACHE_FP8_E4M3 = 1
 DA_CACHE_FP4_E2M1 = 2
@@ -43,7 +45,9 @@ EXPORTED_SYMBOLS = (
     "decode_attn_cached", "decode_attn_cached_workspace_bytes", "decode_attn_rope_table",
     "decode_attn_rope_append", "decode_attn_block_digest", "decode_attn_block_select",
     "decode_attn_block_select_workspace_bytes", "decode_attn_sparse",
-    "decode_attn_sparse_workspace_bytes",
+    "decode_attn_sparse_workspace_bytes", "decode_attn_tree_mask", "decode_attn_tree",
+    "decode_attn_tree_workspace_bytes", "decode_attn_cross", "decode_attn_cross_workspace_bytes",
+    "decode_attn_cache_keep", "decode_attn_cache_read",
 )
 DA_ERR_STATIC_WORKSPACE_LIMIT = -11
 STATIC_WORKSPACE_BYTES = 16 << 20
@@ -98,6 +102,14 @@ class DecodeAttnSelect(ctypes.Structure):
                 ("local", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class DecodeAttnRead(ctypes.Structure):
+    """Mirror of `decode_attn_read`."""
+
+    _fields_ = [("max_tokens", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("stride_batch", ctypes.c_int64),
+                ("stride_token", ctypes.c_int64), ("stride_head", ctypes.c_int64)]
+
+
 class DecodeAttnError(RuntimeError):
     def __init__(self, code: int, where: str):
         super().__init__(f"{where} failed: {decode_attn_status_string(code)} (code {code})")
@@ -146,6 +158,13 @@ def lib() -> ctypes.CDLL:
         L.decode_attn_block_select.argtypes = [P, S] + [vp] * 9 + [sz, vp, vp]
         L.decode_attn_sparse_workspace_bytes.argtypes = [P, C, S, psz]
         L.decode_attn_sparse.argtypes = [P, C, S] + [vp] * 9 + [sz, vp, vp]
+        L.decode_attn_tree_mask.argtypes = [i32, i32, i32] + [vp] * 7
+        L.decode_attn_tree_workspace_bytes.argtypes = [P, C, i32, psz]
+        L.decode_attn_cross_workspace_bytes.argtypes = [P, C, i32, psz]
+        L.decode_attn_tree.argtypes = [P, C, vp, vp, i64, vp, vp, vp, vp, vp, i32, vp, sz, vp, vp]
+        L.decode_attn_cross.argtypes = [P, C, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp, vp]
+        L.decode_attn_cache_keep.argtypes = [P, C, vp, i32] + [vp] * 7
+        L.decode_attn_cache_read.argtypes = [P, C, ctypes.POINTER(DecodeAttnRead)] + [vp] * 8
         for f in ("decode_attn_plan", "decode_attn_plan_slots", "decode_attn_chunk_len",
                   "decode_attn_workspace_bytes",
                   "decode_attn", "decode_attn_split", "decode_attn_combine",
@@ -155,7 +174,10 @@ def lib() -> ctypes.CDLL:
                   "decode_attn_cached_workspace_bytes", "decode_attn_rope_table",
                   "decode_attn_rope_append", "decode_attn_block_digest",
                   "decode_attn_block_select", "decode_attn_block_select_workspace_bytes",
-                  "decode_attn_sparse", "decode_attn_sparse_workspace_bytes"):
+                  "decode_attn_sparse", "decode_attn_sparse_workspace_bytes",
+                  "decode_attn_tree_mask", "decode_attn_tree", "decode_attn_tree_workspace_bytes",
+                  "decode_attn_cross", "decode_attn_cross_workspace_bytes",
+                  "decode_attn_cache_keep", "decode_attn_cache_read"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -576,3 +598,70 @@ def decode_attn_sparse(q, k_cache, v_cache, block_table, seq_lens, digest, diges
     return _calls().sparse(q, k_cache, v_cache, block_table, seq_lens, digest, digest_scale,
                            max_seq_len, top_k, sink, local, causal, scale, k_scale, v_scale, k_sf,
                            v_sf, out, lse, blocks, workspace, status, stream)
+
+
+# ---------------------------------------------------------------------------
+# Trees of drafted tokens, cross attention, and reading a cache back
+
+
+def tree_mask(parents, seq_lens, *, max_seq_len: int, new_lens=None, mask=None, positions=None,
+              status=None, stream=None):
+    """Masks and positions of trees of drafted tokens: (mask int32 [B, q_len,
+    ceil(q_len / 32)], positions int32 [B, q_len]) from `parents`, int32 [B,
+    q_len]: the new token before each one on its path, -1 for those that follow
+    the sequence itself.  Request b's new tokens are the last new_lens[b] (or
+    q_len) of its seq_lens[b]; rows behind them get zeros.  `mask` is what
+    decode_attn_tree() takes, `positions` what rope_append() does."""
+    return _calls().tree_mask(parents, seq_lens, max_seq_len, new_lens, mask, positions, status,
+                              stream)
+
+
+def decode_attn_tree(q, k_cache, v_cache, block_table, seq_lens, mask, *, max_seq_len: int,
+                     new_lens=None, scale: Optional[float] = None, num_splits: int = 0,
+                     k_scale: float = 1.0, v_scale: float = 1.0, k_sf=None, v_sf=None, out=None,
+                     lse=None, workspace=None, status=None, stream=None):
+    """Decode attention of a tree's tokens: (out, lse).  New token t of a request
+    sees the tokens before the new ones and, of those, the ones whose bit is set
+    in its row of `mask` (int32 [B, q_len, ceil(q_len / 32)], or [1, ..] for all
+    requests: tree_mask()'s).  Rows from new_lens[b] on are padding: zeros, and an
+    lse of -inf.  Any cache type, as decode_attn(); the query rows per KV head may
+    exceed 128 (FP8 and 4-bit caches are then read back into the workspace)."""
+    return _calls().tree(q, k_cache, v_cache, block_table, seq_lens, mask, new_lens, max_seq_len,
+                         scale, num_splits, k_scale, v_scale, k_sf, v_sf, out, lse, workspace,
+                         status, stream)
+
+
+def cross_attn(q, k_cache, v_cache, block_table, seq_lens, *, max_seq_len: int, q_lens=None,
+               scale: Optional[float] = None, num_splits: int = 0, k_scale: float = 1.0,
+               v_scale: float = 1.0, k_sf=None, v_sf=None, out=None, lse=None, workspace=None,
+               status=None, stream=None):
+    """Attention of every token over all seq_lens[b] keys (an encoder's states),
+    for one new token or a prompt of any length q_len: (out, lse).  Rows from
+    q_lens[b] on are padding: zeros, and an lse of -inf.  Any cache type and
+    layout, as decode_attn(); above 128 query rows per KV head FP8 and 4-bit
+    caches are read back into the workspace."""
+    return _calls().cross(q, k_cache, v_cache, block_table, seq_lens, q_lens, max_seq_len, scale,
+                          num_splits, k_scale, v_scale, k_sf, v_sf, out, lse, workspace, status,
+                          stream)
+
+
+def cache_keep(k_cache, v_cache, block_table, seq_lens, keep, counts, *, new_tokens: int,
+               max_seq_len: int, new_lens=None, k_sf=None, v_sf=None, out_lens=None, status=None,
+               stream=None):
+    """Keep the accepted tokens of a tree: of each request's last new_lens[b] (or
+    new_tokens) tokens those at keep[b, :counts[b]] (int32, rising) move together,
+    in K and V, and the rest are dropped; returns out_lens, the new lengths (which
+    may not be seq_lens itself).  Digests of the pages are the caller's to renew."""
+    return _calls().cache_keep(k_cache, v_cache, block_table, seq_lens, keep, counts, new_tokens,
+                               max_seq_len, new_lens, k_sf, v_sf, out_lens, status, stream)
+
+
+def cache_read(k_cache, v_cache, block_table, seq_lens, *, max_seq_len: int, starts=None,
+               offsets=None, k_scale: float = 1.0, v_scale: float = 1.0, k_sf=None, v_sf=None,
+               k_out=None, v_out=None, status=None, stream=None):
+    """Read a cache of any type back as bf16: (k, v), [B, tokens, Hkv, 128] with
+    token starts[b] + i of a request in row i; or, with `offsets` (int32 [B]) and
+    outputs [rows, Hkv, 128], in row offsets[b] + i.  Rows that no token goes to
+    are left as they were (zeros in outputs that the call allocates)."""
+    return _calls().cache_read(k_cache, v_cache, block_table, seq_lens, max_seq_len, starts,
+                               offsets, k_scale, v_scale, k_sf, v_sf, k_out, v_out, status, stream)

@@ -11,6 +11,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "cache_kernels.cuh"
 #include "decode_attn.h"
 #include "internal.cuh"
 #include "kernels.cuh"
@@ -668,6 +669,7 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
   a.seq_lens = seq_lens;
   a.len_sb = ext.per_head ? p->num_kv_heads : 1;
   a.len_sh = ext.per_head ? 1 : 0;
+  a.own = ext.own;
   a.status = status;
   a.batch = p->batch;
   a.q_len = p->q_len;
@@ -735,6 +737,212 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
     c.by_row = fp4 ? 1 : 0;
     c.unit_heads = unit > 0 ? unit : 1;
     if (dattn::launch_combine(c, st) != cudaSuccess) return DA_ERR_CUDA;
+  }
+  return DA_OK;
+}
+
+namespace {
+
+// A call of more than DECODE_ATTN_MAX_ROWS rows per KV head: chunks of whole
+// 128-key tiles, and the workspace, [K and V in bf16, where the cache is not]
+// [partials].
+struct TallPlan {
+  int32_t chunk, splits;
+  int64_t tokens;              // of a request in the bf16 copy
+  size_t k, v, part_o, part_lse, total;
+};
+
+constexpr int kTallTile = 128;
+
+int tall_plan(const decode_attn_params* p, const decode_attn_cache* c, int32_t num_splits, TallPlan* l) {
+  if (p->max_seq_len > (1 << 30)) return DA_ERR_BAD_SHAPE;
+  const int64_t rows = static_cast<int64_t>(p->num_q_heads / p->num_kv_heads) * p->q_len;
+  const int64_t pairs = ceil_div64(rows, 2 * kTallTile);
+  const int64_t tiles = std::max<int64_t>(1, ceil_div64(p->max_seq_len, kTallTile));
+  int64_t n = num_splits;
+  if (n <= 0) {
+    DeviceInfo di;
+    const int rc = current_device_info(&di);
+    if (rc != DA_OK) return rc;
+    const int64_t items = std::max<int64_t>(1, pairs * p->num_kv_heads * p->batch);
+    n = std::max<int64_t>(1, std::min<int64_t>(ceil_div64(4 * di.sm_count, items), tiles / 8));
+  }
+  n = std::min(n, tiles);
+  const int64_t chunk = ceil_div64(tiles, n) * kTallTile;
+  n = std::max<int64_t>(1, ceil_div64(p->max_seq_len, chunk));
+  if (pairs * n > 0x7fffffff || rows > 0x7fffffff) return DA_ERR_BAD_SHAPE;
+  l->chunk = static_cast<int32_t>(chunk);
+  l->splits = static_cast<int32_t>(n);
+  l->tokens = std::max<int64_t>(p->max_seq_len, 1);
+  size_t off = 0;
+  l->k = off;
+  l->v = off;
+  if (c->type != DA_CACHE_BF16) {
+    const size_t one = static_cast<size_t>(p->batch) * l->tokens * p->num_kv_heads * kHeadDim * 2;
+    l->v = round256(off + one);
+    off = round256(l->v + one);
+  }
+  const size_t part = n > 1 ? static_cast<size_t>(p->batch) * p->q_len * p->num_q_heads * n : 0;
+  l->part_o = off;
+  off = round256(off + part * kHeadDim * 4);
+  l->part_lse = off;
+  l->total = off + part * 4;
+  return DA_OK;
+}
+
+bool is_tall(const decode_attn_params* p) {
+  return static_cast<int64_t>(p->num_q_heads / p->num_kv_heads) * p->q_len > DECODE_ATTN_MAX_ROWS;
+}
+
+}  // namespace
+
+int rows_workspace_bytes(const decode_attn_params* p, const decode_attn_cache* c, int32_t num_splits,
+                         const DecodeExt& ext, size_t* bytes) {
+  if (!is_tall(p)) return workspace_bytes(p, num_splits, ext, bytes);
+  const int rc = check_shape(p, false);
+  if (rc != DA_OK) return rc;
+  if (bytes == nullptr) return DA_ERR_NULL_POINTER;
+  TallPlan l;
+  const int rc2 = tall_plan(p, c, num_splits, &l);
+  if (rc2 == DA_OK) *bytes = l.total;
+  return rc2;
+}
+
+int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void* q,
+             const int32_t* block_table, const int32_t* seq_lens, void* out, float* lse,
+             int32_t num_splits, void* workspace, size_t workspace_bytes, int32_t* status,
+             void* stream, const DecodeExt& ext) {
+  if (!is_tall(p))
+    return run_decode(p, q, c->k, c->v, block_table, seq_lens, out, lse, num_splits, workspace,
+                      workspace_bytes, status, stream, true, ext);
+  int rc = check_shape(p, false);
+  if (rc != DA_OK) return rc;
+  const bool paged = block_table != nullptr;
+  rc = check_paged(p, paged);
+  if (rc != DA_OK) return rc;
+  if (p->batch == 0) return DA_OK;
+  const bool no_keys = p->max_seq_len == 0;
+  if (q == nullptr || seq_lens == nullptr || out == nullptr || lse == nullptr)
+    return DA_ERR_NULL_POINTER;
+  if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(seq_lens) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(block_table) & 3u) != 0 || !stride_ok(p->q_stride_batch) ||
+      !stride_ok(p->q_stride_token) || !stride_ok(p->q_stride_head) ||
+      !stride_ok(p->o_stride_batch) || !stride_ok(p->o_stride_token) ||
+      !stride_ok(p->o_stride_head))
+    return DA_ERR_ALIGNMENT;
+  if (!no_keys) {
+    rc = check_cache(p, c, true, true);
+    if (rc != DA_OK) return rc;
+  }
+  DeviceInfo di;
+  rc = current_device_info(&di);
+  if (rc != DA_OK) return rc;
+  if (di.major * 10 + di.minor < 100) return DA_ERR_NO_DEVICE;
+  TallPlan l;
+  rc = tall_plan(p, c, num_splits, &l);
+  if (rc != DA_OK) return rc;
+  if (l.total > 0 && (workspace == nullptr || workspace_bytes < l.total || !aligned16(workspace)))
+    return DA_ERR_WORKSPACE;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+
+  // keys and values in bf16, as the tensor maps see them
+  const bool copied = c->type != DA_CACHE_BF16;
+  decode_attn_params kp = *p;
+  kp.flags &= ~static_cast<int32_t>(DA_FLAG_KV_FP8_E4M3);
+  const void* k = c->k;
+  const void* v = c->v;
+  if (copied) {
+    kp.kv_stride_head = kHeadDim;
+    kp.kv_stride_token = static_cast<int64_t>(p->num_kv_heads) * kHeadDim;
+    kp.kv_stride_page = kp.kv_stride_token * l.tokens;
+    k = w + l.k;
+    v = w + l.v;
+    if (!no_keys) {
+      // (without the cache's scales every value is exact in bf16; they go into
+      // the score scale and the output)
+      ReadArgs r;
+      std::memset(&r, 0, sizeof(r));
+      r.c = cache_view(p, c);
+      r.g = paging_view(p, block_table, seq_lens, status);
+      r.k = reinterpret_cast<uint16_t*>(w + l.k);
+      r.v = reinterpret_cast<uint16_t*>(w + l.v);
+      r.sb = kp.kv_stride_page;
+      r.st = kp.kv_stride_token;
+      r.sh = kp.kv_stride_head;
+      r.max_tokens = p->max_seq_len;
+      r.k_scale = 1.f;
+      r.v_scale = 1.f;
+      if (launch_read(r, st) != cudaSuccess) return DA_ERR_CUDA;
+    }
+  }
+  const bool tma_paged = paged && !copied;
+  int box = kTallTile;
+  while (tma_paged && p->page_size % box != 0) box /= 2;
+  CUtensorMap kmap, vmap;
+  std::memset(&kmap, 0, sizeof(kmap));
+  std::memset(&vmap, 0, sizeof(vmap));
+  if (!no_keys) {
+    rc = make_kv_map(&kmap, k, &kp, tma_paged, box, false);
+    if (rc == DA_OK) rc = make_kv_map(&vmap, v, &kp, tma_paged, box, false);
+    if (rc != DA_OK) return rc;
+  }
+
+  SplitArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_sb = p->q_stride_batch;
+  a.q_st = p->q_stride_token;
+  a.q_sh = p->q_stride_head;
+  a.out = static_cast<uint16_t*>(out);
+  a.o_sb = p->o_stride_batch;
+  a.o_st = p->o_stride_token;
+  a.o_sh = p->o_stride_head;
+  a.lse = lse;
+  a.part_o = reinterpret_cast<float*>(w + l.part_o);
+  a.part_lse = reinterpret_cast<float*>(w + l.part_lse);
+  a.block_table = tma_paged ? block_table : nullptr;
+  a.bt_stride = p->block_table_stride;
+  a.seq_lens = seq_lens;
+  a.len_sb = 1;
+  a.status = status;
+  a.batch = p->batch;
+  a.q_len = p->q_len;
+  a.num_q_heads = p->num_q_heads;
+  a.num_kv_heads = p->num_kv_heads;
+  a.group = p->num_q_heads / p->num_kv_heads;
+  a.rows = a.group * p->q_len;
+  a.page_size = tma_paged ? p->page_size : 0;
+  a.num_pages = tma_paged ? p->num_pages : 0;
+  a.paged = tma_paged ? 1 : 0;
+  a.max_seq_len = p->max_seq_len;
+  a.chunk_len = l.chunk;
+  a.num_splits = l.splits;
+  a.scale_log2 = p->scale * (copied ? p->k_scale : 1.f) * 1.4426950408889634f;
+  a.v_scale = copied ? p->v_scale : 1.f;
+  a.own = ext.own;
+  if (launch_tall(kmap, vmap, a, box, st) != cudaSuccess) return DA_ERR_CUDA;
+  if (l.splits > 1) {
+    CombineArgs m = {};
+    m.num_kv_heads = p->num_kv_heads;
+    m.part_o = a.part_o;
+    m.part_lse = a.part_lse;
+    m.seq_lens = seq_lens;
+    m.out = a.out;
+    m.o_sb = a.o_sb;
+    m.o_st = a.o_st;
+    m.o_sh = a.o_sh;
+    m.lse = lse;
+    m.batch = p->batch;
+    m.q_len = p->q_len;
+    m.num_q_heads = p->num_q_heads;
+    m.max_seq_len = p->max_seq_len;
+    m.chunk_len = l.chunk;
+    m.num_splits = l.splits;
+    m.len_sb = 1;
+    m.unit_heads = 1;
+    if (launch_combine(m, st) != cudaSuccess) return DA_ERR_CUDA;
   }
   return DA_OK;
 }

@@ -14,6 +14,8 @@
 namespace {
 
 using dattn::aligned16;
+using dattn::cache_view;
+using dattn::paging_view;
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -30,38 +32,6 @@ int check_type(const decode_attn_params* p, const decode_attn_cache* c) {
   if (c->type != DA_CACHE_BF16 && (!std::isfinite(p->k_scale) || !std::isfinite(p->v_scale)))
     return DA_ERR_BAD_SHAPE;
   return DA_OK;
-}
-
-dattn::CacheView cache_view(const decode_attn_params* p, const decode_attn_cache* c) {
-  const int64_t eb = c->type == DA_CACHE_BF16 ? 2 : 1;
-  dattn::CacheView v;
-  v.k = static_cast<uint8_t*>(c->k);
-  v.v = static_cast<uint8_t*>(c->v);
-  v.ks = static_cast<uint8_t*>(c->k_block_scale);
-  v.vs = static_cast<uint8_t*>(c->v_block_scale);
-  v.page = p->kv_stride_page * eb;
-  v.token = p->kv_stride_token * eb;
-  v.head = p->kv_stride_head * eb;
-  v.sf_page = c->bs_stride_page;
-  v.sf_head = c->bs_stride_head;
-  v.type = c->type;
-  return v;
-}
-
-dattn::PagingView paging_view(const decode_attn_params* p, const int32_t* block_table,
-                              const int32_t* seq_lens, int32_t* status) {
-  dattn::PagingView g;
-  g.block_table = block_table;
-  g.bt_stride = p->block_table_stride;
-  g.seq_lens = seq_lens;
-  g.status = status;
-  g.batch = p->batch;
-  g.q_len = p->q_len;
-  g.page_size = block_table != nullptr ? p->page_size : 0;
-  g.num_pages = block_table != nullptr ? p->num_pages : 0;
-  g.max_seq_len = p->max_seq_len;
-  g.num_kv_heads = p->num_kv_heads;
-  return g;
 }
 
 int check_select(const decode_attn_params* p, const decode_attn_select* s) {

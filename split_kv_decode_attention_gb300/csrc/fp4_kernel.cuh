@@ -66,6 +66,7 @@
 #include "decode_attn.h"
 #include "kernels.cuh"
 #include "ptx.cuh"
+#include "rows.cuh"
 
 namespace dattn {
 namespace fp4 {
@@ -209,7 +210,8 @@ struct HalfWindow {
   }
 };
 
-template <int NT, int HG, bool CM>
+// TR: the rows are a tree's or a padded batch's (rows.cuh).
+template <int NT, int HG, bool CM, bool TR>
 __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMinCtas)
     fp4_kernel(const __grid_constant__ Fp4Maps maps, const SplitArgs a) {
   using C = Fp4Cfg<NT, HG>;
@@ -421,6 +423,11 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
   float rs[NT][2];
   int lim[NT][2];
   int lim_all = t_end;  // every row sees the keys below this
+  OwnRows own;
+  if constexpr (TR) {
+    own = own_rows(a.own, a.q_len, b, L, split == 0 && unit == 0 && threadIdx.x == 0, a.status);
+    lim_all = min(t_end, own.base);
+  }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -431,9 +438,15 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
       else e = __shfl_sync(kFull, q_e, (2 * t4 + rr) * 4);
       rs[nt][rr] = ldexpf(a.scale_log2, e);
       int lm = t_end;
-      if (a.causal && row < rows) lm = min(lm, L - a.q_len + 1 + row / a.group);
+      if constexpr (TR) {
+        // (padding rows are dropped at the end and hold up nothing)
+        if (row / a.group >= own.n) lm = 0;
+        else lim_all = min(lim_all, lm);
+      } else {
+        if (a.causal && row < rows) lm = min(lm, L - a.q_len + 1 + row / a.group);
+        lim_all = min(lim_all, lm);
+      }
       lim[nt][rr] = lm;
-      lim_all = min(lim_all, lm);
     }
   lim_all = __reduce_min_sync(kFull, lim_all);
 
@@ -537,6 +550,17 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
 #pragma unroll
             for (int j = 0; j < 2; ++j)
               if (tok0 + 16 * h + 8 * j + krow >= lim[nt][rr]) sc[h][nt][2 * j + rr] = -INFINITY;
+          if constexpr (TR) {
+            const int t = (nt * 8 + 2 * t4 + rr) / a.group;
+            if (tok0 + kWarpKeys > own.base && t < own.n) {
+              const uint32_t seen = own.bits(t, tok0);
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  if (((seen >> (16 * h + 8 * j + krow)) & 1u) == 0) sc[h][nt][2 * j + rr] = -INFINITY;
+            }
+          }
         }
         const float mx = fmaxf(fmax3(sc[0][nt][rr], sc[0][nt][2 + rr], sc[1][nt][rr]), sc[1][nt][2 + rr]);
         move |= mx > m[nt][rr] + kPTop;
@@ -644,6 +668,20 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
 
   if (!CM && threadIdx.x == 0) allow_dependent_launch();
 
+  if constexpr (TR) {
+    // padding rows weigh nothing, whatever their q held, nor do rows that saw
+    // nothing here, whatever the values hold
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int rr = 0; rr < 2; ++rr)
+        if ((nt * 8 + 2 * t4 + rr) / a.group >= own.n || (m[nt][rr] == -INFINITY && l[nt][rr] == 0.f)) {
+          m[nt][rr] = -INFINITY;
+          l[nt][rr] = 0.f;
+#pragma unroll
+          for (int mt = 0; mt < 8; ++mt) acc[mt][nt][rr] = acc[mt][nt][2 + rr] = 0.f;
+        }
+  }
   // ---- the rows' sums over the lanes of the warp
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -848,8 +886,15 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
   }
 }
 
+// DATTN_ROWS (translation units of their own): the instantiations for rows of a
+// tree or a padded batch.
+#ifndef DATTN_ROWS
+#define DATTN_ROWS 0
+#endif
+constexpr bool kOwnRows = DATTN_ROWS != 0;
+
 // Launch the variant of NT row tiles and HG heads.
-template <int NT, int HG, bool CM = false>
+template <int NT, int HG, bool TR, bool CM = false>
 cudaError_t launch_one(const Fp4Maps& maps, const SplitArgs& a, cudaStream_t stream) {
   using C = Fp4Cfg<NT, HG>;
   cudaLaunchConfig_t cfg = {};
@@ -867,24 +912,24 @@ cudaError_t launch_one(const Fp4Maps& maps, const SplitArgs& a, cudaStream_t str
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CM ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, fp4_kernel<NT, HG, CM>, maps, a);
+  return cudaLaunchKernelEx(&cfg, fp4_kernel<NT, HG, CM, TR>, maps, a);
 }
 
 // Set the variant's attributes on the current device; its resident CTAs per SM.
-template <int NT, int HG>
+template <int NT, int HG, bool TR>
 cudaError_t prepare_one(int* ctas) {
   using C = Fp4Cfg<NT, HG>;
-  cudaError_t e = cudaFuncSetAttribute(fp4_kernel<NT, HG, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(fp4_kernel<NT, HG, false, TR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, fp4_kernel<NT, HG, false>, C::kThreads, C::kSmemBytes);
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, fp4_kernel<NT, HG, false, TR>, C::kThreads, C::kSmemBytes);
 }
 
 // The same for the cluster form, and how many clusters of `splits` CTAs fit at once.
-template <int NT>
+template <int NT, bool TR>
 cudaError_t prepare_clusters(int splits, int* clusters) {
   using C = Fp4Cfg<NT, 1>;
-  auto* kernel = fp4_kernel<NT, 1, true>;
+  auto* kernel = fp4_kernel<NT, 1, true, TR>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
@@ -907,7 +952,7 @@ cudaError_t prepare_clusters(int splits, int* clusters) {
 }
 
 // The variants of one row-tile count (a translation unit each).
-template <int NT>
+template <int NT, bool TR>
 struct Variants {
   static cudaError_t launch(int hg, bool cluster, const Fp4Maps& maps, const SplitArgs& a, cudaStream_t stream);
   static cudaError_t prepare(int hg, int* ctas);
@@ -915,34 +960,34 @@ struct Variants {
   static int warps();  // consumer warps of a CTA
 };
 
-#define DATTN_FP4_VARIANTS(NT)                                                                    \
-  template <>                                                                                     \
-  cudaError_t Variants<NT>::launch(int hg, bool cluster, const Fp4Maps& maps, const SplitArgs& a, \
-                                   cudaStream_t st) {                                             \
-    if (cluster) return launch_one<NT, 1, true>(maps, a, st);                                     \
-    switch (hg) {                                                                                 \
-      case 8: return launch_one<NT, kShape[NT / 2][0] == 8 ? 8 : 4>(maps, a, st);                 \
-      case 4: return launch_one<NT, 4>(maps, a, st);                                              \
-      case 2: return launch_one<NT, 2>(maps, a, st);                                              \
-      default: return launch_one<NT, 1>(maps, a, st);                                             \
-    }                                                                                             \
-  }                                                                                               \
-  template <>                                                                                     \
-  cudaError_t Variants<NT>::prepare(int hg, int* ctas) {                                          \
-    switch (hg) {                                                                                 \
-      case 8: return prepare_one<NT, kShape[NT / 2][0] == 8 ? 8 : 4>(ctas);                       \
-      case 4: return prepare_one<NT, 4>(ctas);                                                    \
-      case 2: return prepare_one<NT, 2>(ctas);                                                    \
-      default: return prepare_one<NT, 1>(ctas);                                                   \
-    }                                                                                             \
-  }                                                                                               \
-  template <>                                                                                     \
-  cudaError_t Variants<NT>::clusters(int splits, int* n) {                                        \
-    return prepare_clusters<NT>(splits, n);                                                       \
-  }                                                                                               \
-  template <>                                                                                     \
-  int Variants<NT>::warps() {                                                                     \
-    return kShape[NT / 2][0];                                                                     \
+#define DATTN_FP4_VARIANTS(NT)                                                                          \
+  template <>                                                                                           \
+  cudaError_t Variants<NT, kOwnRows>::launch(int hg, bool cluster, const Fp4Maps& maps, const SplitArgs& a,\
+                                   cudaStream_t st) {                                                   \
+    if (cluster) return launch_one<NT, 1, kOwnRows, true>(maps, a, st);                                 \
+    switch (hg) {                                                                                       \
+      case 8: return launch_one<NT, kShape[NT / 2][0] == 8 ? 8 : 4, kOwnRows>(maps, a, st);             \
+      case 4: return launch_one<NT, 4, kOwnRows>(maps, a, st);                                          \
+      case 2: return launch_one<NT, 2, kOwnRows>(maps, a, st);                                          \
+      default: return launch_one<NT, 1, kOwnRows>(maps, a, st);                                         \
+    }                                                                                                   \
+  }                                                                                                     \
+  template <>                                                                                           \
+  cudaError_t Variants<NT, kOwnRows>::prepare(int hg, int* ctas) {                                      \
+    switch (hg) {                                                                                       \
+      case 8: return prepare_one<NT, kShape[NT / 2][0] == 8 ? 8 : 4, kOwnRows>(ctas);                   \
+      case 4: return prepare_one<NT, 4, kOwnRows>(ctas);                                                \
+      case 2: return prepare_one<NT, 2, kOwnRows>(ctas);                                                \
+      default: return prepare_one<NT, 1, kOwnRows>(ctas);                                               \
+    }                                                                                                   \
+  }                                                                                                     \
+  template <>                                                                                           \
+  cudaError_t Variants<NT, kOwnRows>::clusters(int splits, int* n) {                                    \
+    return prepare_clusters<NT, kOwnRows>(splits, n);                                                   \
+  }                                                                                                     \
+  template <>                                                                                           \
+  int Variants<NT, kOwnRows>::warps() {                                                                 \
+    return kShape[NT / 2][0];                                                                           \
   }
 
 }  // namespace fp4

@@ -7,7 +7,7 @@
 namespace dattn {
 namespace fp4 {
 // (fp4_kernel.cuh; one translation unit per row-tile count defines each)
-template <int NT>
+template <int NT, bool TR>
 struct Variants {
   static cudaError_t launch(int hg, bool cluster, const Fp4Maps& maps, const SplitArgs& a, cudaStream_t stream);
   static cudaError_t prepare(int hg, int* ctas);
@@ -21,8 +21,8 @@ namespace {
 constexpr int kMaxDev = 64;
 constexpr int kMaxCluster = 16;
 std::mutex g_mu;
-int g_ctas[3][4][kMaxDev];                    // resident CTAs per SM by row tiles and heads; 0: not prepared
-int g_clusters[3][kMaxCluster + 1][kMaxDev];  // clusters that fit, plus one; 0: not asked
+int g_ctas[2][3][4][kMaxDev];                    // resident CTAs per SM by form, row tiles and heads; 0: not prepared
+int g_clusters[2][3][kMaxCluster + 1][kMaxDev];  // clusters that fit, plus one; 0: not asked
 
 int variant_of(int rows) { return rows <= 8 ? 0 : rows <= 16 ? 1 : 2; }
 
@@ -32,17 +32,25 @@ cudaError_t current(int* dev) {
   return *dev < 0 || *dev >= kMaxDev ? cudaErrorInvalidDevice : cudaSuccess;
 }
 
-cudaError_t prepare(int rows, int hg, int* ctas) {
+// f(Variants) for the row-tile count of `rows` and the form of the rows.
+template <typename F>
+auto with_variant(int rows, bool own_rows, F f) {
+  switch (variant_of(rows)) {
+    case 0: return own_rows ? f(fp4::Variants<1, true>()) : f(fp4::Variants<1, false>());
+    case 1: return own_rows ? f(fp4::Variants<2, true>()) : f(fp4::Variants<2, false>());
+    default: return own_rows ? f(fp4::Variants<4, true>()) : f(fp4::Variants<4, false>());
+  }
+}
+
+cudaError_t prepare(int rows, bool own_rows, int hg, int* ctas) {
   int dev = 0;
   cudaError_t e = current(&dev);
   if (e != cudaSuccess) return e;
-  const int v = variant_of(rows);
   std::lock_guard<std::mutex> lk(g_mu);
-  int& n = g_ctas[v][hg == 8 ? 3 : hg >> 1][dev];
+  int& n = g_ctas[own_rows][variant_of(rows)][hg == 8 ? 3 : hg >> 1][dev];
   if (n == 0) {
     int got = 0;
-    e = v == 0 ? fp4::Variants<1>::prepare(hg, &got)
-        : v == 1 ? fp4::Variants<2>::prepare(hg, &got) : fp4::Variants<4>::prepare(hg, &got);
+    e = with_variant(rows, own_rows, [&](auto v) { return v.prepare(hg, &got); });
     if (e != cudaSuccess) return e;
     n = got > 0 ? got : 1;
   }
@@ -50,47 +58,46 @@ cudaError_t prepare(int rows, int hg, int* ctas) {
   return cudaSuccess;
 }
 
+bool clusters_fit(int rows, bool own_rows, int num_splits, int64_t num_clusters) {
+  int dev = 0;
+  if (num_splits < 2 || num_splits > kMaxCluster || current(&dev) != cudaSuccess) return false;
+  std::lock_guard<std::mutex> lk(g_mu);
+  int& n = g_clusters[own_rows][variant_of(rows)][num_splits][dev];
+  if (n == 0) {
+    int got = 0;
+    if (with_variant(rows, own_rows, [&](auto v) { return v.clusters(num_splits, &got); }) != cudaSuccess)
+      return false;
+    n = got + 1;
+  }
+  return num_clusters < n;
+}
+
 }  // namespace
 
 cudaError_t launch_fp4(const Fp4Maps& maps, const SplitArgs& a, int heads_per_cta, bool cluster_merge,
                        cudaStream_t stream) {
-  const cudaError_t e = prepare(a.rows, heads_per_cta, nullptr);
+  const bool own_rows = a.own.on != 0;
+  cudaError_t e = prepare(a.rows, own_rows, heads_per_cta, nullptr);
+  // (the cluster form of the plain rows was prepared when the planner asked whether it fits)
+  if (e == cudaSuccess && own_rows && cluster_merge && !clusters_fit(a.rows, true, a.num_splits, 1))
+    return cudaErrorInvalidConfiguration;
   if (e != cudaSuccess) return e;
-  switch (variant_of(a.rows)) {
-    case 0: return fp4::Variants<1>::launch(heads_per_cta, cluster_merge, maps, a, stream);
-    case 1: return fp4::Variants<2>::launch(heads_per_cta, cluster_merge, maps, a, stream);
-    default: return fp4::Variants<4>::launch(heads_per_cta, cluster_merge, maps, a, stream);
-  }
+  return with_variant(a.rows, own_rows,
+                      [&](auto v) { return v.launch(heads_per_cta, cluster_merge, maps, a, stream); });
 }
 
+// (the plans ask about the plain form; the other has its launch shape)
 int fp4_warps(int rows) {
-  switch (variant_of(rows)) {
-    case 0: return fp4::Variants<1>::warps();
-    case 1: return fp4::Variants<2>::warps();
-    default: return fp4::Variants<4>::warps();
-  }
+  return with_variant(rows, false, [](auto v) { return v.warps(); });
 }
 
 int fp4_ctas_per_sm(int rows, int heads_per_cta) {
   int n = 0;
-  return prepare(rows, heads_per_cta, &n) == cudaSuccess ? n : 1;
+  return prepare(rows, false, heads_per_cta, &n) == cudaSuccess ? n : 1;
 }
 
 bool fp4_cluster_merge_fits(int rows, int num_splits, int64_t num_clusters) {
-  int dev = 0;
-  if (num_splits < 2 || num_splits > kMaxCluster || current(&dev) != cudaSuccess) return false;
-  const int v = variant_of(rows);
-  std::lock_guard<std::mutex> lk(g_mu);
-  int& n = g_clusters[v][num_splits][dev];
-  if (n == 0) {
-    int got = 0;
-    const cudaError_t e = v == 0 ? fp4::Variants<1>::clusters(num_splits, &got)
-                          : v == 1 ? fp4::Variants<2>::clusters(num_splits, &got)
-                                   : fp4::Variants<4>::clusters(num_splits, &got);
-    if (e != cudaSuccess) return false;
-    n = got + 1;
-  }
-  return num_clusters < n;
+  return clusters_fit(rows, false, num_splits, num_clusters);
 }
 
 }  // namespace dattn

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "decode_attn.h"
+#include "kernels.cuh"
 
 namespace dattn {
 
@@ -14,6 +15,8 @@ struct DecodeExt {
   const decode_attn_cache* fp4 = nullptr;  // a 4-bit cache (else the params' flags tell)
   // lengths [batch][Hkv] and block-table rows [batch][Hkv][pages] per kv head
   bool per_head = false;
+  // rows of a tree or of a padded batch (kernels.cuh)
+  RowArgs own = {};
 };
 
 // The current device is usable (DA_OK) or not.
@@ -40,6 +43,17 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
                void* out, float* lse, int32_t num_splits, void* workspace,
                size_t workspace_bytes, int32_t* status, void* stream, bool run_combine,
                const DecodeExt& ext = {});
+
+// Attention of the rows that ext.own says (trees, cross attention): as
+// run_decode for up to DECODE_ATTN_MAX_ROWS rows per KV head; with more, bf16
+// caches go to the kernel for many rows, and others are read back into the
+// workspace first.  c holds k, v and what else its type needs.
+int rows_workspace_bytes(const decode_attn_params* p, const decode_attn_cache* c, int32_t num_splits,
+                         const DecodeExt& ext, size_t* bytes);
+int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void* q,
+             const int32_t* block_table, const int32_t* seq_lens, void* out, float* lse,
+             int32_t num_splits, void* workspace, size_t workspace_bytes, int32_t* status,
+             void* stream, const DecodeExt& ext);
 
 // The host plan for equal lengths (max_seq_len each).
 int plan_uniform(const decode_attn_params* p, const DecodeExt& ext, int32_t* num_splits,

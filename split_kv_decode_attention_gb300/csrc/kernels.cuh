@@ -17,6 +17,16 @@ constexpr int kMaxNarrowRows = 16;     // above this: the tcgen05 kernel
 constexpr int kFp4MaxRows = 32;        // 4-bit kernel: rows of a CTA at most
 constexpr int kWideMaxPlannedBatch = 1024;  // tcgen05 kernel: device-planned calls up to this batch
 
+// What the rows of a call see where that is neither every key nor a causal
+// chain (rows.cuh).  Kernels that look at it are instantiations of their own.
+struct RowArgs {
+  int on;                              // 0: nothing of this applies
+  const uint32_t* mask;                // tree: bits of the new tokens that row t sees; nullptr: every key
+  int64_t mask_sb;                     // words between two requests' masks
+  int words;                           // words of a row
+  const int32_t* own_lens;             // rows of each request (nullptr: q_len); the others are padding
+};
+
 // Arguments of the split kernel (one CTA per (chunk, kv head, request)).
 struct SplitArgs {
   const uint16_t* q;                   // bf16 [B, q_len, Hq, D]
@@ -57,6 +67,7 @@ struct SplitArgs {
   int len_sb, len_sh;
   int64_t bt_sh;
   int box_halves;                      // 4-bit kernel: 16-token halves of a box
+  RowArgs own;                         // trees and padded batches (else .on == 0)
 };
 
 // Tensor maps of a 4-bit cache: values [d (64 B), head, slot, group] in boxes
@@ -141,6 +152,14 @@ struct PageWindow {
 cudaError_t launch_split(const CUtensorMap& k_map, const CUtensorMap& v_map, const SplitArgs& a,
                          bool cluster_merge, cudaStream_t stream);
 
+// The same for rows that see what a.own says (launch_split and the others below
+// call them).
+cudaError_t launch_split_rows(const CUtensorMap& k_map, const CUtensorMap& v_map, const SplitArgs& a,
+                              bool cluster_merge, cudaStream_t stream);
+cudaError_t launch_wide_rows(const CUtensorMap& k_map, const CUtensorMap& v_map, const SplitArgs& a,
+                             cudaStream_t stream);
+cudaError_t launch_wide_fp4_rows(const Fp4Maps& maps, const SplitArgs& a, cudaStream_t stream);
+
 // True when clusters of num_splits CTAs (2..16) are supported and the device
 // can hold num_clusters of them at once (one wave).
 bool split_cluster_merge_fits(int rows, bool fp8, int num_splits, int64_t num_clusters);
@@ -173,6 +192,12 @@ cudaError_t launch_fp4(const Fp4Maps& maps, const SplitArgs& a, int heads_per_ct
 bool fp4_cluster_merge_fits(int rows, int num_splits, int64_t num_clusters);
 int fp4_ctas_per_sm(int rows, int heads_per_cta);
 int fp4_warps(int rows);  // consumer warps of a CTA: its heads divide them
+
+// Launch the kernel for more than 128 query rows per KV head (tall_kernel.cu;
+// bf16 keys and values, boxes of box_tokens tokens, chunks of whole 128-key
+// tiles; partials as launch_split).
+cudaError_t launch_tall(const CUtensorMap& k_map, const CUtensorMap& v_map, const SplitArgs& a,
+                        int box_tokens, cudaStream_t stream);
 
 // Launch the combine kernel (one warp per output row, or with by_row and few rows a CTA).
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream);

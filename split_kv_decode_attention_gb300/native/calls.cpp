@@ -602,6 +602,187 @@ PyObject* block_select(PyObject* const* a, Py_ssize_t n) {
   return give({blocks, pages, tokens});
 }
 
+int64_t mask_words(int64_t T) { return (T + 31) / 32; }
+
+PyObject* tree_mask(PyObject* const* a, Py_ssize_t n) {
+  count(n, 8);  // parents, seq_lens, max_seq_len, new_lens, mask, positions, status, stream
+  const at::Tensor &parents = needed(a[0], "parents"), &lens = needed(a[1], "seq_lens");
+  const at::Tensor& new_lens = tensor(a[3], "new_lens");
+  at::Tensor mask = tensor(a[4], "mask"), pos = tensor(a[5], "positions");
+  const at::Tensor& status = tensor(a[6], "status");
+  type_of(parents, at::kInt, "parents");
+  if (parents.dim() != 2 || !parents.is_contiguous()) refuse("parents must be dense [batch, tokens]");
+  const int64_t B = parents.size(0), T = parents.size(1);
+  if (B > 65535 || T < 1 || T > DECODE_ATTN_MAX_TREE)
+    refuse("parents must be of 1 to " + std::to_string(DECODE_ATTN_MAX_TREE) + " tokens and at most 65535 requests");
+  int_vector(lens, B, "seq_lens");
+  if (new_lens.defined()) int_vector(new_lens, B, "new_lens");
+  on_current_device({&parents, &lens, &new_lens, &mask, &pos, &status});
+  const Stream stream(a[7]);
+  if (mask.defined()) dense(mask, at::kInt, {B, T, mask_words(T)}, "mask");
+  else mask = new_result({B, T, mask_words(T)}, at::kInt, parents, stream);
+  if (pos.defined()) dense(pos, at::kInt, {B, T}, "positions");
+  else pos = new_result({B, T}, at::kInt, parents, stream);
+  check(decode_attn_tree_mask(static_cast<int32_t>(B), static_cast<int32_t>(T), integer32(a[2], "max_seq_len"),
+                              static_cast<const int32_t*>(ptr(parents)), static_cast<const int32_t*>(ptr(new_lens)),
+                              static_cast<const int32_t*>(ptr(lens)), static_cast<uint32_t*>(ptr(mask)),
+                              static_cast<int32_t*>(ptr(pos)), status_of(status), stream.raw),
+        "decode_attn_tree_mask");
+  return give({mask, pos});
+}
+
+// Attention whose rows see what a tree's mask (or, without one, cross
+// attention) says.
+PyObject* rows_attention(PyObject* const* a, const at::Tensor& mask, bool tree) {
+  // q, k_cache, v_cache, block_table, seq_lens, [mask], own_lens, max_seq_len, scale, num_splits,
+  // k_scale, v_scale, k_sf, v_sf, out, lse, workspace, status, stream
+  const at::Tensor& q = needed(a[0], "q");
+  const at::Tensor &kc = needed(a[1], "k_cache"), &vc = needed(a[2], "v_cache");
+  const at::Tensor &bt = tensor(a[3], "block_table"), &lens = needed(a[4], "seq_lens");
+  a += tree ? 1 : 0;
+  const at::Tensor& own = tensor(a[5], tree ? "new_lens" : "q_lens");
+  const at::Tensor &k_sf = tensor(a[11], "k_sf"), &v_sf = tensor(a[12], "v_sf");
+  const at::Tensor &out0 = tensor(a[13], "out"), &lse0 = tensor(a[14], "lse");
+  const at::Tensor &given = tensor(a[15], "workspace"), &status = tensor(a[16], "status");
+  if (q.dim() != 4) refuse("q must be [batch, tokens, heads, 128]");
+  const int64_t B = q.size(0), T = q.size(1);
+  heads_tensor(q, B, T, "q");
+  int_vector(lens, B, "seq_lens");
+  if (own.defined()) int_vector(own, B, tree ? "new_lens" : "q_lens");
+  int64_t mask_step = 0;
+  if (tree) {
+    type_of(mask, at::kInt, "mask");
+    const int64_t W = mask_words(T);
+    if (mask.dim() != 3 || (mask.size(0) != B && mask.size(0) != 1) || mask.size(1) != T || mask.size(2) != W ||
+        (W > 1 && mask.stride(2) != 1) || (T > 1 && mask.stride(1) != W) || (mask.size(0) > 1 && mask.stride(0) < 0))
+      refuse("mask must be " + dims({B, T, W}) + " (or one request's, for all), its rows dense");
+    mask_step = mask.size(0) > 1 ? mask.stride(0) : 0;
+  }
+  const Cache c = cache_args(kc, vc, k_sf, v_sf, true);
+  decode_attn_params p = cache_params(B, T, q.size(2), c, kc, bt, integer32(a[6], "max_seq_len"), false,
+                                      scale_or_default(a[7]), number(a[9]), number(a[10]));
+  on_current_device({&q, &kc, &vc, &k_sf, &v_sf, &bt, &lens, &own, &mask, &given, &status, &out0, &lse0});
+  const Stream stream(a[17]);
+  const at::Tensor out = out_or_new(out0, q, stream), lse = lse_or_new(lse0, q, stream);
+  q_strides(p, q, out);
+  const int32_t splits = std::max<int32_t>(0, integer32(a[8], "num_splits"));
+  const char* where = tree ? "decode_attn_tree" : "decode_attn_cross";
+  size_t need = 0;
+  check(tree ? decode_attn_tree_workspace_bytes(&p, &c.c, splits, &need)
+             : decode_attn_cross_workspace_bytes(&p, &c.c, splits, &need),
+        where);
+  const at::Tensor ws = workspace_or_new(given, need, q);
+  const int32_t *own_p = static_cast<const int32_t*>(ptr(own)), *bt_p = static_cast<const int32_t*>(ptr(bt)),
+                *lens_p = static_cast<const int32_t*>(ptr(lens));
+  check(tree ? decode_attn_tree(&p, &c.c, ptr(q), static_cast<const uint32_t*>(ptr(mask)), mask_step, own_p, bt_p,
+                                lens_p, ptr(out), static_cast<float*>(ptr(lse)), splits, ptr(ws), bytes_of(ws),
+                                status_of(status), stream.raw)
+             : decode_attn_cross(&p, &c.c, ptr(q), own_p, bt_p, lens_p, ptr(out), static_cast<float*>(ptr(lse)),
+                                 splits, ptr(ws), bytes_of(ws), status_of(status), stream.raw),
+        where);
+  return give({out, lse});
+}
+
+PyObject* tree(PyObject* const* a, Py_ssize_t n) {
+  count(n, 19);
+  return rows_attention(a, needed(a[5], "mask"), true);
+}
+
+PyObject* cross(PyObject* const* a, Py_ssize_t n) {
+  count(n, 18);
+  return rows_attention(a, undefined(), false);
+}
+
+PyObject* cache_keep(PyObject* const* a, Py_ssize_t n) {
+  count(n, 14);
+  // k_cache, v_cache, block_table, seq_lens, keep, counts, new_tokens, max_seq_len, new_lens,
+  // k_sf, v_sf, out_lens, status, stream
+  const at::Tensor &kc = needed(a[0], "k_cache"), &vc = needed(a[1], "v_cache");
+  const at::Tensor &bt = tensor(a[2], "block_table"), &lens = needed(a[3], "seq_lens");
+  const at::Tensor &keep = needed(a[4], "keep"), &counts = needed(a[5], "counts");
+  const at::Tensor& new_lens = tensor(a[8], "new_lens");
+  const at::Tensor &k_sf = tensor(a[9], "k_sf"), &v_sf = tensor(a[10], "v_sf");
+  at::Tensor out_lens = tensor(a[11], "out_lens");
+  const at::Tensor& status = tensor(a[12], "status");
+  type_of(keep, at::kInt, "keep");
+  if (keep.dim() != 2 || !keep.is_contiguous()) refuse("keep must be dense [batch, tokens]");
+  const int64_t B = keep.size(0), M = keep.size(1);
+  const int32_t T = integer32(a[6], "new_tokens");
+  if (T < 1 || T > DECODE_ATTN_MAX_TREE || M > T)
+    refuse("new_tokens must be 1 to " + std::to_string(DECODE_ATTN_MAX_TREE) + ", and keep no wider");
+  int_vector(lens, B, "seq_lens");
+  int_vector(counts, B, "counts");
+  if (new_lens.defined()) int_vector(new_lens, B, "new_lens");
+  if (out_lens.defined()) int_vector(out_lens, B, "out_lens");
+  const Cache c = cache_args(kc, vc, k_sf, v_sf, true);
+  const decode_attn_params p =
+      cache_params(B, T, c.heads, c, kc, bt, integer32(a[7], "max_seq_len"), false, 1.f, 1.0, 1.0);
+  on_current_device({&kc, &vc, &bt, &lens, &keep, &counts, &new_lens, &k_sf, &v_sf, &out_lens, &status});
+  const Stream stream(a[13]);
+  if (!out_lens.defined()) out_lens = new_result({B}, at::kInt, lens, stream);
+  check(decode_attn_cache_keep(&p, &c.c, static_cast<const int32_t*>(ptr(keep)), static_cast<int32_t>(M),
+                               static_cast<const int32_t*>(ptr(counts)), static_cast<const int32_t*>(ptr(new_lens)),
+                               static_cast<const int32_t*>(ptr(bt)), static_cast<const int32_t*>(ptr(lens)),
+                               static_cast<int32_t*>(ptr(out_lens)), status_of(status), stream.raw),
+        "decode_attn_cache_keep");
+  return give(out_lens);
+}
+
+PyObject* cache_read(PyObject* const* a, Py_ssize_t n) {
+  count(n, 15);
+  // k_cache, v_cache, block_table, seq_lens, max_seq_len, starts, offsets, k_scale, v_scale,
+  // k_sf, v_sf, k_out, v_out, status, stream
+  const at::Tensor &kc = needed(a[0], "k_cache"), &vc = needed(a[1], "v_cache");
+  const at::Tensor &bt = tensor(a[2], "block_table"), &lens = needed(a[3], "seq_lens");
+  const int32_t max_seq_len = integer32(a[4], "max_seq_len");
+  const at::Tensor &starts = tensor(a[5], "starts"), &offsets = tensor(a[6], "offsets");
+  const at::Tensor &k_sf = tensor(a[9], "k_sf"), &v_sf = tensor(a[10], "v_sf");
+  at::Tensor k = tensor(a[11], "k_out"), v = tensor(a[12], "v_out");
+  const at::Tensor& status = tensor(a[13], "status");
+  if (lens.dim() != 1) refuse("seq_lens must be [batch]");
+  const int64_t B = lens.size(0);
+  int_vector(lens, B, "seq_lens");
+  if (starts.defined()) int_vector(starts, B, "starts");
+  if (offsets.defined()) int_vector(offsets, B, "offsets");
+  const Cache c = cache_args(kc, vc, k_sf, v_sf, true);
+  const decode_attn_params p =
+      cache_params(B, 1, c.heads, c, kc, bt, max_seq_len, false, 1.f, number(a[7]), number(a[8]));
+  if (k.defined() != v.defined()) refuse("k_out and v_out are given together");
+  if (!k.defined() && offsets.defined()) refuse("offsets need k_out and v_out");
+  on_current_device({&kc, &vc, &bt, &lens, &starts, &offsets, &k_sf, &v_sf, &k, &v, &status});
+  const Stream stream(a[14]);
+  if (!k.defined()) {
+    if (max_seq_len < 0) refuse("max_seq_len is negative");
+    for (at::Tensor* t : {&k, &v}) {
+      *t = at::zeros({B, max_seq_len, c.heads, kD}, kc.options().dtype(at::kBFloat16));
+      stream.returns(*t);
+    }
+  }
+  decode_attn_read r;
+  std::memset(&r, 0, sizeof(r));
+  const int64_t first = offsets.defined() ? 0 : 1;  // the dimension of tokens
+  for (const at::Tensor* t : {&k, &v}) {
+    type_of(*t, at::kBFloat16, "k_out or v_out");
+    if (t->dim() != 3 + first || (first == 1 && t->size(0) != B) || t->size(first + 1) != c.heads ||
+        t->size(first + 2) != kD || t->stride(first + 2) != 1)
+      refuse("k_out and v_out must be " +
+             (first == 1 ? "[" + std::to_string(B) + ", tokens, " : std::string("[rows, ")) + std::to_string(c.heads) +
+             ", 128], their last dimension dense");
+  }
+  if (k.sizes() != v.sizes() || !same_steps(k, v)) refuse("k_out and v_out differ in shape or strides");
+  if (k.size(first) > INT32_MAX) refuse("k_out has too many rows");
+  r.max_tokens = offsets.defined() ? max_seq_len : static_cast<int32_t>(k.size(1));
+  r.rows = first == 0 ? k.size(0) : 0;
+  r.stride_batch = first == 1 ? step(k, 0) : 4 * kD;
+  r.stride_token = step(k, first);
+  r.stride_head = step(k, first + 1);
+  check(decode_attn_cache_read(&p, &c.c, &r, static_cast<const int32_t*>(ptr(starts)),
+                               static_cast<const int32_t*>(ptr(offsets)), static_cast<const int32_t*>(ptr(bt)),
+                               static_cast<const int32_t*>(ptr(lens)), ptr(k), ptr(v), status_of(status), stream.raw),
+        "decode_attn_cache_read");
+  return give({k, v});
+}
+
 PyObject* set_error(PyObject* const* a, Py_ssize_t n) {
   count(n, 1);
   Py_INCREF(a[0]);
@@ -646,6 +827,11 @@ PyMethodDef g_methods[] = {
     {"decode_cached", fast<decode_cached>(), METH_FASTCALL, nullptr},
     {"block_select", fast<block_select>(), METH_FASTCALL, nullptr},
     {"sparse", fast<sparse>(), METH_FASTCALL, nullptr},
+    {"tree_mask", fast<tree_mask>(), METH_FASTCALL, nullptr},
+    {"tree", fast<tree>(), METH_FASTCALL, nullptr},
+    {"cross", fast<cross>(), METH_FASTCALL, nullptr},
+    {"cache_keep", fast<cache_keep>(), METH_FASTCALL, nullptr},
+    {"cache_read", fast<cache_read>(), METH_FASTCALL, nullptr},
     {"set_error", fast<set_error>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
