@@ -744,7 +744,7 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
 namespace {
 
 // A call of more than DECODE_ATTN_MAX_ROWS rows per KV head: chunks of whole
-// 128-key tiles, and the workspace, [K and V in bf16, where the cache is not]
+// 128-token tiles, and the workspace, [K and V in bf16, where the cache is not]
 // [partials].
 struct TallPlan {
   int32_t chunk, splits;
@@ -756,8 +756,9 @@ constexpr int kTallTile = 128;
 
 int tall_plan(const decode_attn_params* p, const decode_attn_cache* c, int32_t num_splits, TallPlan* l) {
   if (p->max_seq_len > (1 << 30)) return DA_ERR_BAD_SHAPE;
-  const int64_t rows = static_cast<int64_t>(p->num_q_heads / p->num_kv_heads) * p->q_len;
-  const int64_t pairs = ceil_div64(rows, 2 * kTallTile);
+  const int64_t group = p->num_q_heads / p->num_kv_heads;
+  const int64_t rows = group * p->q_len;
+  const int64_t pairs = ceil_div64(p->q_len, 2 * tall_tile_tokens(static_cast<int>(group)));
   const int64_t tiles = std::max<int64_t>(1, ceil_div64(p->max_seq_len, kTallTile));
   int64_t n = num_splits;
   if (n <= 0) {
@@ -878,11 +879,24 @@ int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void
     }
   }
   const bool tma_paged = paged && !copied;
-  int box = kTallTile;
+  int box = 128;
   while (tma_paged && p->page_size % box != 0) box /= 2;
-  CUtensorMap kmap, vmap;
+  CUtensorMap qmap, kmap, vmap;
   std::memset(&kmap, 0, sizeof(kmap));
   std::memset(&vmap, 0, sizeof(vmap));
+  const int group = p->num_q_heads / p->num_kv_heads;
+  {
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(p->num_q_heads),
+                                static_cast<cuuint64_t>(p->q_len), static_cast<cuuint64_t>(p->batch)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p->q_stride_head) * 2,
+                                   static_cast<cuuint64_t>(p->q_stride_token) * 2,
+                                   static_cast<cuuint64_t>(p->q_stride_batch) * 2};
+    const cuuint32_t qbox[4] = {64, static_cast<cuuint32_t>(group),
+                                static_cast<cuuint32_t>(tall_tile_tokens(group)), 1};
+    rc = encode_map(&qmap, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, qbox, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    if (rc != DA_OK) return rc;
+  }
   if (!no_keys) {
     rc = make_kv_map(&kmap, k, &kp, tma_paged, box, false);
     if (rc == DA_OK) rc = make_kv_map(&vmap, v, &kp, tma_paged, box, false);
@@ -911,8 +925,8 @@ int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void
   a.q_len = p->q_len;
   a.num_q_heads = p->num_q_heads;
   a.num_kv_heads = p->num_kv_heads;
-  a.group = p->num_q_heads / p->num_kv_heads;
-  a.rows = a.group * p->q_len;
+  a.group = group;
+  a.rows = group * p->q_len;
   a.page_size = tma_paged ? p->page_size : 0;
   a.num_pages = tma_paged ? p->num_pages : 0;
   a.paged = tma_paged ? 1 : 0;
@@ -922,7 +936,7 @@ int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void
   a.scale_log2 = p->scale * (copied ? p->k_scale : 1.f) * 1.4426950408889634f;
   a.v_scale = copied ? p->v_scale : 1.f;
   a.own = ext.own;
-  if (launch_tall(kmap, vmap, a, box, st) != cudaSuccess) return DA_ERR_CUDA;
+  if (launch_tall(qmap, kmap, vmap, a, box, st) != cudaSuccess) return DA_ERR_CUDA;
   if (l.splits > 1) {
     CombineArgs m = {};
     m.num_kv_heads = p->num_kv_heads;

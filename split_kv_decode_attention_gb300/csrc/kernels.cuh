@@ -194,10 +194,12 @@ int fp4_ctas_per_sm(int rows, int heads_per_cta);
 int fp4_warps(int rows);  // consumer warps of a CTA: its heads divide them
 
 // Launch the kernel for more than 128 query rows per KV head (tall_kernel.cu;
-// bf16 keys and values, boxes of box_tokens tokens, chunks of whole 128-key
-// tiles; partials as launch_split).
-cudaError_t launch_tall(const CUtensorMap& k_map, const CUtensorMap& v_map, const SplitArgs& a,
-                        int box_tokens, cudaStream_t stream);
+// bf16 keys and values, boxes of box_tokens tokens, chunks of whole 64-key
+// steps; partials as launch_split).
+// Boxes of Q: 64 d of a group's heads, tall_tile_tokens() tokens.
+cudaError_t launch_tall(const CUtensorMap& q_map, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                        const SplitArgs& a, int box_tokens, cudaStream_t stream);
+int tall_tile_tokens(int group);
 
 // Launch the combine kernel (one warp per output row, or with by_row and few rows a CTA).
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream);

@@ -101,6 +101,23 @@ __device__ __forceinline__ bool mbar_wait_lazy(uint64_t* bar, uint32_t parity) {
   return mbar_wait_for(bar, parity, kWaitLimitNs);
 }
 
+// The whole warp waits (its result is the same in every lane): for the role that
+// feeds the tensor cores, where every instruction between a completed phase and
+// the next MMA counts.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar_addr, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar_addr), "r"(parity)
+      : "memory");
+  if (__all_sync(0xffffffffu, done != 0)) return true;
+  uint64_t* bar = static_cast<uint64_t*>(__cvta_shared_to_generic(bar_addr));
+  return __all_sync(0xffffffffu, mbar_wait_lazy(bar, parity)) != 0;
+}
+
 // Wait for the phase with the given parity to complete; false on time-out.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   return mbar_wait_for(bar, parity, kWaitLimitNs);
@@ -342,6 +359,34 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Cluster launch control: ask for the next CTA of this grid that has not begun,
+// in its place; 16 bytes of answer arrive in `answer` (16-byte aligned) and count
+// on `bar`, which expects them.
+__device__ __forceinline__ void try_cancel(void* answer, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_addr(answer)),
+      "r"(smem_addr(bar))
+      : "memory");
+}
+
+// The answer: false when no CTA is left (then no further one may be asked for),
+// else its block index.
+__device__ __forceinline__ bool canceled_block(const void* answer, uint32_t& x, uint32_t& y, uint32_t& z) {
+  uint32_t got;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
+      "ld.shared.b128 h, [%4];\n\t"
+      "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, %3, _}, h;\n\t}"
+      : "=&r"(got), "=&r"(x), "=&r"(y), "=&r"(z)
+      : "r"(smem_addr(answer))
+      : "memory");
+  return got != 0;
 }
 
 // Programmatic dependent launch: wait until the grids this one depends on

@@ -7,24 +7,35 @@
 //     s_rj = scale q_r . k_j,   o_r = sum_j softmax(s_r)_j v_j,
 // in one pass with the running maximum m and sum l: when m grows, l and o are
 // scaled by 2^(m - m').  With 256 rows a key is used 256 times per read, so the
-// tensor pipe bounds the kernel and not HBM: per 128 keys and 256 rows it is busy
-// for 4 x 128^3 x 2 multiply-adds, and everything else has to fit beside that.
+// tensor pipe bounds the kernel and not HBM, and everything else has to fit
+// beside it.
 //
-// A CTA takes 256 rows as two tiles of 128, one per softmax warpgroup, over a
-// chunk of the keys, 128 at a time.  Per key tile and row tile the tensor core
-// makes S = Q K^T (Q, K from shared memory) and O += P V (P from TMEM): while it
-// works for one row tile, the other's warpgroup turns its scores into P, so that
-// neither waits for long.  TMEM holds S of both tiles (128 columns each; P, in
-// bf16, replaces the first 64 of them) and both O: all 512 columns.  The MMAs of
-// one thread run in the order of their issue, so the next S of a tile is issued
-// behind the P V that reads the P it overwrites, and its completion also says
-// that O may be touched.
+// An item is two tiles of up to 128 rows (whole tokens: 128 / G of them each)
+// over a chunk of the keys, 64 keys a step.  Per step and row tile the tensor
+// core makes S = Q K^T (both from shared memory) and O += P V (P from TMEM); a
+// warpgroup per row tile turns S into P.  TMEM holds both O (256 columns) and
+// for each tile two buffers of S (64 columns each; P, in bf16, replaces the
+// first half of its S), so that the S of the next step is made while a
+// warpgroup works on this one, and the tensor core waits for neither.  (With
+// one buffer of 128 keys per tile every step was a chain of softmax, P V and S:
+// 3590 cycles per 128 keys and 256 rows, of which the tensor core worked 2000.)
+// The MMAs of one thread run in the order of their issue: S of step i + 2 is
+// issued behind the P V of step i, whose P it overwrites.
 // O is rescaled only when a row's maximum has grown by more than 2^8 (P stays
-// below 2^8 and is exact in the end's division), which is rare after the first
-// tiles.  P is rounded to bf16; O is divided by the sum of the rounded weights,
-// the log-sum-exp takes the sum of the fp32 ones.
-// Three producer warps fill a ring of five 32 KB slots (128 keys of K or of V)
-// with TMA boxes of up to 128 tokens (what divides a page).
+// below 2^8, and the end's division is exact about it), which is rare after the
+// first steps; the warpgroup then waits until the P V before has been done.  P
+// is rounded to bf16 for the product, 2^-9 of each weight; the sum that O is
+// divided by is that of the unrounded ones (summing the rounded ones too, as the
+// kernels for fewer rows do, took 9 % longer).
+//
+// A CTA per SM takes item after item: it asks the hardware for the grid's next
+// block in place of a CTA of its own (cluster launch control), so items of
+// unequal lengths balance without a counter in memory, and the copies and the
+// first S of an item overlap the end of the one before.  Roles: warp 0
+// MMA, 1 schedule and Q, 2-6 K and V, 8-15 softmax.  K and V go through a ring of
+// five 32 KB slots (128 keys of K or of V), a warp to each; TMA boxes are of up to
+// 128 tokens (what divides a page).  Boxes that one warp issues are serialised
+// (130 to 240 cycles), and a step of 16-token pages has 32.
 // Values of keys behind a sequence may be anything: they are zeroed in shared
 // memory (0 x NaN is NaN).  Every wait is bounded.
 
@@ -41,31 +52,54 @@ namespace {
 
 constexpr float kLn2t = 0.6931471805599453f;
 constexpr int kTRows = 128;                       // rows of a tile (MMA M)
-constexpr int kTKeys = 128;                       // keys of a tile (MMA N of S, K of P V)
-constexpr int kTHalf = kTKeys * 128;              // [128 tokens][64 d] bf16 = 16 KB
-constexpr int kTSlot = 2 * kTHalf;                // K or V of a key tile
+constexpr int kTKeys = 128;                       // keys of a step (MMA N of S, K of P V)
+constexpr int kTQHalf = kTRows * 128;             // [128 rows][64 d] bf16
+constexpr int kTQTile = 2 * kTQHalf;
+constexpr int kTHalf = kTKeys * 128;              // [64 tokens][64 d] bf16
+constexpr int kTSlot = 2 * kTHalf;                // K or V of a step
 constexpr int kTSlots = 5;
-constexpr int kTProducers = 3;
-constexpr int kTMmaWarp = 8;
-constexpr int kTThreads = 32 * (kTMmaWarp + 1 + kTProducers);
-constexpr int kTOffRing = 2 * kTSlot;             // behind the two Q tiles
+constexpr int kTMmaWarp = 0;
+constexpr int kTSchedWarp = 1;
+constexpr int kTProdWarp = 2;
+constexpr int kTSoftmaxWarp = 8;                  // to 15: the last two warpgroups
+// A producer warp per slot: one that filled slots in turn with others could
+// meet a slot's barrier a whole round early, where its parity says "free".
+constexpr int kTProducers = kTSlots;
+constexpr int kTThreads = 512;                    // (one warp is idle: setmaxnreg takes whole warpgroups)
+static_assert(kTProdWarp + kTProducers <= kTSoftmaxWarp && 32 * (kTSoftmaxWarp + 8) == kTThreads, "warps");
+constexpr int kTReaders = 8 + 1 + kTProducers;    // warps that read an item's descriptor
+constexpr int kTOffRing = 2 * kTQTile;
 constexpr int kTOffBar = kTOffRing + kTSlots * kTSlot;
-constexpr int kTBars = 2 * kTSlots + 1 + 2 + 2 + 2 + 1;
-constexpr int kTSmem = 1024 + kTOffBar + kTBars * 8 + 16;
+constexpr int kTBars = 2 * kTSlots + 2 + 2 + 2 + 4 + 2 + 2 + 2 + 1 + 1;
+constexpr int kTOffItems = kTOffBar + kTBars * 8 + 8;      // 16-byte aligned below
+constexpr int kTSmem = 1024 + kTOffItems + 16 + 2 * 64 + 32;
 static_assert(kTSmem <= 227 * 1024, "shared memory");
 constexpr uint32_t kTTmemCols = 512;
-constexpr uint32_t kTColO = 256;
-constexpr float kTRescale = 8.f;                  // log2 units
-// registers: 65536 / 384 threads, rounded down to 8, is what the launch gives
+constexpr uint32_t kTColO = 256;                  // S of tile g at 128 g, O at 256 + 128 g
+constexpr float kTRescale = 64.f;                 // log2 units
+constexpr int kTAhead = 4;                        // steps before an item's end when the next is asked for
+// registers: 65536 / 512 threads is what the launch gives
 constexpr int kTLaunchRegs = 65536 / kTThreads / 8 * 8;
 constexpr int kTSoftmaxRegs = 208;
-constexpr int kTOtherRegs = 80;
-static_assert(256 * kTSoftmaxRegs + 128 * kTOtherRegs <= kTThreads * kTLaunchRegs,
+constexpr int kTOtherRegs = 48;
+static_assert(256 * kTSoftmaxRegs + (kTThreads - 256) * kTOtherRegs <= kTThreads * kTLaunchRegs,
               "the register split would wait forever");
 
 struct TallMaps {
-  CUtensorMap k, v;
+  CUtensorMap q, k, v;
 };
+
+// One item, in shared memory: written by the scheduler warp.
+struct TallItem {
+  int valid;             // 0: no item is left
+  int b, kvh, split;
+  int tok0;              // first token of the two row tiles
+  int L, own, base;      // length, the request's own tokens, first key that goes by the mask
+  int t_begin, t_end;    // keys
+  int steps;             // 0 where no row sees a key
+  int tiles;             // row tiles with own rows (0 with steps)
+};
+static_assert(sizeof(TallItem) <= 64, "item slots");
 
 __global__ void __launch_bounds__(kTThreads, 1)
     tall_kernel(const __grid_constant__ TallMaps maps, const SplitArgs a, const int box_tokens) {
@@ -74,381 +108,492 @@ __global__ void __launch_bounds__(kTThreads, 1)
   const int warp = tid >> 5;
   const int lane = tid & 31;
 
-  grid_dependency_wait();
-
-  // ---- this CTA's item: chunk `split` of request b, KV head kvh, rows r0 ..
-  const int S = a.num_splits;
-  const int pair = blockIdx.x / S;
-  const int split = blockIdx.x - pair * S;
-  const int kvh = blockIdx.y;
-  const int b = blockIdx.z;
-  const int chunk = a.chunk_len;
-  int L = a.seq_lens[b];
-  const bool report = blockIdx.x == 0 && kvh == 0 && tid == 0;
-  if (L < 0 || L > a.max_seq_len) {
-    if (report && a.status != nullptr) atomicOr(a.status, static_cast<int32_t>(DA_STATUS_SEQ_LEN));
-    L = L < 0 ? 0 : a.max_seq_len;
-  }
-  const OwnRows own = own_rows(a.own, a.q_len, b, L, report, a.status);
-  const int nsplit_b = L > 0 ? (L + chunk - 1) / chunk : 1;
-  if (split >= nsplit_b) return;
-  const int t_begin = split * chunk;
-  const int t_end = min(L, t_begin + chunk);
-  const int n_iters = t_end > t_begin ? (t_end - t_begin + kTKeys - 1) / kTKeys : 0;
-  const int r0 = pair * 2 * kTRows;
-  const int own_rows_n = min(a.rows, own.n * a.group);  // (rows are (t, g), t slowest)
-  // row tiles with rows of the request's own; none without keys
-  const int tiles = n_iters == 0 ? 0 : r0 + kTRows < own_rows_n ? 2 : r0 < own_rows_n ? 1 : 0;
-
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + kTOffBar);  // [slots] bytes landed
   uint64_t* empty_bar = full_bar + kTSlots;                           // [slots] read by the MMAs
-  uint64_t* q_full = empty_bar + kTSlots;                             // Q in shared memory
-  uint64_t* s_full = q_full + 1;                                      // [2] scores in TMEM
-  uint64_t* p_full = s_full + 2;                                      // [2] P in TMEM
-  uint64_t* o_done = p_full + 2;                                      // [2] the last P V
-  uint64_t* tmem_done = o_done + 2;
+  uint64_t* q_full = empty_bar + kTSlots;                             // [2] Q tile landed
+  uint64_t* q_empty = q_full + 2;                                     // [2] read by the item's last S
+  uint64_t* s_full = q_empty + 2;                                     // [2] S in TMEM, the P V before done
+  uint64_t* p_full = s_full + 2;                                      // [tile][half] 64 keys of P in TMEM
+  uint64_t* o_done = p_full + 4;                                      // [2] the item's last P V
+  uint64_t* item_full = o_done + 2;                                   // [2] descriptor written
+  uint64_t* item_empty = item_full + 2;                               // [2] descriptor read
+  uint64_t* ask_bar = item_empty + 2;                                 // the scheduler's answer
+  uint64_t* tmem_done = ask_bar + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tmem_done + 1);
+  int* near_end = reinterpret_cast<int*>(tmem_slot + 1);              // items that the MMA warp is about to end
+  uint8_t* answer = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem + kTOffItems) + 15) & ~static_cast<uintptr_t>(15));
+  TallItem* items = reinterpret_cast<TallItem*>(answer + 16);         // [2], 64 bytes each
+  auto item_slot = [&](int k) { return reinterpret_cast<TallItem*>(reinterpret_cast<uint8_t*>(items) + (k & 1) * 64); };
 
-  if (tiles > 0) {  // (the same for the whole CTA)
-    if (tid == 0) {
-      for (int s = 0; s < kTSlots; ++s) {
-        mbar_init(&full_bar[s], 1);
-        mbar_init(&empty_bar[s], 1);
-      }
-      mbar_init(q_full, 8);
-      for (int g = 0; g < 2; ++g) {
-        mbar_init(&s_full[g], 1);
-        mbar_init(&p_full[g], 4);
-        mbar_init(&o_done[g], 1);
-      }
-      mbar_init(tmem_done, 8);
-      fence_mbar_init();
+  if (tid == 0) {
+    for (int s = 0; s < kTSlots; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
     }
-    if (warp == kTMmaWarp) {
-      tmem_alloc(tmem_slot, kTTmemCols);
-      tmem_relinquish();
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&o_done[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], kTReaders);
     }
-    tc_fence_before_sync();
-    __syncthreads();
-    tc_fence_after_sync();
+    for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], 4);
+    mbar_init(ask_bar, 1);
+    mbar_init(tmem_done, 8);
+    fence_mbar_init();
+    *near_end = 0;
   }
+  if (warp == kTMmaWarp) {
+    tmem_alloc(tmem_slot, kTTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  grid_dependency_wait();
   const uint32_t smem_base = smem_addr(smem);
+  const int S = a.num_splits;
+  const int tile_tokens = kTRows / a.group;  // of a row tile
+  auto report = [&]() {
+    if (lane == 0 && a.status != nullptr) atomicOr(a.status, static_cast<int32_t>(DA_STATUS_TIMEOUT));
+  };
+  // Item k as every role but the scheduler gets it; false at the end, or (with
+  // ok false) when the wait ran out.
+  bool ok = true;
+  auto next_item = [&](int k) {
+    ok = __all_sync(kFull, mbar_wait(&item_full[k & 1], (k >> 1) & 1)) != 0;
+    return ok && item_slot(k)->valid != 0;
+  };
+  auto leave_item = [&](int k) {  // its descriptor may be overwritten
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_empty[k & 1]);
+  };
 
-  if (warp >= kTMmaWarp) {
+  if (warp < kTSoftmaxWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTOtherRegs));
-    if (tiles == 0) return;
-    const uint32_t tmem = *tmem_slot;
-    if (warp > kTMmaWarp) {
-      // ========================================================== TMA producers
-      // unit u: K (even) or V (odd) of key tile u / 2, in slot u % kTSlots; each
-      // producer warp takes every third.  A lane issues one box.
-      const int pw = warp - kTMmaWarp - 1;
+    if (warp == kTSchedWarp) {
+      // ===================================================== schedule, and Q
+      if (lane == 0) {
+        prefetch_tensor_map(&maps.q);
+        uint32_t x = blockIdx.x, y = blockIdx.y, z = blockIdx.z;
+        bool have = true;
+        int q_use[2] = {0, 0};
+        const uint32_t q_bytes = static_cast<uint32_t>(tile_tokens * a.group) * 256u;
+        for (int k = 0; ok; ++k) {
+          if (k > 0) {
+            // the next item once the one before nears its end
+            const unsigned long long t0 = global_timer_ns();
+            while (*static_cast<volatile int*>(near_end) < k) {
+              __nanosleep(100);
+              if (global_timer_ns() - t0 > 4 * kWaitLimitNs) {
+                ok = false;
+                break;
+              }
+            }
+            if (!ok) break;
+            mbar_arrive_expect_tx(ask_bar, 16);
+            try_cancel(answer, ask_bar);
+            ok = mbar_wait(ask_bar, (k - 1) & 1);
+            if (!ok) break;
+            have = canceled_block(answer, x, y, z);
+            fence_proxy_async_smem();  // (read before the next answer is written)
+          }
+          TallItem it = {};
+          it.valid = have ? 1 : 0;
+          if (have) {
+            it.b = static_cast<int>(z);
+            it.kvh = static_cast<int>(y);
+            const int pair = static_cast<int>(x) / S;
+            it.split = static_cast<int>(x) - pair * S;
+            it.tok0 = pair * 2 * tile_tokens;
+            const bool first = x == 0 && y == 0;
+            int L = a.seq_lens[it.b];
+            if (L < 0 || L > a.max_seq_len) {
+              if (first && a.status != nullptr) atomicOr(a.status, static_cast<int32_t>(DA_STATUS_SEQ_LEN));
+              L = L < 0 ? 0 : a.max_seq_len;
+            }
+            const OwnRows own = own_rows(a.own, a.q_len, it.b, L, first, a.status);
+            it.L = L;
+            it.own = own.n;
+            it.base = own.base;
+            it.t_begin = it.split * a.chunk_len;
+            it.t_end = min(L, it.t_begin + a.chunk_len);
+            it.steps = it.t_end > it.t_begin ? (it.t_end - it.t_begin + kTKeys - 1) / kTKeys : 0;
+            it.tiles = own.n > it.tok0 + tile_tokens ? 2 : own.n > it.tok0 ? 1 : 0;
+            if (it.steps == 0 || it.tiles == 0) it.steps = it.tiles = 0;
+          }
+          if (k > 1) ok = mbar_wait(&item_empty[k & 1], ((k >> 1) - 1) & 1);
+          if (!ok) break;
+          *item_slot(k) = it;
+          mbar_arrive(&item_full[k & 1]);
+          if (!have) break;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            if (g >= it.tiles) break;
+            if (q_use[g] > 0) ok = mbar_wait(&q_empty[g], (q_use[g] - 1) & 1);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&q_full[g], q_bytes);
+            for (int h = 0; h < 2; ++h)
+              tma_load_4d_plain(smem + g * kTQTile + h * kTQHalf, &maps.q, &q_full[g], h * 64, it.kvh * a.group,
+                                it.tok0 + g * tile_tokens, it.b);
+            ++q_use[g];
+          }
+        }
+        if (!ok) {
+          report();
+#pragma unroll
+          for (int g = 0; g < 2; ++g)  // no copy may still be landing when the CTA exits
+            if (q_use[g] > 0) mbar_wait(&q_full[g], (q_use[g] - 1) & 1);
+        }
+      }
+      return;
+    }
+    if (warp >= kTProdWarp) {
+      // ====================================================== K and V copies
+      // unit u (over all items): K (even) or V (odd) of a step, in slot u %
+      // kTSlots, which is filled by the warp of that number.  A lane issues one box.
+      const int pw = warp - kTProdWarp;
+      if (pw >= kTProducers) return;
       if (lane == 0 && pw == 0) {
         prefetch_tensor_map(&maps.k);
         prefetch_tensor_map(&maps.v);
       }
-      const int boxes = 2 * (kTKeys / box_tokens);  // of a unit: [token box][d half]
+      const int boxes = kTKeys / box_tokens;         // of a d half
       const int half = lane & 1;
-      const int box_tok = (lane >> 1) * box_tokens;  // of the lane's box in the tile
+      const int box_tok = (lane >> 1) * box_tokens;  // of the lane's box in the step
       const uint32_t box_bytes = static_cast<uint32_t>(box_tokens) * 128u;
-      const int32_t* bt_row = a.paged ? a.block_table + static_cast<int64_t>(b) * a.bt_stride : nullptr;
-      auto page_of = [&](int u) {
-        const int64_t tok = static_cast<int64_t>(t_begin) + static_cast<int64_t>(u >> 1) * kTKeys + box_tok;
-        return bt_row != nullptr && lane < boxes && tok < t_end ? __ldg(bt_row + tok / a.page_size) : 0;
-      };
-      const int units = 2 * n_iters;
-      int last = -1;
-      bool ok = true;
-      int pg_next = page_of(pw);
-      for (int u = pw; u < units; u += kTProducers) {
-        const int s = u % kTSlots, use = u / kTSlots;
-        int pg = pg_next;
-        pg_next = page_of(u + kTProducers);
-        if (use > 0) ok = __all_sync(kFull, mbar_wait_lazy(&empty_bar[s], (use - 1) & 1)) != 0;
-        if (!ok) break;
-        const int tok0 = t_begin + (u >> 1) * kTKeys;
-        const int live = min(kTKeys / box_tokens, (t_end - tok0 + box_tokens - 1) / box_tokens);
-        if (lane == 0) mbar_arrive_expect_tx(&full_bar[s], 2u * live * box_bytes);
-        __syncwarp();
-        if (lane < 2 * live) {
-          if (a.paged && static_cast<unsigned>(pg) >= static_cast<unsigned>(a.num_pages)) {
-            if (a.status != nullptr) atomicOr(a.status, static_cast<int32_t>(DA_STATUS_BAD_PAGE));
-            pg = 0;
+      int ubase = 0, last = -1;
+      for (int k = 0; next_item(k); ++k) {
+        const TallItem it = *item_slot(k);
+        leave_item(k);
+        const int32_t* bt_row = a.paged ? a.block_table + static_cast<int64_t>(it.b) * a.bt_stride : nullptr;
+        auto page_of = [&](int u) {
+          const int tok = it.t_begin + (u >> 1) * kTKeys + box_tok;  // (max_seq_len is at most 2^30)
+          return bt_row != nullptr && lane < 2 * boxes && tok < it.t_end ? __ldg(bt_row + tok / a.page_size) : 0;
+        };
+        const int units = 2 * it.steps;
+        int u = (pw - ubase) % kTProducers;  // the warp's first unit of the item
+        if (u < 0) u += kTProducers;
+        int pg_next = page_of(u);
+        for (; u < units; u += kTProducers) {
+          const int s = pw, use = (ubase + u) / kTSlots;
+          int pg = pg_next;
+          pg_next = page_of(u + kTProducers);
+          if (use > 0) ok = __all_sync(kFull, mbar_wait_lazy(&empty_bar[s], (use - 1) & 1)) != 0;
+          if (!ok) break;
+          const int tok0 = it.t_begin + (u >> 1) * kTKeys;
+          const int live = min(boxes, (it.t_end - tok0 + box_tokens - 1) / box_tokens);
+          if (lane == 0) mbar_arrive_expect_tx(&full_bar[s], 2u * live * box_bytes);
+          __syncwarp();
+          if (lane < 2 * live) {
+            if (a.paged && static_cast<unsigned>(pg) >= static_cast<unsigned>(a.num_pages)) {
+              if (a.status != nullptr) atomicOr(a.status, static_cast<int32_t>(DA_STATUS_BAD_PAGE));
+              pg = 0;
+            }
+            const int tok = tok0 + box_tok;
+            // (other CTAs read the same keys: no eviction hint)
+            tma_load_4d_plain(smem + kTOffRing + s * kTSlot + half * kTHalf + box_tok * 128,
+                              (u & 1) ? &maps.v : &maps.k, &full_bar[s], half * 64, it.kvh,
+                              a.paged ? tok % a.page_size : tok, a.paged ? pg : it.b);
           }
-          const int tok = tok0 + box_tok;
-          uint8_t* dst = smem + kTOffRing + s * kTSlot + half * kTHalf + box_tok * 128;
-          // (other CTAs read the same keys: no eviction hint)
-          tma_load_4d_plain(dst, (u & 1) ? &maps.v : &maps.k, &full_bar[s], half * 64, kvh,
-                            a.paged ? tok % a.page_size : tok, a.paged ? pg : b);
+          __syncwarp();
+          last = ubase + u;
         }
-        __syncwarp();
-        last = u;
+        if (!ok) break;
+        ubase += units;
       }
-      if (lane == 0) {
-        if (!ok && a.status != nullptr) atomicOr(a.status, static_cast<int32_t>(DA_STATUS_TIMEOUT));
-        // no copy of this warp may still be landing when the CTA exits: wait
-        // (bounded) for its units whose slots no later unit uses
-        const int first = ok ? units - kTSlots : last - kTSlots + 1;
-        for (int u = last; u >= max(0, first); u -= kTProducers)
-          mbar_wait(&full_bar[u % kTSlots], (u / kTSlots) & 1);
+      if (!ok) {
+        report();
+        // no copy of this warp may still be landing when the CTA exits (without
+        // a failure every one has been waited for by the MMA warp)
+        if (lane == 0 && last >= 0) mbar_wait(&full_bar[pw], (last / kTSlots) & 1);
       }
       return;
     }
 
     // ============================================================== MMA issuer
+    const uint32_t tmem = *tmem_slot;
     constexpr uint32_t kIdescS = umma_idesc_bf16(kTRows, kTKeys, false, false);
     constexpr uint32_t kIdescO = umma_idesc_bf16(kTRows, kHeadDim, false, true);
     const uint64_t q_desc = umma_smem_desc(smem_base, 16, 1024);
     const uint64_t k_desc = umma_smem_desc(smem_base + kTOffRing, 16, 1024);
-    // V [128 keys][2 x 64 d], MN-major: d halves kTHalf apart, 8-key groups 1 KB
+    // V [64 keys][2 x 64 d], MN-major: d halves kTHalf apart, 8-key groups 1 KB
     const uint64_t v_desc = umma_smem_desc(smem_base + kTOffRing, kTHalf, 1024);
-    auto issue_s = [&](int g, int slot) {
-      const uint64_t qd = q_desc + static_cast<uint64_t>(g * (kTSlot >> 4));
-      const uint64_t kd = k_desc + static_cast<uint64_t>(slot * (kTSlot >> 4));
-      const uint32_t d = tmem + g * kTKeys;
-#pragma unroll
-      for (int kk = 0; kk < kHeadDim / 16; ++kk) {
-        const uint32_t off = ((kk >> 2) * kTHalf + (kk & 3) * 32) >> 4;
-        umma_bf16_ss_warp(d, qd + off, kd + off, kIdescS, kk > 0 ? 1u : 0u);
+    // the slot and the phase parity of the next K and of the next V (units 2 i and
+    // 2 i + 1 of all steps, in slots in turn)
+    int k_slot = 0, v_slot = 1;
+    uint32_t k_par = 0, v_par = 0;
+    auto advance = [](int& slot, uint32_t& par) {
+      slot += 2;
+      if (slot >= kTSlots) {
+        slot -= kTSlots;
+        par ^= 1u;
       }
-      umma_commit_warp(&s_full[g]);
     };
-    auto issue_o = [&](int g, int slot, bool first) {
-      const uint64_t vd = v_desc + static_cast<uint64_t>(slot * (kTSlot >> 4));
-      const uint32_t d = tmem + kTColO + g * kHeadDim;
+    uint32_t par[2] = {0, 0};              // of the next step of each tile
+    uint32_t q_par[2] = {0, 0};
+    const uint32_t full0 = smem_addr(full_bar), s_full0 = smem_addr(s_full), p_full0 = smem_addr(p_full);
+    for (int k = 0; next_item(k); ++k) {
+      const int n = item_slot(k)->steps, tiles = item_slot(k)->tiles;
+      leave_item(k);
+      if (n == 0) {
+        if (lane == 0) *static_cast<volatile int*>(near_end) = k + 1;
+        continue;
+      }
+      // S of the next K for tile g; behind the last tile the slot is free, behind
+      // an item's last step Q is
+      auto issue_s = [&](int g, bool last_step) {
+        umma_bf16_ss_k128_warp<kTQHalf, kTHalf>(tmem + g * kTKeys, q_desc + static_cast<uint64_t>(g * (kTQTile >> 4)),
+                                                k_desc + static_cast<uint64_t>(k_slot * (kTSlot >> 4)), kIdescS,
+                                                s_full0 + 8 * g);
+        if (last_step) umma_commit_warp(&q_empty[g]);
+        if (g == tiles - 1) {
+          umma_commit_warp(&empty_bar[k_slot]);
+          advance(k_slot, k_par);
+        }
+      };
+      ok = mbar_wait_warp(full0 + 8 * k_slot, k_par);
 #pragma unroll
-      for (int kk = 0; kk < kTKeys / 16; ++kk)
-        umma_bf16_ts_warp(d, tmem + g * kTKeys + kk * 8, vd + kk * (2048 >> 4), kIdescO,
-                          (!first || kk > 0) ? 1u : 0u);
-    };
-    auto landed = [&](int u) {
-      return __all_sync(kFull, mbar_wait_lazy(&full_bar[u % kTSlots], (u / kTSlots) & 1)) != 0;
-    };
-    bool ok = __all_sync(kFull, mbar_wait_lazy(q_full, 0)) != 0 && landed(0);
-    if (ok) {
-      tc_fence_after_sync();
-      for (int g = 0; g < tiles; ++g) issue_s(g, 0);
-      umma_commit_warp(&empty_bar[0]);
-    }
-    for (int j = 0; ok && j < n_iters; ++j) {
-      const int uv = 2 * j + 1, uk = 2 * j + 2;
-      const bool more = j + 1 < n_iters;
-      ok = landed(uv);
-      for (int g = 0; ok && g < tiles; ++g) {
-        ok = __all_sync(kFull, mbar_wait_lazy(&p_full[g], j & 1)) != 0;
+      for (int g = 0; g < 2; ++g) {
+        if (!ok || g >= tiles) break;
+        ok = mbar_wait_warp(smem_addr(&q_full[g]), q_par[g]);
         if (!ok) break;
+        q_par[g] ^= 1u;
         tc_fence_after_sync();
-        issue_o(g, uv % kTSlots, j == 0);
-        if (g == tiles - 1) umma_commit_warp(&empty_bar[uv % kTSlots]);
-        if (more) {
-          if (g == 0) ok = landed(uk);
+        issue_s(g, n == 1);
+      }
+      for (int i = 0; ok && i < n; ++i) {
+        if (lane == 0 && (i == n - kTAhead || (i == 0 && n < kTAhead))) *static_cast<volatile int*>(near_end) = k + 1;
+        const bool more = i + 1 < n;
+        ok = mbar_wait_warp(full0 + 8 * v_slot, v_par);
+        if (ok && more) ok = mbar_wait_warp(full0 + 8 * k_slot, k_par);
+        const uint64_t vd = v_desc + static_cast<uint64_t>(v_slot * (kTSlot >> 4));
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (!ok || g >= tiles) break;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // 64 keys of P at a time
+            if (ok) ok = mbar_wait_warp(p_full0 + 8 * (2 * g + h), par[g]);
+            if (!ok) break;
+            tc_fence_after_sync();
+            umma_bf16_ts_k64_warp<2048>(tmem + kTColO + g * kHeadDim, tmem + g * kTKeys + h * 32,
+                                        vd + h * (4 * 2048 >> 4), kIdescO, i > 0 || h > 0 ? 1u : 0u);
+          }
           if (!ok) break;
-          issue_s(g, uk % kTSlots);
-          if (g == tiles - 1) umma_commit_warp(&empty_bar[uk % kTSlots]);
-        } else {
-          umma_commit_warp(&o_done[g]);
+          par[g] ^= 1u;
+          if (g == tiles - 1) {
+            umma_commit_warp(&empty_bar[v_slot]);
+            advance(v_slot, v_par);
+          }
+          if (more) issue_s(g, i + 2 == n);
+          else umma_commit_warp(&o_done[g]);
         }
       }
+      if (!ok) break;
     }
-    // TMEM is released once the softmax warps are done with it.  After a wait
-    // that ran out a softmax warp passes at most one more (o_done) before it
-    // arrives here; five limits cover it, and past them TMEM is released anyway.
-    ok = (__all_sync(kFull, mbar_wait_for(tmem_done, 0, 5 * kWaitLimitNs + n_iters * 100000ull)) != 0) && ok;
-    if (!ok && lane == 0 && a.status != nullptr)
-      atomicOr(a.status, static_cast<int32_t>(DA_STATUS_TIMEOUT));
+    // TMEM is released once the softmax warps are done with it: after a failure
+    // each passes at most a few waits that run out, and past ten limits it is
+    // released anyway.
+    const bool done = __all_sync(kFull, mbar_wait_for(tmem_done, 0, 10 * kWaitLimitNs)) != 0;
+    if (!ok || !done) report();
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTTmemCols);
     return;
   }
 
-  // =================================================== softmax warpgroups (0-7)
+  // =================================================== softmax warpgroups
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTSoftmaxRegs));
-  const int g = warp >> 2;         // row tile
-  const int row = r0 + tid;        // (tid = 128 g + the lane of TMEM)
-  const bool direct = nsplit_b == 1;
-  const int t = row < a.rows ? row / a.group : 0;
-  const int h = kvh * a.group + (row - t * a.group);
-  const int64_t prow = (static_cast<int64_t>(b) * a.q_len + t) * a.num_q_heads + h;
-  const bool mine = row < own_rows_n;
-  bool ok = true;
-  float m_used = -INFINITY;  // reference maximum of P (log2 domain), raised lazily
-  float l = 0.f, lq = 0.f;   // sums of the fp32 weights, and of the rounded ones
-  uint32_t tmem = 0;
-  if (tiles > 0) {
-    tmem = *tmem_slot + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    // ---- the row of Q into shared memory, in the layout of a TMA tile
-    if (g < tiles) {
-      uint4 v[16];
-      if (mine) {
-        const uint4* q = reinterpret_cast<const uint4*>(
-            a.q + static_cast<int64_t>(b) * a.q_sb + static_cast<int64_t>(t) * a.q_st +
-            static_cast<int64_t>(h) * a.q_sh);
+  const int g = (warp - kTSoftmaxWarp) >> 2;  // row tile
+  const int r = tid & 127;         // its row, and the lane of TMEM
+  const int rt = r / a.group;      // its token in the tile
+  const bool in_tile = rt < tile_tokens;
+  const uint32_t lane_base = *tmem_slot + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+  const uint32_t s_col = lane_base + g * kTKeys;
+  const uint32_t o_col = lane_base + kTColO + g * kHeadDim;
+  const float sc = a.scale_log2;
+  const bool raw = sc > 0.f;  // (the scores stay unscaled; the exponent's multiply-add scales)
+  const float s_fma = raw ? sc : 1.f;
+  int ubase = 0, seq = 0, o_use = 0;
+  for (int k = 0; next_item(k); ++k) {
+    const TallItem& it = *item_slot(k);  // (stays in shared memory)
+    const int n = it.steps;
+    const int t = it.tok0 + g * tile_tokens + rt;
+    const bool mine = in_tile && t < it.own;
+    float m_used = -INFINITY;  // reference maximum of P (log2 domain), raised seldom
+    float l = 0.f;             // sum of the weights
+    const bool active = g < it.tiles;
+    if (active) {
+      // keys below are all seen (what padding rows see does not matter: the same
+      // limit for the whole CTA)
+      const int t_begin = it.t_begin, t_end = it.t_end;
+      const int lim = min(t_end, it.base);
+      for (int i = 0; i < n; ++i) {
+        ok = __all_sync(kFull, mbar_wait_lazy(&s_full[g], (seq + i) & 1)) != 0;
+        if (!ok) break;
+        tc_fence_after_sync();
+        float x[kTKeys];
+        {
+          float y[4][32];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) v[c] = __ldg(q + c);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 16; ++c) v[c] = make_uint4(0u, 0u, 0u, 0u);
-      }
-      const int r = tid & 127;
-      uint8_t* dst = smem + g * kTSlot + r * 128;
-#pragma unroll
-      for (int c = 0; c < 16; ++c)
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * kTHalf + (((c & 7) ^ (r & 7)) << 4)) = v[c];
-      fence_proxy_async_smem();
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(q_full);
-  }
-  if (g < tiles) {
-    const uint32_t s_col = tmem + g * kTKeys;
-    const uint32_t o_col = tmem + kTColO + g * kHeadDim;
-    const float sc = a.scale_log2;
-    const bool raw = sc > 0.f;  // (the scores stay unscaled; the exponent's multiply-add scales)
-    const float s_fma = raw ? sc : 1.f;
-    const int lim = mine ? min(t_end, own.base) : 0;  // keys below are all seen
-    for (int j = 0; j < n_iters; ++j) {
-      ok = __all_sync(kFull, mbar_wait_lazy(&s_full[g], j & 1)) != 0;
-      if (!ok) break;
-      tc_fence_after_sync();
-      float x[kTKeys];
-      {
-        float y[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, y[c]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < kTKeys; ++i) x[i] = y[i / 32][i % 32];
-      }
-      const int tok0 = t_begin + j * kTKeys;
-      if (tok0 + kTKeys > lim) {
-        // some key is hidden from this row: behind the chunk's end, or by the mask
-        const int end = mine ? t_end : 0;
-#pragma unroll
-        for (int w = 0; w < kTKeys / 32; ++w) {
-          const int left = end - (tok0 + 32 * w);
-          uint32_t seen = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1u : 0u;
-          if (seen != 0 && tok0 + 32 * w + 32 > own.base) seen &= own.bits(t, tok0 + 32 * w);
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            x[32 * w + i] = (seen >> i) & 1u ? x[32 * w + i] * (raw ? 1.f : sc) : -INFINITY;
-        }
-      } else if (!raw) {
-#pragma unroll
-        for (int i = 0; i < kTKeys; ++i) x[i] *= sc;
-      }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int i = 0; i < kTKeys; i += 8)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) mx[c] = fmax3(mx[c], x[i + 2 * c], x[i + 2 * c + 1]);
-      float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      if (raw) mt *= sc;
-      const bool raise = mt != -INFINITY && (m_used == -INFINITY || mt > m_used + kTRescale);
-      const float alpha = raise ? (m_used == -INFINITY ? 0.f : ex2(m_used - mt)) : 1.f;
-      if (raise) m_used = mt;
-      const float mref = m_used == -INFINITY ? 0.f : m_used;  // (nothing seen yet: P = 0)
-      if (j > 0 && __any_sync(kFull, raise && alpha != 1.f)) {
-        // (S of this tile was complete, so was the P V issued before it)
-#pragma unroll 1
-        for (int c = 0; c < kHeadDim / 32; ++c) {
-          float o[32];
-          tmem_ld32(o_col + c * 32, o);
+          for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, y[c]);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= alpha;
-          tmem_st32(o_col + c * 32, o);
+          for (int e = 0; e < kTKeys; ++e) x[e] = y[e / 32][e % 32];
         }
-        tmem_wait_st();
-      }
-      float2 ps = make_float2(0.f, 0.f), qs = make_float2(0.f, 0.f);
-      const float2 s2 = make_float2(s_fma, s_fma);
-      const float2 nm2 = make_float2(-mref, -mref);
+        const int tok0 = t_begin + i * kTKeys;
+        if (tok0 + kTKeys > lim) {
+          // some key is hidden from a row: behind the chunk's end, or by the mask
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float w[32];
+          for (int w = 0; w < kTKeys / 32; ++w) {
+            const int left = t_end - (tok0 + 32 * w);
+            uint32_t seen = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1u : 0u;
+            if (mine && seen != 0 && tok0 + 32 * w + 32 > it.base) {
+              const OwnRows own{it.own, it.base, a.own.mask + it.b * a.own.mask_sb, a.own.words};
+              seen &= own.bits(t, tok0 + 32 * w);
+            }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float2 e = __ffma2_rn(make_float2(x[64 * c + 2 * i], x[64 * c + 2 * i + 1]), s2, nm2);
-          const float p0 = ex2(e.x);
-          const float p1 = ex2(e.y);
-          ps = __fadd2_rn(ps, make_float2(p0, p1));
-          const uint32_t pk = pack_bf16x2(p0, p1);
-          qs = __fadd2_rn(qs, make_float2(packed_lo(pk, false), packed_hi(pk, false)));
-          w[i] = __uint_as_float(pk);
+            for (int e = 0; e < 32; ++e)
+              x[32 * w + e] = (seen >> e) & 1u ? x[32 * w + e] * (raw ? 1.f : sc) : -INFINITY;
+          }
+        } else if (!raw) {
+#pragma unroll
+          for (int e = 0; e < kTKeys; ++e) x[e] *= sc;
         }
-        tmem_st32(s_col + 32 * c, w);
-      }
-      l = l * alpha + (ps.x + ps.y);
-      lq = lq * alpha + (qs.x + qs.y);
-      // values of keys behind the chunk's end (P V of both tiles follows p_full[0])
-      const int n_valid = t_end - tok0;
-      if (g == 0 && n_valid < kTKeys) {
-        const int u = 2 * j + 1;
-        ok = __all_sync(kFull, mbar_wait_lazy(&full_bar[u % kTSlots], (u / kTSlots) & 1)) != 0;
-        if (!ok) break;
-        uint8_t* vs = smem + kTOffRing + (u % kTSlots) * kTSlot;
-        for (int idx = tid; idx < (kTKeys - n_valid) * 16; idx += 128)
-          *reinterpret_cast<uint4*>(vs + ((idx >> 3) & 1) * kTHalf + (n_valid + (idx >> 4)) * 128 + (idx & 7) * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
-      }
-      tmem_wait_st();
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[g]);
-    }
-    if (ok) {
-      ok = __all_sync(kFull, mbar_wait_lazy(&o_done[g], 0)) != 0;
-      tc_fence_after_sync();
-    }
-  }
-  if (tid == 0) allow_dependent_launch();
-
-  // ---- the row's output
-  const float inv = (lq == 0.f ? 0.f : 1.f / lq) * a.v_scale;  // (NaN stays NaN)
-  const bool have = ok && g < tiles;
-  const int64_t pidx = prow * S + split;
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < kTKeys; e += 8)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) mx[c] = fmax3(mx[c], x[e + 2 * c], x[e + 2 * c + 1]);
+        const float mt = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * s_fma;
+        const bool raise = mt > m_used + kTRescale;  // (from -inf by anything that is seen)
+        if (__any_sync(kFull, raise)) {
+          const float alpha = raise ? ex2(m_used - mt) : 1.f;
+          if (raise) m_used = mt;
+          l *= alpha;
+          if (i > 0) {  // (S of this step is complete, so is the P V issued before it)
 #pragma unroll 1
-  for (int c = 0; c < kHeadDim / 32; ++c) {
-    float o[32];
-    if (g < tiles) {
-      tmem_ld32(tmem + kTColO + g * kHeadDim + c * 32, o);
-      tmem_wait_ld();
+            for (int c = 0; c < kHeadDim / 16; ++c) {
+              float o[16];
+              tmem_ld16(o_col + c * 16, o);
+              tmem_wait_ld();
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
+              tmem_st16(o_col + c * 16, w);
+            }
+          }
+        }
+        const float mref = m_used == -INFINITY ? 0.f : m_used;  // (nothing seen yet: P = 0)
+        float2 ps = make_float2(0.f, 0.f);
+        const float2 s2 = make_float2(s_fma, s_fma);
+        const float2 nm2 = make_float2(-mref, -mref);
+        const int n_valid = t_end - tok0;
+        auto p_ready = [&](int h) {
+          tmem_wait_st();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * g + h]);
+        };
+        // values of keys behind the chunk's end are zeroed before the first P V
+        // (that of tile 0) may read them
+        if (g == 0 && n_valid < kTKeys) {
+          const int u = ubase + 2 * i + 1;
+          ok = __all_sync(kFull, mbar_wait_lazy(&full_bar[u % kTSlots], (u / kTSlots) & 1)) != 0;
+          if (!ok) break;
+          uint8_t* vs = smem + kTOffRing + (u % kTSlots) * kTSlot;
+          for (int z = r; z < (kTKeys - n_valid) * 16; z += 128)
+            *reinterpret_cast<uint4*>(vs + ((z >> 3) & 1) * kTHalf + (n_valid + (z >> 4)) * 128 + (z & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 y = __ffma2_rn(make_float2(x[32 * c + 2 * e], x[32 * c + 2 * e + 1]), s2, nm2);
+            const float p0 = ex2(y.x);
+            const float p1 = ex2(y.y);
+            ps = __fadd2_rn(ps, make_float2(p0, p1));
+            w[e] = pack_bf16x2(p0, p1);
+          }
+          if (c == 2) {
+            // the first half has been stored meanwhile; the last quarter stays
+            // behind its release (the compiler would take it first)
+            p_ready(0);
+#pragma unroll
+            for (int e = 96; e < 128; e += 8)
+              asm volatile("" : "+f"(x[e]), "+f"(x[e + 1]), "+f"(x[e + 2]), "+f"(x[e + 3]), "+f"(x[e + 4]), "+f"(x[e + 5]),
+                           "+f"(x[e + 6]), "+f"(x[e + 7]));
+          }
+          tmem_st16(s_col + 16 * c, w);
+        }
+        p_ready(1);
+        l += ps.x + ps.y;
+      }
+      if (ok) {
+        ok = __all_sync(kFull, mbar_wait_lazy(&o_done[g], o_use & 1)) != 0;
+        tc_fence_after_sync();
+      }
+      seq += n;
+      ++o_use;
     }
+    ubase += 2 * n;
+
+    // ---- the row's output (chunks behind the request's last one have none)
+    const int chunks = it.L > 0 ? (it.L + a.chunk_len - 1) / a.chunk_len : 1;
+    const bool direct = chunks == 1;
+    const bool writes = in_tile && t < a.q_len && it.split < chunks;
+    const int h = it.kvh * a.group + (r - rt * a.group);
+    const int64_t prow = (static_cast<int64_t>(it.b) * a.q_len + t) * a.num_q_heads + h;
+    const int64_t pidx = prow * S + it.split;
+    const float inv = (l == 0.f ? 0.f : 1.f / l) * a.v_scale;  // (NaN stays NaN)
+    const bool have = ok && active && mine && l != 0.f;
+#pragma unroll 1
+    for (int c = 0; c < kHeadDim / 32; ++c) {
+      float o[32];
+      if (active) {
+        tmem_ld32(o_col + c * 32, o);
+        tmem_wait_ld();
+      }
 #pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] = have && l != 0.f ? o[i] * inv : 0.f;
-    if (row < a.rows) {
-      if (direct) {
-        uint16_t* dst = a.out + static_cast<int64_t>(b) * a.o_sb + static_cast<int64_t>(t) * a.o_st +
-                        static_cast<int64_t>(h) * a.o_sh + c * 32;
+      for (int e = 0; e < 32; ++e) o[e] = have ? o[e] * inv : 0.f;
+      if (writes) {
+        if (direct) {
+          uint16_t* dst = a.out + static_cast<int64_t>(it.b) * a.o_sb + static_cast<int64_t>(t) * a.o_st +
+                          static_cast<int64_t>(h) * a.o_sh + c * 32;
 #pragma unroll
-        for (int i = 0; i < 32; i += 8)
-          *reinterpret_cast<uint4*>(dst + i) =
-              make_uint4(pack_bf16x2(o[i], o[i + 1]), pack_bf16x2(o[i + 2], o[i + 3]),
-                         pack_bf16x2(o[i + 4], o[i + 5]), pack_bf16x2(o[i + 6], o[i + 7]));
-      } else {
-        float* dst = a.part_o + pidx * kHeadDim + c * 32;
+          for (int e = 0; e < 32; e += 8)
+            *reinterpret_cast<uint4*>(dst + e) =
+                make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
+                           pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
+        } else {
+          float* dst = a.part_o + pidx * kHeadDim + c * 32;
 #pragma unroll
-        for (int i = 0; i < 32; i += 4)
-          *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
       }
     }
-  }
-  if (row < a.rows) {
-    const float lse = l == 0.f ? -INFINITY : (m_used == -INFINITY ? 0.f : m_used) * kLn2t + logf(l);
-    if (direct) a.lse[prow] = lse;
-    else a.part_lse[pidx] = lse;
-  }
-  if (!ok && lane == 0 && a.status != nullptr)
-    atomicOr(a.status, static_cast<int32_t>(DA_STATUS_TIMEOUT));
-  if (tiles > 0) {
+    if (writes) {
+      const float lse = !mine || l == 0.f ? -INFINITY : (m_used == -INFINITY ? 0.f : m_used) * kLn2t + logf(l);
+      if (direct) a.lse[prow] = lse;
+      else a.part_lse[pidx] = lse;
+    }
+    leave_item(k);
+    // O was read before this warp's next P, which the next item's P V waits for
     tc_fence_before_sync();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(tmem_done);
+    if (!ok) break;
   }
+  if (!ok) report();
+  tc_fence_before_sync();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(tmem_done);
 }
 
 std::mutex g_tall_mu;
@@ -456,8 +601,10 @@ bool g_tall_attr[64];
 
 }  // namespace
 
-cudaError_t launch_tall(const CUtensorMap& k_map, const CUtensorMap& v_map, const SplitArgs& a,
-                        int box_tokens, cudaStream_t stream) {
+int tall_tile_tokens(int group) { return kTRows / group; }
+
+cudaError_t launch_tall(const CUtensorMap& q_map, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                        const SplitArgs& a, int box_tokens, cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -470,9 +617,9 @@ cudaError_t launch_tall(const CUtensorMap& k_map, const CUtensorMap& v_map, cons
       g_tall_attr[dev] = true;
     }
   }
-  const int pairs = (a.rows + 2 * kTRows - 1) / (2 * kTRows);
+  const int pair = 2 * (kTRows / a.group);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(pairs) * a.num_splits, a.num_kv_heads, a.batch);
+  cfg.gridDim = dim3(static_cast<unsigned>((a.q_len + pair - 1) / pair) * a.num_splits, a.num_kv_heads, a.batch);
   cfg.blockDim = dim3(kTThreads);
   cfg.dynamicSmemBytes = kTSmem;
   cfg.stream = stream;
@@ -481,7 +628,7 @@ cudaError_t launch_tall(const CUtensorMap& k_map, const CUtensorMap& v_map, cons
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tall_kernel, TallMaps{k_map, v_map}, a, box_tokens);
+  return cudaLaunchKernelEx(&cfg, tall_kernel, TallMaps{q_map, k_map, v_map}, a, box_tokens);
 }
 
 }  // namespace dattn
