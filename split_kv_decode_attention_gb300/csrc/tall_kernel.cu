@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     };
     uint32_t par[2] = {0, 0};              // of the next step of each tile
     uint32_t q_par[2] = {0, 0};
-    const uint32_t full0 = smem_addr(full_bar), s_full0 = smem_addr(s_full), p_full0 = smem_addr(p_full);
+    const uint32_t full0 = smem_addr(full_bar), empty0 = smem_addr(empty_bar), o_done0 = smem_addr(o_done), s_full0 = smem_addr(s_full), p_full0 = smem_addr(p_full);
     for (int k = 0; next_item(k); ++k) {
       const int n = item_slot(k)->steps, tiles = item_slot(k)->tiles;
       leave_item(k);
@@ -348,14 +348,12 @@ __global__ void __launch_bounds__(kTThreads, 1)
       // S of the next K for tile g; behind the last tile the slot is free, behind
       // an item's last step Q is
       auto issue_s = [&](int g, bool last_step) {
+        const bool last_tile = g == tiles - 1;
         umma_bf16_ss_k128_warp<kTQHalf, kTHalf>(tmem + g * kTKeys, q_desc + static_cast<uint64_t>(g * (kTQTile >> 4)),
                                                 k_desc + static_cast<uint64_t>(k_slot * (kTSlot >> 4)), kIdescS,
-                                                s_full0 + 8 * g);
+                                                s_full0 + 8 * g, last_tile ? empty0 + 8 * k_slot : 0u);
         if (last_step) umma_commit_warp(&q_empty[g]);
-        if (g == tiles - 1) {
-          umma_commit_warp(&empty_bar[k_slot]);
-          advance(k_slot, k_par);
-        }
+        if (last_tile) advance(k_slot, k_par);
       };
       ok = mbar_wait_warp(full0 + 8 * k_slot, k_par);
 #pragma unroll
@@ -368,30 +366,34 @@ __global__ void __launch_bounds__(kTThreads, 1)
         issue_s(g, n == 1);
       }
       for (int i = 0; ok && i < n; ++i) {
-        if (lane == 0 && (i == n - kTAhead || (i == 0 && n < kTAhead))) *static_cast<volatile int*>(near_end) = k + 1;
         const bool more = i + 1 < n;
-        ok = mbar_wait_warp(full0 + 8 * v_slot, v_par);
-        if (ok && more) ok = mbar_wait_warp(full0 + 8 * k_slot, k_par);
         const uint64_t vd = v_desc + static_cast<uint64_t>(v_slot * (kTSlot >> 4));
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           if (!ok || g >= tiles) break;
+          const bool last_tile = g == tiles - 1;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // 64 keys of P at a time
-            if (ok) ok = mbar_wait_warp(p_full0 + 8 * (2 * g + h), par[g]);
+            const uint32_t p_bar = p_full0 + 8 * (2 * g + h);
+            // (a step's V and the next one's K have long landed when its first P comes)
+            if (g == 0 && h == 0)
+              ok = mbar_wait3_warp(full0 + 8 * v_slot, v_par, more ? full0 + 8 * k_slot : full0 + 8 * v_slot,
+                                   more ? k_par : v_par, p_bar, par[g]);
+            else if (ok)
+              ok = mbar_wait_warp(p_bar, par[g]);
             if (!ok) break;
             tc_fence_after_sync();
             umma_bf16_ts_k64_warp<2048>(tmem + kTColO + g * kHeadDim, tmem + g * kTKeys + h * 32,
-                                        vd + h * (4 * 2048 >> 4), kIdescO, i > 0 || h > 0 ? 1u : 0u);
+                                        vd + h * (4 * 2048 >> 4), kIdescO, i > 0 || h > 0 ? 1u : 0u,
+                                        h == 0 ? 0u : last_tile ? empty0 + 8 * v_slot : more ? 0u : o_done0 + 8 * g);
           }
           if (!ok) break;
           par[g] ^= 1u;
-          if (g == tiles - 1) {
-            umma_commit_warp(&empty_bar[v_slot]);
-            advance(v_slot, v_par);
-          }
           if (more) issue_s(g, i + 2 == n);
-          else umma_commit_warp(&o_done[g]);
+          else if (last_tile) umma_commit_warp(&o_done[g]);
+          if (last_tile) advance(v_slot, v_par);
+          if (g == 0 && lane == 0 && (i == n - kTAhead || (i == 0 && n < kTAhead)))
+            *static_cast<volatile int*>(near_end) = k + 1;
         }
       }
       if (!ok) break;

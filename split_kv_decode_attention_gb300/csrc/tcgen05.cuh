@@ -92,11 +92,11 @@ __device__ __forceinline__ void umma_bf16_ts_warp(uint32_t d_tmem, uint32_t a_tm
 // A whole product's MMAs with one elect.sync (warp-collective, as above).  A and
 // B from shared memory, both K-major with 128-byte swizzle, 128 deep in two
 // halves of 64: half h of A is kHalfA bytes behind the first, of B kHalfB.  One
-// arrival on `bar` (a shared-memory address) when they and what this thread issued
-// before are done.
+// arrival on `bar`, and one on `bar2` where that is not 0 (shared-memory addresses),
+// when they and what this thread issued before are done.
 template <int kHalfA, int kHalfB>
 __device__ __forceinline__ void umma_bf16_ss_k128_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                                       uint32_t idesc, uint32_t bar) {
+                                                       uint32_t idesc, uint32_t bar, uint32_t bar2) {
   asm volatile(
       "{\n\t.reg .pred e, t, f;\n\t.reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3, b4, b5, b6, b7;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
@@ -116,16 +116,18 @@ __device__ __forceinline__ void umma_bf16_ss_k128_warp(uint32_t d_tmem, uint64_t
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a5, b5, %3, t;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a6, b6, %3, t;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a7, b7, %3, t;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n\t}"
-      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "n"(kHalfA >> 4), "n"(kHalfB >> 4), "r"(bar)
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n\t"
+      "setp.ne.and.u32 t, %7, 0, e;\n\t"
+      "@t tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%7];\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "n"(kHalfA >> 4), "n"(kHalfB >> 4), "r"(bar), "r"(bar2)
       : "memory");
 }
 
 // A from tensor memory (8 columns a K-step), B MN-major: 64 deep, 16 k's a
-// K-step of kStepB bytes.
+// K-step of kStepB bytes.  An arrival on `bar` where that is not 0, as above.
 template <int kStepB>
 __device__ __forceinline__ void umma_bf16_ts_k64_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                                      uint32_t idesc, uint32_t accumulate) {
+                                                      uint32_t idesc, uint32_t accumulate, uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred e, t, p;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
@@ -135,8 +137,10 @@ __device__ __forceinline__ void umma_bf16_ts_k64_warp(uint32_t d_tmem, uint32_t 
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}"
-      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(kStepB >> 4)
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t"
+      "setp.ne.and.u32 t, %6, 0, e;\n\t"
+      "@t tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(kStepB >> 4), "r"(bar)
       : "memory");
 }
 
