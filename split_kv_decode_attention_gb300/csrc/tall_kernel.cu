@@ -547,45 +547,87 @@ __global__ void __launch_bounds__(kTThreads, 1)
     }
     ubase += 2 * n;
 
-    // ---- the row's output (chunks behind the request's last one have none)
+    // ---- the rows' outputs (chunks behind the request's last one have none).
+    // A lane that wrote its own row would touch a sector of each of 32 rows with
+    // every store, and the tensor core waits meanwhile (6000 cycles for a partial):
+    // so O is read as 16-row fragments, where four lanes hold eight neighbouring
+    // columns of a row.
     const int chunks = it.L > 0 ? (it.L + a.chunk_len - 1) / a.chunk_len : 1;
     const bool direct = chunks == 1;
     const bool writes = in_tile && t < a.q_len && it.split < chunks;
     const int h = it.kvh * a.group + (r - rt * a.group);
     const int64_t prow = (static_cast<int64_t>(it.b) * a.q_len + t) * a.num_q_heads + h;
     const int64_t pidx = prow * S + it.split;
-    const float inv = (l == 0.f ? 0.f : 1.f / l) * a.v_scale;  // (NaN stays NaN)
     const bool have = ok && active && mine && l != 0.f;
-#pragma unroll 1
-    for (int c = 0; c < kHeadDim / 32; ++c) {
-      float o[32];
-      if (active) {
-        tmem_ld32(o_col + c * 32, o);
-        tmem_wait_ld();
-      }
-#pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] = have ? o[e] * inv : 0.f;
-      if (writes) {
-        if (direct) {
-          uint16_t* dst = a.out + static_cast<int64_t>(it.b) * a.o_sb + static_cast<int64_t>(t) * a.o_st +
-                          static_cast<int64_t>(h) * a.o_sh + c * 32;
-#pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4*>(dst + e) =
-                make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
-                           pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
-        } else {
-          float* dst = a.part_o + pidx * kHeadDim + c * 32;
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-        }
-      }
-    }
+    const float inv = have ? (1.f / l) * a.v_scale : 0.f;  // (NaN stays NaN)
+    // byte offset of the row, -1 where nothing is written
+    const int64_t row_at = !writes ? -1
+                           : direct ? 2 * (static_cast<int64_t>(it.b) * a.o_sb + static_cast<int64_t>(t) * a.o_st +
+                                           static_cast<int64_t>(h) * a.o_sh)
+                                    : 4 * kHeadDim * pidx;
     if (writes) {
-      const float lse = !mine || l == 0.f ? -INFINITY : (m_used == -INFINITY ? 0.f : m_used) * kLn2t + logf(l);
+      const float lse = !have ? -INFINITY : (m_used == -INFINITY ? 0.f : m_used) * kLn2t + logf(l);
       if (direct) a.lse[prow] = lse;
       else a.part_lse[pidx] = lse;
+    }
+    uint8_t* const dst = direct ? reinterpret_cast<uint8_t*>(a.out) : reinterpret_cast<uint8_t*>(a.part_o);
+    // (rolled up: the code is met once an item, and its first pass waits for the
+    // instructions)
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {  // rows 16 half + lane / 4, and 8 further
+      float f[2];
+      int64_t at[2];
+      bool some[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int owner = 16 * half + 8 * e + (lane >> 2);
+        f[e] = __shfl_sync(kFull, inv, owner);
+        at[e] = __shfl_sync(kFull, row_at, owner);
+        some[e] = __shfl_sync(kFull, have ? 1 : 0, owner) != 0;
+      }
+#pragma unroll 1
+      for (int c = 0; c < kHeadDim / 32; ++c) {
+        float o[16];
+        if (active) {
+          tmem_ld_16x32(o_col + (static_cast<uint32_t>(16 * half) << 16) + c * 32, o);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float y[8];  // columns 8 q + 2 (lane % 4) and + 1
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            y[2 * q] = some[e] ? o[4 * q + 2 * e] * f[e] : 0.f;
+            y[2 * q + 1] = some[e] ? o[4 * q + 2 * e + 1] * f[e] : 0.f;
+          }
+          if (direct) {
+            // the four lanes of a row trade, so that each has the eight columns of
+            // one group: 16 bytes, 64 in a row
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[q] = pack_bf16x2(y[2 * q], y[2 * q + 1]);
+#pragma unroll
+            for (int d = 1; d <= 2; d *= 2) {
+              const bool up = (lane & d) != 0;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if ((q & d) != 0) continue;
+                const uint32_t give = up ? w[q] : w[q + d];
+                const uint32_t got = __shfl_xor_sync(kFull, give, d);
+                if (up) w[q] = got;
+                else w[q + d] = got;
+              }
+            }
+            if (at[e] >= 0)
+              *reinterpret_cast<uint4*>(dst + at[e] + c * 64 + (lane & 3) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+          } else if (at[e] >= 0) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<float2*>(dst + at[e] + c * 128 + q * 32 + (lane & 3) * 8) =
+                  make_float2(y[2 * q], y[2 * q + 1]);
+          }
+        }
+      }
     }
     leave_item(k);
     // O was read before this warp's next P, which the next item's P V waits for
