@@ -654,8 +654,9 @@ int decode_attn_tree_mask(int32_t batch, int32_t q_len, int32_t max_seq_len,
  * p->causal is not used, nor is DA_FLAG_TEST_WITHHOLD_COPY above
  * DECODE_ATTN_MAX_ROWS.  (Hq / Hkv) * q_len may exceed DECODE_ATTN_MAX_ROWS;
  * Hq / Hkv may not, nor q_len DECODE_ATTN_MAX_TREE.  Above that many rows the
- * workspace also holds, for FP8 and 4-bit caches, the batch's keys and values in
- * bf16 (B * max_seq_len * Hkv * 512 bytes).
+ * call cuts its work evenly on the device, num_splits is not used, and the
+ * workspace holds 40 MB of partials and, for FP8 and 4-bit caches, the batch's
+ * keys and values in bf16 (B * max_seq_len * Hkv * 512 bytes).
  * Status as decode_attn(); DA_STATUS_SHORT_CAUSAL where L < n_b (the first
  * n_b - L new tokens then have no key).
  */
@@ -673,7 +674,9 @@ int decode_attn_tree(const decode_attn_params *p, const decode_attn_cache *c, co
  * or a whole prompt.  Request b has q_lens[b] tokens (q_len when NULL); rows
  * behind them are padding: their q is not used, out = 0 and lse = -inf.
  * p->causal is not used.  Rows, workspace and status as decode_attn_tree(), but
- * q_len has no limit of its own ((Hq / Hkv) * q_len < 2^31).
+ * q_len has no limit of its own (above DECODE_ATTN_MAX_ROWS rows 3 * B * Hkv *
+ * ceil((Hq / Hkv) * q_len / 256) * ceil(max_seq_len / 128) stays below 2^32, else
+ * DA_ERR_BAD_SHAPE).
  */
 int decode_attn_cross_workspace_bytes(const decode_attn_params *p, const decode_attn_cache *c,
                                       int32_t num_splits, size_t *bytes);

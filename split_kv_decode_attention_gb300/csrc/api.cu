@@ -743,37 +743,21 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
 
 namespace {
 
-// A call of more than DECODE_ATTN_MAX_ROWS rows per KV head: chunks of whole
-// 128-token tiles, and the workspace, [K and V in bf16, where the cache is not]
-// [partials].
-struct TallPlan {
-  int32_t chunk, splits;
+// Workspace of a call of more than DECODE_ATTN_MAX_ROWS rows per KV head: [K and V
+// in bf16, where the cache is not] [partials].
+struct TallLayout {
   int64_t tokens;              // of a request in the bf16 copy
-  size_t k, v, part_o, part_lse, total;
+  size_t k, v, part_o, part_lse, join, total;
 };
 
-constexpr int kTallTile = 128;
-
-int tall_plan(const decode_attn_params* p, const decode_attn_cache* c, int32_t num_splits, TallPlan* l) {
-  if (p->max_seq_len > (1 << 30)) return DA_ERR_BAD_SHAPE;
+int tall_layout(const decode_attn_params* p, const decode_attn_cache* c, TallLayout* l) {
+  const int64_t rows = static_cast<int64_t>(p->num_q_heads / p->num_kv_heads) * p->q_len;
+  if (p->max_seq_len > (1 << 30) || rows > 0x7fffffff) return DA_ERR_BAD_SHAPE;
+  // (the kernel adds up the costs of its steps in 32 bits)
   const int64_t group = p->num_q_heads / p->num_kv_heads;
-  const int64_t rows = group * p->q_len;
-  const int64_t pairs = ceil_div64(p->q_len, 2 * tall_tile_tokens(static_cast<int>(group)));
-  const int64_t tiles = std::max<int64_t>(1, ceil_div64(p->max_seq_len, kTallTile));
-  int64_t n = num_splits;
-  if (n <= 0) {
-    DeviceInfo di;
-    const int rc = current_device_info(&di);
-    if (rc != DA_OK) return rc;
-    const int64_t items = std::max<int64_t>(1, pairs * p->num_kv_heads * p->batch);
-    n = std::max<int64_t>(1, std::min<int64_t>(ceil_div64(4 * di.sm_count, items), tiles / 8));
-  }
-  n = std::min(n, tiles);
-  const int64_t chunk = ceil_div64(tiles, n) * kTallTile;
-  n = std::max<int64_t>(1, ceil_div64(p->max_seq_len, chunk));
-  if (pairs * n > 0x7fffffff || rows > 0x7fffffff) return DA_ERR_BAD_SHAPE;
-  l->chunk = static_cast<int32_t>(chunk);
-  l->splits = static_cast<int32_t>(n);
+  const double pairs = static_cast<double>(ceil_div64(p->q_len, 2 * tall_tile_tokens(static_cast<int>(group))));
+  if (3.0 * p->batch * p->num_kv_heads * pairs * static_cast<double>(ceil_div64(p->max_seq_len, 128)) >= 4294967295.0)
+    return DA_ERR_BAD_SHAPE;
   l->tokens = std::max<int64_t>(p->max_seq_len, 1);
   size_t off = 0;
   l->k = off;
@@ -783,11 +767,13 @@ int tall_plan(const decode_attn_params* p, const decode_attn_cache* c, int32_t n
     l->v = round256(off + one);
     off = round256(l->v + one);
   }
-  const size_t part = n > 1 ? static_cast<size_t>(p->batch) * p->q_len * p->num_q_heads * n : 0;
+  const size_t part = static_cast<size_t>(kTallSlots) * kTallSlotRows;
   l->part_o = off;
-  off = round256(off + part * kHeadDim * 4);
+  off += part * kHeadDim * 4;
   l->part_lse = off;
-  l->total = off + part * 4;
+  off += part * 4;
+  l->join = off;
+  l->total = off + static_cast<size_t>(kTallCtas) * kTallJoinBytes;
   return DA_OK;
 }
 
@@ -803,8 +789,8 @@ int rows_workspace_bytes(const decode_attn_params* p, const decode_attn_cache* c
   const int rc = check_shape(p, false);
   if (rc != DA_OK) return rc;
   if (bytes == nullptr) return DA_ERR_NULL_POINTER;
-  TallPlan l;
-  const int rc2 = tall_plan(p, c, num_splits, &l);
+  TallLayout l;
+  const int rc2 = tall_layout(p, c, &l);
   if (rc2 == DA_OK) *bytes = l.total;
   return rc2;
 }
@@ -840,10 +826,10 @@ int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void
   rc = current_device_info(&di);
   if (rc != DA_OK) return rc;
   if (di.major * 10 + di.minor < 100) return DA_ERR_NO_DEVICE;
-  TallPlan l;
-  rc = tall_plan(p, c, num_splits, &l);
+  TallLayout l;
+  rc = tall_layout(p, c, &l);
   if (rc != DA_OK) return rc;
-  if (l.total > 0 && (workspace == nullptr || workspace_bytes < l.total || !aligned16(workspace)))
+  if (workspace == nullptr || workspace_bytes < l.total || !aligned16(workspace))
     return DA_ERR_WORKSPACE;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -916,6 +902,7 @@ int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void
   a.lse = lse;
   a.part_o = reinterpret_cast<float*>(w + l.part_o);
   a.part_lse = reinterpret_cast<float*>(w + l.part_lse);
+  a.join = w + l.join;
   a.block_table = tma_paged ? block_table : nullptr;
   a.bt_stride = p->block_table_stride;
   a.seq_lens = seq_lens;
@@ -931,34 +918,10 @@ int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void
   a.num_pages = tma_paged ? p->num_pages : 0;
   a.paged = tma_paged ? 1 : 0;
   a.max_seq_len = p->max_seq_len;
-  a.chunk_len = l.chunk;
-  a.num_splits = l.splits;
   a.scale_log2 = p->scale * (copied ? p->k_scale : 1.f) * 1.4426950408889634f;
   a.v_scale = copied ? p->v_scale : 1.f;
   a.own = ext.own;
-  if (launch_tall(qmap, kmap, vmap, a, box, st) != cudaSuccess) return DA_ERR_CUDA;
-  if (l.splits > 1) {
-    CombineArgs m = {};
-    m.num_kv_heads = p->num_kv_heads;
-    m.part_o = a.part_o;
-    m.part_lse = a.part_lse;
-    m.seq_lens = seq_lens;
-    m.out = a.out;
-    m.o_sb = a.o_sb;
-    m.o_st = a.o_st;
-    m.o_sh = a.o_sh;
-    m.lse = lse;
-    m.batch = p->batch;
-    m.q_len = p->q_len;
-    m.num_q_heads = p->num_q_heads;
-    m.max_seq_len = p->max_seq_len;
-    m.chunk_len = l.chunk;
-    m.num_splits = l.splits;
-    m.len_sb = 1;
-    m.unit_heads = 1;
-    if (launch_combine(m, st) != cudaSuccess) return DA_ERR_CUDA;
-  }
-  return DA_OK;
+  return launch_tall(qmap, kmap, vmap, a, box, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 int plan_uniform(const decode_attn_params* p, const DecodeExt& ext, int32_t* num_splits,

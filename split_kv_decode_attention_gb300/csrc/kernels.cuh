@@ -67,6 +67,7 @@ struct SplitArgs {
   int len_sb, len_sh;
   int64_t bt_sh;
   int box_halves;                      // 4-bit kernel: 16-token halves of a box
+  uint8_t* join;                       // kernel for many rows: records for its merge
   RowArgs own;                         // trees and padded batches (else .on == 0)
 };
 
@@ -193,10 +194,15 @@ bool fp4_cluster_merge_fits(int rows, int num_splits, int64_t num_clusters);
 int fp4_ctas_per_sm(int rows, int heads_per_cta);
 int fp4_warps(int rows);  // consumer warps of a CTA: its heads divide them
 
-// Launch the kernel for more than 128 query rows per KV head (tall_kernel.cu;
-// bf16 keys and values, boxes of box_tokens tokens, chunks of whole 64-key
-// steps; partials as launch_split).
-// Boxes of Q: 64 d of a group's heads, tall_tile_tokens() tokens.
+// Launch the kernel for more than 128 query rows per KV head and the merge of its
+// partials (tall_kernel.cu; bf16 keys and values, boxes of box_tokens tokens; Q's
+// boxes: 64 d of a group's heads, tall_tile_tokens() tokens).  part_o holds
+// kTallSlots x 256 rows, part_lse as many LSEs, join kTallCtas records; chunk_len
+// and num_splits are not used.
+constexpr int kTallCtas = 152;         // one for each SM
+constexpr int kTallSlots = 2 * kTallCtas;
+constexpr int kTallSlotRows = 256;
+constexpr int kTallJoinBytes = 32;
 cudaError_t launch_tall(const CUtensorMap& q_map, const CUtensorMap& k_map, const CUtensorMap& v_map,
                         const SplitArgs& a, int box_tokens, cudaStream_t stream);
 int tall_tile_tokens(int group);

@@ -379,34 +379,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Cluster launch control: ask for the next CTA of this grid that has not begun,
-// in its place; 16 bytes of answer arrive in `answer` (16-byte aligned) and count
-// on `bar`, which expects them.
-__device__ __forceinline__ void try_cancel(void* answer, uint64_t* bar) {
-  asm volatile(
-      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-          smem_addr(answer)),
-      "r"(smem_addr(bar))
-      : "memory");
-}
-
-// The answer: false when no CTA is left (then no further one may be asked for),
-// else its block index.
-__device__ __forceinline__ bool canceled_block(const void* answer, uint32_t& x, uint32_t& y, uint32_t& z) {
-  uint32_t got;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
-      "ld.shared.b128 h, [%4];\n\t"
-      "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
-      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t"
-      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, %3, _}, h;\n\t}"
-      : "=&r"(got), "=&r"(x), "=&r"(y), "=&r"(z)
-      : "r"(smem_addr(answer))
-      : "memory");
-  return got != 0;
-}
-
 // Programmatic dependent launch: wait until the grids this one depends on
 // have completed and their memory is visible (no-op without a dependency) ...
 __device__ __forceinline__ void grid_dependency_wait() {

@@ -28,10 +28,14 @@
 // divided by is that of the unrounded ones (summing the rounded ones too, as the
 // kernels for fewer rows do, took 9 % longer).
 //
-// A CTA per SM takes item after item: it asks the hardware for the grid's next
-// block in place of a CTA of its own (cluster launch control), so items of
-// unequal lengths balance without a counter in memory, and the copies and the
-// first S of an item overlap the end of the one before.  Roles: warp 0
+// The work is cut evenly, whatever the lengths: all steps of all items stand in
+// one list, (request, kv head, pair of row tiles) by (request, kv head, pair), and
+// each of kTallCtas CTAs takes the same share of it, in steps (a step of two row
+// tiles counts 3, of one 2: their measured times).  So at most two of a CTA's
+// items are not whole; those leave fp32 partials in the CTA's two slots of the
+// workspace, and tall_join_kernel merges them.  Every CTA works its share out from
+// the lengths in device memory (tall_share), and so does the merge.  The copies
+// and the first S of an item overlap the end of the one before.  Roles: warp 0
 // MMA, 1 schedule and Q, 2-6 K and V, 8-15 softmax.  K and V go through a ring of
 // five 32 KB slots (128 keys of K or of V), a warp to each; TMA boxes are of up to
 // 128 tokens (what divides a page).  Boxes that one warp issues are serialised
@@ -70,14 +74,13 @@ static_assert(kTProdWarp + kTProducers <= kTSoftmaxWarp && 32 * (kTSoftmaxWarp +
 constexpr int kTReaders = 8 + 1 + kTProducers;    // warps that read an item's descriptor
 constexpr int kTOffRing = 2 * kTQTile;
 constexpr int kTOffBar = kTOffRing + kTSlots * kTSlot;
-constexpr int kTBars = 2 * kTSlots + 2 + 2 + 2 + 4 + 2 + 2 + 2 + 1 + 1;
-constexpr int kTOffItems = kTOffBar + kTBars * 8 + 8;      // 16-byte aligned below
-constexpr int kTSmem = 1024 + kTOffItems + 16 + 2 * 64 + 32;
+constexpr int kTBars = 2 * kTSlots + 2 + 2 + 2 + 4 + 2 + 2 + 2 + 1;
+constexpr int kTOffItems = (kTOffBar + kTBars * 8 + 8 + 15) / 16 * 16;
+constexpr int kTSmem = 1024 + kTOffItems + 2 * 64;
 static_assert(kTSmem <= 227 * 1024, "shared memory");
 constexpr uint32_t kTTmemCols = 512;
 constexpr uint32_t kTColO = 256;                  // S of tile g at 128 g, O at 256 + 128 g
 constexpr float kTRescale = 64.f;                 // log2 units
-constexpr int kTAhead = 4;                        // steps before an item's end when the next is asked for
 // registers: 65536 / 512 threads is what the launch gives
 constexpr int kTLaunchRegs = 65536 / kTThreads / 8 * 8;
 constexpr int kTSoftmaxRegs = 208;
@@ -89,17 +92,135 @@ struct TallMaps {
   CUtensorMap q, k, v;
 };
 
-// One item, in shared memory: written by the scheduler warp.
+// One piece of an item, in shared memory: written by the scheduler warp.
 struct TallItem {
   int valid;             // 0: no item is left
-  int b, kvh, split;
+  int b, kvh;
   int tok0;              // first token of the two row tiles
-  int L, own, base;      // length, the request's own tokens, first key that goes by the mask
+  int own, base;         // the request's own tokens, first key that goes by the mask
   int t_begin, t_end;    // keys
-  int steps;             // 0 where no row sees a key
-  int tiles;             // row tiles with own rows (0 with steps)
+  int steps;
+  int tiles;             // row tiles with own rows
+  int slot;              // of the partials; -1: a whole item, written to out
 };
 static_assert(sizeof(TallItem) <= 64, "item slots");
+
+constexpr int kTCostBoth = 3, kTCostOne = 2;     // of a step of two row tiles, and of one
+constexpr uint32_t kTCostLeast = 12;             // of a CTA's share: four steps, about a prologue
+
+// The list's entries of a request.  (The host keeps the cost of the list below
+// 2^32.)
+struct TallRequest {
+  int L, own;
+  int steps;             // of an item
+  int both, one;         // pairs of two row tiles with own rows, and of one (0 or 1)
+  __device__ __forceinline__ uint32_t cost_head() const {
+    return static_cast<uint32_t>(steps) * static_cast<uint32_t>(kTCostBoth * both + kTCostOne * one);
+  }
+};
+
+__device__ __forceinline__ TallRequest tall_request(const SplitArgs& a, int b, int tile_tokens, bool report) {
+  TallRequest q;
+  q.L = a.seq_lens[b];
+  if (q.L < 0 || q.L > a.max_seq_len) {
+    if (report && a.status != nullptr) atomicOr(a.status, static_cast<int32_t>(DA_STATUS_SEQ_LEN));
+    q.L = q.L < 0 ? 0 : a.max_seq_len;
+  }
+  q.own = own_rows(a.own, a.q_len, b, q.L, report, a.status).n;
+  q.steps = (q.L + kTKeys - 1) / kTKeys;
+  q.both = q.own / (2 * tile_tokens);
+  const int left = q.own - q.both * 2 * tile_tokens;
+  q.one = left > 0 && left <= tile_tokens ? 1 : 0;
+  q.both += left > tile_tokens ? 1 : 0;
+  return q;
+}
+
+// A place in the list: step `step` of an item.
+struct TallPlace {
+  int b, kvh, pair, step;
+  TallRequest q;         // of request b
+  uint32_t item_cost;    // cost of the list before the item
+  __device__ __forceinline__ uint32_t per_step() const { return pair < q.both ? kTCostBoth : kTCostOne; }
+  __device__ __forceinline__ bool same_item(const TallPlace& o) const {
+    return b == o.b && kvh == o.kvh && pair == o.pair;
+  }
+};
+
+// The cost of the list, cut into shares as even as can be: share c begins at
+// begin(c).
+struct TallShares {
+  uint32_t total, n, each, more;  // `more` shares have one more
+  __device__ __forceinline__ uint32_t begin(uint32_t c) const { return each * c + min(c, more); }
+};
+
+// The whole warp.  The requests of lanes 0 .. 31 come back in `mine`.
+__device__ __forceinline__ TallShares tall_shares(const SplitArgs& a, int tile_tokens, bool report, TallRequest& mine) {
+  const int lane = threadIdx.x & 31;
+  uint32_t sum = 0;
+  mine = TallRequest{};
+  for (int b = lane; b < a.batch; b += 32) {
+    const TallRequest q = tall_request(a, b, tile_tokens, report);
+    if (b == lane) mine = q;
+    sum += q.cost_head();
+  }
+  TallShares h;
+  h.total = __reduce_add_sync(0xffffffffu, sum) * static_cast<uint32_t>(a.num_kv_heads);
+  h.n = min(static_cast<uint32_t>(kTallCtas), max(h.total / kTCostLeast, 1u));
+  h.each = h.total / h.n;
+  h.more = h.total - h.each * h.n;
+  return h;
+}
+
+// The whole warp: the place at cost x (below the total) of the list.
+__device__ __forceinline__ TallPlace tall_place(const SplitArgs& a, int tile_tokens, uint32_t x, const TallRequest& mine) {
+  const int lane = threadIdx.x & 31;
+  TallPlace p = {};
+  uint32_t before = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    TallRequest q = {};
+    if (b0 == 0) q = mine;
+    else if (b0 + lane < a.batch) q = tall_request(a, b0 + lane, tile_tokens, false);
+    const uint32_t cost = q.cost_head() * static_cast<uint32_t>(a.num_kv_heads);
+    uint32_t upto = cost;  // inclusive scan
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, before + upto > x);
+    if (past != 0) {
+      const int at = __ffs(past) - 1;
+      p.b = b0 + at;
+      p.q.L = __shfl_sync(0xffffffffu, q.L, at);
+      p.q.own = __shfl_sync(0xffffffffu, q.own, at);
+      p.q.steps = __shfl_sync(0xffffffffu, q.steps, at);
+      p.q.both = __shfl_sync(0xffffffffu, q.both, at);
+      p.q.one = __shfl_sync(0xffffffffu, q.one, at);
+      p.item_cost = before + __shfl_sync(0xffffffffu, upto - cost, at);
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  const uint32_t head = p.q.cost_head(), both = static_cast<uint32_t>(kTCostBoth) * p.q.steps;
+  uint32_t left = x - p.item_cost;
+  const uint32_t kvh = left / head;
+  left -= kvh * head;
+  const uint32_t pair = min(left / both, static_cast<uint32_t>(p.q.both));
+  left -= pair * both;
+  p.kvh = static_cast<int>(kvh);
+  p.pair = static_cast<int>(pair);
+  p.step = static_cast<int>(left / p.per_step());
+  p.item_cost = x - left;
+  return p;
+}
+
+// What the merge has to do for a CTA (in the workspace): the item that its share
+// begins in the middle of and ends, in n pieces, the first in share `first` (n 0:
+// there is none).
+struct TallJoin {
+  int n, first, b, kvh, pair;
+};
+static_assert(sizeof(TallJoin) <= kTallJoinBytes, "merge records");
 
 __global__ void __launch_bounds__(kTThreads, 1)
     tall_kernel(const __grid_constant__ TallMaps maps, const SplitArgs a, const int box_tokens) {
@@ -120,14 +241,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
   uint64_t* o_done = p_full + 4;                                      // [2] the item's last P V
   uint64_t* item_full = o_done + 2;                                   // [2] descriptor written
   uint64_t* item_empty = item_full + 2;                               // [2] descriptor read
-  uint64_t* ask_bar = item_empty + 2;                                 // the scheduler's answer
-  uint64_t* tmem_done = ask_bar + 1;
+  uint64_t* tmem_done = item_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tmem_done + 1);
-  int* near_end = reinterpret_cast<int*>(tmem_slot + 1);              // items that the MMA warp is about to end
-  uint8_t* answer = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem + kTOffItems) + 15) & ~static_cast<uintptr_t>(15));
-  TallItem* items = reinterpret_cast<TallItem*>(answer + 16);         // [2], 64 bytes each
-  auto item_slot = [&](int k) { return reinterpret_cast<TallItem*>(reinterpret_cast<uint8_t*>(items) + (k & 1) * 64); };
+  auto item_slot = [&](int k) { return reinterpret_cast<TallItem*>(smem + kTOffItems + (k & 1) * 64); };
 
   if (tid == 0) {
     for (int s = 0; s < kTSlots; ++s) {
@@ -143,10 +259,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
       mbar_init(&item_empty[i], kTReaders);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], 4);
-    mbar_init(ask_bar, 1);
     mbar_init(tmem_done, 8);
     fence_mbar_init();
-    *near_end = 0;
   }
   if (warp == kTMmaWarp) {
     tmem_alloc(tmem_slot, kTTmemCols);
@@ -157,7 +271,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
   tc_fence_after_sync();
   grid_dependency_wait();
   const uint32_t smem_base = smem_addr(smem);
-  const int S = a.num_splits;
   const int tile_tokens = kTRows / a.group;  // of a row tile
   auto report = [&]() {
     if (lane == 0 && a.status != nullptr) atomicOr(a.status, static_cast<int32_t>(DA_STATUS_TIMEOUT));
@@ -178,60 +291,62 @@ __global__ void __launch_bounds__(kTThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTOtherRegs));
     if (warp == kTSchedWarp) {
       // ===================================================== schedule, and Q
+      const int cta = static_cast<int>(blockIdx.x);
+      TallRequest mine;
+      const TallShares share = tall_shares(a, tile_tokens, cta == 0, mine);
+      TallPlace at = {}, end = {};
+      const bool some = share.total > 0 && static_cast<uint32_t>(cta) < share.n;
+      const bool to_end = static_cast<uint32_t>(cta) + 1 == share.n;  // the share runs to the list's end
+      if (some) {
+        at = tall_place(a, tile_tokens, share.begin(cta), mine);
+        if (!to_end) end = tall_place(a, tile_tokens, share.begin(cta + 1), mine);
+      }
       if (lane == 0) {
         prefetch_tensor_map(&maps.q);
-        uint32_t x = blockIdx.x, y = blockIdx.y, z = blockIdx.z;
-        bool have = true;
         int q_use[2] = {0, 0};
         const uint32_t q_bytes = static_cast<uint32_t>(tile_tokens * a.group) * 256u;
+        bool more = some;
+        const TallPlace first_place = at;
+        const bool begins_inside = at.step > 0;
         for (int k = 0; ok; ++k) {
-          if (k > 0) {
-            // the next item once the one before nears its end
-            const unsigned long long t0 = global_timer_ns();
-            while (*static_cast<volatile int*>(near_end) < k) {
-              __nanosleep(100);
-              if (global_timer_ns() - t0 > 4 * kWaitLimitNs) {
-                ok = false;
-                break;
+          TallItem it = {};
+          if (more) {
+            const bool last = !to_end && at.same_item(end);
+            const int stop = last ? end.step : at.q.steps;
+            if (stop > at.step) {
+              it.valid = 1;
+              it.b = at.b;
+              it.kvh = at.kvh;
+              it.tok0 = at.pair * 2 * tile_tokens;
+              it.own = at.q.own;
+              it.base = a.own.mask != nullptr ? at.q.L - at.q.own : INT_MAX;
+              it.t_begin = at.step * kTKeys;
+              it.t_end = min(at.q.L, stop * kTKeys);
+              it.steps = stop - at.step;
+              it.tiles = at.pair < at.q.both ? 2 : 1;
+              it.slot = at.step > 0 ? 2 * cta : stop < at.q.steps ? 2 * cta + 1 : -1;
+            }
+            more = !last;
+            // the next item of the list
+            at.step = 0;
+            if (more && ++at.pair >= at.q.both + at.q.one) {
+              at.pair = 0;
+              if (++at.kvh >= a.num_kv_heads) {
+                at.kvh = 0;
+                do {
+                  ++at.b;
+                  more = at.b < a.batch;
+                  if (more) at.q = tall_request(a, at.b, tile_tokens, false);
+                } while (more && at.q.cost_head() == 0);
               }
             }
-            if (!ok) break;
-            mbar_arrive_expect_tx(ask_bar, 16);
-            try_cancel(answer, ask_bar);
-            ok = mbar_wait(ask_bar, (k - 1) & 1);
-            if (!ok) break;
-            have = canceled_block(answer, x, y, z);
-            fence_proxy_async_smem();  // (read before the next answer is written)
-          }
-          TallItem it = {};
-          it.valid = have ? 1 : 0;
-          if (have) {
-            it.b = static_cast<int>(z);
-            it.kvh = static_cast<int>(y);
-            const int pair = static_cast<int>(x) / S;
-            it.split = static_cast<int>(x) - pair * S;
-            it.tok0 = pair * 2 * tile_tokens;
-            const bool first = x == 0 && y == 0;
-            int L = a.seq_lens[it.b];
-            if (L < 0 || L > a.max_seq_len) {
-              if (first && a.status != nullptr) atomicOr(a.status, static_cast<int32_t>(DA_STATUS_SEQ_LEN));
-              L = L < 0 ? 0 : a.max_seq_len;
-            }
-            const OwnRows own = own_rows(a.own, a.q_len, it.b, L, first, a.status);
-            it.L = L;
-            it.own = own.n;
-            it.base = own.base;
-            it.t_begin = it.split * a.chunk_len;
-            it.t_end = min(L, it.t_begin + a.chunk_len);
-            it.steps = it.t_end > it.t_begin ? (it.t_end - it.t_begin + kTKeys - 1) / kTKeys : 0;
-            it.tiles = own.n > it.tok0 + tile_tokens ? 2 : own.n > it.tok0 ? 1 : 0;
-            if (it.steps == 0 || it.tiles == 0) it.steps = it.tiles = 0;
           }
           if (k > 1) ok = mbar_wait(&item_empty[k & 1], ((k >> 1) - 1) & 1);
           if (!ok) break;
           *item_slot(k) = it;
           mbar_arrive(&item_full[k & 1]);
-          if (!have) break;
+          if (it.valid == 0) break;  // (only the last item of a share can be empty)
+          if (!more) allow_dependent_launch();
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             if (g >= it.tiles) break;
@@ -244,6 +359,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
             ++q_use[g];
           }
         }
+        // for the merge: the share it begins in is the last that starts before the
+        // item's first step ends
+        TallJoin join = {};
+        if (some && begins_inside && (to_end || !first_place.same_item(end))) {
+          int first = cta;
+          while (first > 0 && share.begin(first) >= first_place.item_cost + first_place.per_step()) --first;
+          join = TallJoin{cta - first + 1, first, first_place.b, first_place.kvh, first_place.pair};
+        }
+        *reinterpret_cast<TallJoin*>(a.join + cta * kTallJoinBytes) = join;
         if (!ok) {
           report();
 #pragma unroll
@@ -259,7 +383,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       // kTSlots, which is filled by the warp of that number.  A lane issues one box.
       const int pw = warp - kTProdWarp;
       if (pw >= kTProducers) return;
-      if (lane == 0 && pw == 0) {
+      if (lane == 0 && pw == 0 && a.max_seq_len > 0) {
         prefetch_tensor_map(&maps.k);
         prefetch_tensor_map(&maps.v);
       }
@@ -341,10 +465,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
     for (int k = 0; next_item(k); ++k) {
       const int n = item_slot(k)->steps, tiles = item_slot(k)->tiles;
       leave_item(k);
-      if (n == 0) {
-        if (lane == 0) *static_cast<volatile int*>(near_end) = k + 1;
-        continue;
-      }
       // S of the next K for tile g; behind the last tile the slot is free, behind
       // an item's last step Q is
       auto issue_s = [&](int g, bool last_step) {
@@ -392,8 +512,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
           if (more) issue_s(g, i + 2 == n);
           else if (last_tile) umma_commit_warp(&o_done[g]);
           if (last_tile) advance(v_slot, v_par);
-          if (g == 0 && lane == 0 && (i == n - kTAhead || (i == 0 && n < kTAhead)))
-            *static_cast<volatile int*>(near_end) = k + 1;
         }
       }
       if (!ok) break;
@@ -547,17 +665,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
     }
     ubase += 2 * n;
 
-    // ---- the rows' outputs (chunks behind the request's last one have none).
-    // A lane that wrote its own row would touch a sector of each of 32 rows with
-    // every store, and the tensor core waits meanwhile (6000 cycles for a partial):
-    // so O is read as 16-row fragments, where four lanes hold eight neighbouring
-    // columns of a row.
-    const int chunks = it.L > 0 ? (it.L + a.chunk_len - 1) / a.chunk_len : 1;
-    const bool direct = chunks == 1;
-    const bool writes = in_tile && t < a.q_len && it.split < chunks;
+    // ---- the rows' outputs.  A lane that wrote its own row would touch a sector of
+    // each of 32 rows with every store, and the tensor core waits meanwhile: so O is
+    // read as 16-row fragments, where four lanes hold eight neighbouring columns of
+    // a row.
+    const bool direct = it.slot < 0;
+    const bool writes = in_tile && t < a.q_len;
     const int h = it.kvh * a.group + (r - rt * a.group);
     const int64_t prow = (static_cast<int64_t>(it.b) * a.q_len + t) * a.num_q_heads + h;
-    const int64_t pidx = prow * S + it.split;
+    const int64_t pidx = static_cast<int64_t>(it.slot) * (2 * kTRows) + g * kTRows + r;
     const bool have = ok && active && mine && l != 0.f;
     const float inv = have ? (1.f / l) * a.v_scale : 0.f;  // (NaN stays NaN)
     // byte offset of the row, -1 where nothing is written
@@ -640,6 +756,75 @@ __global__ void __launch_bounds__(kTThreads, 1)
   if (lane == 0) mbar_arrive(tmem_done);
 }
 
+// Merges the pieces of the items that CTA blockIdx.x of the attention kernel has
+// ended and not begun: piece 0 in slot 2 j + 1 of the CTA j that began it, the
+// others in slots 2 (j + 1), 2 (j + 2), ..; a warp per row, lane i d = 4 i .. + 3.
+//     M = max_s lse_s,  w_s = exp(lse_s - M),  out = sum w_s O_s / sum w_s.
+// It also writes the rows that are in no item: those of requests without keys and
+// of pairs of tiles that are all padding.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinBlocks = 8;                    // of an item's 256 rows
+
+__global__ void __launch_bounds__(32 * kJoinWarps) tall_join_kernel(const SplitArgs a) {
+  constexpr uint32_t kFull = 0xffffffffu;
+  constexpr float kLog2e = 1.4426950408889634f;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tile_tokens = kTRows / a.group;
+  grid_dependency_wait();
+  const TallJoin join = *reinterpret_cast<const TallJoin*>(a.join + blockIdx.x * kTallJoinBytes);
+  // ---- rows in no item: (request, pair) by (request, pair)
+  const int pairs = (a.q_len + 2 * tile_tokens - 1) / (2 * tile_tokens);
+  const int64_t slots = static_cast<int64_t>(a.batch) * pairs;
+  for (int64_t e = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x; e < slots;
+       e += static_cast<int64_t>(gridDim.x) * gridDim.y) {
+    const int b = static_cast<int>(e / pairs), pair = static_cast<int>(e - static_cast<int64_t>(b) * pairs);
+    const TallRequest q = tall_request(a, b, tile_tokens, false);
+    if (q.steps > 0 && pair < q.both + q.one) continue;
+    const int t0 = pair * 2 * tile_tokens;
+    const int rows = min(2 * tile_tokens, a.q_len - t0) * a.num_q_heads;
+    for (int r = warp; r < rows; r += kJoinWarps) {
+      const int t = t0 + r / a.num_q_heads, h = r % a.num_q_heads;
+      *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(b) * a.o_sb + static_cast<int64_t>(t) * a.o_st +
+                                static_cast<int64_t>(h) * a.o_sh + lane * 4) = make_uint2(0u, 0u);
+      if (lane == 0) a.lse[(static_cast<int64_t>(b) * a.q_len + t) * a.num_q_heads + h] = -INFINITY;
+    }
+  }
+  // ---- the item that this CTA ended and did not begin
+  const int n = join.n;
+  if (n == 0) return;
+  auto slot_of = [&](int s) { return s == 0 ? 2 * join.first + 1 : 2 * (join.first + s); };
+  for (int row = static_cast<int>(blockIdx.y) * kJoinWarps + warp; row < 2 * kTRows; row += kJoinBlocks * kJoinWarps) {
+    const int g = row / kTRows, r = row - g * kTRows, rt = r / a.group;
+    const int t = join.pair * 2 * tile_tokens + g * tile_tokens + rt;
+    if (rt >= tile_tokens || t >= a.q_len) continue;
+    const int h = join.kvh * a.group + (r - rt * a.group);
+    float M = -INFINITY;
+    for (int s = lane; s < n; s += 32) M = fmax_nan(M, a.part_lse[static_cast<int64_t>(slot_of(s)) * (2 * kTRows) + row]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmax_nan(M, __shfl_xor_sync(kFull, M, o));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float W = 0.f;
+    if (M != -INFINITY) {
+      for (int s = 0; s < n; ++s) {
+        const int64_t at_s = static_cast<int64_t>(slot_of(s)) * (2 * kTRows) + row;
+        const float w = ex2((a.part_lse[at_s] - M) * kLog2e);
+        const float4 x = *reinterpret_cast<const float4*>(a.part_o + at_s * kHeadDim + lane * 4);
+        W += w;
+        acc.x += w * x.x;
+        acc.y += w * x.y;
+        acc.z += w * x.z;
+        acc.w += w * x.w;
+      }
+    }
+    const float inv = W == 0.f ? 0.f : 1.f / W;
+    *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(join.b) * a.o_sb + static_cast<int64_t>(t) * a.o_st +
+                              static_cast<int64_t>(h) * a.o_sh + lane * 4) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (lane == 0)
+      a.lse[(static_cast<int64_t>(join.b) * a.q_len + t) * a.num_q_heads + h] = W == 0.f ? -INFINITY : M + logf(W);
+  }
+}
+
 std::mutex g_tall_mu;
 bool g_tall_attr[64];
 
@@ -661,9 +846,8 @@ cudaError_t launch_tall(const CUtensorMap& q_map, const CUtensorMap& k_map, cons
       g_tall_attr[dev] = true;
     }
   }
-  const int pair = 2 * (kTRows / a.group);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.q_len + pair - 1) / pair) * a.num_splits, a.num_kv_heads, a.batch);
+  cfg.gridDim = dim3(kTallCtas);
   cfg.blockDim = dim3(kTThreads);
   cfg.dynamicSmemBytes = kTSmem;
   cfg.stream = stream;
@@ -672,7 +856,12 @@ cudaError_t launch_tall(const CUtensorMap& q_map, const CUtensorMap& k_map, cons
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tall_kernel, TallMaps{q_map, k_map, v_map}, a, box_tokens);
+  e = cudaLaunchKernelEx(&cfg, tall_kernel, TallMaps{q_map, k_map, v_map}, a, box_tokens);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(kTallCtas, kJoinBlocks);
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, tall_join_kernel, a);
 }
 
 }  // namespace dattn
