@@ -29,9 +29,11 @@
 // kernels for fewer rows do, took 9 % longer).
 //
 // The work is cut evenly, whatever the lengths: all steps of all items stand in
-// one list, (request, kv head, pair of row tiles) by (request, kv head, pair), and
-// each of kTallCtas CTAs takes the same share of it, in steps (a step of two row
-// tiles counts 3, of one 2: their measured times).  So at most two of a CTA's
+// one list, by pair of row tiles, request and kv head, and each of kTallCtas CTAs
+// takes the same share of it, in steps (a step of two row tiles counts 3, of one 2:
+// their measured times).  With the pairs outermost, those of a (request, kv head)
+// are worked on at about the same time and meet its keys in L2 (4 x 2048 tokens x
+// 4096 keys, 32 heads with keys of their own: 422 us with the pairs innermost).  So at most two of a CTA's
 // items are not whole; those leave fp32 partials in the CTA's two slots of the
 // workspace, and tall_join_kernel merges them.  Every CTA works its share out from
 // the lengths in device memory (tall_share), and so does the merge.  The copies
@@ -114,8 +116,14 @@ struct TallRequest {
   int L, own;
   int steps;             // of an item
   int both, one;         // pairs of two row tiles with own rows, and of one (0 or 1)
-  __device__ __forceinline__ uint32_t cost_head() const {
-    return static_cast<uint32_t>(steps) * static_cast<uint32_t>(kTCostBoth * both + kTCostOne * one);
+  // cost of an item of pair p, and of the pairs below p, for one head
+  __device__ __forceinline__ uint32_t per_step(int p) const {
+    return p < both ? kTCostBoth : p == both && one != 0 ? kTCostOne : 0;
+  }
+  __device__ __forceinline__ uint32_t cost(int p) const { return static_cast<uint32_t>(steps) * per_step(p); }
+  __device__ __forceinline__ uint32_t cost_below(int p) const {
+    return static_cast<uint32_t>(steps) *
+           static_cast<uint32_t>(kTCostBoth * min(p, both) + (p > both ? kTCostOne * one : 0));
   }
 };
 
@@ -140,7 +148,6 @@ struct TallPlace {
   int b, kvh, pair, step;
   TallRequest q;         // of request b
   uint32_t item_cost;    // cost of the list before the item
-  __device__ __forceinline__ uint32_t per_step() const { return pair < q.both ? kTCostBoth : kTCostOne; }
   __device__ __forceinline__ bool same_item(const TallPlace& o) const {
     return b == o.b && kvh == o.kvh && pair == o.pair;
   }
@@ -153,18 +160,27 @@ struct TallShares {
   __device__ __forceinline__ uint32_t begin(uint32_t c) const { return each * c + min(c, more); }
 };
 
-// The whole warp.  The requests of lanes 0 .. 31 come back in `mine`.
-__device__ __forceinline__ TallShares tall_shares(const SplitArgs& a, int tile_tokens, bool report, TallRequest& mine) {
+// The whole warp: cost of the pairs below p, for all requests.  `mine` are the
+// requests of lanes 0 .. 31.
+__device__ __forceinline__ uint32_t tall_cost_below(const SplitArgs& a, int tile_tokens, const TallRequest& mine, int p) {
+  uint32_t sum = mine.cost_below(p);
+  for (int b = 32 + (threadIdx.x & 31); b < a.batch; b += 32)
+    sum += tall_request(a, b, tile_tokens, false).cost_below(p);
+  return __reduce_add_sync(0xffffffffu, sum) * static_cast<uint32_t>(a.num_kv_heads);
+}
+
+// The whole warp.
+__device__ __forceinline__ TallShares tall_shares(const SplitArgs& a, int tile_tokens, int pairs, bool report,
+                                                  TallRequest& mine) {
   const int lane = threadIdx.x & 31;
-  uint32_t sum = 0;
   mine = TallRequest{};
   for (int b = lane; b < a.batch; b += 32) {
     const TallRequest q = tall_request(a, b, tile_tokens, report);
     if (b == lane) mine = q;
-    sum += q.cost_head();
+    else if (!report) break;  // (the others are for the status bits)
   }
   TallShares h;
-  h.total = __reduce_add_sync(0xffffffffu, sum) * static_cast<uint32_t>(a.num_kv_heads);
+  h.total = tall_cost_below(a, tile_tokens, mine, pairs);
   h.n = min(static_cast<uint32_t>(kTallCtas), max(h.total / kTCostLeast, 1u));
   h.each = h.total / h.n;
   h.more = h.total - h.each * h.n;
@@ -172,15 +188,28 @@ __device__ __forceinline__ TallShares tall_shares(const SplitArgs& a, int tile_t
 }
 
 // The whole warp: the place at cost x (below the total) of the list.
-__device__ __forceinline__ TallPlace tall_place(const SplitArgs& a, int tile_tokens, uint32_t x, const TallRequest& mine) {
+__device__ __forceinline__ TallPlace tall_place(const SplitArgs& a, int tile_tokens, int pairs, uint32_t x,
+                                                const TallRequest& mine) {
   const int lane = threadIdx.x & 31;
   TallPlace p = {};
+  // the last pair that begins at or before x
   uint32_t before = 0;
+  int past_it = pairs;
+  while (past_it - p.pair > 1) {
+    const int mid = (p.pair + past_it) >> 1;
+    const uint32_t c = tall_cost_below(a, tile_tokens, mine, mid);
+    if (c <= x) {
+      p.pair = mid;
+      before = c;
+    } else {
+      past_it = mid;
+    }
+  }
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
     TallRequest q = {};
     if (b0 == 0) q = mine;
     else if (b0 + lane < a.batch) q = tall_request(a, b0 + lane, tile_tokens, false);
-    const uint32_t cost = q.cost_head() * static_cast<uint32_t>(a.num_kv_heads);
+    const uint32_t cost = q.cost(p.pair) * static_cast<uint32_t>(a.num_kv_heads);
     uint32_t upto = cost;  // inclusive scan
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -196,21 +225,16 @@ __device__ __forceinline__ TallPlace tall_place(const SplitArgs& a, int tile_tok
       p.q.steps = __shfl_sync(0xffffffffu, q.steps, at);
       p.q.both = __shfl_sync(0xffffffffu, q.both, at);
       p.q.one = __shfl_sync(0xffffffffu, q.one, at);
-      p.item_cost = before + __shfl_sync(0xffffffffu, upto - cost, at);
+      before += __shfl_sync(0xffffffffu, upto - cost, at);
       break;
     }
     before += __shfl_sync(0xffffffffu, upto, 31);
   }
-  const uint32_t head = p.q.cost_head(), both = static_cast<uint32_t>(kTCostBoth) * p.q.steps;
-  uint32_t left = x - p.item_cost;
-  const uint32_t kvh = left / head;
-  left -= kvh * head;
-  const uint32_t pair = min(left / both, static_cast<uint32_t>(p.q.both));
-  left -= pair * both;
+  const uint32_t item = p.q.cost(p.pair);
+  const uint32_t kvh = (x - before) / item;
   p.kvh = static_cast<int>(kvh);
-  p.pair = static_cast<int>(pair);
-  p.step = static_cast<int>(left / p.per_step());
-  p.item_cost = x - left;
+  p.item_cost = before + kvh * item;
+  p.step = static_cast<int>((x - p.item_cost) / p.q.per_step(p.pair));
   return p;
 }
 
@@ -293,13 +317,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
       // ===================================================== schedule, and Q
       const int cta = static_cast<int>(blockIdx.x);
       TallRequest mine;
-      const TallShares share = tall_shares(a, tile_tokens, cta == 0, mine);
+      const int pairs = (a.q_len + 2 * tile_tokens - 1) / (2 * tile_tokens);
+      const TallShares share = tall_shares(a, tile_tokens, pairs, cta == 0, mine);
       TallPlace at = {}, end = {};
       const bool some = share.total > 0 && static_cast<uint32_t>(cta) < share.n;
       const bool to_end = static_cast<uint32_t>(cta) + 1 == share.n;  // the share runs to the list's end
       if (some) {
-        at = tall_place(a, tile_tokens, share.begin(cta), mine);
-        if (!to_end) end = tall_place(a, tile_tokens, share.begin(cta + 1), mine);
+        at = tall_place(a, tile_tokens, pairs, share.begin(cta), mine);
+        if (!to_end) end = tall_place(a, tile_tokens, pairs, share.begin(cta + 1), mine);
       }
       if (lane == 0) {
         prefetch_tensor_map(&maps.q);
@@ -329,16 +354,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
             more = !last;
             // the next item of the list
             at.step = 0;
-            if (more && ++at.pair >= at.q.both + at.q.one) {
-              at.pair = 0;
-              if (++at.kvh >= a.num_kv_heads) {
-                at.kvh = 0;
-                do {
-                  ++at.b;
-                  more = at.b < a.batch;
-                  if (more) at.q = tall_request(a, at.b, tile_tokens, false);
-                } while (more && at.q.cost_head() == 0);
-              }
+            if (more && ++at.kvh >= a.num_kv_heads) {
+              at.kvh = 0;
+              do {
+                if (++at.b >= a.batch) {
+                  at.b = 0;
+                  more = ++at.pair < pairs;
+                }
+                if (more) at.q = tall_request(a, at.b, tile_tokens, false);
+              } while (more && at.q.cost(at.pair) == 0);
             }
           }
           if (k > 1) ok = mbar_wait(&item_empty[k & 1], ((k >> 1) - 1) & 1);
@@ -364,7 +388,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         TallJoin join = {};
         if (some && begins_inside && (to_end || !first_place.same_item(end))) {
           int first = cta;
-          while (first > 0 && share.begin(first) >= first_place.item_cost + first_place.per_step()) --first;
+          while (first > 0 && share.begin(first) >= first_place.item_cost + first_place.q.per_step(first_place.pair)) --first;
           join = TallJoin{cta - first + 1, first, first_place.b, first_place.kvh, first_place.pair};
         }
         *reinterpret_cast<TallJoin*>(a.join + cta * kTallJoinBytes) = join;
@@ -763,7 +787,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
 // It also writes the rows that are in no item: those of requests without keys and
 // of pairs of tiles that are all padding.
 constexpr int kJoinWarps = 8;
-constexpr int kJoinBlocks = 8;                    // of an item's 256 rows
+constexpr int kJoinBlocks = 16;                   // of an item's 256 rows
 
 __global__ void __launch_bounds__(32 * kJoinWarps) tall_join_kernel(const SplitArgs a) {
   constexpr uint32_t kFull = 0xffffffffu;
@@ -798,22 +822,43 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tall_join_kernel(const SplitA
     const int t = join.pair * 2 * tile_tokens + g * tile_tokens + rt;
     if (rt >= tile_tokens || t >= a.q_len) continue;
     const int h = join.kvh * a.group + (r - rt * a.group);
-    float M = -INFINITY;
-    for (int s = lane; s < n; s += 32) M = fmax_nan(M, a.part_lse[static_cast<int64_t>(slot_of(s)) * (2 * kTRows) + row]);
+    // the first 32 pieces' LSEs, one per lane, and four partial rows together
+    constexpr int kAhead = 4;
+    const float* lses = a.part_lse + row;
+    const float* parts = a.part_o + static_cast<int64_t>(row) * kHeadDim + lane * 4;
+    auto lse_of = [&](int s) { return s < n ? lses[static_cast<int64_t>(slot_of(s)) * (2 * kTRows)] : -INFINITY; };
+    float4 x[kAhead];
+    auto fetch = [&](int s0) {
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e)
+        if (s0 + e < n)
+          x[e] = *reinterpret_cast<const float4*>(parts + static_cast<int64_t>(slot_of(s0 + e)) * (2 * kTRows * kHeadDim));
+    };
+    const float lse0 = lse_of(lane);
+    fetch(0);
+    float M = lse0;
+    for (int s = 32 + lane; s < n; s += 32) M = fmax_nan(M, lse_of(s));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmax_nan(M, __shfl_xor_sync(kFull, M, o));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float W = 0.f;
     if (M != -INFINITY) {
-      for (int s = 0; s < n; ++s) {
-        const int64_t at_s = static_cast<int64_t>(slot_of(s)) * (2 * kTRows) + row;
-        const float w = ex2((a.part_lse[at_s] - M) * kLog2e);
-        const float4 x = *reinterpret_cast<const float4*>(a.part_o + at_s * kHeadDim + lane * 4);
-        W += w;
-        acc.x += w * x.x;
-        acc.y += w * x.y;
-        acc.z += w * x.z;
-        acc.w += w * x.w;
+      for (int s0 = 0; s0 < n; s0 += 32) {
+        const float w_mine = ex2(((s0 == 0 ? lse0 : lse_of(s0 + lane)) - M) * kLog2e);
+        const int here = min(32, n - s0);
+        for (int s1 = 0; s1 < here; s1 += kAhead) {
+          if (s0 + s1 > 0) fetch(s0 + s1);
+#pragma unroll
+          for (int e = 0; e < kAhead; ++e) {
+            if (s1 + e >= here) break;
+            const float w = __shfl_sync(kFull, w_mine, s1 + e);
+            W += w;
+            acc.x += w * x[e].x;
+            acc.y += w * x[e].y;
+            acc.z += w * x[e].z;
+            acc.w += w * x[e].w;
+          }
+        }
       }
     }
     const float inv = W == 0.f ? 0.f : 1.f / W;
