@@ -654,9 +654,8 @@ int decode_attn_tree_mask(int32_t batch, int32_t q_len, int32_t max_seq_len,
  * p->causal is not used, nor is DA_FLAG_TEST_WITHHOLD_COPY above
  * DECODE_ATTN_MAX_ROWS.  (Hq / Hkv) * q_len may exceed DECODE_ATTN_MAX_ROWS;
  * Hq / Hkv may not, nor q_len DECODE_ATTN_MAX_TREE.  Above that many rows the
- * call cuts its work evenly on the device, num_splits is not used, and the
- * workspace holds 40 MB of partials and, for FP8 and 4-bit caches, the batch's
- * keys and values in bf16 (B * max_seq_len * Hkv * 512 bytes).
+ * call cuts its work evenly on the device: num_splits is not used, and the
+ * workspace holds 40 MB of partials whatever the sizes.
  * Status as decode_attn(); DA_STATUS_SHORT_CAUSAL where L < n_b (the first
  * n_b - L new tokens then have no key).
  */

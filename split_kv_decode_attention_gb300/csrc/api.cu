@@ -11,7 +11,6 @@
 #include <cstring>
 #include <mutex>
 
-#include "cache_kernels.cuh"
 #include "decode_attn.h"
 #include "internal.cuh"
 #include "kernels.cuh"
@@ -309,11 +308,11 @@ int fp4_box_halves(const decode_attn_params* p, bool paged, int unit) {
   return h;
 }
 
-// A map of a 4-bit cache: its values, or (scales) its block scales.  (Encoded
+// A map of a 4-bit cache, in boxes of `tokens` tokens of `unit` heads: its values, or
+// (scales) its block scales.  (Encoded
 // for every call: 36 ns.)
 int make_fp4_map(CUtensorMap* map, const void* base, const decode_attn_params* p,
-                 const decode_attn_cache* c, bool paged, int unit, bool scales, bool own_pages) {
-  const cuuint32_t tokens = static_cast<cuuint32_t>(16 * fp4_box_halves(p, paged, unit));
+                 const decode_attn_cache* c, bool paged, int unit, cuuint32_t tokens, bool scales, bool own_pages) {
   const cuuint64_t slots = static_cast<cuuint64_t>(paged ? p->page_size : std::max(p->max_seq_len, 1));
   const cuuint64_t groups = static_cast<cuuint64_t>(paged ? p->num_pages : std::max(p->batch, 1));
   const cuuint64_t heads = static_cast<cuuint64_t>(p->num_kv_heads);
@@ -635,10 +634,11 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
     std::memset(&maps4, 0, sizeof(maps4));
     if (!no_keys) {
       const decode_attn_cache* c = ext.fp4;
-      rc = make_fp4_map(&maps4.k, c->k, p, c, paged, unit, false, ext.per_head);
-      if (rc == DA_OK) rc = make_fp4_map(&maps4.v, c->v, p, c, paged, unit, false, ext.per_head);
-      if (rc == DA_OK) rc = make_fp4_map(&maps4.ks, c->k_block_scale, p, c, paged, unit, true, ext.per_head);
-      if (rc == DA_OK) rc = make_fp4_map(&maps4.vs, c->v_block_scale, p, c, paged, unit, true, ext.per_head);
+      const cuuint32_t box4 = static_cast<cuuint32_t>(16 * fp4_box_halves(p, paged, unit));
+      rc = make_fp4_map(&maps4.k, c->k, p, c, paged, unit, box4, false, ext.per_head);
+      if (rc == DA_OK) rc = make_fp4_map(&maps4.v, c->v, p, c, paged, unit, box4, false, ext.per_head);
+      if (rc == DA_OK) rc = make_fp4_map(&maps4.ks, c->k_block_scale, p, c, paged, unit, box4, true, ext.per_head);
+      if (rc == DA_OK) rc = make_fp4_map(&maps4.vs, c->v_block_scale, p, c, paged, unit, box4, true, ext.per_head);
       if (rc != DA_OK) return rc;
     }
   } else if (!no_keys) {
@@ -743,14 +743,13 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
 
 namespace {
 
-// Workspace of a call of more than DECODE_ATTN_MAX_ROWS rows per KV head: [K and V
-// in bf16, where the cache is not] [partials].
+// Workspace of a call of more than DECODE_ATTN_MAX_ROWS rows per KV head: partials
+// and the records of their merge.
 struct TallLayout {
-  int64_t tokens;              // of a request in the bf16 copy
-  size_t k, v, part_o, part_lse, join, total;
+  size_t part_o, part_lse, join, total;
 };
 
-int tall_layout(const decode_attn_params* p, const decode_attn_cache* c, TallLayout* l) {
+int tall_layout(const decode_attn_params* p, TallLayout* l) {
   const int64_t rows = static_cast<int64_t>(p->num_q_heads / p->num_kv_heads) * p->q_len;
   if (p->max_seq_len > (1 << 30) || rows > 0x7fffffff) return DA_ERR_BAD_SHAPE;
   // (the kernel adds up the costs of its steps in 32 bits)
@@ -758,22 +757,11 @@ int tall_layout(const decode_attn_params* p, const decode_attn_cache* c, TallLay
   const double pairs = static_cast<double>(ceil_div64(p->q_len, 2 * tall_tile_tokens(static_cast<int>(group))));
   if (3.0 * p->batch * p->num_kv_heads * pairs * static_cast<double>(ceil_div64(p->max_seq_len, 128)) >= 4294967295.0)
     return DA_ERR_BAD_SHAPE;
-  l->tokens = std::max<int64_t>(p->max_seq_len, 1);
-  size_t off = 0;
-  l->k = off;
-  l->v = off;
-  if (c->type != DA_CACHE_BF16) {
-    const size_t one = static_cast<size_t>(p->batch) * l->tokens * p->num_kv_heads * kHeadDim * 2;
-    l->v = round256(off + one);
-    off = round256(l->v + one);
-  }
   const size_t part = static_cast<size_t>(kTallSlots) * kTallSlotRows;
-  l->part_o = off;
-  off += part * kHeadDim * 4;
-  l->part_lse = off;
-  off += part * 4;
-  l->join = off;
-  l->total = off + static_cast<size_t>(kTallCtas) * kTallJoinBytes;
+  l->part_o = 0;
+  l->part_lse = part * kHeadDim * 4;
+  l->join = l->part_lse + part * 4;
+  l->total = l->join + static_cast<size_t>(kTallCtas) * kTallJoinBytes;
   return DA_OK;
 }
 
@@ -790,7 +778,7 @@ int rows_workspace_bytes(const decode_attn_params* p, const decode_attn_cache* c
   if (rc != DA_OK) return rc;
   if (bytes == nullptr) return DA_ERR_NULL_POINTER;
   TallLayout l;
-  const int rc2 = tall_layout(p, c, &l);
+  const int rc2 = tall_layout(p, &l);
   if (rc2 == DA_OK) *bytes = l.total;
   return rc2;
 }
@@ -827,49 +815,18 @@ int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void
   if (rc != DA_OK) return rc;
   if (di.major * 10 + di.minor < 100) return DA_ERR_NO_DEVICE;
   TallLayout l;
-  rc = tall_layout(p, c, &l);
+  rc = tall_layout(p, &l);
   if (rc != DA_OK) return rc;
   if (workspace == nullptr || workspace_bytes < l.total || !aligned16(workspace))
     return DA_ERR_WORKSPACE;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
 
-  // keys and values in bf16, as the tensor maps see them
-  const bool copied = c->type != DA_CACHE_BF16;
-  decode_attn_params kp = *p;
-  kp.flags &= ~static_cast<int32_t>(DA_FLAG_KV_FP8_E4M3);
-  const void* k = c->k;
-  const void* v = c->v;
-  if (copied) {
-    kp.kv_stride_head = kHeadDim;
-    kp.kv_stride_token = static_cast<int64_t>(p->num_kv_heads) * kHeadDim;
-    kp.kv_stride_page = kp.kv_stride_token * l.tokens;
-    k = w + l.k;
-    v = w + l.v;
-    if (!no_keys) {
-      // (without the cache's scales every value is exact in bf16; they go into
-      // the score scale and the output)
-      ReadArgs r;
-      std::memset(&r, 0, sizeof(r));
-      r.c = cache_view(p, c);
-      r.g = paging_view(p, block_table, seq_lens, status);
-      r.k = reinterpret_cast<uint16_t*>(w + l.k);
-      r.v = reinterpret_cast<uint16_t*>(w + l.v);
-      r.sb = kp.kv_stride_page;
-      r.st = kp.kv_stride_token;
-      r.sh = kp.kv_stride_head;
-      r.max_tokens = p->max_seq_len;
-      r.k_scale = 1.f;
-      r.v_scale = 1.f;
-      if (launch_read(r, st) != cudaSuccess) return DA_ERR_CUDA;
-    }
-  }
-  const bool tma_paged = paged && !copied;
   int box = 128;
-  while (tma_paged && p->page_size % box != 0) box /= 2;
-  CUtensorMap qmap, kmap, vmap;
-  std::memset(&kmap, 0, sizeof(kmap));
-  std::memset(&vmap, 0, sizeof(vmap));
+  while (paged && p->page_size % box != 0) box /= 2;
+  CUtensorMap qmap;
+  Fp4Maps maps;  // (ks and vs: 4-bit caches)
+  std::memset(&maps, 0, sizeof(maps));
   const int group = p->num_q_heads / p->num_kv_heads;
   {
     const cuuint64_t dims[4] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(p->num_q_heads),
@@ -883,9 +840,16 @@ int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
     if (rc != DA_OK) return rc;
   }
-  if (!no_keys) {
-    rc = make_kv_map(&kmap, k, &kp, tma_paged, box, false);
-    if (rc == DA_OK) rc = make_kv_map(&vmap, v, &kp, tma_paged, box, false);
+  if (!no_keys && c->type == DA_CACHE_FP4_E2M1) {
+    const cuuint32_t tokens = static_cast<cuuint32_t>(box);
+    rc = make_fp4_map(&maps.k, c->k, p, c, paged, 1, tokens, false, false);
+    if (rc == DA_OK) rc = make_fp4_map(&maps.v, c->v, p, c, paged, 1, tokens, false, false);
+    if (rc == DA_OK) rc = make_fp4_map(&maps.ks, c->k_block_scale, p, c, paged, 1, tokens, true, false);
+    if (rc == DA_OK) rc = make_fp4_map(&maps.vs, c->v_block_scale, p, c, paged, 1, tokens, true, false);
+    if (rc != DA_OK) return rc;
+  } else if (!no_keys) {
+    rc = make_kv_map(&maps.k, c->k, p, paged, box, false);
+    if (rc == DA_OK) rc = make_kv_map(&maps.v, c->v, p, paged, box, false);
     if (rc != DA_OK) return rc;
   }
 
@@ -903,7 +867,7 @@ int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void
   a.part_o = reinterpret_cast<float*>(w + l.part_o);
   a.part_lse = reinterpret_cast<float*>(w + l.part_lse);
   a.join = w + l.join;
-  a.block_table = tma_paged ? block_table : nullptr;
+  a.block_table = block_table;
   a.bt_stride = p->block_table_stride;
   a.seq_lens = seq_lens;
   a.len_sb = 1;
@@ -914,14 +878,15 @@ int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void
   a.num_kv_heads = p->num_kv_heads;
   a.group = group;
   a.rows = group * p->q_len;
-  a.page_size = tma_paged ? p->page_size : 0;
-  a.num_pages = tma_paged ? p->num_pages : 0;
-  a.paged = tma_paged ? 1 : 0;
+  a.page_size = paged ? p->page_size : 0;
+  a.num_pages = paged ? p->num_pages : 0;
+  a.paged = paged ? 1 : 0;
   a.max_seq_len = p->max_seq_len;
-  a.scale_log2 = p->scale * (copied ? p->k_scale : 1.f) * 1.4426950408889634f;
-  a.v_scale = copied ? p->v_scale : 1.f;
+  const bool scaled = c->type != DA_CACHE_BF16;
+  a.scale_log2 = p->scale * (scaled ? p->k_scale : 1.f) * 1.4426950408889634f;
+  a.v_scale = scaled ? p->v_scale : 1.f;
   a.own = ext.own;
-  return launch_tall(qmap, kmap, vmap, a, box, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  return launch_tall(c->type, qmap, maps, a, box, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 int plan_uniform(const decode_attn_params* p, const DecodeExt& ext, int32_t* num_splits,

@@ -45,9 +45,8 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
                const DecodeExt& ext = {});
 
 // Attention of the rows that ext.own says (trees, cross attention): as
-// run_decode for up to DECODE_ATTN_MAX_ROWS rows per KV head; with more, bf16
-// caches go to the kernel for many rows, and others are read back into the
-// workspace first.  c holds k, v and what else its type needs.
+// run_decode for up to DECODE_ATTN_MAX_ROWS rows per KV head, and through the
+// kernel for many rows above.  c holds k, v and what else its type needs.
 int rows_workspace_bytes(const decode_attn_params* p, const decode_attn_cache* c, int32_t num_splits,
                          const DecodeExt& ext, size_t* bytes);
 int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void* q,

@@ -195,16 +195,17 @@ int fp4_ctas_per_sm(int rows, int heads_per_cta);
 int fp4_warps(int rows);  // consumer warps of a CTA: its heads divide them
 
 // Launch the kernel for more than 128 query rows per KV head and the merge of its
-// partials (tall_kernel.cu; bf16 keys and values, boxes of box_tokens tokens; Q's
-// boxes: 64 d of a group's heads, tall_tile_tokens() tokens).  part_o holds
-// kTallSlots x 256 rows, part_lse as many LSEs, join kTallCtas records; chunk_len
-// and num_splits are not used.
+// partials (tall_kernel.cu), over a cache of type `type` (DA_CACHE_*; ks and vs of
+// the maps: 4-bit caches) in boxes of box_tokens tokens; Q's boxes: 64 d of a
+// group's heads, tall_tile_tokens() tokens.  part_o holds kTallSlots x 256 rows,
+// part_lse as many LSEs, join kTallCtas records; chunk_len and num_splits are not
+// used.
 constexpr int kTallCtas = 152;         // one for each SM
 constexpr int kTallSlots = 2 * kTallCtas;
 constexpr int kTallSlotRows = 256;
 constexpr int kTallJoinBytes = 32;
-cudaError_t launch_tall(const CUtensorMap& q_map, const CUtensorMap& k_map, const CUtensorMap& v_map,
-                        const SplitArgs& a, int box_tokens, cudaStream_t stream);
+cudaError_t launch_tall(int type, const CUtensorMap& q_map, const Fp4Maps& kv, const SplitArgs& a, int box_tokens,
+                        cudaStream_t stream);
 int tall_tile_tokens(int group);
 
 // Launch the combine kernel (one warp per output row, or with by_row and few rows a CTA).

@@ -1,6 +1,6 @@
 // tall_kernel.cu -- attention of more than 128 query rows per KV head (prompts
-// over an encoder's states, large trees of drafts) over bf16 keys and values, on
-// the fifth-generation tensor cores.
+// over an encoder's states, large trees of drafts), on the fifth-generation tensor
+// cores.
 //
 // For the rows r = (t, g) of a (request, kv head), t a token and g a head of the
 // group, over the keys j that rows.cuh says they see:
@@ -42,6 +42,9 @@
 // five 32 KB slots (128 keys of K or of V), a warp to each; TMA boxes are of up to
 // 128 tokens (what divides a page).  Boxes that one warp issues are serialised
 // (130 to 240 cycles), and a step of 16-token pages has 32.
+// FP8 and 4-bit caches: warps 2 and 3 bring the cache's bytes to two 16 KB slots,
+// warps 4-7 convert them to f16 in four operand slots (and Q's rows in place), and
+// the products run in f16.
 // Values of keys behind a sequence may be anything: they are zeroed in shared
 // memory (0 x NaN is NaN).  Every wait is bounded.
 
@@ -63,26 +66,15 @@ constexpr int kTQHalf = kTRows * 128;             // [128 rows][64 d] bf16
 constexpr int kTQTile = 2 * kTQHalf;
 constexpr int kTHalf = kTKeys * 128;              // [64 tokens][64 d] bf16
 constexpr int kTSlot = 2 * kTHalf;                // K or V of a step
-constexpr int kTSlots = 5;
 constexpr int kTMmaWarp = 0;
 constexpr int kTSchedWarp = 1;
 constexpr int kTProdWarp = 2;
+constexpr int kTConvWarp = 4;                     // FP8 and 4-bit caches: the second warpgroup converts
+constexpr int kTConverters = 4;
 constexpr int kTSoftmaxWarp = 8;                  // to 15: the last two warpgroups
-// A producer warp per slot: one that filled slots in turn with others could
-// meet a slot's barrier a whole round early, where its parity says "free".
-constexpr int kTProducers = kTSlots;
-constexpr int kTThreads = 512;                    // (one warp is idle: setmaxnreg takes whole warpgroups)
-static_assert(kTProdWarp + kTProducers <= kTSoftmaxWarp && 32 * (kTSoftmaxWarp + 8) == kTThreads, "warps");
-constexpr int kTReaders = 8 + 1 + kTProducers;    // warps that read an item's descriptor
-constexpr int kTOffRing = 2 * kTQTile;
-constexpr int kTOffBar = kTOffRing + kTSlots * kTSlot;
-constexpr int kTBars = 2 * kTSlots + 2 + 2 + 2 + 4 + 2 + 2 + 2 + 1;
-constexpr int kTOffItems = (kTOffBar + kTBars * 8 + 8 + 15) / 16 * 16;
-constexpr int kTSmem = 1024 + kTOffItems + 2 * 64;
-static_assert(kTSmem <= 227 * 1024, "shared memory");
+constexpr int kTThreads = 512;                    // (setmaxnreg takes whole warpgroups)
 constexpr uint32_t kTTmemCols = 512;
 constexpr uint32_t kTColO = 256;                  // S of tile g at 128 g, O at 256 + 128 g
-constexpr float kTRescale = 64.f;                 // log2 units
 // registers: 65536 / 512 threads is what the launch gives
 constexpr int kTLaunchRegs = 65536 / kTThreads / 8 * 8;
 constexpr int kTSoftmaxRegs = 208;
@@ -90,8 +82,38 @@ constexpr int kTOtherRegs = 48;
 static_assert(256 * kTSoftmaxRegs + (kTThreads - 256) * kTOtherRegs <= kTThreads * kTLaunchRegs,
               "the register split would wait forever");
 
+// KV: the cache's type (DA_CACHE_*).
+template <int KV>
+struct TCfg {
+  static constexpr bool kConv = KV != DA_CACHE_BF16;       // operands are converted to f16
+  static constexpr bool kFp4 = KV == DA_CACHE_FP4_E2M1;
+  static constexpr int kSlots = kConv ? 4 : 5;             // operand slots: K or V of a step, 32 KB
+  static constexpr int kRaw = kConv ? 2 : 0;               // slots of the cache's bytes
+  static constexpr int kRawBytes = 16384;                  // 4-bit: 8 KB of values, 1 KB of scales
+  static constexpr int kRawScales = 8192;
+  // A producer warp per slot that it fills: one that filled slots in turn with
+  // others could meet a slot's barrier a whole round early, where its parity says
+  // "free".
+  static constexpr int kProducers = kConv ? kRaw : kSlots;
+  static_assert(kTProdWarp + kProducers <= (kConv ? kTConvWarp : kTSoftmaxWarp), "warps");
+  static constexpr int kReaders = 8 + 1 + kProducers + (kConv ? kTConverters : 0);  // of an item's descriptor
+  static constexpr int kOffRing = 2 * kTQTile;
+  static constexpr int kOffRaw = kOffRing + kSlots * kTSlot;
+  static constexpr int kOffBar = kOffRaw + kRaw * kRawBytes;
+  static constexpr int kBars = 2 * kSlots + 2 * kRaw + 2 + 2 + 2 + 2 + 4 + 2 + 2 + 2 + 1;
+  static constexpr int kOffItems = (kOffBar + kBars * 8 + 8 + 15) / 16 * 16;
+  static constexpr int kOffExp = kOffItems + 2 * 64;       // [2 items][256 rows] exponents of Q's scales
+  static constexpr int kSmem = 1024 + kOffExp + (kConv ? 2 * 2 * kTRows * 2 : 0);
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  // P = 2^(x - m + kShift) with m the row's maximum when it was last raised; it is
+  // raised when P would pass 2^(kShift + kRaise).  In bf16 nothing is lost below
+  // 2^64; f16 ends at 2^16 and keeps weights down to 2^-24 of 2^kShift.
+  static constexpr float kRaise = kConv ? 8.f : 64.f;      // log2 units
+  static constexpr float kShift = kConv ? 6.f : 0.f;
+};
+
 struct TallMaps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, ks, vs;  // (ks, vs: block scales of 4-bit caches)
 };
 
 // One piece of an item, in shared memory: written by the scheduler warp.
@@ -246,8 +268,10 @@ struct TallJoin {
 };
 static_assert(sizeof(TallJoin) <= kTallJoinBytes, "merge records");
 
+template <int KV>
 __global__ void __launch_bounds__(kTThreads, 1)
     tall_kernel(const __grid_constant__ TallMaps maps, const SplitArgs a, const int box_tokens) {
+  using C = TCfg<KV>;
   constexpr uint32_t kFull = 0xffffffffu;
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -256,10 +280,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + kTOffBar);  // [slots] bytes landed
-  uint64_t* empty_bar = full_bar + kTSlots;                           // [slots] read by the MMAs
-  uint64_t* q_full = empty_bar + kTSlots;                             // [2] Q tile landed
-  uint64_t* q_empty = q_full + 2;                                     // [2] read by the item's last S
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // [slots] operand landed (or converted)
+  uint64_t* empty_bar = full_bar + C::kSlots;                         // [slots] read by the MMAs
+  uint64_t* raw_full = empty_bar + C::kSlots;                         // [raw] bytes landed
+  uint64_t* raw_empty = raw_full + C::kRaw;                           // [raw] converted
+  uint64_t* q_full = raw_empty + C::kRaw;                             // [2] Q tile landed
+  uint64_t* q_conv = q_full + 2;                                      // [2] and converted
+  uint64_t* q_empty = q_conv + 2;                                     // [2] read by the item's last S
   uint64_t* s_full = q_empty + 2;                                     // [2] S in TMEM, the P V before done
   uint64_t* p_full = s_full + 2;                                      // [tile][half] 64 keys of P in TMEM
   uint64_t* o_done = p_full + 4;                                      // [2] the item's last P V
@@ -267,20 +294,26 @@ __global__ void __launch_bounds__(kTThreads, 1)
   uint64_t* item_empty = item_full + 2;                               // [2] descriptor read
   uint64_t* tmem_done = item_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tmem_done + 1);
-  auto item_slot = [&](int k) { return reinterpret_cast<TallItem*>(smem + kTOffItems + (k & 1) * 64); };
+  auto item_slot = [&](int k) { return reinterpret_cast<TallItem*>(smem + C::kOffItems + (k & 1) * 64); };
+  int16_t* q_exp = reinterpret_cast<int16_t*>(smem + C::kOffExp);
 
   if (tid == 0) {
-    for (int s = 0; s < kTSlots; ++s) {
-      mbar_init(&full_bar[s], 1);
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(&full_bar[s], C::kConv ? kTConverters : 1);
       mbar_init(&empty_bar[s], 1);
+    }
+    for (int s = 0; s < C::kRaw; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], kTConverters);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
+      mbar_init(&q_conv[i], kTConverters);
       mbar_init(&q_empty[i], 1);
       mbar_init(&o_done[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&item_full[i], 1);
-      mbar_init(&item_empty[i], kTReaders);
+      mbar_init(&item_empty[i], C::kReaders);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], 4);
     mbar_init(tmem_done, 8);
@@ -401,20 +434,140 @@ __global__ void __launch_bounds__(kTThreads, 1)
       }
       return;
     }
+    if (C::kConv && warp >= kTConvWarp) {
+      // ================================================ conversion to f16
+      // An E4M3 value, and a block scale times an E2M1 value, is an f16 value; a row
+      // of Q is brought to [2^14, 2^15) by a power of two, which the scores are
+      // scaled back by.  The slots' layouts are those of TMA tiles in 128-byte
+      // swizzle, so that a warp's loads and stores meet all banks.
+      const int ct = tid - 32 * kTConvWarp;
+      const int cj = ct & 7;
+      int ubase = 0;
+      int q_use[2] = {0, 0};
+      for (int k = 0; next_item(k); ++k) {
+        const int steps = item_slot(k)->steps, tiles = item_slot(k)->tiles, t_begin = item_slot(k)->t_begin,
+                  t_end = item_slot(k)->t_end;
+        leave_item(k);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (!ok || g >= tiles) break;
+          ok = __all_sync(kFull, mbar_wait_lazy(&q_full[g], q_use[g] & 1)) != 0;
+          if (!ok) break;
+          ++q_use[g];
+          uint8_t* row = smem + g * kTQTile + ct * 128;
+          auto chunk = [&](int c) { return reinterpret_cast<uint4*>(row + (c >> 3) * kTQHalf + (((c & 7) ^ cj) << 4)); };
+          uint32_t top = 0;  // the largest magnitude's bits (bf16 orders like integers)
+#pragma unroll 4
+          for (int c = 0; c < 16; ++c) {
+            const uint4 v = *chunk(c);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+          }
+          // (rows of zeros, or with infinities or NaN, as they are)
+          const int e2 = top > 0 && top < 0x7f80u ? max(static_cast<int>(top >> 7), 1) - 127 - 14 : 0;
+          // times 2^-e2, in two factors since -e2 may exceed an exponent's range
+          const float f1 = __uint_as_float(static_cast<uint32_t>(127 - e2 / 2) << 23);
+          const float f2 = __uint_as_float(static_cast<uint32_t>(127 - (e2 - e2 / 2)) << 23);
+          auto f16 = [&](uint32_t x) {
+            return pack_f16x2(__uint_as_float(x << 16) * f1 * f2, __uint_as_float(x & 0xffff0000u) * f1 * f2);
+          };
+#pragma unroll 4
+          for (int c = 0; c < 16; ++c) {
+            const uint4 v = *chunk(c);
+            *chunk(c) = make_uint4(f16(v.x), f16(v.y), f16(v.z), f16(v.w));
+          }
+          q_exp[(k & 1) * 2 * kTRows + g * kTRows + ct] = static_cast<int16_t>(e2);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_conv[g]);
+        }
+        for (int u = 0; ok && u < 2 * steps; ++u) {
+          const int U = ubase + u, rs = U % 2, os = U % C::kSlots;
+          ok = __all_sync(kFull, mbar_wait_lazy(&raw_full[rs], (U / 2) & 1)) != 0;
+          if (ok && U >= C::kSlots)
+            ok = __all_sync(kFull, mbar_wait_lazy(&empty_bar[os], (U / C::kSlots - 1) & 1)) != 0;
+          if (!ok) break;
+          const uint8_t* src = smem + C::kOffRaw + rs * C::kRawBytes;
+          uint8_t* dst = smem + C::kOffRing + os * kTSlot;
+          // values of keys behind the chunk's end may be anything: zeros
+          const int rows = (u & 1) != 0 ? t_end - (t_begin + (u >> 1) * kTKeys) : kTKeys;
+          if constexpr (C::kFp4) {
+            // 16 bytes of a row are 32 values, two whole blocks: chunks 4 (c & 1) .. + 3
+            // of half c / 2
+            const int c = (ct >> 3) & 3, r0 = (ct >> 5) * 8 + cj;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const int row = r0 + 32 * v;
+              const uint4 w = *reinterpret_cast<const uint4*>(src + row * 64 + ((c ^ ((cj >> 1) & 3)) << 4));
+              const uint32_t s2 = e4m3x2_to_f16x2(
+                  *reinterpret_cast<const uint16_t*>(src + C::kRawScales + row * 8 + 2 * c));
+              const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t x[4];
+                e2m1x8_to_f16(words[e], x);
+                const uint32_t s1 = __byte_perm(s2, 0, e < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) x[q] = row < rows ? mul_f16x2(x[q], s1) : 0u;
+                *reinterpret_cast<uint4*>(dst + (c >> 1) * kTHalf + row * 128 + (((4 * (c & 1) + e) ^ cj) << 4)) =
+                    make_uint4(x[0], x[1], x[2], x[3]);
+              }
+            }
+          } else {
+            // 16 bytes of a row are 16 values: chunks 2 c and 2 c + 1, of half c / 4
+            const int c = (ct >> 3) & 7, r0 = (ct >> 6) * 8 + cj, c2 = (2 * c) & 7;
+#pragma unroll 4
+            for (int v = 0; v < 8; ++v) {
+              const int row = r0 + 16 * v;
+              const uint4 w = *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ cj) << 4));
+              uint4 lo, hi;
+              e4m3x4_to_f16x4(w.x, lo.x, lo.y);
+              e4m3x4_to_f16x4(w.y, lo.z, lo.w);
+              e4m3x4_to_f16x4(w.z, hi.x, hi.y);
+              e4m3x4_to_f16x4(w.w, hi.z, hi.w);
+              if (row >= rows) lo = hi = make_uint4(0u, 0u, 0u, 0u);
+              uint8_t* to = dst + (c >> 2) * kTHalf + row * 128;
+              *reinterpret_cast<uint4*>(to + ((c2 ^ cj) << 4)) = lo;
+              *reinterpret_cast<uint4*>(to + (((c2 + 1) ^ cj) << 4)) = hi;
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&full_bar[os]);
+            mbar_arrive(&raw_empty[rs]);
+          }
+        }
+        if (!ok) break;
+        ubase += 2 * steps;
+      }
+      if (!ok) report();
+      return;
+    }
     if (warp >= kTProdWarp) {
       // ====================================================== K and V copies
-      // unit u (over all items): K (even) or V (odd) of a step, in slot u %
-      // kTSlots, which is filled by the warp of that number.  A lane issues one box.
+      // unit u (over all items): K (even) or V (odd) of a step, in the slot that this
+      // warp fills.  A lane issues one box: bf16, half the d of box_tokens tokens;
+      // FP8, all of them; 4-bit, values (even lanes) or block scales.
       const int pw = warp - kTProdWarp;
-      if (pw >= kTProducers) return;
+      if (pw >= C::kProducers) return;
       if (lane == 0 && pw == 0 && a.max_seq_len > 0) {
         prefetch_tensor_map(&maps.k);
         prefetch_tensor_map(&maps.v);
+        if constexpr (C::kFp4) {
+          prefetch_tensor_map(&maps.ks);
+          prefetch_tensor_map(&maps.vs);
+        }
       }
-      const int boxes = kTKeys / box_tokens;         // of a d half
-      const int half = lane & 1;
-      const int box_tok = (lane >> 1) * box_tokens;  // of the lane's box in the step
-      const uint32_t box_bytes = static_cast<uint32_t>(box_tokens) * 128u;
+      uint64_t* const full = C::kConv ? raw_full : full_bar;
+      uint64_t* const empty = C::kConv ? raw_empty : empty_bar;
+      constexpr int kPer = KV == DA_CACHE_FP8_E4M3 ? 1 : 2;  // boxes of the same tokens
+      const int boxes = kTKeys / box_tokens;
+      const int half = lane & (kPer - 1);
+      const int box_tok = lane / kPer * box_tokens;  // of the lane's box in the step
+      // bytes of box_tokens tokens
+      const uint32_t tok_bytes = static_cast<uint32_t>(box_tokens) * (C::kFp4 ? 72u : C::kConv ? 128u : 256u);
       int ubase = 0, last = -1;
       for (int k = 0; next_item(k); ++k) {
         const TallItem it = *item_slot(k);
@@ -422,32 +575,44 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const int32_t* bt_row = a.paged ? a.block_table + static_cast<int64_t>(it.b) * a.bt_stride : nullptr;
         auto page_of = [&](int u) {
           const int tok = it.t_begin + (u >> 1) * kTKeys + box_tok;  // (max_seq_len is at most 2^30)
-          return bt_row != nullptr && lane < 2 * boxes && tok < it.t_end ? __ldg(bt_row + tok / a.page_size) : 0;
+          return bt_row != nullptr && lane < kPer * boxes && tok < it.t_end ? __ldg(bt_row + tok / a.page_size) : 0;
         };
         const int units = 2 * it.steps;
-        int u = (pw - ubase) % kTProducers;  // the warp's first unit of the item
-        if (u < 0) u += kTProducers;
+        int u = (pw - ubase) % C::kProducers;  // the warp's first unit of the item
+        if (u < 0) u += C::kProducers;
         int pg_next = page_of(u);
-        for (; u < units; u += kTProducers) {
-          const int s = pw, use = (ubase + u) / kTSlots;
+        for (; u < units; u += C::kProducers) {
+          const int use = (ubase + u) / C::kProducers;
           int pg = pg_next;
-          pg_next = page_of(u + kTProducers);
-          if (use > 0) ok = __all_sync(kFull, mbar_wait_lazy(&empty_bar[s], (use - 1) & 1)) != 0;
+          pg_next = page_of(u + C::kProducers);
+          if (use > 0) ok = __all_sync(kFull, mbar_wait_lazy(&empty[pw], (use - 1) & 1)) != 0;
           if (!ok) break;
           const int tok0 = it.t_begin + (u >> 1) * kTKeys;
           const int live = min(boxes, (it.t_end - tok0 + box_tokens - 1) / box_tokens);
-          if (lane == 0) mbar_arrive_expect_tx(&full_bar[s], 2u * live * box_bytes);
+          if (lane == 0) mbar_arrive_expect_tx(&full[pw], live * tok_bytes);
           __syncwarp();
-          if (lane < 2 * live) {
+          if (lane < kPer * live) {
             if (a.paged && static_cast<unsigned>(pg) >= static_cast<unsigned>(a.num_pages)) {
               if (a.status != nullptr) atomicOr(a.status, static_cast<int32_t>(DA_STATUS_BAD_PAGE));
               pg = 0;
             }
             const int tok = tok0 + box_tok;
+            const int slot = a.paged ? tok % a.page_size : tok, group = a.paged ? pg : it.b;
             // (other CTAs read the same keys: no eviction hint)
-            tma_load_4d_plain(smem + kTOffRing + s * kTSlot + half * kTHalf + box_tok * 128,
-                              (u & 1) ? &maps.v : &maps.k, &full_bar[s], half * 64, it.kvh,
-                              a.paged ? tok % a.page_size : tok, a.paged ? pg : it.b);
+            if constexpr (C::kFp4) {
+              uint8_t* dst = smem + C::kOffRaw + pw * C::kRawBytes;
+              if (half == 0)
+                tma_load_4d_plain(dst + box_tok * 64, (u & 1) ? &maps.v : &maps.k, &full[pw], 0, it.kvh, slot, group);
+              else
+                tma_load_4d_plain(dst + C::kRawScales + box_tok * 8, (u & 1) ? &maps.vs : &maps.ks, &full[pw], slot,
+                                  it.kvh, 0, group);
+            } else if constexpr (C::kConv) {
+              tma_load_4d_plain(smem + C::kOffRaw + pw * C::kRawBytes + box_tok * 128, (u & 1) ? &maps.v : &maps.k,
+                                &full[pw], 0, it.kvh, slot, group);
+            } else {
+              tma_load_4d_plain(smem + C::kOffRing + pw * kTSlot + half * kTHalf + box_tok * 128,
+                                (u & 1) ? &maps.v : &maps.k, &full[pw], half * 64, it.kvh, slot, group);
+            }
           }
           __syncwarp();
           last = ubase + u;
@@ -458,28 +623,28 @@ __global__ void __launch_bounds__(kTThreads, 1)
       if (!ok) {
         report();
         // no copy of this warp may still be landing when the CTA exits (without
-        // a failure every one has been waited for by the MMA warp)
-        if (lane == 0 && last >= 0) mbar_wait(&full_bar[pw], (last / kTSlots) & 1);
+        // a failure every one has been waited for by its readers)
+        if (lane == 0 && last >= 0) mbar_wait(&full[pw], (last / C::kProducers) & 1);
       }
       return;
     }
 
     // ============================================================== MMA issuer
     const uint32_t tmem = *tmem_slot;
-    constexpr uint32_t kIdescS = umma_idesc_bf16(kTRows, kTKeys, false, false);
-    constexpr uint32_t kIdescO = umma_idesc_bf16(kTRows, kHeadDim, false, true);
+    constexpr uint32_t kIdescS = umma_idesc_bf16(kTRows, kTKeys, false, false, C::kConv);
+    constexpr uint32_t kIdescO = umma_idesc_bf16(kTRows, kHeadDim, false, true, C::kConv);
     const uint64_t q_desc = umma_smem_desc(smem_base, 16, 1024);
-    const uint64_t k_desc = umma_smem_desc(smem_base + kTOffRing, 16, 1024);
+    const uint64_t k_desc = umma_smem_desc(smem_base + C::kOffRing, 16, 1024);
     // V [64 keys][2 x 64 d], MN-major: d halves kTHalf apart, 8-key groups 1 KB
-    const uint64_t v_desc = umma_smem_desc(smem_base + kTOffRing, kTHalf, 1024);
+    const uint64_t v_desc = umma_smem_desc(smem_base + C::kOffRing, kTHalf, 1024);
     // the slot and the phase parity of the next K and of the next V (units 2 i and
     // 2 i + 1 of all steps, in slots in turn)
     int k_slot = 0, v_slot = 1;
     uint32_t k_par = 0, v_par = 0;
     auto advance = [](int& slot, uint32_t& par) {
       slot += 2;
-      if (slot >= kTSlots) {
-        slot -= kTSlots;
+      if (slot >= C::kSlots) {
+        slot -= C::kSlots;
         par ^= 1u;
       }
     };
@@ -503,7 +668,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         if (!ok || g >= tiles) break;
-        ok = mbar_wait_warp(smem_addr(&q_full[g]), q_par[g]);
+        ok = mbar_wait_warp(smem_addr(C::kConv ? &q_conv[g] : &q_full[g]), q_par[g]);
         if (!ok) break;
         q_par[g] ^= 1u;
         tc_fence_after_sync();
@@ -559,9 +724,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   const uint32_t lane_base = *tmem_slot + (static_cast<uint32_t>((warp & 3) * 32) << 16);
   const uint32_t s_col = lane_base + g * kTKeys;
   const uint32_t o_col = lane_base + kTColO + g * kHeadDim;
-  const float sc = a.scale_log2;
-  const bool raw = sc > 0.f;  // (the scores stay unscaled; the exponent's multiply-add scales)
-  const float s_fma = raw ? sc : 1.f;
+  const bool raw = a.scale_log2 > 0.f;  // (the scores stay unscaled; the exponent's multiply-add scales)
   int ubase = 0, seq = 0, o_use = 0;
   for (int k = 0; next_item(k); ++k) {
     const TallItem& it = *item_slot(k);  // (stays in shared memory)
@@ -571,6 +734,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     float m_used = -INFINITY;  // reference maximum of P (log2 domain), raised seldom
     float l = 0.f;             // sum of the weights
     const bool active = g < it.tiles;
+    float sc = a.scale_log2, s_fma = raw ? sc : 1.f;
     if (active) {
       // keys below are all seen (what padding rows see does not matter: the same
       // limit for the whole CTA)
@@ -580,6 +744,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
         ok = __all_sync(kFull, mbar_wait_lazy(&s_full[g], (seq + i) & 1)) != 0;
         if (!ok) break;
         tc_fence_after_sync();
+        if (C::kConv && i == 0) {  // (a row of Q is held at 2^-e of itself)
+          sc = ldexpf(a.scale_log2, q_exp[(k & 1) * 2 * kTRows + g * kTRows + r]);
+          s_fma = raw ? sc : 1.f;
+        }
         float x[kTKeys];
         {
           float y[4][32];
@@ -614,7 +782,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) mx[c] = fmax3(mx[c], x[e + 2 * c], x[e + 2 * c + 1]);
         const float mt = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * s_fma;
-        const bool raise = mt > m_used + kTRescale;  // (from -inf by anything that is seen)
+        const bool raise = mt > m_used + C::kRaise;  // (from -inf by anything that is seen)
         if (__any_sync(kFull, raise)) {
           const float alpha = raise ? ex2(m_used - mt) : 1.f;
           if (raise) m_used = mt;
@@ -635,7 +803,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const float mref = m_used == -INFINITY ? 0.f : m_used;  // (nothing seen yet: P = 0)
         float2 ps = make_float2(0.f, 0.f);
         const float2 s2 = make_float2(s_fma, s_fma);
-        const float2 nm2 = make_float2(-mref, -mref);
+        const float2 nm2 = make_float2(C::kShift - mref, C::kShift - mref);
         const int n_valid = t_end - tok0;
         auto p_ready = [&](int h) {
           tmem_wait_st();
@@ -645,11 +813,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
         };
         // values of keys behind the chunk's end are zeroed before the first P V
         // (that of tile 0) may read them
-        if (g == 0 && n_valid < kTKeys) {
+        if (!C::kConv && g == 0 && n_valid < kTKeys) {
           const int u = ubase + 2 * i + 1;
-          ok = __all_sync(kFull, mbar_wait_lazy(&full_bar[u % kTSlots], (u / kTSlots) & 1)) != 0;
+          ok = __all_sync(kFull, mbar_wait_lazy(&full_bar[u % C::kSlots], (u / C::kSlots) & 1)) != 0;
           if (!ok) break;
-          uint8_t* vs = smem + kTOffRing + (u % kTSlots) * kTSlot;
+          uint8_t* vs = smem + C::kOffRing + (u % C::kSlots) * kTSlot;
           for (int z = r; z < (kTKeys - n_valid) * 16; z += 128)
             *reinterpret_cast<uint4*>(vs + ((z >> 3) & 1) * kTHalf + (n_valid + (z >> 4)) * 128 + (z & 7) * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
@@ -664,7 +832,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             const float p0 = ex2(y.x);
             const float p1 = ex2(y.y);
             ps = __fadd2_rn(ps, make_float2(p0, p1));
-            w[e] = pack_bf16x2(p0, p1);
+            w[e] = C::kConv ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
           }
           if (c == 2) {
             // the first half has been stored meanwhile; the last quarter stays
@@ -706,7 +874,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                                            static_cast<int64_t>(h) * a.o_sh)
                                     : 4 * kHeadDim * pidx;
     if (writes) {
-      const float lse = !have ? -INFINITY : (m_used == -INFINITY ? 0.f : m_used) * kLn2t + logf(l);
+      const float lse = !have ? -INFINITY : (m_used == -INFINITY ? 0.f : m_used - C::kShift) * kLn2t + logf(l);
       if (direct) a.lse[prow] = lse;
       else a.part_lse[pidx] = lse;
     }
@@ -871,42 +1039,52 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tall_join_kernel(const SplitA
 }
 
 std::mutex g_tall_mu;
-bool g_tall_attr[64];
+bool g_tall_attr[3][64];
 
-}  // namespace
-
-int tall_tile_tokens(int group) { return kTRows / group; }
-
-cudaError_t launch_tall(const CUtensorMap& q_map, const CUtensorMap& k_map, const CUtensorMap& v_map,
-                        const SplitArgs& a, int box_tokens, cudaStream_t stream) {
+template <int KV>
+cudaError_t launch_tall_t(const TallMaps& maps, const SplitArgs& a, int box_tokens, cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   {
     std::lock_guard<std::mutex> lk(g_tall_mu);
-    if (!g_tall_attr[dev]) {
-      e = cudaFuncSetAttribute(tall_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTSmem);
+    if (!g_tall_attr[KV][dev]) {
+      e = cudaFuncSetAttribute(tall_kernel<KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, TCfg<KV>::kSmem);
       if (e != cudaSuccess) return e;
-      g_tall_attr[dev] = true;
+      g_tall_attr[KV][dev] = true;
     }
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kTallCtas);
   cfg.blockDim = dim3(kTThreads);
-  cfg.dynamicSmemBytes = kTSmem;
+  cfg.dynamicSmemBytes = TCfg<KV>::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, tall_kernel, TallMaps{q_map, k_map, v_map}, a, box_tokens);
+  e = cudaLaunchKernelEx(&cfg, tall_kernel<KV>, maps, a, box_tokens);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(kTallCtas, kJoinBlocks);
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, tall_join_kernel, a);
+}
+
+}  // namespace
+
+int tall_tile_tokens(int group) { return kTRows / group; }
+
+cudaError_t launch_tall(int type, const CUtensorMap& q_map, const Fp4Maps& kv, const SplitArgs& a, int box_tokens,
+                        cudaStream_t stream) {
+  const TallMaps maps{q_map, kv.k, kv.v, kv.ks, kv.vs};
+  switch (type) {
+    case DA_CACHE_BF16: return launch_tall_t<DA_CACHE_BF16>(maps, a, box_tokens, stream);
+    case DA_CACHE_FP8_E4M3: return launch_tall_t<DA_CACHE_FP8_E4M3>(maps, a, box_tokens, stream);
+    default: return launch_tall_t<DA_CACHE_FP4_E2M1>(maps, a, box_tokens, stream);
+  }
 }
 
 }  // namespace dattn
