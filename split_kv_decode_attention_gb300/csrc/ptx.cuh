@@ -118,6 +118,22 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar_addr, uint32_t parit
   return __all_sync(0xffffffffu, mbar_wait_lazy(bar, parity)) != 0;
 }
 
+// The same for two phases together.
+__device__ __forceinline__ bool mbar_wait2_warp(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "and.pred p, p, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar0), "r"(parity0), "r"(bar1), "r"(parity1)
+      : "memory");
+  if (__all_sync(0xffffffffu, done != 0)) return true;
+  return mbar_wait_warp(bar0, parity0) && mbar_wait_warp(bar1, parity1);
+}
+
 // The same for three phases together, the last the one that is really waited for.
 __device__ __forceinline__ bool mbar_wait3_warp(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1,
                                                 uint32_t bar2, uint32_t parity2) {

@@ -49,6 +49,7 @@
 // memory (0 x NaN is NaN).  Every wait is bounded.
 
 #include <mutex>
+#include <type_traits>
 
 #include "decode_attn.h"
 #include "kernels.cuh"
@@ -442,7 +443,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
       // swizzle, so that a warp's loads and stores meet all banks.
       const int ct = tid - 32 * kTConvWarp;
       const int cj = ct & 7;
-      int ubase = 0;
+      int step = 0;  // over all items
+      static_assert(!C::kConv || (C::kRaw == 2 && C::kSlots % 2 == 0), "K and V have slots of their own");
       int q_use[2] = {0, 0};
       for (int k = 0; next_item(k); ++k) {
         const int steps = item_slot(k)->steps, tiles = item_slot(k)->tiles, t_begin = item_slot(k)->t_begin,
@@ -482,16 +484,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&q_conv[g]);
         }
-        for (int u = 0; ok && u < 2 * steps; ++u) {
-          const int U = ubase + u, rs = U % 2, os = U % C::kSlots;
-          ok = __all_sync(kFull, mbar_wait_lazy(&raw_full[rs], (U / 2) & 1)) != 0;
-          if (ok && U >= C::kSlots)
-            ok = __all_sync(kFull, mbar_wait_lazy(&empty_bar[os], (U / C::kSlots - 1) & 1)) != 0;
-          if (!ok) break;
-          const uint8_t* src = smem + C::kOffRaw + rs * C::kRawBytes;
-          uint8_t* dst = smem + C::kOffRing + os * kTSlot;
-          // values of keys behind the chunk's end may be anything: zeros
-          const int rows = (u & 1) != 0 ? t_end - (t_begin + (u >> 1) * kTKeys) : kTKeys;
+        // a unit whose rows from `rows` on become zeros
+        auto convert = [&](const uint8_t* src, uint8_t* dst, auto tail, int rows) {
+          constexpr bool kTail = decltype(tail)::value;
           if constexpr (C::kFp4) {
             // 16 bytes of a row are 32 values, two whole blocks: chunks 4 (c & 1) .. + 3
             // of half c / 2
@@ -509,7 +504,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 e2m1x8_to_f16(words[e], x);
                 const uint32_t s1 = __byte_perm(s2, 0, e < 2 ? 0x1010 : 0x3232);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) x[q] = row < rows ? mul_f16x2(x[q], s1) : 0u;
+                for (int q = 0; q < 4; ++q) x[q] = !kTail || row < rows ? mul_f16x2(x[q], s1) : 0u;
                 *reinterpret_cast<uint4*>(dst + (c >> 1) * kTHalf + row * 128 + (((4 * (c & 1) + e) ^ cj) << 4)) =
                     make_uint4(x[0], x[1], x[2], x[3]);
               }
@@ -517,30 +512,51 @@ __global__ void __launch_bounds__(kTThreads, 1)
           } else {
             // 16 bytes of a row are 16 values: chunks 2 c and 2 c + 1, of half c / 4
             const int c = (ct >> 3) & 7, r0 = (ct >> 6) * 8 + cj, c2 = (2 * c) & 7;
-#pragma unroll 4
-            for (int v = 0; v < 8; ++v) {
-              const int row = r0 + 16 * v;
-              const uint4 w = *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ cj) << 4));
-              uint4 lo, hi;
-              e4m3x4_to_f16x4(w.x, lo.x, lo.y);
-              e4m3x4_to_f16x4(w.y, lo.z, lo.w);
-              e4m3x4_to_f16x4(w.z, hi.x, hi.y);
-              e4m3x4_to_f16x4(w.w, hi.z, hi.w);
-              if (row >= rows) lo = hi = make_uint4(0u, 0u, 0u, 0u);
-              uint8_t* to = dst + (c >> 2) * kTHalf + row * 128;
-              *reinterpret_cast<uint4*>(to + ((c2 ^ cj) << 4)) = lo;
-              *reinterpret_cast<uint4*>(to + (((c2 + 1) ^ cj) << 4)) = hi;
+            const uint8_t* from = src + r0 * 128 + ((c ^ cj) << 4);
+            uint8_t* to = dst + (c >> 2) * kTHalf + r0 * 128;
+            const int lo_at = (c2 ^ cj) << 4, hi_at = ((c2 + 1) ^ cj) << 4;
+#pragma unroll
+            for (int v0 = 0; v0 < 8; v0 += 4) {
+              uint4 w[4];
+#pragma unroll
+              for (int v = 0; v < 4; ++v) w[v] = *reinterpret_cast<const uint4*>(from + (v0 + v) * 2048);
+#pragma unroll
+              for (int v = 0; v < 4; ++v) {
+                uint4 lo, hi;
+                e4m3x4_to_f16x4(w[v].x, lo.x, lo.y);
+                e4m3x4_to_f16x4(w[v].y, lo.z, lo.w);
+                e4m3x4_to_f16x4(w[v].z, hi.x, hi.y);
+                e4m3x4_to_f16x4(w[v].w, hi.z, hi.w);
+                if (kTail && r0 + 16 * (v0 + v) >= rows) lo = hi = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(to + (v0 + v) * 2048 + lo_at) = lo;
+                *reinterpret_cast<uint4*>(to + (v0 + v) * 2048 + hi_at) = hi;
+              }
             }
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&full_bar[os]);
-            mbar_arrive(&raw_empty[rs]);
+        };
+        for (int i = 0; ok && i < steps; ++i, ++step) {
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {  // K, then V
+            const int os = (2 * step + v) % C::kSlots;
+            // (the phase before a slot's first use counts as complete)
+            ok = mbar_wait2_warp(smem_addr(&raw_full[v]), step & 1, smem_addr(&empty_bar[os]),
+                                 ((2 * step + v) / C::kSlots + 1) & 1);
+            if (!ok) break;
+            const uint8_t* src = smem + C::kOffRaw + v * C::kRawBytes;
+            uint8_t* dst = smem + C::kOffRing + os * kTSlot;
+            // values of keys behind the chunk's end may be anything
+            const int rows = t_end - (t_begin + i * kTKeys);
+            if (v == 1 && rows < kTKeys) convert(src, dst, std::true_type{}, rows);
+            else convert(src, dst, std::false_type{}, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&full_bar[os]);
+              mbar_arrive(&raw_empty[v]);
+            }
           }
         }
         if (!ok) break;
-        ubase += 2 * steps;
       }
       if (!ok) report();
       return;
