@@ -655,7 +655,9 @@ int decode_attn_tree_mask(int32_t batch, int32_t q_len, int32_t max_seq_len,
  * DECODE_ATTN_MAX_ROWS.  (Hq / Hkv) * q_len may exceed DECODE_ATTN_MAX_ROWS;
  * Hq / Hkv may not, nor q_len DECODE_ATTN_MAX_TREE.  Above that many rows the
  * call cuts its work evenly on the device: num_splits is not used, and the
- * workspace holds 40 MB of partials whatever the sizes.
+ * workspace holds 40 MB of partials whatever the sizes and, for FP8 and 4-bit
+ * caches and more than 512 (256) rows per KV head, K and V in bf16 (B * max_seq_len
+ * * Hkv * 512 bytes) where those are at most 2 GB.
  * Status as decode_attn(); DA_STATUS_SHORT_CAUSAL where L < n_b (the first
  * n_b - L new tokens then have no key).
  */

@@ -11,6 +11,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "cache_kernels.cuh"
 #include "decode_attn.h"
 #include "internal.cuh"
 #include "kernels.cuh"
@@ -743,23 +744,42 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
 
 namespace {
 
-// Workspace of a call of more than DECODE_ATTN_MAX_ROWS rows per KV head: partials
-// and the records of their merge.
+// FP8 and 4-bit caches of calls with this many pairs of row tiles per KV head are
+// read back to bf16 in the workspace first; with fewer pairs the kernel converts
+// them itself, once for each.  GB300, 8 requests of 2048 tokens, 32 / 8 heads, us
+// copied and converted: FP8 with 1, 2, 3, 8 pairs 53 / 42, 68 / 65, 82 / 89, 138 /
+// 177; 4-bit 55 / 46, 70 / 72, 84 / 99, 140 / 211.  A copy of more than kTallCopyMost
+// bytes is not made (it would save at most a third of the time).
+constexpr int64_t kTallCopyPairsFp8 = 3;
+constexpr int64_t kTallCopyPairsFp4 = 2;
+constexpr size_t kTallCopyMost = size_t{2} << 30;
+
+// Workspace of a call of more than DECODE_ATTN_MAX_ROWS rows per KV head: [K and V
+// in bf16, where they are copied], partials, and the records of their merge.
 struct TallLayout {
-  size_t part_o, part_lse, join, total;
+  bool copied;
+  int64_t tokens;              // of a request in the copy
+  size_t k, v, part_o, part_lse, join, total;
 };
 
-int tall_layout(const decode_attn_params* p, TallLayout* l) {
+int tall_layout(const decode_attn_params* p, const decode_attn_cache* c, TallLayout* l) {
   const int64_t rows = static_cast<int64_t>(p->num_q_heads / p->num_kv_heads) * p->q_len;
   if (p->max_seq_len > (1 << 30) || rows > 0x7fffffff) return DA_ERR_BAD_SHAPE;
   // (the kernel adds up the costs of its steps in 32 bits)
   const int64_t group = p->num_q_heads / p->num_kv_heads;
-  const double pairs = static_cast<double>(ceil_div64(p->q_len, 2 * tall_tile_tokens(static_cast<int>(group))));
-  if (3.0 * p->batch * p->num_kv_heads * pairs * static_cast<double>(ceil_div64(p->max_seq_len, 128)) >= 4294967295.0)
+  const int64_t pairs = ceil_div64(p->q_len, 2 * tall_tile_tokens(static_cast<int>(group)));
+  if (3.0 * p->batch * p->num_kv_heads * static_cast<double>(pairs) * static_cast<double>(ceil_div64(p->max_seq_len, 128)) >= 4294967295.0)
     return DA_ERR_BAD_SHAPE;
   const size_t part = static_cast<size_t>(kTallSlots) * kTallSlotRows;
-  l->part_o = 0;
-  l->part_lse = part * kHeadDim * 4;
+  l->tokens = std::max<int64_t>(p->max_seq_len, 1);
+  size_t copy = static_cast<size_t>(p->batch) * l->tokens * p->num_kv_heads * kHeadDim * 2;
+  l->copied = c->type != DA_CACHE_BF16 && 2 * copy <= kTallCopyMost &&
+              pairs >= (c->type == DA_CACHE_FP4_E2M1 ? kTallCopyPairsFp4 : kTallCopyPairsFp8);
+  if (!l->copied) copy = 0;
+  l->k = 0;
+  l->v = round256(copy);
+  l->part_o = round256(l->v + copy);
+  l->part_lse = l->part_o + part * kHeadDim * 4;
   l->join = l->part_lse + part * 4;
   l->total = l->join + static_cast<size_t>(kTallCtas) * kTallJoinBytes;
   return DA_OK;
@@ -778,7 +798,7 @@ int rows_workspace_bytes(const decode_attn_params* p, const decode_attn_cache* c
   if (rc != DA_OK) return rc;
   if (bytes == nullptr) return DA_ERR_NULL_POINTER;
   TallLayout l;
-  const int rc2 = tall_layout(p, &l);
+  const int rc2 = tall_layout(p, c, &l);
   if (rc2 == DA_OK) *bytes = l.total;
   return rc2;
 }
@@ -815,15 +835,47 @@ int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void
   if (rc != DA_OK) return rc;
   if (di.major * 10 + di.minor < 100) return DA_ERR_NO_DEVICE;
   TallLayout l;
-  rc = tall_layout(p, &l);
+  rc = tall_layout(p, c, &l);
   if (rc != DA_OK) return rc;
   if (workspace == nullptr || workspace_bytes < l.total || !aligned16(workspace))
     return DA_ERR_WORKSPACE;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
 
+  // keys and values as the kernel reads them
+  decode_attn_params kp = *p;
+  int type = c->type;
+  const void* k = c->k;
+  const void* v = c->v;
+  if (l.copied) {
+    type = DA_CACHE_BF16;
+    kp.flags &= ~static_cast<int32_t>(DA_FLAG_KV_FP8_E4M3);
+    kp.kv_stride_head = kHeadDim;
+    kp.kv_stride_token = static_cast<int64_t>(p->num_kv_heads) * kHeadDim;
+    kp.kv_stride_page = kp.kv_stride_token * l.tokens;
+    k = w + l.k;
+    v = w + l.v;
+    if (!no_keys) {
+      // (without the cache's scales every value is exact in bf16; they go into
+      // the score scale and the output)
+      ReadArgs r;
+      std::memset(&r, 0, sizeof(r));
+      r.c = cache_view(p, c);
+      r.g = paging_view(p, block_table, seq_lens, status);
+      r.k = reinterpret_cast<uint16_t*>(w + l.k);
+      r.v = reinterpret_cast<uint16_t*>(w + l.v);
+      r.sb = kp.kv_stride_page;
+      r.st = kp.kv_stride_token;
+      r.sh = kp.kv_stride_head;
+      r.max_tokens = p->max_seq_len;
+      r.k_scale = 1.f;
+      r.v_scale = 1.f;
+      if (launch_read(r, st) != cudaSuccess) return DA_ERR_CUDA;
+    }
+  }
+  const bool in_pages = paged && !l.copied;
   int box = 128;
-  while (paged && p->page_size % box != 0) box /= 2;
+  while (in_pages && p->page_size % box != 0) box /= 2;
   CUtensorMap qmap;
   Fp4Maps maps;  // (ks and vs: 4-bit caches)
   std::memset(&maps, 0, sizeof(maps));
@@ -840,7 +892,7 @@ int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
     if (rc != DA_OK) return rc;
   }
-  if (!no_keys && c->type == DA_CACHE_FP4_E2M1) {
+  if (!no_keys && type == DA_CACHE_FP4_E2M1) {
     const cuuint32_t tokens = static_cast<cuuint32_t>(box);
     rc = make_fp4_map(&maps.k, c->k, p, c, paged, 1, tokens, false, false);
     if (rc == DA_OK) rc = make_fp4_map(&maps.v, c->v, p, c, paged, 1, tokens, false, false);
@@ -848,8 +900,8 @@ int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void
     if (rc == DA_OK) rc = make_fp4_map(&maps.vs, c->v_block_scale, p, c, paged, 1, tokens, true, false);
     if (rc != DA_OK) return rc;
   } else if (!no_keys) {
-    rc = make_kv_map(&maps.k, c->k, p, paged, box, false);
-    if (rc == DA_OK) rc = make_kv_map(&maps.v, c->v, p, paged, box, false);
+    rc = make_kv_map(&maps.k, k, &kp, in_pages, box, false);
+    if (rc == DA_OK) rc = make_kv_map(&maps.v, v, &kp, in_pages, box, false);
     if (rc != DA_OK) return rc;
   }
 
@@ -867,7 +919,7 @@ int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void
   a.part_o = reinterpret_cast<float*>(w + l.part_o);
   a.part_lse = reinterpret_cast<float*>(w + l.part_lse);
   a.join = w + l.join;
-  a.block_table = block_table;
+  a.block_table = in_pages ? block_table : nullptr;
   a.bt_stride = p->block_table_stride;
   a.seq_lens = seq_lens;
   a.len_sb = 1;
@@ -878,15 +930,15 @@ int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void
   a.num_kv_heads = p->num_kv_heads;
   a.group = group;
   a.rows = group * p->q_len;
-  a.page_size = paged ? p->page_size : 0;
-  a.num_pages = paged ? p->num_pages : 0;
-  a.paged = paged ? 1 : 0;
+  a.page_size = in_pages ? p->page_size : 0;
+  a.num_pages = in_pages ? p->num_pages : 0;
+  a.paged = in_pages ? 1 : 0;
   a.max_seq_len = p->max_seq_len;
   const bool scaled = c->type != DA_CACHE_BF16;
   a.scale_log2 = p->scale * (scaled ? p->k_scale : 1.f) * 1.4426950408889634f;
   a.v_scale = scaled ? p->v_scale : 1.f;
   a.own = ext.own;
-  return launch_tall(c->type, qmap, maps, a, box, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  return launch_tall(type, qmap, maps, a, box, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 int plan_uniform(const decode_attn_params* p, const DecodeExt& ext, int32_t* num_splits,

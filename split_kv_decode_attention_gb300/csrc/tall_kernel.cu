@@ -980,22 +980,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tall_join_kernel(const SplitA
   const int tile_tokens = kTRows / a.group;
   grid_dependency_wait();
   const TallJoin join = *reinterpret_cast<const TallJoin*>(a.join + blockIdx.x * kTallJoinBytes);
-  // ---- rows in no item: (request, pair) by (request, pair)
-  const int pairs = (a.q_len + 2 * tile_tokens - 1) / (2 * tile_tokens);
-  const int64_t slots = static_cast<int64_t>(a.batch) * pairs;
-  for (int64_t e = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x; e < slots;
-       e += static_cast<int64_t>(gridDim.x) * gridDim.y) {
-    const int b = static_cast<int>(e / pairs), pair = static_cast<int>(e - static_cast<int64_t>(b) * pairs);
+  // ---- the rows in no item, a warp to a token of a request
+  const int64_t tokens = static_cast<int64_t>(a.batch) * a.q_len;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * gridDim.y * kJoinWarps;
+  for (int64_t e = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kJoinWarps + warp; e < tokens; e += warps) {
+    const int b = static_cast<int>(e / a.q_len), t = static_cast<int>(e - static_cast<int64_t>(b) * a.q_len);
     const TallRequest q = tall_request(a, b, tile_tokens, false);
-    if (q.steps > 0 && pair < q.both + q.one) continue;
-    const int t0 = pair * 2 * tile_tokens;
-    const int rows = min(2 * tile_tokens, a.q_len - t0) * a.num_q_heads;
-    for (int r = warp; r < rows; r += kJoinWarps) {
-      const int t = t0 + r / a.num_q_heads, h = r % a.num_q_heads;
-      *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(b) * a.o_sb + static_cast<int64_t>(t) * a.o_st +
-                                static_cast<int64_t>(h) * a.o_sh + lane * 4) = make_uint2(0u, 0u);
-      if (lane == 0) a.lse[(static_cast<int64_t>(b) * a.q_len + t) * a.num_q_heads + h] = -INFINITY;
-    }
+    if (q.steps > 0 && t < static_cast<int64_t>(q.both + q.one) * 2 * tile_tokens) continue;
+    uint16_t* row = a.out + static_cast<int64_t>(b) * a.o_sb + static_cast<int64_t>(t) * a.o_st + lane * 4;
+    for (int h = 0; h < a.num_q_heads; ++h)
+      *reinterpret_cast<uint2*>(row + static_cast<int64_t>(h) * a.o_sh) = make_uint2(0u, 0u);
+    for (int h = lane; h < a.num_q_heads; h += 32) a.lse[e * a.num_q_heads + h] = -INFINITY;
   }
   // ---- the item that this CTA ended and did not begin
   const int n = join.n;

@@ -69,16 +69,22 @@ def test_cross_attention_of_very_many_rows(lib):  # noqa: F811
 
 
 def test_workspace_of_many_rows(lib):  # noqa: F811
-    """Needs no device and no chunk count: partials (two pieces of 256 rows for each of 152 CTAs) and their merge's records."""
+    """Needs no device and no chunk count: partials (two pieces of 256 rows for each of 152 CTAs) and their merge's records;
+    for a 4-bit cache and 400 rows (two pairs of tiles) also K and V of every request in bf16, unless those are more than 2 GB."""
     n = ctypes.c_size_t()
-    for fp4 in (False, True):
-        p = params(fp4=fp4, q_len=50, max_pages_per_seq=40, block_table_stride=40, max_seq_len=640)
+    part = 2 * 152 * 256 * 129 * 4 + 152 * 32
+    for fp4, copy in ((False, 0), (True, 2 * 2 * 640 * 2 * 128 * 2)):
+        p = params(fp4=fp4, q_len=100, max_pages_per_seq=40, block_table_stride=40, max_seq_len=640)
         c = cache() if fp4 else cache(da.DA_CACHE_BF16)
         for f in (lib.decode_attn_tree_workspace_bytes, lib.decode_attn_cross_workspace_bytes):
             for splits in (0, 1, 99):
-                assert f(ref(p), ref(c), splits, ctypes.byref(n)) == 0 and n.value == 2 * 152 * 256 * 129 * 4 + 152 * 32
+                assert f(ref(p), ref(c), splits, ctypes.byref(n)) == 0 and n.value == copy + part
             assert f(ref(p), ref(c), 1, None) == -1
             assert f(ref(p), None, 1, ctypes.byref(n)) == -1
+    long = params(q_len=100, max_pages_per_seq=1 << 18, block_table_stride=1 << 18, max_seq_len=1 << 21)
+    assert lib.decode_attn_cross_workspace_bytes(ref(long), ref(cache()), 0, ctypes.byref(n)) == 0 and n.value == part
+    few = params(q_len=50, max_pages_per_seq=40, block_table_stride=40, max_seq_len=640)
+    assert lib.decode_attn_cross_workspace_bytes(ref(few), ref(cache()), 0, ctypes.byref(n)) == 0 and n.value == part
     far = params(q_len=1 << 28, max_seq_len=1 << 30, max_pages_per_seq=1 << 26, block_table_stride=1 << 26, num_kv_heads=1 << 13,
                  num_q_heads=1 << 13, batch=60000)
     assert lib.decode_attn_cross_workspace_bytes(ref(far), ref(cache(da.DA_CACHE_BF16)), 0, ctypes.byref(n)) == -2
