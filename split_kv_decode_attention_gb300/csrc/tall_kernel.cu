@@ -103,7 +103,8 @@ struct TCfg {
   static constexpr int kOffBar = kOffRaw + kRaw * kRawBytes;
   static constexpr int kBars = 2 * kSlots + 2 * kRaw + 2 + 2 + 2 + 2 + 4 + 2 + 2 + 2 + 1;
   static constexpr int kOffItems = (kOffBar + kBars * 8 + 8 + 15) / 16 * 16;
-  static constexpr int kOffExp = kOffItems + 2 * 64;       // [2 items][256 rows] exponents of Q's scales
+  static constexpr int kOffEnd = kOffItems + 2 * 64;
+  static constexpr int kOffExp = kOffEnd + 64;             // [2 items][256 rows] exponents of Q's scales
   static constexpr int kSmem = 1024 + kOffExp + (kConv ? 2 * 2 * kTRows * 2 : 0);
   static_assert(kSmem <= 227 * 1024, "shared memory");
   // P = 2^(x - m + kShift) with m the row's maximum when it was last raised; it is
@@ -132,6 +133,10 @@ static_assert(sizeof(TallItem) <= 64, "item slots");
 
 constexpr int kTCostBoth = 3, kTCostOne = 2;     // of a step of two row tiles, and of one
 constexpr uint32_t kTCostLeast = 12;             // of a CTA's share: four steps, about a prologue
+// A cut within this many steps of an item's end is moved there: a piece costs about
+// five steps of its own (Q, the first copies, its output).
+constexpr int kTSnap = 3;
+static_assert(kTCostLeast / kTCostBoth > kTSnap, "no share inside an item is empty");
 
 // The list's entries of a request.  (The host keeps the cost of the list below
 // 2^32.)
@@ -166,7 +171,7 @@ __device__ __forceinline__ TallRequest tall_request(const SplitArgs& a, int b, i
   return q;
 }
 
-// A place in the list: step `step` of an item.
+// A place in the list: step `step` of an item (q.steps: its end).
 struct TallPlace {
   int b, kvh, pair, step;
   TallRequest q;         // of request b
@@ -175,6 +180,8 @@ struct TallPlace {
     return b == o.b && kvh == o.kvh && pair == o.pair;
   }
 };
+
+static_assert(sizeof(TallPlace) <= 64, "its place in shared memory");
 
 // The cost of the list, cut into shares as even as can be: share c begins at
 // begin(c).
@@ -258,12 +265,13 @@ __device__ __forceinline__ TallPlace tall_place(const SplitArgs& a, int tile_tok
   p.kvh = static_cast<int>(kvh);
   p.item_cost = before + kvh * item;
   p.step = static_cast<int>((x - p.item_cost) / p.q.per_step(p.pair));
+  if (p.step < kTSnap) p.step = 0;
+  else if (p.q.steps - p.step < kTSnap) p.step = p.q.steps;
   return p;
 }
 
-// What the merge has to do for a CTA (in the workspace): the item that its share
-// begins in the middle of and ends, in n pieces, the first in share `first` (n 0:
-// there is none).
+// For the merge (in the workspace): the item that a CTA's share begins in the middle
+// of, in n pieces, the first in share `first` (n 0: there is none).
 struct TallJoin {
   int n, first, b, kvh, pair;
 };
@@ -295,8 +303,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
   uint64_t* item_empty = item_full + 2;                               // [2] descriptor read
   uint64_t* tmem_done = item_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tmem_done + 1);
-  auto item_slot = [&](int k) { return reinterpret_cast<TallItem*>(smem + C::kOffItems + (k & 1) * 64); };
   int16_t* q_exp = reinterpret_cast<int16_t*>(smem + C::kOffExp);
+  auto item_slot = [&](int k) { return reinterpret_cast<TallItem*>(smem + C::kOffItems + (k & 1) * 64); };
 
   if (tid == 0) {
     for (int s = 0; s < C::kSlots; ++s) {
@@ -358,15 +366,33 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const bool to_end = static_cast<uint32_t>(cta) + 1 == share.n;  // the share runs to the list's end
       if (some) {
         at = tall_place(a, tile_tokens, pairs, share.begin(cta), mine);
-        if (!to_end) end = tall_place(a, tile_tokens, pairs, share.begin(cta + 1), mine);
       }
+      asm volatile("bar.sync 1, 64;" ::: "memory");
+      if (some && !to_end) end = *reinterpret_cast<const TallPlace*>(smem + C::kOffEnd);
       if (lane == 0) {
         prefetch_tensor_map(&maps.q);
         int q_use[2] = {0, 0};
         const uint32_t q_bytes = static_cast<uint32_t>(tile_tokens * a.group) * 256u;
         bool more = some;
         const TallPlace first_place = at;
-        const bool begins_inside = at.step > 0;
+        const bool begins_inside = at.step > 0 && at.step < at.q.steps;
+        // the next item of the list
+        auto next = [&]() {
+          at.step = 0;
+          if (++at.kvh < a.num_kv_heads) return;
+          at.kvh = 0;
+          do {
+            if (++at.b >= a.batch) {
+              at.b = 0;
+              more = ++at.pair < pairs;
+            }
+            if (more) at.q = tall_request(a, at.b, tile_tokens, false);
+          } while (more && at.q.cost(at.pair) == 0);
+        };
+        if (more && at.step == at.q.steps) {
+          more = to_end || !at.same_item(end);
+          if (more) next();
+        }
         for (int k = 0; ok; ++k) {
           TallItem it = {};
           if (more) {
@@ -386,18 +412,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
               it.slot = at.step > 0 ? 2 * cta : stop < at.q.steps ? 2 * cta + 1 : -1;
             }
             more = !last;
-            // the next item of the list
-            at.step = 0;
-            if (more && ++at.kvh >= a.num_kv_heads) {
-              at.kvh = 0;
-              do {
-                if (++at.b >= a.batch) {
-                  at.b = 0;
-                  more = ++at.pair < pairs;
-                }
-                if (more) at.q = tall_request(a, at.b, tile_tokens, false);
-              } while (more && at.q.cost(at.pair) == 0);
-            }
+            if (more) next();
           }
           if (k > 1) ok = mbar_wait(&item_empty[k & 1], ((k >> 1) - 1) & 1);
           if (!ok) break;
@@ -417,13 +432,16 @@ __global__ void __launch_bounds__(kTThreads, 1)
             ++q_use[g];
           }
         }
-        // for the merge: the share it begins in is the last that starts before the
-        // item's first step ends
+        // the item's pieces: its first share is the last that starts before its step
+        // kTSnap, its last one the last that starts up to kTSnap steps before its end
         TallJoin join = {};
-        if (some && begins_inside && (to_end || !first_place.same_item(end))) {
-          int first = cta;
-          while (first > 0 && share.begin(first) >= first_place.item_cost + first_place.q.per_step(first_place.pair)) --first;
-          join = TallJoin{cta - first + 1, first, first_place.b, first_place.kvh, first_place.pair};
+        if (some && begins_inside) {
+          const uint32_t per_step = first_place.q.per_step(first_place.pair);
+          int first = cta, past = cta + 1;
+          while (first > 0 && share.begin(first) >= first_place.item_cost + kTSnap * per_step) --first;
+          const uint32_t before = first_place.item_cost + (first_place.q.steps - kTSnap + 1) * per_step;
+          while (past < static_cast<int>(share.n) && share.begin(past) < before) ++past;
+          join = TallJoin{past - first, first, first_place.b, first_place.kvh, first_place.pair};
         }
         *reinterpret_cast<TallJoin*>(a.join + cta * kTallJoinBytes) = join;
         if (!ok) {
@@ -437,53 +455,18 @@ __global__ void __launch_bounds__(kTThreads, 1)
     }
     if (C::kConv && warp >= kTConvWarp) {
       // ================================================ conversion to f16
-      // An E4M3 value, and a block scale times an E2M1 value, is an f16 value; a row
-      // of Q is brought to [2^14, 2^15) by a power of two, which the scores are
-      // scaled back by.  The slots' layouts are those of TMA tiles in 128-byte
-      // swizzle, so that a warp's loads and stores meet all banks.
+      // An E4M3 value, and a block scale times an E2M1 value, is an f16 value.  The
+      // slots' layouts are those of TMA tiles in 128-byte swizzle, so that a warp's
+      // loads and stores meet all banks.
       const int ct = tid - 32 * kTConvWarp;
       const int cj = ct & 7;
-      int step = 0;  // over all items
-      static_assert(!C::kConv || (C::kRaw == 2 && C::kSlots % 2 == 0), "K and V have slots of their own");
+      int done = 0;            // units, over all items
       int q_use[2] = {0, 0};
+      static_assert(!C::kConv || (C::kRaw == 2 && C::kSlots % 2 == 0), "K and V have slots of their own");
       for (int k = 0; next_item(k); ++k) {
-        const int steps = item_slot(k)->steps, tiles = item_slot(k)->tiles, t_begin = item_slot(k)->t_begin,
-                  t_end = item_slot(k)->t_end;
+        const int units = 2 * item_slot(k)->steps, t_begin = item_slot(k)->t_begin, t_end = item_slot(k)->t_end;
+        const int tiles = item_slot(k)->tiles;
         leave_item(k);
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          if (!ok || g >= tiles) break;
-          ok = __all_sync(kFull, mbar_wait_lazy(&q_full[g], q_use[g] & 1)) != 0;
-          if (!ok) break;
-          ++q_use[g];
-          uint8_t* row = smem + g * kTQTile + ct * 128;
-          auto chunk = [&](int c) { return reinterpret_cast<uint4*>(row + (c >> 3) * kTQHalf + (((c & 7) ^ cj) << 4)); };
-          uint32_t top = 0;  // the largest magnitude's bits (bf16 orders like integers)
-#pragma unroll 4
-          for (int c = 0; c < 16; ++c) {
-            const uint4 v = *chunk(c);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-          }
-          // (rows of zeros, or with infinities or NaN, as they are)
-          const int e2 = top > 0 && top < 0x7f80u ? max(static_cast<int>(top >> 7), 1) - 127 - 14 : 0;
-          // times 2^-e2, in two factors since -e2 may exceed an exponent's range
-          const float f1 = __uint_as_float(static_cast<uint32_t>(127 - e2 / 2) << 23);
-          const float f2 = __uint_as_float(static_cast<uint32_t>(127 - (e2 - e2 / 2)) << 23);
-          auto f16 = [&](uint32_t x) {
-            return pack_f16x2(__uint_as_float(x << 16) * f1 * f2, __uint_as_float(x & 0xffff0000u) * f1 * f2);
-          };
-#pragma unroll 4
-          for (int c = 0; c < 16; ++c) {
-            const uint4 v = *chunk(c);
-            *chunk(c) = make_uint4(f16(v.x), f16(v.y), f16(v.z), f16(v.w));
-          }
-          q_exp[(k & 1) * 2 * kTRows + g * kTRows + ct] = static_cast<int16_t>(e2);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&q_conv[g]);
-        }
         // a unit whose rows from `rows` on become zeros
         auto convert = [&](const uint8_t* src, uint8_t* dst, auto tail, int rows) {
           constexpr bool kTail = decltype(tail)::value;
@@ -534,27 +517,69 @@ __global__ void __launch_bounds__(kTThreads, 1)
             }
           }
         };
-        for (int i = 0; ok && i < steps; ++i, ++step) {
-#pragma unroll
-          for (int v = 0; v < 2; ++v) {  // K, then V
-            const int os = (2 * step + v) % C::kSlots;
-            // (the phase before a slot's first use counts as complete)
-            ok = mbar_wait2_warp(smem_addr(&raw_full[v]), step & 1, smem_addr(&empty_bar[os]),
-                                 ((2 * step + v) / C::kSlots + 1) & 1);
-            if (!ok) break;
-            const uint8_t* src = smem + C::kOffRaw + v * C::kRawBytes;
-            uint8_t* dst = smem + C::kOffRing + os * kTSlot;
-            // values of keys behind the chunk's end may be anything
-            const int rows = t_end - (t_begin + i * kTKeys);
-            if (v == 1 && rows < kTKeys) convert(src, dst, std::true_type{}, rows);
-            else convert(src, dst, std::false_type{}, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&full_bar[os]);
-              mbar_arrive(&raw_empty[v]);
+        // Q, whose tiles land before the first K; those of a later item only after
+        // the last S of the one before, when its first K and V have long landed
+        const int q_at = k == 0 ? 0 : 2;
+        for (int e = 0; ok && e <= units; ++e) {
+          if (e == q_at) {
+            // Rows of Q become f16, each brought to [2^14, 2^15) by a power of two
+            // (at most 2^127), which the scores are scaled back by.
+#pragma unroll 1
+            for (int g = 0; ok && g < tiles; ++g) {
+              ok = __all_sync(kFull, mbar_wait_lazy(&q_full[g], q_use[g] & 1)) != 0;
+              if (!ok) break;
+              ++q_use[g];
+              uint8_t* const row = smem + g * kTQTile + ct * 128;
+              auto chunk = [&](int c) {
+                return reinterpret_cast<uint4*>(row + (c >> 3) * kTQHalf + (((c & 7) ^ cj) << 4));
+              };
+              uint32_t top = 0;  // the largest magnitudes' bits (bf16 orders like integers)
+#pragma unroll 4
+              for (int c = 0; c < 16; ++c) {
+                const uint4 v = *chunk(c);
+                top = __vmaxu2(__vmaxu2(top, v.x & 0x7fff7fffu), __vmaxu2(v.y & 0x7fff7fffu, v.z & 0x7fff7fffu));
+                top = __vmaxu2(top, v.w & 0x7fff7fffu);
+              }
+              top = max(top & 0xffffu, top >> 16);
+              // (rows of zeros, or with infinities or NaN, as they are)
+              const int e2 = top > 0 && top < 0x7f80u ? max(static_cast<int>(top >> 7) - 127 - 14, -127) : 0;
+              const uint32_t f = static_cast<uint32_t>(127 - e2) << 7;  // 2^-e2 in bf16
+              auto f16 = [&](uint32_t x) {
+                const uint32_t y = mul_bf16x2(x, f | f << 16);
+                return pack_f16x2(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u));
+              };
+#pragma unroll 4
+              for (int c = 0; c < 16; ++c) {
+                uint4* const at = chunk(c);
+                const uint4 v = *at;
+                *at = make_uint4(f16(v.x), f16(v.y), f16(v.z), f16(v.w));
+              }
+              q_exp[(k & 1) * 2 * kTRows + g * kTRows + ct] = static_cast<int16_t>(e2);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&q_conv[g]);
             }
+            continue;
           }
+          const int u = e - (e > q_at ? 1 : 0), v = u & 1;  // K, then V
+          const int os = done % C::kSlots;
+          // (the phase before a slot's first use counts as complete)
+          ok = mbar_wait2_warp(smem_addr(&raw_full[v]), (done >> 1) & 1, smem_addr(&empty_bar[os]),
+                               (done / C::kSlots + 1) & 1);
+          if (!ok) break;
+          const uint8_t* src = smem + C::kOffRaw + v * C::kRawBytes;
+          uint8_t* dst = smem + C::kOffRing + os * kTSlot;
+          // values of keys behind the chunk's end may be anything
+          const int rows = t_end - (t_begin + (u >> 1) * kTKeys);
+          if (v == 1 && rows < kTKeys) convert(src, dst, std::true_type{}, rows);
+          else convert(src, dst, std::false_type{}, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&full_bar[os]);
+            mbar_arrive(&raw_empty[v]);
+          }
+          ++done;
         }
         if (!ok) break;
       }
@@ -646,6 +671,18 @@ __global__ void __launch_bounds__(kTThreads, 1)
     }
 
     // ============================================================== MMA issuer
+    {
+      // (meanwhile: where the share ends)
+      TallRequest mine;
+      const int pairs = (a.q_len + 2 * tile_tokens - 1) / (2 * tile_tokens);
+      const TallShares share = tall_shares(a, tile_tokens, pairs, false, mine);
+      if (share.total > 0 && blockIdx.x + 1 < share.n) {
+        const TallPlace end = tall_place(a, tile_tokens, pairs, share.begin(blockIdx.x + 1), mine);
+        if (lane == 0) *reinterpret_cast<TallPlace*>(smem + C::kOffEnd) = end;
+      }
+      __syncwarp();
+      asm volatile("bar.arrive 1, 64;" ::: "memory");
+    }
     const uint32_t tmem = *tmem_slot;
     constexpr uint32_t kIdescS = umma_idesc_bf16(kTRows, kTKeys, false, false, C::kConv);
     constexpr uint32_t kIdescO = umma_idesc_bf16(kTRows, kHeadDim, false, true, C::kConv);
@@ -741,6 +778,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
   const uint32_t s_col = lane_base + g * kTKeys;
   const uint32_t o_col = lane_base + kTColO + g * kHeadDim;
   const bool raw = a.scale_log2 > 0.f;  // (the scores stay unscaled; the exponent's multiply-add scales)
+  // Code that not every step meets is rolled up: its instructions come from L2 at
+  // about a byte a cycle when they are first met.
   int ubase = 0, seq = 0, o_use = 0;
   for (int k = 0; next_item(k); ++k) {
     const TallItem& it = *item_slot(k);  // (stays in shared memory)
@@ -756,13 +795,41 @@ __global__ void __launch_bounds__(kTThreads, 1)
       // limit for the whole CTA)
       const int t_begin = it.t_begin, t_end = it.t_end;
       const int lim = min(t_end, it.base);
-      for (int i = 0; i < n; ++i) {
+      for (int i = 0; ok && i < n; ++i) {
         ok = __all_sync(kFull, mbar_wait_lazy(&s_full[g], (seq + i) & 1)) != 0;
         if (!ok) break;
         tc_fence_after_sync();
         if (C::kConv && i == 0) {  // (a row of Q is held at 2^-e of itself)
           sc = ldexpf(a.scale_log2, q_exp[(k & 1) * 2 * kTRows + g * kTRows + r]);
           s_fma = raw ? sc : 1.f;
+        }
+        const int tok0 = t_begin + i * kTKeys;
+        const bool edge = tok0 + kTKeys > lim;
+        if (edge) {
+          // some key is hidden from a row, behind the chunk's end or by the mask: its
+          // S becomes -inf
+#pragma unroll 1
+          for (int c = 0; c < kTKeys / 32; ++c) {
+            float y[32];
+            tmem_ld32(s_col + 32 * c, y);
+            const int at = tok0 + 32 * c, left = t_end - at;
+            uint32_t seen = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1u : 0u;
+            if (mine && seen != 0 && at + 32 > it.base) {
+              const OwnRows own{it.own, it.base, a.own.mask + it.b * a.own.mask_sb, a.own.words};
+              seen &= own.bits(t, at);
+            }
+            const float f = raw ? 1.f : sc;
+            tmem_wait_ld();
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              uint32_t z[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                z[e] = __float_as_uint((seen >> (16 * w + e)) & 1u ? y[16 * w + e] * f : -INFINITY);
+              tmem_st16(s_col + 32 * c + 16 * w, z);
+            }
+          }
+          tmem_wait_st();
         }
         float x[kTKeys];
         {
@@ -773,22 +840,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll
           for (int e = 0; e < kTKeys; ++e) x[e] = y[e / 32][e % 32];
         }
-        const int tok0 = t_begin + i * kTKeys;
-        if (tok0 + kTKeys > lim) {
-          // some key is hidden from a row: behind the chunk's end, or by the mask
-#pragma unroll
-          for (int w = 0; w < kTKeys / 32; ++w) {
-            const int left = t_end - (tok0 + 32 * w);
-            uint32_t seen = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1u : 0u;
-            if (mine && seen != 0 && tok0 + 32 * w + 32 > it.base) {
-              const OwnRows own{it.own, it.base, a.own.mask + it.b * a.own.mask_sb, a.own.words};
-              seen &= own.bits(t, tok0 + 32 * w);
-            }
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              x[32 * w + e] = (seen >> e) & 1u ? x[32 * w + e] * (raw ? 1.f : sc) : -INFINITY;
-          }
-        } else if (!raw) {
+        if (!raw && !edge) {
 #pragma unroll
           for (int e = 0; e < kTKeys; ++e) x[e] *= sc;
         }
@@ -964,23 +1016,24 @@ __global__ void __launch_bounds__(kTThreads, 1)
   if (lane == 0) mbar_arrive(tmem_done);
 }
 
-// Merges the pieces of the items that CTA blockIdx.x of the attention kernel has
-// ended and not begun: piece 0 in slot 2 j + 1 of the CTA j that began it, the
-// others in slots 2 (j + 1), 2 (j + 2), ..; a warp per row, lane i d = 4 i .. + 3.
-//     M = max_s lse_s,  w_s = exp(lse_s - M),  out = sum w_s O_s / sum w_s.
-// It also writes the rows that are in no item: those of requests without keys and
-// of pairs of tiles that are all padding.
+// Merges the pieces of items: piece 0 in slot 2 j + 1 of the CTA j that began it, the
+// others in slots 2 (j + 1), 2 (j + 2), ..; half a warp per row, 8 d a lane.
+//     M = max_s lse_s,  w_s = exp(lse_s - M),  out = sum w_s O_s / sum w_s,
+// kJoinAhead pieces at a time.  The blocks blockIdx.x of all CTAs with a later piece
+// share the item's rows.  It also writes the rows that are in no item: those of
+// requests without keys and of pairs of tiles that are all padding.
+// What bounds it is the latency of the chain (record, pieces, output) and, with a
+// warp per row, was the number of instructions.
 constexpr int kJoinWarps = 8;
-constexpr int kJoinBlocks = 16;                   // of an item's 256 rows
+constexpr int kJoinBlocks = 4;                    // of a piece: all blocks are on the SMs together
+constexpr int kJoinAhead = 4;
 
-__global__ void __launch_bounds__(32 * kJoinWarps) tall_join_kernel(const SplitArgs a) {
-  constexpr uint32_t kFull = 0xffffffffu;
+__global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocks) tall_join_kernel(const SplitArgs a) {
   constexpr float kLog2e = 1.4426950408889634f;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tile_tokens = kTRows / a.group;
-  grid_dependency_wait();
-  const TallJoin join = *reinterpret_cast<const TallJoin*>(a.join + blockIdx.x * kTallJoinBytes);
-  // ---- the rows in no item, a warp to a token of a request
+  // ---- the rows in no item, a warp to a token of a request (before the wait: the
+  // attention kernel does not touch them)
   const int64_t tokens = static_cast<int64_t>(a.batch) * a.q_len;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * gridDim.y * kJoinWarps;
   for (int64_t e = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kJoinWarps + warp; e < tokens; e += warps) {
@@ -992,59 +1045,62 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tall_join_kernel(const SplitA
       *reinterpret_cast<uint2*>(row + static_cast<int64_t>(h) * a.o_sh) = make_uint2(0u, 0u);
     for (int h = lane; h < a.num_q_heads; h += 32) a.lse[e * a.num_q_heads + h] = -INFINITY;
   }
-  // ---- the item that this CTA ended and did not begin
+  // ---- the item's share of this block
+  grid_dependency_wait();
+  const TallJoin join = *reinterpret_cast<const TallJoin*>(a.join + blockIdx.x * kTallJoinBytes);
   const int n = join.n;
   if (n == 0) return;
   auto slot_of = [&](int s) { return s == 0 ? 2 * join.first + 1 : 2 * (join.first + s); };
-  for (int row = static_cast<int>(blockIdx.y) * kJoinWarps + warp; row < 2 * kTRows; row += kJoinBlocks * kJoinWarps) {
+  const int share = (static_cast<int>(blockIdx.x) - join.first - 1) * kJoinBlocks + static_cast<int>(blockIdx.y);
+  const int sub = lane & 15;
+  constexpr int64_t kSlotLse = 2 * kTRows, kSlotO = kSlotLse * kHeadDim;
+  for (int row = (share * kJoinWarps + warp) * 2 + (lane >> 4); row < 2 * kTRows;
+       row += (n - 1) * kJoinBlocks * kJoinWarps * 2) {
     const int g = row / kTRows, r = row - g * kTRows, rt = r / a.group;
     const int t = join.pair * 2 * tile_tokens + g * tile_tokens + rt;
     if (rt >= tile_tokens || t >= a.q_len) continue;
     const int h = join.kvh * a.group + (r - rt * a.group);
-    // the first 32 pieces' LSEs, one per lane, and four partial rows together
-    constexpr int kAhead = 4;
-    const float* lses = a.part_lse + row;
-    const float* parts = a.part_o + static_cast<int64_t>(row) * kHeadDim + lane * 4;
-    auto lse_of = [&](int s) { return s < n ? lses[static_cast<int64_t>(slot_of(s)) * (2 * kTRows)] : -INFINITY; };
-    float4 x[kAhead];
-    auto fetch = [&](int s0) {
+    // piece s >= 1 is 2 s slots further than this
+    const float* const lses = a.part_lse + row + 2 * join.first * kSlotLse;
+    const float* const parts = a.part_o + row * kHeadDim + sub * 8 + 2 * join.first * kSlotO;
+    float M = -INFINITY, W = 0.f;
+    float acc[8] = {};
+    for (int s0 = 0; s0 < n; s0 += kJoinAhead) {
+      float l[kJoinAhead];
+      float4 x[kJoinAhead][2];
 #pragma unroll
-      for (int e = 0; e < kAhead; ++e)
-        if (s0 + e < n)
-          x[e] = *reinterpret_cast<const float4*>(parts + static_cast<int64_t>(slot_of(s0 + e)) * (2 * kTRows * kHeadDim));
-    };
-    const float lse0 = lse_of(lane);
-    fetch(0);
-    float M = lse0;
-    for (int s = 32 + lane; s < n; s += 32) M = fmax_nan(M, lse_of(s));
+      for (int e = 0; e < kJoinAhead; ++e) {
+        const int at = s0 + e == 0 ? 1 : 2 * (s0 + e);
+        const bool have = s0 + e < n;
+        l[e] = have ? lses[at * kSlotLse] : -INFINITY;
+        const float4* from = reinterpret_cast<const float4*>(parts + at * kSlotO);
+        x[e][0] = have ? from[0] : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[e][1] = have ? from[1] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float m = M;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmax_nan(M, __shfl_xor_sync(kFull, M, o));
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float W = 0.f;
-    if (M != -INFINITY) {
-      for (int s0 = 0; s0 < n; s0 += 32) {
-        const float w_mine = ex2(((s0 == 0 ? lse0 : lse_of(s0 + lane)) - M) * kLog2e);
-        const int here = min(32, n - s0);
-        for (int s1 = 0; s1 < here; s1 += kAhead) {
-          if (s0 + s1 > 0) fetch(s0 + s1);
+      for (int e = 0; e < kJoinAhead; ++e) m = fmax_nan(m, l[e]);
+      const float ref = m == -INFINITY ? 0.f : m;
+      const float alpha = ex2((M - ref) * kLog2e);
+      M = m;
+      W *= alpha;
 #pragma unroll
-          for (int e = 0; e < kAhead; ++e) {
-            if (s1 + e >= here) break;
-            const float w = __shfl_sync(kFull, w_mine, s1 + e);
-            W += w;
-            acc.x += w * x[e].x;
-            acc.y += w * x[e].y;
-            acc.z += w * x[e].z;
-            acc.w += w * x[e].w;
-          }
-        }
+      for (int d = 0; d < 8; ++d) acc[d] *= alpha;
+#pragma unroll
+      for (int e = 0; e < kJoinAhead; ++e) {
+        const float w = ex2((l[e] - ref) * kLog2e);
+        const float y[8] = {x[e][0].x, x[e][0].y, x[e][0].z, x[e][0].w, x[e][1].x, x[e][1].y, x[e][1].z, x[e][1].w};
+        W += w;
+#pragma unroll
+        for (int d = 0; d < 8; ++d) acc[d] += w * y[d];
       }
     }
     const float inv = W == 0.f ? 0.f : 1.f / W;
-    *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(join.b) * a.o_sb + static_cast<int64_t>(t) * a.o_st +
-                              static_cast<int64_t>(h) * a.o_sh + lane * 4) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (lane == 0)
+    *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(join.b) * a.o_sb + static_cast<int64_t>(t) * a.o_st +
+                              static_cast<int64_t>(h) * a.o_sh + sub * 8) =
+        make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                   pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+    if (sub == 0)
       a.lse[(static_cast<int64_t>(join.b) * a.q_len + t) * a.num_q_heads + h] = W == 0.f ? -INFINITY : M + logf(W);
   }
 }
