@@ -676,8 +676,8 @@ int decode_attn_tree(const decode_attn_params *p, const decode_attn_cache *c, co
  * behind them are padding: their q is not used, out = 0 and lse = -inf.
  * p->causal is not used.  Rows, workspace and status as decode_attn_tree(), but
  * q_len has no limit of its own (above DECODE_ATTN_MAX_ROWS rows 3 * B * Hkv *
- * ceil((Hq / Hkv) * q_len / 256) * ceil(max_seq_len / 128) stays below 2^32, else
- * DA_ERR_BAD_SHAPE).
+ * ceil(q_len / (2 * floor(128 * Hkv / Hq))) * ceil(max_seq_len / 128) stays below
+ * 2^32, else DA_ERR_BAD_SHAPE).
  */
 int decode_attn_cross_workspace_bytes(const decode_attn_params *p, const decode_attn_cache *c,
                                       int32_t num_splits, size_t *bytes);
@@ -695,7 +695,9 @@ int decode_attn_cross(const decode_attn_params *p, const decode_attn_cache *c, c
  * and out_lens[b] = L - n_b + counts[b].  The bytes are moved as they are (a
  * key keeps the rotation it was appended with).
  *   keep      int32 [B, max_keep], 0 <= max_keep <= p->q_len
- *   out_lens  int32 [B], or NULL; not seq_lens itself
+ *   out_lens  int32 [B], or NULL; shares no memory with the inputs
+ * V may be K itself (c->v == c->k, with the same block scales); otherwise they
+ * share no memory.
  * p->q_len <= DECODE_ATTN_MAX_TREE; of *p the shapes, paging and cache strides
  * are used.  Pages that hold new tokens belong to one request of the call.
  * Status: DA_STATUS_TREE where an entry does not rise or is no new token (it and

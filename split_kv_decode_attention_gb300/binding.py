@@ -651,7 +651,7 @@ def cache_keep(k_cache, v_cache, block_table, seq_lens, keep, counts, *, new_tok
     """Keep the accepted tokens of a tree: of each request's last new_lens[b] (or
     new_tokens) tokens those at keep[b, :counts[b]] (int32, rising) move together,
     in K and V, and the rest are dropped; returns out_lens, the new lengths (which
-    may not be seq_lens itself).  Digests of the pages are the caller's to renew."""
+    share no memory with the inputs).  Digests of the pages are the caller's to renew."""
     return _calls().cache_keep(k_cache, v_cache, block_table, seq_lens, keep, counts, new_tokens,
                                max_seq_len, new_lens, k_sf, v_sf, out_lens, status, stream)
 

@@ -17,6 +17,13 @@ using dattn::aligned16;
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Whether two arrays of 4-byte entries share memory.
+bool overlap4(const void* x, int64_t nx, const void* y, int64_t ny) {
+  if (x == nullptr || y == nullptr) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+  return a < b + static_cast<uintptr_t>(ny) * 4 && b < a + static_cast<uintptr_t>(nx) * 4;
+}
+
 bool row_stride_ok(int64_t s) { return s > 0 && s % 8 == 0 && s < (int64_t{1} << 39); }
 
 int check_type(const decode_attn_params* p, const decode_attn_cache* c) {
@@ -160,7 +167,10 @@ int decode_attn_cache_keep(const decode_attn_params* p, const decode_attn_cache*
   if (!aligned4(keep) || !aligned4(counts) || !aligned4(new_lens) || !aligned4(block_table) ||
       !aligned4(seq_lens) || !aligned4(out_lens) || !aligned4(status))
     return DA_ERR_ALIGNMENT;
-  if (out_lens == seq_lens) return DA_ERR_BAD_SHAPE;  // (read while it is written)
+  const int64_t n = cp.batch;  // (the inputs are read while out_lens is written)
+  if (overlap4(out_lens, n, seq_lens, n) || overlap4(out_lens, n, counts, n) || overlap4(out_lens, n, new_lens, n) ||
+      overlap4(out_lens, n, keep, n * max_keep))
+    return DA_ERR_BAD_SHAPE;
   if (cp.max_seq_len > 0) {  // (no token has a place otherwise)
     rc = dattn::check_cache(&cp, c, true, true);
     if (rc != DA_OK) return rc;

@@ -138,8 +138,9 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const KeepArgs a) {
   // bytes of a head's block scales, K's and V's
   const int pieces = c.type == DA_CACHE_BF16 ? 16 : c.type == DA_CACHE_FP8_E4M3 ? 8 : 4;
   const int heads = a.g.num_kv_heads;
-  const int values = 2 * heads * pieces;
-  const int columns = values + (c.type == DA_CACHE_FP4_E2M1 ? 2 * heads : 0);
+  const int sides = c.v == c.k ? 1 : 2;  // (the moves of a place are one thread's)
+  const int values = sides * heads * pieces;
+  const int columns = values + (c.type == DA_CACHE_FP4_E2M1 ? (c.vs == c.ks ? 1 : 2) * heads : 0);
   const int col = blockIdx.x * kKeepThreads + tid;
   if (col >= columns) return;
   if (col < values) {

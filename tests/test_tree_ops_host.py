@@ -9,6 +9,7 @@ from split_kv_decode_attention_gb300 import binding as da
 from tests.test_cache_ops_host import A, NO_DEVICE_OR_OK, cache, lib, params, ref  # noqa: F401
 
 NULL_OK = NO_DEVICE_OR_OK
+B = 2 << 20  # another
 
 
 def test_struct_size():
@@ -96,7 +97,8 @@ def keep_call(lib, p, c, keep=A, most=4, counts=A, own=None, bt=A, lens=A, out=N
 
 @pytest.mark.parametrize("c_kw,p_kw,kw,code", [
     ({}, {}, dict(keep=None), -1), ({}, {}, dict(counts=None), -1), ({}, {}, dict(lens=None), -1), ({}, {}, dict(most=9), -2),
-    ({}, {}, dict(most=-1), -2), ({}, {}, dict(out=A), -2), ({}, {}, dict(keep=A + 2), -6), ({}, {}, dict(counts=A + 2), -6),
+    ({}, {}, dict(most=-1), -2), ({}, {}, dict(out=A), -2), ({}, {}, dict(out=A + 4), -2), ({}, {}, dict(out=B, counts=B - 4), -2),
+    ({}, {}, dict(out=B, own=B + 4), -2), ({}, {}, dict(out=B, keep=B - 28), -2), ({}, {}, dict(keep=A + 2), -6), ({}, {}, dict(counts=A + 2), -6),
     ({}, {}, dict(own=A + 2), -6), ({}, {}, dict(bt=A + 2), -6), ({}, {}, dict(out=A + 6), -6), ({}, {}, dict(status=A + 1), -6),
     (dict(k=0), {}, {}, -1), (dict(v_block_scale=0), {}, {}, -1), (dict(type=3), {}, {}, -12), ({}, dict(q_len=1025), {}, -2),
     ({}, dict(page_size=8), {}, -4), ({}, dict(kv_stride_page=8), {}, -6), ({}, dict(batch=0), dict(keep=None), 0)])
