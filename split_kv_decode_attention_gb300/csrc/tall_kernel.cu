@@ -48,6 +48,7 @@
 // Values of keys behind a sequence may be anything: they are zeroed in shared
 // memory (0 x NaN is NaN).  Every wait is bounded.
 
+#include <cfloat>
 #include <mutex>
 #include <type_traits>
 
@@ -801,7 +802,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         tc_fence_after_sync();
         if (C::kConv && i == 0) {  // (a row of Q is held at 2^-e of itself)
           sc = ldexpf(a.scale_log2, q_exp[(k & 1) * 2 * kTRows + g * kTRows + r]);
-          s_fma = raw ? sc : 1.f;
+          if (raw) s_fma = sc = fminf(fmaxf(sc, FLT_MIN), FLT_MAX);  // (0 x -inf would be NaN)
         }
         const int tok0 = t_begin + i * kTKeys;
         const bool edge = tok0 + kTKeys > lim;

@@ -60,11 +60,13 @@ def tolerance_for(kind, G, T):
     return R.bf16_p_tolerance if kind == "bf16" or pairs >= (2 if kind == "fp4" else 3) else R.out_tolerance
 
 
-def check_rows(c, q, out, lse, own, seen_new, scale=SCALE):
-    """Every request's rows of out / lse against 64 bits; seen_new[b] bool [own, own] or None."""
+def check_rows(c, q, out, lse, own, seen_new, scale=SCALE, lost=0.0):
+    """Every request's rows of out / lse against 64 bits; seen_new[b] bool [own, own] or None.  lost: an absolute error
+    that outputs may have besides."""
     B, T, Hq, _ = q.shape
     G = Hq // c.heads
-    tol = tolerance_for(c.kind, G, T)
+    base = tolerance_for(c.kind, G, T)
+    tol = (lambda o, wabs, mag: base(o, wabs, mag) + lost) if lost else base
     kv, vv = (c.values(w) * s for w, s in (("k", c.ks), ("v", c.vs)))
     out, lse = out.double().cpu(), lse.double().cpu()
     for b, n in enumerate(c.lens):
@@ -606,3 +608,202 @@ def test_speculative_steps_captured_in_a_graph(da, kind, T, G):
                 for j in range(n):
                     at = (int(bt[b, j // page]), j % page) if x.shape[1] == page else (int(bt[b, j // page]), slice(None), j % page)
                     assert torch.equal(x[at], y[at]), (i, b, j)
+
+
+# ------------------------------------------------------------------ many rows, in calls of every shape
+def cross_call(da, c, q, **kw):
+    return da.cross_attn(q, c.dk, c.dv, c.dbt, c.dlens, max_seq_len=c.max_len, **c.scales(), **kw)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("seed", range(6))
+def test_many_rows_of_any_shape(da, kind, seed):
+    """Lengths on both sides of a step's 128 keys and of the cuts, empty requests and padding, odd groups."""
+    r = random.Random(seed)
+    G = [1, 5, 7, 100, 3, 16][seed]
+    heads, B = r.randint(1, 3), [70, 9, 5, 3, 2, 40][seed]
+    T = r.randint(128 // G + 1, 128 // G + [60, 40, 150, 3, 600, 9][seed])
+    most = [200, 700, 1500, 600, 5000, 300][seed]
+    lens = [r.choice([0, 1, 128 * r.randint(1, most // 128 + 1) + r.randint(-1, 1), r.randint(1, most)]) for _ in range(B)]
+    own = [r.choice([0, 1, T, r.randint(0, T)]) for _ in range(B)]
+    lens[-1], own[-1] = most, T
+    c = Paged(kind, lens, heads, r.choice([0, 16, 64, 128]), 400 + seed).gpu()
+    q = bf16(gen(seed), B, T, heads * G, D, std=2.0)
+    status = status_word()
+    out, lse = cross_call(da, c, q.cuda(), q_lens=ints(own), status=status)
+    check_rows(c, q, out, lse, own, None)
+    assert int(status) == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("lens,T,G", [([40000], 130, 1), ([20000, 1, 3], 65, 4)])
+def test_few_rows_over_long_keys_in_many_pieces(da, kind, lens, T, G):
+    c = Paged(kind, lens, 1, 64, 12).gpu()
+    q = bf16(gen(9), len(lens), T, G, D, std=2.0)
+    out, lse = cross_call(da, c, q.cuda())
+    check_rows(c, q, out, lse, [T] * len(lens), None)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
+def test_many_rows_of_more_heads_than_ctas(da, kind):
+    """Several whole items to a CTA."""
+    heads = 330
+    c = Paged(kind, [150, 20], heads, 16, 13).gpu()
+    q = bf16(gen(10), 2, 140, heads, D, std=2.0)
+    out, lse = cross_call(da, c, q.cuda(), q_lens=ints([140, 77]))
+    check_rows(c, q, out, lse, [140, 77], None)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("T", [40, 300])
+def test_many_rows_of_nothing_but_padding(da, kind, T):
+    c = Paged(kind, [100, 30], 2, 16, 14).gpu()
+    q = torch.full((2, T, 8, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    out, lse = cross_call(da, c, q, q_lens=ints([0, 0]))
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("T", [40, 100, 250])
+def test_status_bits_of_many_rows(da, kind, T):
+    """As for few rows, also where the cache is read back first."""
+    c = Paged(kind, [100, 50], 1, 16, 15).gpu()
+    q = bf16(gen(3), 2, T, 4, D).cuda()
+
+    def bits(lens=c.dlens, bt=c.dbt, own=None):
+        status = status_word()
+        da.cross_attn(q, c.dk, c.dv, bt, lens, max_seq_len=c.max_len, q_lens=own, status=status, **c.scales())
+        return int(status)
+
+    bad = c.dbt.clone()
+    bad[0, 1] = 1000
+    assert bits() == 0 and bits(bt=bad) == 1 and bits(lens=ints([101, -1])) == 2 and bits(own=ints([T, T + 1])) == 2
+    assert bits(own=ints([-1, 0])) == 2
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
+def test_many_rows_on_two_streams_and_in_one_workspace(da, kind):
+    """Calls that overlap on two streams, and calls of different shapes that follow one another in one workspace, give
+    the bits of calls alone."""
+    shapes = [([700, 90], 2, 4, 50), ([300, 1200, 5], 1, 5, 90), ([90] * 6, 3, 1, 140), ([2500], 1, 8, 17)]
+    cases = []
+    for i, (lens, heads, G, T) in enumerate(shapes):
+        c = Paged(kind, lens, heads, 16, 20 + i).gpu()
+        q = bf16(gen(i), len(lens), T, heads * G, D, std=2.0).cuda()
+        cases.append((c, q, cross_call(da, c, q)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for rep in range(6):
+        for i, (c, q, _) in enumerate(cases):
+            got.append((i, cross_call(da, c, q, stream=streams[(i + rep) % 2])))
+    torch.cuda.synchronize()
+    ws = torch.full((1 << 24,), float("nan"), device="cuda")
+    for rep in range(3):
+        for i, (c, q, _) in enumerate(cases):
+            got.append((i, cross_call(da, c, q, workspace=ws)))
+    torch.cuda.synchronize()
+    for i, (out, lse) in got:
+        assert torch.equal(out, cases[i][2][0]) and torch.equal(lse, cases[i][2][1]), i
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
+def test_many_rows_replayed_with_other_lengths(da, kind):
+    """The plan is made on the device: a captured call follows the lengths, the pages and the rows."""
+    c = Paged(kind, [900, 333, 64], 2, 16, 21).gpu()
+    T = 60
+    q = bf16(gen(11), 3, T, 8, D, std=2.0)
+    lens, own, dq = c.dlens.clone(), ints([T, T, T]), q.cuda()
+    out = torch.empty(3, T, 8, D, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(3, T, 8, device="cuda")
+
+    def call():
+        da.cross_attn(dq, c.dk, c.dv, c.dbt, lens, max_seq_len=900, q_lens=own, out=out, lse=lse, **c.scales())
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        call()
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for now, rows in (([900, 333, 64], [60, 60, 60]), ([1, 0, 17], [60, 3, 0]), ([0, 0, 0], [60, 60, 60]), ([890, 129, 64], [1, 60, 33])):
+        lens.copy_(ints(now))
+        own.copy_(ints(rows))
+        out.fill_(3)
+        graph.replay()
+        torch.cuda.synchronize()
+        c.lens = now
+        check_rows(c, q, out, lse, rows, None)
+
+
+@pytest.mark.parametrize("T", [4, 50])
+def test_infinite_keys_weigh_nothing_or_everything(da, T):
+    """A key whose score is -inf is as if it were not there; one of +inf makes its rows NaN, and those alone."""
+    c = Paged("bf16", [300], 1, 16, 22).gpu()
+    q = bf16(gen(12), 1, T, 4, D)
+    q[..., 0] = q[..., 0].abs() + 0.5
+    q[0, 1, :, 0] = -1.0
+    at = (int(c.bt[0, 77 // 16]), 77 % 16)
+    c.dk[at[0], at[1], 0, 0] = -math.inf
+    out, lse = cross_call(da, c, q.cuda())
+    assert bool(out[0, 1].isnan().all()) and bool(lse[0, 1].isnan().all())
+    k, v = (R.gather(c.values(w) * 1.0, c.bt, 0, 300)[:, 0] for w in "kv")
+    seen = torch.ones(4 * (T - 1), 300, dtype=torch.bool)
+    seen[:, 77] = False
+    rest = [t for t in range(T) if t != 1]
+    assert_attention(out[0, rest].double().cpu().reshape(-1, D), lse[0, rest].double().cpu().reshape(-1),
+                     q[0, rest].double().reshape(-1, D), k, v, seen, SCALE, tolerance_for("bf16", 4, T))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
+def test_rows_of_any_magnitude(da, kind):
+    """Rows of q as large and as small as bf16 goes: with 16-bit operands each is scaled by itself."""
+    T = 150
+    c = Paged(kind, [200], 1, 16, 23).gpu()
+    q = bf16(gen(13), 1, T, 1, D)
+    for t in range(T):
+        q[0, t] = (q[0, t].float() * 2.0 ** (-120 + 1.6 * t)).to(torch.bfloat16)
+    q[0, 7] = 0
+    scale = 2.0 ** -100
+    out, lse = cross_call(da, c, q.cuda(), scale=scale)
+    # Weights of at most 2^-30 of the largest are subnormal in f16, which holds them to 2^-25 (half its last step) of 2^6:
+    # 200 of them can be off by 2^-31 each.  (With one key of all the weight that is more than the relative tolerance.)
+    lost = 0.0 if kind == "bf16" else 200 * 2.0 ** -31 * float((c.values("v") * c.vs).abs().max())
+    check_rows(c, q, out, lse, [T], None, scale=scale, lost=lost)
+
+
+def test_far_pages_and_tokens(da):
+    """Pages and tokens behind 2^32 bytes of a cache: attention of few and of many rows, kept tokens, reading back."""
+    page, heads, lens = 16, 2, [200, 75]
+    near = Paged("bf16", lens, heads, page, 24).gpu()
+    per_page = page * heads * D * 2
+    first = (1 << 32) // per_page + 5
+    pages = first + near.k.shape[0]
+    k, v = (torch.empty(pages, page, heads, D, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    k[first:], v[first:] = near.dk, near.dv
+    bt = near.dbt + first
+    for T in (3, 60):
+        q = bf16(gen(14), 2, T, 4 * heads, D, std=2.0).cuda()
+        want = cross_call(da, near, q)
+        got = da.cross_attn(q, k, v, bt, near.dlens, max_seq_len=200)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    got = da.cache_read(k, v, bt, near.dlens, max_seq_len=200)
+    want = da.cache_read(near.dk, near.dv, near.dbt, near.dlens, max_seq_len=200)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for kc, vc, b in ((k, v, bt), (near.dk, near.dv, near.dbt)):
+        da.cache_keep(kc, vc, b, near.dlens, ints([[1, 4, 7], [0, 3, 5]]), ints([3, 3]), new_tokens=8, max_seq_len=200)
+    assert torch.equal(k[first:], near.dk) and torch.equal(v[first:], near.dv)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp4"])
+def test_kept_tokens_of_a_cache_whose_values_are_its_keys(da, kind):
+    T = 600
+    c = Paged(kind, [T + 9], 2, 16, 25).gpu()
+    other = [None if x is None else x.clone() for x in (c.dk, c.dk_sf)]
+    keep = ints([list(range(1, T, 2))])
+    counts = ints([T // 2])
+    da.cache_keep(c.dk, c.dk, c.dbt, c.dlens, keep, counts, new_tokens=T, max_seq_len=c.max_len, k_sf=c.dk_sf, v_sf=c.dk_sf)
+    v, v_sf = (None if x is None else x.clone() for x in (c.dv, c.dv_sf))
+    da.cache_keep(other[0], v, c.dbt, c.dlens, keep, counts, new_tokens=T, max_seq_len=c.max_len, k_sf=other[1], v_sf=v_sf)
+    assert torch.equal(c.dk, other[0]) and (c.dk_sf is None or torch.equal(c.dk_sf, other[1]))
