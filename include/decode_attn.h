@@ -675,9 +675,9 @@ int decode_attn_tree(const decode_attn_params *p, const decode_attn_cache *c, co
  * or a whole prompt.  Request b has q_lens[b] tokens (q_len when NULL); rows
  * behind them are padding: their q is not used, out = 0 and lse = -inf.
  * p->causal is not used.  Rows, workspace and status as decode_attn_tree(), but
- * q_len has no limit of its own (above DECODE_ATTN_MAX_ROWS rows 3 * B * Hkv *
- * ceil(q_len / (2 * floor(128 * Hkv / Hq))) * ceil(max_seq_len / 128) stays below
- * 2^32, else DA_ERR_BAD_SHAPE).
+ * q_len has no limit of its own (above DECODE_ATTN_MAX_ROWS rows B * Hkv *
+ * ceil(q_len / (2 * floor(128 * Hkv / Hq))) * (8 * ceil(max_seq_len / 128) + 24)
+ * stays below 2^32, else DA_ERR_BAD_SHAPE).
  */
 int decode_attn_cross_workspace_bytes(const decode_attn_params *p, const decode_attn_cache *c,
                                       int32_t num_splits, size_t *bytes);

@@ -768,8 +768,8 @@ int tall_layout(const decode_attn_params* p, const decode_attn_cache* c, TallLay
   // (the kernel adds up the costs of its steps in 32 bits)
   const int64_t group = p->num_q_heads / p->num_kv_heads;
   const int64_t pairs = ceil_div64(p->q_len, 2 * tall_tile_tokens(static_cast<int>(group)));
-  if (3.0 * p->batch * p->num_kv_heads * static_cast<double>(pairs) * static_cast<double>(ceil_div64(p->max_seq_len, 128)) >= 4294967295.0)
-    return DA_ERR_BAD_SHAPE;
+  const double item = static_cast<double>(kTallCostBoth * ceil_div64(p->max_seq_len, 128) + kTallCostItem);
+  if (item * p->batch * p->num_kv_heads * static_cast<double>(pairs) >= 4294967295.0) return DA_ERR_BAD_SHAPE;
   const size_t part = static_cast<size_t>(kTallSlots) * kTallSlotRows;
   l->tokens = std::max<int64_t>(p->max_seq_len, 1);
   size_t copy = static_cast<size_t>(p->batch) * l->tokens * p->num_kv_heads * kHeadDim * 2;

@@ -204,6 +204,9 @@ constexpr int kTallCtas = 152;         // one for each SM
 constexpr int kTallSlots = 2 * kTallCtas;
 constexpr int kTallSlotRows = 256;
 constexpr int kTallJoinBytes = 32;
+// Cost of a step of an item (two tiles of query rows over 128 keys), and of an item
+// besides: the total of a call is below 2^32.
+constexpr int kTallCostBoth = 8, kTallCostItem = 24;
 cudaError_t launch_tall(int type, const CUtensorMap& q_map, const Fp4Maps& kv, const SplitArgs& a, int box_tokens,
                         cudaStream_t stream);
 int tall_tile_tokens(int group);

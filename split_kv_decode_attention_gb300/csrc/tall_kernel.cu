@@ -30,8 +30,7 @@
 //
 // The work is cut evenly, whatever the lengths: all steps of all items stand in
 // one list, by pair of row tiles, request and kv head, and each of kTallCtas CTAs
-// takes the same share of it, in steps (a step of two row tiles counts 3, of one 2:
-// their measured times).  With the pairs outermost, those of a (request, kv head)
+// takes the same share of it by measured costs (kTCostBoth).  With the pairs outermost, those of a (request, kv head)
 // are worked on at about the same time and meet its keys in L2 (4 x 2048 tokens x
 // 4096 keys, 32 heads with keys of their own: 422 us with the pairs innermost).  So at most two of a CTA's
 // items are not whole; those leave fp32 partials in the CTA's two slots of the
@@ -132,12 +131,15 @@ struct TallItem {
 };
 static_assert(sizeof(TallItem) <= 64, "item slots");
 
-constexpr int kTCostBoth = 3, kTCostOne = 2;     // of a step of two row tiles, and of one
-constexpr uint32_t kTCostLeast = 12;             // of a CTA's share: four steps, about a prologue
-// A cut within this many steps of an item's end is moved there: a piece costs about
-// five steps of its own (Q, the first copies, its output).
+// Costs: of a step of two row tiles (about 2900 cycles) and of one (2650: softmax,
+// P V and S then follow one another), and of an item besides (Q, the first copies, the
+// masked step, its output).
+constexpr int kTCostBoth = kTallCostBoth, kTCostOne = 7, kTCostItem = kTallCostItem;
+static_assert(kTCostOne <= kTCostBoth, "the host bounds the list's cost");
+// A cut within this many steps of an item's end is moved there.
 constexpr int kTSnap = 3;
-static_assert(kTCostLeast / kTCostBoth > kTSnap, "no share inside an item is empty");
+// The least share: three steps.  (One whose ends are moved to the same place is empty.)
+constexpr uint32_t kTCostLeast = 3 * kTCostBoth;
 
 // The list's entries of a request.  (The host keeps the cost of the list below
 // 2^32.)
@@ -149,10 +151,20 @@ struct TallRequest {
   __device__ __forceinline__ uint32_t per_step(int p) const {
     return p < both ? kTCostBoth : p == both && one != 0 ? kTCostOne : 0;
   }
-  __device__ __forceinline__ uint32_t cost(int p) const { return static_cast<uint32_t>(steps) * per_step(p); }
+  __device__ __forceinline__ uint32_t cost(int p) const {
+    const uint32_t c = per_step(p);
+    return steps > 0 && c > 0 ? static_cast<uint32_t>(steps) * c + kTCostItem : 0;
+  }
   __device__ __forceinline__ uint32_t cost_below(int p) const {
-    return static_cast<uint32_t>(steps) *
-           static_cast<uint32_t>(kTCostBoth * min(p, both) + (p > both ? kTCostOne * one : 0));
+    if (steps <= 0) return 0;
+    const uint32_t n = min(p, both), n1 = p > both ? one : 0;
+    return static_cast<uint32_t>(steps) * (kTCostBoth * n + kTCostOne * n1) + kTCostItem * (n + n1);
+  }
+  // the step of an item of pair p at cost x of it; a cut near the item's begin or end
+  // is moved there
+  __device__ __forceinline__ int step_at(int p, uint32_t x) const {
+    const int s = x <= kTCostItem ? 0 : static_cast<int>((x - kTCostItem) / per_step(p));
+    return s < kTSnap ? 0 : steps - s < kTSnap ? steps : s;
   }
 };
 
@@ -265,9 +277,7 @@ __device__ __forceinline__ TallPlace tall_place(const SplitArgs& a, int tile_tok
   const uint32_t kvh = (x - before) / item;
   p.kvh = static_cast<int>(kvh);
   p.item_cost = before + kvh * item;
-  p.step = static_cast<int>((x - p.item_cost) / p.q.per_step(p.pair));
-  if (p.step < kTSnap) p.step = 0;
-  else if (p.q.steps - p.step < kTSnap) p.step = p.q.steps;
+  p.step = p.q.step_at(p.pair, x - p.item_cost);
   return p;
 }
 
@@ -433,15 +443,18 @@ __global__ void __launch_bounds__(kTThreads, 1)
             ++q_use[g];
           }
         }
-        // the item's pieces: its first share is the last that starts before its step
-        // kTSnap, its last one the last that starts up to kTSnap steps before its end
+        // the item's pieces: its first share is the last that starts at or before its
+        // first step, its last one the last that starts inside
         TallJoin join = {};
         if (some && begins_inside) {
-          const uint32_t per_step = first_place.q.per_step(first_place.pair);
+          auto begins_at = [&](int c) {
+            return first_place.q.step_at(first_place.pair, share.begin(c) - first_place.item_cost);
+          };
+          const uint32_t item_end = first_place.item_cost + first_place.q.cost(first_place.pair);
           int first = cta, past = cta + 1;
-          while (first > 0 && share.begin(first) >= first_place.item_cost + kTSnap * per_step) --first;
-          const uint32_t before = first_place.item_cost + (first_place.q.steps - kTSnap + 1) * per_step;
-          while (past < static_cast<int>(share.n) && share.begin(past) < before) ++past;
+          while (first > 0 && share.begin(first) > first_place.item_cost && begins_at(first) > 0) --first;
+          while (past < static_cast<int>(share.n) && share.begin(past) < item_end && begins_at(past) < first_place.q.steps)
+            ++past;
           join = TallJoin{past - first, first, first_place.b, first_place.kvh, first_place.pair};
         }
         *reinterpret_cast<TallJoin*>(a.join + cta * kTallJoinBytes) = join;
