@@ -137,7 +137,7 @@ static_assert(sizeof(TallItem) <= 64, "item slots");
 constexpr int kTCostBoth = kTallCostBoth, kTCostOne = 7, kTCostItem = kTallCostItem;
 static_assert(kTCostOne <= kTCostBoth, "the host bounds the list's cost");
 // A cut within this many steps of an item's end is moved there.
-constexpr int kTSnap = 3;
+constexpr int kTSnap = 2;
 // The least share: three steps.  (One whose ends are moved to the same place is empty.)
 constexpr uint32_t kTCostLeast = 3 * kTCostBoth;
 
