@@ -11,41 +11,52 @@
 // beside it.
 //
 // An item is two tiles of up to 128 rows (whole tokens: 128 / G of them each)
-// over a chunk of the keys, 64 keys a step.  Per step and row tile the tensor
+// over a chunk of the keys, 128 keys a step.  Per step and row tile the tensor
 // core makes S = Q K^T (both from shared memory) and O += P V (P from TMEM); a
-// warpgroup per row tile turns S into P.  TMEM holds both O (256 columns) and
-// for each tile two buffers of S (64 columns each; P, in bf16, replaces the
-// first half of its S), so that the S of the next step is made while a
-// warpgroup works on this one, and the tensor core waits for neither.  (With
-// one buffer of 128 keys per tile every step was a chain of softmax, P V and S:
-// 3590 cycles per 128 keys and 256 rows, of which the tensor core worked 2000.)
-// The MMAs of one thread run in the order of their issue: S of step i + 2 is
-// issued behind the P V of step i, whose P it overwrites.
-// O is rescaled only when a row's maximum has grown by more than 2^8 (P stays
-// below 2^8, and the end's division is exact about it), which is rare after the
-// first steps; the warpgroup then waits until the P V before has been done.  P
-// is rounded to bf16 for the product, 2^-9 of each weight; the sum that O is
-// divided by is that of the unrounded ones (summing the rounded ones too, as the
-// kernels for fewer rows do, took 9 % longer).
+// warpgroup per row tile turns S into P.  TMEM holds S (P, in 16 bits, replaces
+// its first half) and O of both tiles, all 512 columns; while one tile's S is in
+// its warpgroup, the tensor core works for the other.  A tile's chain of softmax
+// (about 1300 cycles), P V (514) and S (524) bounds a step at 2900 cycles, where
+// the tensor core works 2080.  So: P V of the first 64 keys starts before the rest
+// of P is there; the maximum is taken while the first quarter's exponentials run
+// against the old one; an MMA warp elects one thread per product and folds the
+// commits into it.  (64 keys a step with two buffers of S per tile, so that S is
+// made ahead: slower, the smaller products cost as much as the larger.)
+// O is rescaled only when a row's maximum has grown by more than 2^kRaise (the
+// end's division is exact about it), which is rare after the first steps.  P is
+// rounded to 16 bits for the product; the sum that O is divided by is that of the
+// unrounded ones (summing the rounded ones too, as the kernels for fewer rows do,
+// took 9 % longer).
 //
 // The work is cut evenly, whatever the lengths: all steps of all items stand in
 // one list, by pair of row tiles, request and kv head, and each of kTallCtas CTAs
-// takes the same share of it by measured costs (kTCostBoth).  With the pairs outermost, those of a (request, kv head)
-// are worked on at about the same time and meet its keys in L2 (4 x 2048 tokens x
-// 4096 keys, 32 heads with keys of their own: 422 us with the pairs innermost).  So at most two of a CTA's
-// items are not whole; those leave fp32 partials in the CTA's two slots of the
-// workspace, and tall_join_kernel merges them.  Every CTA works its share out from
-// the lengths in device memory (tall_share), and so does the merge.  The copies
-// and the first S of an item overlap the end of the one before.  Roles: warp 0
-// MMA, 1 schedule and Q, 2-6 K and V, 8-15 softmax.  K and V go through a ring of
-// five 32 KB slots (128 keys of K or of V), a warp to each; TMA boxes are of up to
-// 128 tokens (what divides a page).  Boxes that one warp issues are serialised
-// (130 to 240 cycles), and a step of 16-token pages has 32.
+// takes the same share of it by measured costs (kTCostBoth).  With the pairs
+// outermost, those of a (request, kv head) are worked on at about the same time and
+// meet its keys in L2 (4 x 2048 tokens x 4096 keys, 32 heads with keys of their own:
+// 422 us with the pairs innermost, 367 so).  At most two of a CTA's items are not
+// whole; those leave fp32 partials in the CTA's two slots of the workspace, and
+// tall_join_kernel merges them.  Every CTA works its share out from the lengths in
+// device memory, its begin in one warp and its end in another.  (Whole items, taken
+// by CTAs as they finish: 5 % faster where all lengths are equal and there are
+// several items per CTA, up to twice as slow where they are not.)  The copies and
+// the first S of an item overlap the end of the one before.  Roles: warp 0 MMA, 1
+// schedule and Q, 2-6 K and V, 8-15 softmax.  K and V go through a ring of five
+// 32 KB slots (128 keys of K or of V), a warp to each; TMA boxes are of up to 128
+// tokens (what divides a page).  Boxes that one warp issues are serialised (130 to
+// 240 cycles), and a step of 16-token pages has 32.
 // FP8 and 4-bit caches: warps 2 and 3 bring the cache's bytes to two 16 KB slots,
 // warps 4-7 convert them to f16 in four operand slots (and Q's rows in place), and
-// the products run in f16.
+// the products run in f16.  A step then takes about 3200 cycles, of which the
+// converters work all: shared memory bounds it.
 // Values of keys behind a sequence may be anything: they are zeroed in shared
 // memory (0 x NaN is NaN).  Every wait is bounded.
+//
+// GB300, us: 8192 tokens x 8192 keys, 32 / 8 heads: 675 (1630 TFLOP/s, 0.86 of a
+// library product's burst); 4 x 2048 x 4096, 32 / 8 heads: 358 (1535); 16 requests
+// of 4K to 16K keys, 256 rows per head: 132 (4.8 TB/s; HBM bounds its steps, 20 us
+// are the first copies, the last output and the merge); 8 requests of up to 448
+// tokens over up to 1500 FP8 states, 20 heads: 64, most of it the items' begins and
+// ends (7 steps each).
 
 #include <cfloat>
 #include <mutex>
@@ -91,7 +102,7 @@ struct TCfg {
   static constexpr int kSlots = kConv ? 4 : 5;             // operand slots: K or V of a step, 32 KB
   static constexpr int kRaw = kConv ? 2 : 0;               // slots of the cache's bytes
   static constexpr int kRawBytes = 16384;                  // 4-bit: 8 KB of values, 1 KB of scales
-  static constexpr int kRawScales = 8192;
+  [[maybe_unused]] static constexpr int kRawScales = 8192;
   // A producer warp per slot that it fills: one that filled slots in turn with
   // others could meet a slot's barrier a whole round early, where its parity says
   // "free".
@@ -845,6 +856,25 @@ __global__ void __launch_bounds__(kTThreads, 1)
           }
           tmem_wait_st();
         }
+        // P of the first quarter as if no maximum grew, while the others' S comes and
+        // their maximum is taken
+        const float2 s2 = make_float2(s_fma, s_fma);
+        float2 ps;
+        uint32_t w0[16];
+        auto quarter = [&](const float* x, uint32_t* w, float2 nm2) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 y = __ffma2_rn(make_float2(x[2 * e], x[2 * e + 1]), s2, nm2);
+            const float p0 = ex2(y.x);
+            const float p1 = ex2(y.y);
+            ps = __fadd2_rn(ps, make_float2(p0, p1));
+            w[e] = C::kConv ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+          }
+        };
+        auto shift = [&]() {
+          const float mref = m_used == -INFINITY ? 0.f : m_used;  // (nothing seen yet: P = 0)
+          return make_float2(C::kShift - mref, C::kShift - mref);
+        };
         float x[kTKeys];
         {
           float y[4][32];
@@ -852,11 +882,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
           for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, y[c]);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < kTKeys; ++e) x[e] = y[e / 32][e % 32];
+          for (int e = 0; e < 32; ++e) x[e] = !raw && !edge ? y[0][e] * sc : y[0][e];
+          ps = make_float2(0.f, 0.f);
+          quarter(x, w0, shift());
+#pragma unroll
+          for (int e = 32; e < kTKeys; ++e) x[e] = y[e / 32][e % 32];
         }
         if (!raw && !edge) {
 #pragma unroll
-          for (int e = 0; e < kTKeys; ++e) x[e] *= sc;
+          for (int e = 32; e < kTKeys; ++e) x[e] *= sc;
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -881,11 +915,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
               tmem_st16(o_col + c * 16, w);
             }
           }
+          ps = make_float2(0.f, 0.f);
+          quarter(x, w0, shift());
         }
-        const float mref = m_used == -INFINITY ? 0.f : m_used;  // (nothing seen yet: P = 0)
-        float2 ps = make_float2(0.f, 0.f);
-        const float2 s2 = make_float2(s_fma, s_fma);
-        const float2 nm2 = make_float2(C::kShift - mref, C::kShift - mref);
+        const float2 nm2 = shift();
         const int n_valid = t_end - tok0;
         auto p_ready = [&](int h) {
           tmem_wait_st();
@@ -905,17 +938,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 make_uint4(0u, 0u, 0u, 0u);
           fence_proxy_async_smem();
         }
+        tmem_st16(s_col, w0);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 1; c < 4; ++c) {
           uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 y = __ffma2_rn(make_float2(x[32 * c + 2 * e], x[32 * c + 2 * e + 1]), s2, nm2);
-            const float p0 = ex2(y.x);
-            const float p1 = ex2(y.y);
-            ps = __fadd2_rn(ps, make_float2(p0, p1));
-            w[e] = C::kConv ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
-          }
+          quarter(x + 32 * c, w, nm2);
           if (c == 2) {
             // the first half has been stored meanwhile; the last quarter stays
             // behind its release (the compiler would take it first)
@@ -1046,29 +1073,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocks) tall_join_kernel
   constexpr float kLog2e = 1.4426950408889634f;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tile_tokens = kTRows / a.group;
-  // ---- the rows in no item, a warp to a token of a request (before the wait: the
-  // attention kernel does not touch them)
-  const int64_t tokens = static_cast<int64_t>(a.batch) * a.q_len;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * gridDim.y * kJoinWarps;
-  for (int64_t e = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kJoinWarps + warp; e < tokens; e += warps) {
-    const int b = static_cast<int>(e / a.q_len), t = static_cast<int>(e - static_cast<int64_t>(b) * a.q_len);
-    const TallRequest q = tall_request(a, b, tile_tokens, false);
-    if (q.steps > 0 && t < static_cast<int64_t>(q.both + q.one) * 2 * tile_tokens) continue;
-    uint16_t* row = a.out + static_cast<int64_t>(b) * a.o_sb + static_cast<int64_t>(t) * a.o_st + lane * 4;
-    for (int h = 0; h < a.num_q_heads; ++h)
-      *reinterpret_cast<uint2*>(row + static_cast<int64_t>(h) * a.o_sh) = make_uint2(0u, 0u);
-    for (int h = lane; h < a.num_q_heads; h += 32) a.lse[e * a.num_q_heads + h] = -INFINITY;
-  }
   // ---- the item's share of this block
   grid_dependency_wait();
   const TallJoin join = *reinterpret_cast<const TallJoin*>(a.join + blockIdx.x * kTallJoinBytes);
   const int n = join.n;
-  if (n == 0) return;
-  auto slot_of = [&](int s) { return s == 0 ? 2 * join.first + 1 : 2 * (join.first + s); };
   const int share = (static_cast<int>(blockIdx.x) - join.first - 1) * kJoinBlocks + static_cast<int>(blockIdx.y);
   const int sub = lane & 15;
   constexpr int64_t kSlotLse = 2 * kTRows, kSlotO = kSlotLse * kHeadDim;
-  for (int row = (share * kJoinWarps + warp) * 2 + (lane >> 4); row < 2 * kTRows;
+  for (int row = (share * kJoinWarps + warp) * 2 + (lane >> 4); n > 0 && row < 2 * kTRows;
        row += (n - 1) * kJoinBlocks * kJoinWarps * 2) {
     const int g = row / kTRows, r = row - g * kTRows, rt = r / a.group;
     const int t = join.pair * 2 * tile_tokens + g * tile_tokens + rt;
@@ -1116,6 +1128,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocks) tall_join_kernel
                    pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
     if (sub == 0)
       a.lse[(static_cast<int64_t>(join.b) * a.q_len + t) * a.num_q_heads + h] = W == 0.f ? -INFINITY : M + logf(W);
+  }
+  // ---- the rows in no item, a warp to a token of a request
+  const int64_t tokens = static_cast<int64_t>(a.batch) * a.q_len;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * gridDim.y * kJoinWarps;
+  for (int64_t e = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kJoinWarps + warp; e < tokens; e += warps) {
+    const int b = static_cast<int>(e / a.q_len), t = static_cast<int>(e - static_cast<int64_t>(b) * a.q_len);
+    const TallRequest q = tall_request(a, b, tile_tokens, false);
+    if (q.steps > 0 && t < static_cast<int64_t>(q.both + q.one) * 2 * tile_tokens) continue;
+    uint16_t* row = a.out + static_cast<int64_t>(b) * a.o_sb + static_cast<int64_t>(t) * a.o_st + lane * 4;
+    for (int h = 0; h < a.num_q_heads; ++h)
+      *reinterpret_cast<uint2*>(row + static_cast<int64_t>(h) * a.o_sh) = make_uint2(0u, 0u);
+    for (int h = lane; h < a.num_q_heads; h += 32) a.lse[e * a.num_q_heads + h] = -INFINITY;
   }
 }
 
