@@ -84,6 +84,7 @@ constexpr int kTProdWarp = 2;
 constexpr int kTConvWarp = 4;                     // FP8 and 4-bit caches: the second warpgroup converts
 constexpr int kTConverters = 4;
 constexpr int kTSoftmaxWarp = 8;                  // to 15: the last two warpgroups
+constexpr int kTRawScales = 8192;                 // 4-bit caches: the block scales behind 128 keys' values
 constexpr int kTThreads = 512;                    // (setmaxnreg takes whole warpgroups)
 constexpr uint32_t kTTmemCols = 512;
 constexpr uint32_t kTColO = 256;                  // S of tile g at 128 g, O at 256 + 128 g
@@ -102,7 +103,6 @@ struct TCfg {
   static constexpr int kSlots = kConv ? 4 : 5;             // operand slots: K or V of a step, 32 KB
   static constexpr int kRaw = kConv ? 2 : 0;               // slots of the cache's bytes
   static constexpr int kRawBytes = 16384;                  // 4-bit: 8 KB of values, 1 KB of scales
-  [[maybe_unused]] static constexpr int kRawScales = 8192;
   // A producer warp per slot that it fills: one that filled slots in turn with
   // others could meet a slot's barrier a whole round early, where its parity says
   // "free".
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
               const int row = r0 + 32 * v;
               const uint4 w = *reinterpret_cast<const uint4*>(src + row * 64 + ((c ^ ((cj >> 1) & 3)) << 4));
               const uint32_t s2 = e4m3x2_to_f16x2(
-                  *reinterpret_cast<const uint16_t*>(src + C::kRawScales + row * 8 + 2 * c));
+                  *reinterpret_cast<const uint16_t*>(src + kTRawScales + row * 8 + 2 * c));
               const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
               if (half == 0)
                 tma_load_4d_plain(dst + box_tok * 64, (u & 1) ? &maps.v : &maps.k, &full[pw], 0, it.kvh, slot, group);
               else
-                tma_load_4d_plain(dst + C::kRawScales + box_tok * 8, (u & 1) ? &maps.vs : &maps.ks, &full[pw], slot,
+                tma_load_4d_plain(dst + kTRawScales + box_tok * 8, (u & 1) ? &maps.vs : &maps.ks, &full[pw], slot,
                                   it.kvh, 0, group);
             } else if constexpr (C::kConv) {
               tma_load_4d_plain(smem + C::kOffRaw + pw * C::kRawBytes + box_tok * 128, (u & 1) ? &maps.v : &maps.k,
