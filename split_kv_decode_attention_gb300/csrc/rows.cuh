@@ -38,18 +38,16 @@ struct OwnRows {
   }
 };
 
-// The rows of request b of (clamped) length L; `report` (one thread per request)
+// The rows of request b of (clamped) length L and `own` rows as given; `report` (one thread per request)
 // sets the status bits.
-__device__ __forceinline__ OwnRows own_rows(const RowArgs& r, int q_len, int b, int L, bool report, int32_t* status) {
+__device__ __forceinline__ OwnRows own_rows(const RowArgs& r, int q_len, int b, int L, int own, bool report,
+                                            int32_t* status) {
   OwnRows o;
-  o.n = q_len;
+  o.n = own;
   uint32_t bad = 0;
-  if (r.own_lens != nullptr) {
-    o.n = __ldg(r.own_lens + b);
-    if (o.n < 0 || o.n > q_len) {
-      bad |= DA_STATUS_SEQ_LEN;
-      o.n = o.n < 0 ? 0 : q_len;
-    }
+  if (own < 0 || own > q_len) {
+    bad |= DA_STATUS_SEQ_LEN;
+    o.n = own < 0 ? 0 : q_len;
   }
   o.base = INT_MAX;
   o.mask = nullptr;
@@ -61,6 +59,10 @@ __device__ __forceinline__ OwnRows own_rows(const RowArgs& r, int q_len, int b, 
   }
   if (report && bad != 0 && status != nullptr) atomicOr(status, static_cast<int32_t>(bad));
   return o;
+}
+
+__device__ __forceinline__ OwnRows own_rows(const RowArgs& r, int q_len, int b, int L, bool report, int32_t* status) {
+  return own_rows(r, q_len, b, L, r.own_lens != nullptr ? __ldg(r.own_lens + b) : q_len, report, status);
 }
 
 }  // namespace dattn

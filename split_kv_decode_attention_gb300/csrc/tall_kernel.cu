@@ -182,11 +182,12 @@ struct TallRequest {
 __device__ __forceinline__ TallRequest tall_request(const SplitArgs& a, int b, int tile_tokens, bool report) {
   TallRequest q;
   q.L = a.seq_lens[b];
+  const int own = a.own.own_lens != nullptr ? __ldg(a.own.own_lens + b) : a.q_len;
   if (q.L < 0 || q.L > a.max_seq_len) {
     if (report && a.status != nullptr) atomicOr(a.status, static_cast<int32_t>(DA_STATUS_SEQ_LEN));
     q.L = q.L < 0 ? 0 : a.max_seq_len;
   }
-  q.own = own_rows(a.own, a.q_len, b, q.L, report, a.status).n;
+  q.own = own_rows(a.own, a.q_len, b, q.L, own, report, a.status).n;
   q.steps = (q.L + kTKeys - 1) / kTKeys;
   q.both = q.own / (2 * tile_tokens);
   const int left = q.own - q.both * 2 * tile_tokens;
@@ -376,19 +377,26 @@ __global__ void __launch_bounds__(kTThreads, 1)
   };
 
   if (warp < kTSoftmaxWarp) {
+    // The plan: the scheduler warp finds where the CTA's share begins, the MMA warp,
+    // in the same code (whose instructions come once for both), where it ends.
+    static_assert(kTMmaWarp < 2 && kTSchedWarp < 2, "the first two warps");
+    const int cta = static_cast<int>(blockIdx.x);
+    const int pairs = (a.q_len + 2 * tile_tokens - 1) / (2 * tile_tokens);
+    TallShares share = {};
+    TallPlace place = {};
+    if (warp < 2) {
+      TallRequest mine;
+      share = tall_shares(a, tile_tokens, pairs, cta == 0 && warp == kTSchedWarp, mine);
+      const uint32_t c = static_cast<uint32_t>(cta) + (warp == kTMmaWarp ? 1 : 0);
+      if (share.total > 0 && c < share.n) place = tall_place(a, tile_tokens, pairs, share.begin(c), mine);
+      if (warp == kTMmaWarp && lane == 0) *reinterpret_cast<TallPlace*>(smem + C::kOffEnd) = place;
+    }
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTOtherRegs));
     if (warp == kTSchedWarp) {
       // ===================================================== schedule, and Q
-      const int cta = static_cast<int>(blockIdx.x);
-      TallRequest mine;
-      const int pairs = (a.q_len + 2 * tile_tokens - 1) / (2 * tile_tokens);
-      const TallShares share = tall_shares(a, tile_tokens, pairs, cta == 0, mine);
-      TallPlace at = {}, end = {};
+      TallPlace at = place, end = {};
       const bool some = share.total > 0 && static_cast<uint32_t>(cta) < share.n;
       const bool to_end = static_cast<uint32_t>(cta) + 1 == share.n;  // the share runs to the list's end
-      if (some) {
-        at = tall_place(a, tile_tokens, pairs, share.begin(cta), mine);
-      }
       asm volatile("bar.sync 1, 64;" ::: "memory");
       if (some && !to_end) end = *reinterpret_cast<const TallPlace*>(smem + C::kOffEnd);
       if (lane == 0) {
@@ -696,18 +704,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
     }
 
     // ============================================================== MMA issuer
-    {
-      // (meanwhile: where the share ends)
-      TallRequest mine;
-      const int pairs = (a.q_len + 2 * tile_tokens - 1) / (2 * tile_tokens);
-      const TallShares share = tall_shares(a, tile_tokens, pairs, false, mine);
-      if (share.total > 0 && blockIdx.x + 1 < share.n) {
-        const TallPlace end = tall_place(a, tile_tokens, pairs, share.begin(blockIdx.x + 1), mine);
-        if (lane == 0) *reinterpret_cast<TallPlace*>(smem + C::kOffEnd) = end;
-      }
-      __syncwarp();
-      asm volatile("bar.arrive 1, 64;" ::: "memory");
-    }
+    __syncwarp();
+    asm volatile("bar.arrive 1, 64;" ::: "memory");
     const uint32_t tmem = *tmem_slot;
     constexpr uint32_t kIdescS = umma_idesc_bf16(kTRows, kTKeys, false, false, C::kConv);
     constexpr uint32_t kIdescO = umma_idesc_bf16(kTRows, kHeadDim, false, true, C::kConv);
