@@ -789,11 +789,42 @@ bool is_tall(const decode_attn_params* p) {
   return static_cast<int64_t>(p->num_q_heads / p->num_kv_heads) * p->q_len > DECODE_ATTN_MAX_ROWS;
 }
 
+// Chunks per request of a call that leaves them open.  A plan on the device costs two
+// launches beside the attention's; where chunks of at most kRowsChunk tokens of every
+// request, taken as max_seq_len long, are on the GPU together, no plan does better.
+// GB300, bf16, us planned on the device and so: 2 requests of 507 tokens, 8 KV heads,
+// 4 rows 15.1 / 4.7; 7 of 3388, one head, 18 rows 22.0 / 13.7; 2 of 1559, 8 heads, 90
+// rows 23.0 / 15.6; 3 of up to 14439, one head, 4 rows 20.7 / 15.6.
+// Up to 16 rows, chunks of 128 tokens that merge in a cluster are faster still (the
+// first of these 7.7 with one chunk; FP8 10.5 / 6.2, 4-bit 7.7 / 6.7), but not for 256
+// tokens or less (2 of 222 tokens, 12 rows 6.3 / 6.5, 4-bit 7.3 / 8.7).
+constexpr int kRowsChunk = 640, kRowsShortChunk = 128, kRowsShort = 256;
+
+int32_t rows_splits(const decode_attn_params* p, int32_t num_splits, const DecodeExt& ext) {
+  const bool planned = device_planned(p, num_splits);
+  if (num_splits > 0 || (p->batch != 1 && !planned)) return num_splits;
+  const int unit = unit_heads(p, ext);
+  int64_t slots = 0;
+  int32_t n = 0, chunk = 0;
+  if (split_slots(p, &slots, unit) != DA_OK || plan_impl(p, nullptr, &n, &chunk, unit) != DA_OK) return num_splits;
+  const int64_t units = static_cast<int64_t>(p->batch) * (p->num_kv_heads / (unit > 0 ? unit : 1));
+  if (planned && chunk > kRowsChunk) n = static_cast<int32_t>(ceil_div64(p->max_seq_len, kRowsChunk));
+  if (rows_of(p) <= kMaxNarrowRows && p->max_seq_len > kRowsShort) {
+    const int32_t most = static_cast<int32_t>(std::min<int64_t>(
+        std::min<int64_t>(kMaxClusterSplits, slots / units), ceil_div64(p->max_seq_len, kRowsShortChunk)));
+    if (most > n && use_cluster_merge(p, most, unit)) n = most;
+  }
+  return !planned || units * n <= slots ? n : num_splits;
+}
+
 }  // namespace
 
 int rows_workspace_bytes(const decode_attn_params* p, const decode_attn_cache* c, int32_t num_splits,
                          const DecodeExt& ext, size_t* bytes) {
-  if (!is_tall(p)) return workspace_bytes(p, num_splits, ext, bytes);
+  if (!is_tall(p)) {
+    const int rc = check_shape(p);
+    return rc != DA_OK ? rc : workspace_bytes(p, rows_splits(p, num_splits, ext), ext, bytes);
+  }
   const int rc = check_shape(p, false);
   if (rc != DA_OK) return rc;
   if (bytes == nullptr) return DA_ERR_NULL_POINTER;
@@ -807,9 +838,12 @@ int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void
              const int32_t* block_table, const int32_t* seq_lens, void* out, float* lse,
              int32_t num_splits, void* workspace, size_t workspace_bytes, int32_t* status,
              void* stream, const DecodeExt& ext) {
-  if (!is_tall(p))
-    return run_decode(p, q, c->k, c->v, block_table, seq_lens, out, lse, num_splits, workspace,
+  if (!is_tall(p)) {
+    const int rc = check_shape(p);
+    if (rc != DA_OK) return rc;
+    return run_decode(p, q, c->k, c->v, block_table, seq_lens, out, lse, rows_splits(p, num_splits, ext), workspace,
                       workspace_bytes, status, stream, true, ext);
+  }
   int rc = check_shape(p, false);
   if (rc != DA_OK) return rc;
   const bool paged = block_table != nullptr;
