@@ -753,6 +753,11 @@ namespace {
 constexpr int64_t kTallCopyPairsFp8 = 3;
 constexpr int64_t kTallCopyPairsFp4 = 2;
 constexpr size_t kTallCopyMost = size_t{2} << 30;
+// Up to this many keys items are not cut, and nothing is merged.  GB300, bf16, us cut
+// and whole: 2 requests of 33 tokens, 8 / 2 heads, over 250, 510, 760 and 1020 keys 14.7 /
+// 13.1, 20.9 / 16.0, 20.8 / 18.4, 19.3 / 21.1; 34 of 34, 32 / 4 heads, 24.6 / 23.0, 36.8 /
+// 31.9, 42.5 / 34.7, 47.5 / 43.0.
+constexpr int kTallWhole = 768;
 
 // Workspace of a call of more than DECODE_ATTN_MAX_ROWS rows per KV head: [K and V
 // in bf16, where they are copied], partials, and the records of their merge.
@@ -952,7 +957,7 @@ int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void
   a.lse = lse;
   a.part_o = reinterpret_cast<float*>(w + l.part_o);
   a.part_lse = reinterpret_cast<float*>(w + l.part_lse);
-  a.join = w + l.join;
+  a.join = p->max_seq_len <= kTallWhole ? nullptr : w + l.join;
   a.block_table = in_pages ? block_table : nullptr;
   a.bt_stride = p->block_table_stride;
   a.seq_lens = seq_lens;

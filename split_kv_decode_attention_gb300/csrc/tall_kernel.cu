@@ -172,9 +172,10 @@ struct TallRequest {
     return static_cast<uint32_t>(steps) * (kTCostBoth * n + kTCostOne * n1) + kTCostItem * (n + n1);
   }
   // the step of an item of pair p at cost x of it; a cut near the item's begin or end
-  // is moved there
-  __device__ __forceinline__ int step_at(int p, uint32_t x) const {
+  // (with `whole`, any) is moved there
+  __device__ __forceinline__ int step_at(int p, uint32_t x, bool whole) const {
     const int s = x <= kTCostItem ? 0 : static_cast<int>((x - kTCostItem) / per_step(p));
+    if (whole) return 2 * s < steps ? 0 : steps;
     return s < kTSnap ? 0 : steps - s < kTSnap ? steps : s;
   }
 };
@@ -289,8 +290,25 @@ __device__ __forceinline__ TallPlace tall_place(const SplitArgs& a, int tile_tok
   const uint32_t kvh = (x - before) / item;
   p.kvh = static_cast<int>(kvh);
   p.item_cost = before + kvh * item;
-  p.step = p.q.step_at(p.pair, x - p.item_cost);
+  p.step = p.q.step_at(p.pair, x - p.item_cost, a.join == nullptr);
   return p;
+}
+
+// The rows that are in no item (of requests without keys, and of pairs of tiles that
+// are all padding): a warp to a token of a request, `first` of `warps`.
+__device__ __forceinline__ void zero_rows(const SplitArgs& a, int64_t first, int64_t warps) {
+  const int lane = threadIdx.x & 31;
+  const int tile_tokens = kTRows / a.group;
+  const int64_t tokens = static_cast<int64_t>(a.batch) * a.q_len;
+  for (int64_t e = first; e < tokens; e += warps) {
+    const int b = static_cast<int>(e / a.q_len), t = static_cast<int>(e - static_cast<int64_t>(b) * a.q_len);
+    const TallRequest q = tall_request(a, b, tile_tokens, false);
+    if (q.steps > 0 && t < static_cast<int64_t>(q.both + q.one) * 2 * tile_tokens) continue;
+    uint16_t* row = a.out + static_cast<int64_t>(b) * a.o_sb + static_cast<int64_t>(t) * a.o_st + lane * 4;
+    for (int h = 0; h < a.num_q_heads; ++h)
+      *reinterpret_cast<uint2*>(row + static_cast<int64_t>(h) * a.o_sh) = make_uint2(0u, 0u);
+    for (int h = lane; h < a.num_q_heads; h += 32) a.lse[e * a.num_q_heads + h] = -INFINITY;
+  }
 }
 
 // For the merge (in the workspace): the item that a CTA's share begins in the middle
@@ -462,21 +480,23 @@ __global__ void __launch_bounds__(kTThreads, 1)
             ++q_use[g];
           }
         }
-        // the item's pieces: its first share is the last that starts at or before its
-        // first step, its last one the last that starts inside
-        TallJoin join = {};
-        if (some && begins_inside) {
-          auto begins_at = [&](int c) {
-            return first_place.q.step_at(first_place.pair, share.begin(c) - first_place.item_cost);
-          };
-          const uint32_t item_end = first_place.item_cost + first_place.q.cost(first_place.pair);
-          int first = cta, past = cta + 1;
-          while (first > 0 && share.begin(first) > first_place.item_cost && begins_at(first) > 0) --first;
-          while (past < static_cast<int>(share.n) && share.begin(past) < item_end && begins_at(past) < first_place.q.steps)
-            ++past;
-          join = TallJoin{past - first, first, first_place.b, first_place.kvh, first_place.pair};
+        if (a.join != nullptr) {
+          // the item's pieces, for the merge: its first share is the last that starts at or before its
+          // first step, its last one the last that starts inside
+          TallJoin join = {};
+          if (some && begins_inside) {
+            auto begins_at = [&](int c) {
+              return first_place.q.step_at(first_place.pair, share.begin(c) - first_place.item_cost, false);
+            };
+            const uint32_t item_end = first_place.item_cost + first_place.q.cost(first_place.pair);
+            int first = cta, past = cta + 1;
+            while (first > 0 && share.begin(first) > first_place.item_cost && begins_at(first) > 0) --first;
+            while (past < static_cast<int>(share.n) && share.begin(past) < item_end && begins_at(past) < first_place.q.steps)
+              ++past;
+            join = TallJoin{past - first, first, first_place.b, first_place.kvh, first_place.pair};
+          }
+          *reinterpret_cast<TallJoin*>(a.join + cta * kTallJoinBytes) = join;
         }
-        *reinterpret_cast<TallJoin*>(a.join + cta * kTallJoinBytes) = join;
         if (!ok) {
           report();
 #pragma unroll
@@ -1053,14 +1073,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
   tc_fence_before_sync();
   __syncwarp();
   if (lane == 0) mbar_arrive(tmem_done);
+  if (a.join == nullptr)  // (no merge follows)
+    zero_rows(a, static_cast<int64_t>(warp - kTSoftmaxWarp) * gridDim.x + blockIdx.x, 8 * static_cast<int64_t>(gridDim.x));
 }
 
 // Merges the pieces of items: piece 0 in slot 2 j + 1 of the CTA j that began it, the
 // others in slots 2 (j + 1), 2 (j + 2), ..; half a warp per row, 8 d a lane.
 //     M = max_s lse_s,  w_s = exp(lse_s - M),  out = sum w_s O_s / sum w_s,
 // kJoinAhead pieces at a time.  The blocks blockIdx.x of all CTAs with a later piece
-// share the item's rows.  It also writes the rows that are in no item: those of
-// requests without keys and of pairs of tiles that are all padding.
+// share the item's rows.  It also writes the rows that are in no item.
 // What bounds it is the latency of the chain (record, pieces, output) and, with a
 // warp per row, was the number of instructions.
 constexpr int kJoinWarps = 8;
@@ -1127,18 +1148,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinBlocks) tall_join_kernel
     if (sub == 0)
       a.lse[(static_cast<int64_t>(join.b) * a.q_len + t) * a.num_q_heads + h] = W == 0.f ? -INFINITY : M + logf(W);
   }
-  // ---- the rows in no item, a warp to a token of a request
-  const int64_t tokens = static_cast<int64_t>(a.batch) * a.q_len;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * gridDim.y * kJoinWarps;
-  for (int64_t e = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kJoinWarps + warp; e < tokens; e += warps) {
-    const int b = static_cast<int>(e / a.q_len), t = static_cast<int>(e - static_cast<int64_t>(b) * a.q_len);
-    const TallRequest q = tall_request(a, b, tile_tokens, false);
-    if (q.steps > 0 && t < static_cast<int64_t>(q.both + q.one) * 2 * tile_tokens) continue;
-    uint16_t* row = a.out + static_cast<int64_t>(b) * a.o_sb + static_cast<int64_t>(t) * a.o_st + lane * 4;
-    for (int h = 0; h < a.num_q_heads; ++h)
-      *reinterpret_cast<uint2*>(row + static_cast<int64_t>(h) * a.o_sh) = make_uint2(0u, 0u);
-    for (int h = lane; h < a.num_q_heads; h += 32) a.lse[e * a.num_q_heads + h] = -INFINITY;
-  }
+  zero_rows(a, (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kJoinWarps + warp,
+            static_cast<int64_t>(gridDim.x) * gridDim.y * kJoinWarps);
 }
 
 std::mutex g_tall_mu;
@@ -1169,7 +1180,7 @@ cudaError_t launch_tall_t(const TallMaps& maps, const SplitArgs& a, int box_toke
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, tall_kernel<KV>, maps, a, box_tokens);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.join == nullptr) return e;
   cfg.gridDim = dim3(kTallCtas, kJoinBlocks);
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.dynamicSmemBytes = 0;
