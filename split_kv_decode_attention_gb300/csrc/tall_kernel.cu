@@ -984,10 +984,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
     }
     ubase += 2 * n;
 
-    // ---- the rows' outputs.  A lane that wrote its own row would touch a sector of
-    // each of 32 rows with every store, and the tensor core waits meanwhile: so O is
-    // read as 16-row fragments, where four lanes hold eight neighbouring columns of
-    // a row.
+    // ---- the rows' outputs.  A lane holds 16 columns of its row at a time; two lanes
+    // trade, so that they write 32 bytes, a sector, of one of their rows and then of
+    // the other (16 bytes of each row at a time take longer, and more instructions do:
+    // they are met once an item)
     const bool direct = it.slot < 0;
     const bool writes = in_tile && t < a.q_len;
     const int h = it.kvh * a.group + (r - rt * a.group);
@@ -1008,59 +1008,40 @@ __global__ void __launch_bounds__(kTThreads, 1)
     uint8_t* const dst = direct ? reinterpret_cast<uint8_t*>(a.out) : reinterpret_cast<uint8_t*>(a.part_o);
     // (rolled up: the code is met once an item, and its first pass waits for the
     // instructions)
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {  // rows 16 half + lane / 4, and 8 further
-      float f[2];
-      int64_t at[2];
-      bool some[2];
+    const bool odd = (lane & 1) != 0;
+    const int64_t pair_at = __shfl_xor_sync(kFull, row_at, 1);
+    const int64_t at0 = odd ? pair_at : row_at, at1 = odd ? row_at : pair_at;  // of the even and the odd lane's row
+    auto write = [&](const uint32_t (&w)[8], int offset) {
+      uint32_t got[4];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int owner = 16 * half + 8 * e + (lane >> 2);
-        f[e] = __shfl_sync(kFull, inv, owner);
-        at[e] = __shfl_sync(kFull, row_at, owner);
-        some[e] = __shfl_sync(kFull, have ? 1 : 0, owner) != 0;
+      for (int e = 0; e < 4; ++e) got[e] = __shfl_xor_sync(kFull, odd ? w[e] : w[4 + e], 1);
+      uint8_t* const to = dst + offset + (odd ? 16 : 0);
+      if (at0 >= 0)
+        *reinterpret_cast<uint4*>(to + at0) =
+            odd ? make_uint4(got[0], got[1], got[2], got[3]) : make_uint4(w[0], w[1], w[2], w[3]);
+      if (at1 >= 0)
+        *reinterpret_cast<uint4*>(to + at1) =
+            odd ? make_uint4(w[4], w[5], w[6], w[7]) : make_uint4(got[0], got[1], got[2], got[3]);
+    };
+#pragma unroll 1
+    for (int c = 0; c < kHeadDim / 16; ++c) {
+      float o[16];
+      if (active) {
+        tmem_ld16(o_col + c * 16, o);
+        tmem_wait_ld();
       }
-#pragma unroll 1
-      for (int c = 0; c < kHeadDim / 32; ++c) {
-        float o[16];
-        if (active) {
-          tmem_ld_16x32(o_col + (static_cast<uint32_t>(16 * half) << 16) + c * 32, o);
-          tmem_wait_ld();
-        }
+      if (direct) {
+        uint32_t w[8];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float y[8];  // columns 8 q + 2 (lane % 4) and + 1
+        for (int e = 0; e < 8; ++e) w[e] = have ? pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
+        write(w, c * 32);
+      } else {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            y[2 * q] = some[e] ? o[4 * q + 2 * e] * f[e] : 0.f;
-            y[2 * q + 1] = some[e] ? o[4 * q + 2 * e + 1] * f[e] : 0.f;
-          }
-          if (direct) {
-            // the four lanes of a row trade, so that each has the eight columns of
-            // one group: 16 bytes, 64 in a row
-            uint32_t w[4];
+        for (int d = 0; d < 2; ++d) {
+          uint32_t w[8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) w[q] = pack_bf16x2(y[2 * q], y[2 * q + 1]);
-#pragma unroll
-            for (int d = 1; d <= 2; d *= 2) {
-              const bool up = (lane & d) != 0;
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                if ((q & d) != 0) continue;
-                const uint32_t give = up ? w[q] : w[q + d];
-                const uint32_t got = __shfl_xor_sync(kFull, give, d);
-                if (up) w[q] = got;
-                else w[q + d] = got;
-              }
-            }
-            if (at[e] >= 0)
-              *reinterpret_cast<uint4*>(dst + at[e] + c * 64 + (lane & 3) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-          } else if (at[e] >= 0) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<float2*>(dst + at[e] + c * 128 + q * 32 + (lane & 3) * 8) =
-                  make_float2(y[2 * q], y[2 * q + 1]);
-          }
+          for (int e = 0; e < 8; ++e) w[e] = have ? __float_as_uint(o[8 * d + e] * inv) : 0u;
+          write(w, c * 64 + d * 32);
         }
       }
     }
