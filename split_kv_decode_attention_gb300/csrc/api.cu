@@ -754,10 +754,10 @@ constexpr int64_t kTallCopyPairsFp8 = 3;
 constexpr int64_t kTallCopyPairsFp4 = 2;
 constexpr size_t kTallCopyMost = size_t{2} << 30;
 // Up to this many keys items are not cut, and nothing is merged.  GB300, bf16, us cut
-// and whole: 2 requests of 33 tokens, 8 / 2 heads, over 250, 510, 760 and 1020 keys 14.7 /
-// 13.1, 20.9 / 16.0, 20.8 / 18.4, 19.3 / 21.1; 34 of 34, 32 / 4 heads, 24.6 / 23.0, 36.8 /
-// 31.9, 42.5 / 34.7, 47.5 / 43.0.
-constexpr int kTallWhole = 768;
+// and whole: 2 requests of 33 tokens, 8 / 2 heads, over 250, 510, 760 and 1020 keys 13.3 /
+// 11.7, 19.6 / 14.8, 19.5 / 17.0, 19.2 / 19.6; 34 of 34, 32 / 4 heads, 23.3 / 21.7, 35.2 /
+// 29.7, 41.1 / 33.1, 46.0 / 40.5.  (1500 keys, one head, 256 rows: 20.3 / 28.9.)
+constexpr int kTallWhole = 1024;
 
 // Workspace of a call of more than DECODE_ATTN_MAX_ROWS rows per KV head: [K and V
 // in bf16, where they are copied], partials, and the records of their merge.
