@@ -51,12 +51,12 @@
 // Values of keys behind a sequence may be anything: they are zeroed in shared
 // memory (0 x NaN is NaN).  Every wait is bounded.
 //
-// GB300, us: 8192 tokens x 8192 keys, 32 / 8 heads: 675 (1630 TFLOP/s, 0.86 of a
-// library product's burst); 4 x 2048 x 4096, 32 / 8 heads: 358 (1535); 16 requests
-// of 4K to 16K keys, 256 rows per head: 132 (4.8 TB/s; HBM bounds its steps, 20 us
-// are the first copies, the last output and the merge); 8 requests of up to 448
-// tokens over up to 1500 FP8 states, 20 heads: 64, most of it the items' begins and
-// ends (7 steps each).
+// GB300, us: 8192 tokens x 8192 keys, 32 / 8 heads: 675 to 705 as the clock goes (1560
+// to 1630 TFLOP/s, 0.83 to 0.86 of a library product's burst); 4 x 2048 x 4096, 32 / 8
+// heads: 356 (1545); 16 requests of 4K to 16K keys, 256 rows per head: 132 (4.8 TB/s; a
+// step is bound by HBM, 20 us are the first copies, the last output and the merge); 8
+// requests of up to 448 tokens over up to 1500 FP8 states, 20 heads: 62, half of it the
+// items' begins and ends (7 steps each).
 
 #include <cfloat>
 #include <mutex>
