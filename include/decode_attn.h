@@ -652,12 +652,15 @@ int decode_attn_tree_mask(int32_t batch, int32_t q_len, int32_t max_seq_len,
  *   mask_stride_batch   words from a request's rows to the next one's; 0: one
  *                       mask for all
  * p->causal is not used, nor is DA_FLAG_TEST_WITHHOLD_COPY above
- * DECODE_ATTN_MAX_ROWS.  (Hq / Hkv) * q_len may exceed DECODE_ATTN_MAX_ROWS;
- * Hq / Hkv may not, nor q_len DECODE_ATTN_MAX_TREE.  Above that many rows the
- * call cuts its work evenly on the device: num_splits is not used, and the
- * workspace holds 40 MB of partials whatever the sizes and, for FP8 and 4-bit
- * caches and more than 512 (256) rows per KV head, K and V in bf16 (B * max_seq_len
- * * Hkv * 512 bytes) where those are at most 2 GB.
+ * DECODE_ATTN_MAX_ROWS.  num_splits <= 0: calls whose chunks of every request,
+ * taken as max_seq_len long, are short and on the GPU together are cut so; the
+ * others as decode_attn() plans them.
+ * (Hq / Hkv) * q_len may exceed DECODE_ATTN_MAX_ROWS; Hq / Hkv may not, nor q_len
+ * DECODE_ATTN_MAX_TREE.  Above that many rows the call cuts its work evenly on the
+ * device: num_splits is not used, and the workspace holds 40 MB of partials
+ * whatever the sizes and, for FP8 and 4-bit caches and more than two pairs (one
+ * pair) of tiles of 128 rows per KV head, K and V in bf16 (B * max_seq_len * Hkv *
+ * 512 bytes) where those are at most 2 GB.
  * Status as decode_attn(); DA_STATUS_SHORT_CAUSAL where L < n_b (the first
  * n_b - L new tokens then have no key).
  */
