@@ -640,6 +640,8 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty_bar[s]);
   }
+  // (an empty chunk's early stage lands where the merge writes next)
+  if (CM && early && n_iters == 0) ok = __all_sync(kFull, mbar_wait(&full_bar[0], 0)) != 0;
   if (!ok && lane == 0 && a.status != nullptr)
     atomicOr(a.status, static_cast<int32_t>(DA_STATUS_TIMEOUT));
 
