@@ -673,7 +673,7 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
   a.own = ext.own;
   a.status = status;
   a.batch = p->batch;
-  a.q_len = p->q_len;
+  a.q_len = ext.q_len > 0 ? ext.q_len : p->q_len;
   a.num_q_heads = p->num_q_heads;
   a.num_kv_heads = p->num_kv_heads;
   a.group = p->num_q_heads / p->num_kv_heads;
@@ -822,13 +822,61 @@ int32_t rows_splits(const decode_attn_params* p, int32_t num_splits, const Decod
   return !planned || units * n <= slots ? n : num_splits;
 }
 
+// Calls of more rows than the split kernel holds, where a CTA for each 16 of them (whole
+// tokens) and for each short chunk is on the GPU at once: the split kernel reads the keys
+// once per 16 rows, from L2, and merges the chunks in a cluster, one launch for two or
+// three.  GB300, bf16, us on the tcgen05 kernel and so: one request of 16 tokens, 32 / 8
+// heads (64 rows) over 130, 300, 600 and 1000 keys 9.0 / 8.0, 10.4 / 8.2, 13.3 / 10.7,
+// 14.1 / 10.8; of 32 tokens 10.7 / 8.1, 11.9 / 10.6, 15.3 / 12.2, 17.4 / 13.9; 7 of 9
+// tokens, 2 heads, over 2000 13.2 / 10.3.  More and larger clusters are slower (the first
+// over 2000, 512 CTAs in clusters of 16, 14.3 / 16.0), and so are longer chunks (over
+// 4096 14.4 / 22.2).  *gp and *ge become the call as the split kernel sees it, *n its
+// chunks.
+constexpr int kGroupChunk = 160, kGroupCluster = 8, kGroupCtas = 256;
+
+bool grouped_rows(const decode_attn_params* p, const DecodeExt& ext, int32_t num_splits, decode_attn_params* gp,
+                  DecodeExt* ge, int32_t* n) {
+  const int group = p->num_q_heads / p->num_kv_heads;
+  if (num_splits > 0 || ext.fp4 != nullptr || rows_of(p) <= kMaxNarrowRows || group > kMaxNarrowRows || p->batch < 1 ||
+      p->max_seq_len < 1)
+    return false;
+  const int tokens = kMaxNarrowRows / group, groups = (p->q_len + tokens - 1) / tokens;
+  if (static_cast<int64_t>(p->batch) * groups > 65535) return false;
+  *gp = *p;
+  gp->q_len = tokens;
+  gp->batch = p->batch * groups;
+  *ge = ext;
+  ge->own.groups = groups;
+  ge->own.tokens = tokens;
+  ge->q_len = p->q_len;
+  int64_t slots = 0;
+  if (split_slots(gp, &slots, 0) != DA_OK) return false;
+  const int64_t units = static_cast<int64_t>(gp->batch) * p->num_kv_heads;
+  const bool one = p->max_seq_len <= kRowsShort;
+  const int64_t chunks = one ? 1 : ceil_div64(p->max_seq_len, kRowsShortChunk);
+  for (int64_t i = std::min<int64_t>(std::min<int64_t>(kMaxClusterSplits, chunks), slots / units); i >= 1; --i) {
+    if (!one && ceil_div64(p->max_seq_len, i) > kGroupChunk) return false;
+    *n = static_cast<int32_t>(i);
+    if ((i <= kGroupCluster || units * i <= kGroupCtas) && (i == 1 || use_cluster_merge(gp, *n))) return true;
+  }
+  return false;
+}
+
 }  // namespace
 
 int rows_workspace_bytes(const decode_attn_params* p, const decode_attn_cache* c, int32_t num_splits,
                          const DecodeExt& ext, size_t* bytes) {
   if (!is_tall(p)) {
     const int rc = check_shape(p);
-    return rc != DA_OK ? rc : workspace_bytes(p, rows_splits(p, num_splits, ext), ext, bytes);
+    if (rc != DA_OK) return rc;
+    decode_attn_params gp;
+    DecodeExt ge;
+    int32_t n = 0;
+    if (bytes != nullptr && grouped_rows(p, ext, num_splits, &gp, &ge, &n)) {
+      *bytes = 0;  // (nothing is merged outside the cluster)
+      return DA_OK;
+    }
+    return workspace_bytes(p, rows_splits(p, num_splits, ext), ext, bytes);
   }
   const int rc = check_shape(p, false);
   if (rc != DA_OK) return rc;
@@ -846,6 +894,12 @@ int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void
   if (!is_tall(p)) {
     const int rc = check_shape(p);
     if (rc != DA_OK) return rc;
+    decode_attn_params gp;
+    DecodeExt ge;
+    int32_t n = 0;
+    if (grouped_rows(p, ext, num_splits, &gp, &ge, &n))
+      return run_decode(&gp, q, c->k, c->v, block_table, seq_lens, out, lse, n, workspace, workspace_bytes, status, stream,
+                        true, ge);
     return run_decode(p, q, c->k, c->v, block_table, seq_lens, out, lse, rows_splits(p, num_splits, ext), workspace,
                       workspace_bytes, status, stream, true, ext);
   }

@@ -17,6 +17,7 @@ struct DecodeExt {
   bool per_head = false;
   // rows of a tree or of a padded batch (kernels.cuh)
   RowArgs own = {};
+  int32_t q_len = 0;  // of a request, where the params have those of a group of its rows
 };
 
 // The current device is usable (DA_OK) or not.

@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
 
   // ---- this CTA's work item and key range [t_begin, t_end)
   int split, kvh, b, L, chunk;
+  int t0 = 0, rows = a.rows;  // first token of this CTA's rows, and their number
   if constexpr (listed) {
     // item slot blockIdx.x of the planner's list (slots past its count exit)
     const int n_items = a.plan[1];
@@ -163,6 +164,13 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
     split = blockIdx.x;
     kvh = blockIdx.y;
     b = blockIdx.z;
+    if constexpr (TR) {
+      if (a.own.groups > 1) {
+        t0 = b % a.own.groups * a.own.tokens;
+        b /= a.own.groups;
+        rows = min(rows, (a.q_len - t0) * a.group);
+      }
+    }
     L = a.seq_lens[static_cast<int64_t>(b) * a.len_sb + static_cast<int64_t>(kvh) * a.len_sh];  // (under the cluster merge its load overlaps the set-up)
     chunk = a.chunk_len;
   }
@@ -356,10 +364,10 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
   // Q^T as the B operand: rows r = 8*nt + g4, d pairs 2*t4 (+8) of k-step ks
   // (FP8: 4*t4 and 4*t4 + 2, the d permutation of the FP8 K fragments)
   auto q_row = [&](int r) -> const uint16_t* {
-    if (r >= a.rows) return nullptr;
+    if (r >= rows) return nullptr;
     const int t = r / a.group;
     const int g = r - t * a.group;
-    return a.q + static_cast<int64_t>(b) * a.q_sb + static_cast<int64_t>(t) * a.q_st +
+    return a.q + static_cast<int64_t>(b) * a.q_sb + static_cast<int64_t>(t0 + t) * a.q_st +
            static_cast<int64_t>(kvh * a.group + g) * a.q_sh;
   };
   constexpr int kQfSteps = C::kQSmem ? 1 : 8;  // fragments held in registers
@@ -416,9 +424,9 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
       const int row = nt * 8 + 2 * t4 + rr;
       int lm = t_end;
       if constexpr (TR) {
-        if (row / a.group >= own.n) lm = 0;
+        if (t0 + row / a.group >= own.n) lm = 0;
       } else {
-        if (a.causal && row < a.rows) lm = min(lm, L - a.q_len + 1 + row / a.group);
+        if (a.causal && row < rows) lm = min(lm, L - a.q_len + 1 + row / a.group);
       }
       lim[nt][rr] = lm;
     }
@@ -524,7 +532,7 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int rr = 0; rr < 2; ++rr) {
-              const int t = (nt * 8 + 2 * t4 + rr) / a.group;
+              const int t = t0 + (nt * 8 + 2 * t4 + rr) / a.group;
               if (t >= own.n) continue;
               if (!own.sees(t, j0)) hidden |= 1u << (nt * 4 + rr);
               if (!own.sees(t, j1)) hidden |= 1u << (nt * 4 + 2 + rr);
@@ -756,7 +764,7 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
     // its units from its own shared memory (the same max / weighted-sum merge
     // as the combine kernel) -- no remote loads, no second barrier
     const int S = gridDim.x;  // cluster = all chunks of this (kv head, request), <= 16
-    const int units = a.rows * 32;
+    const int units = rows * 32;
     const int slots = (units + S - 1) / S;
     cluster_wait();  // every peer has started: its inbox may be written
     for (int u = threadIdx.x; u < units; u += 32 * TPS) {
@@ -790,8 +798,8 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
         }
       }
       const float inv = W == 0.f ? 0.f : 1.f / W;
-      const int t = row / a.group;
-      const int h = kvh * a.group + (row - t * a.group);
+      const int tr = row / a.group, t = t0 + tr;
+      const int h = kvh * a.group + (row - tr * a.group);
       *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(b) * a.o_sb +
                                 static_cast<int64_t>(t) * a.o_st +
                                 static_cast<int64_t>(h) * a.o_sh + d) =
@@ -808,12 +816,12 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
     // cluster reduce the rows over all CTAs through distributed shared
     // memory (the same max / weighted-sum merge as the combine kernel)
     float* xo = reinterpret_cast<float*>(smem + C::kXoOffset);
-    for (int idx = threadIdx.x; idx < a.rows * 32; idx += 32 * TPS) {
+    for (int idx = threadIdx.x; idx < rows * 32; idx += 32 * TPS) {
       const int row = idx >> 5;
       const int d = (idx & 31) * 4;
       *reinterpret_cast<float4*>(xo + row * kHeadDim + d) = merged(row, d);
     }
-    if (threadIdx.x < a.rows) xl[threadIdx.x] = row_lse(threadIdx.x);
+    if (threadIdx.x < rows) xl[threadIdx.x] = row_lse(threadIdx.x);
     cluster_sync();  // every CTA's (O, lse) is visible cluster-wide
 
     const int S = gridDim.x;  // cluster = all chunks of this (kv head, request), <= 16
@@ -821,7 +829,7 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
     const uint32_t xl_addr = smem_addr(xl);
     // (row, 4 d) units interleaved over the CTAs of the cluster (unit u goes
     // to CTA u mod S), so every CTA reduces an equal share
-    for (int u = threadIdx.x * S + split; u < a.rows * 32; u += 32 * TPS * S) {
+    for (int u = threadIdx.x * S + split; u < rows * 32; u += 32 * TPS * S) {
       const int row = u >> 5;
       const int d = (u & 31) * 4;
       // every peer's LSE and the first 8 peers' output slices in one round
@@ -866,8 +874,8 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
         }
       }
       const float inv = W == 0.f ? 0.f : 1.f / W;
-      const int t = row / a.group;
-      const int h = kvh * a.group + (row - t * a.group);
+      const int tr = row / a.group, t = t0 + tr;
+      const int h = kvh * a.group + (row - tr * a.group);
       *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(b) * a.o_sb +
                                 static_cast<int64_t>(t) * a.o_st +
                                 static_cast<int64_t>(h) * a.o_sh + d) =
@@ -883,12 +891,12 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
   } else {
     const bool direct = nsplit_b == 1;
     const int S = a.num_splits;
-    for (int idx = threadIdx.x; idx < a.rows * 32; idx += 32 * TPS) {
+    for (int idx = threadIdx.x; idx < rows * 32; idx += 32 * TPS) {
       const int row = idx >> 5;
       const int d = (idx & 31) * 4;
       const float4 v = merged(row, d);
-      const int t = row / a.group;
-      const int h = kvh * a.group + (row - t * a.group);
+      const int tr = row / a.group, t = t0 + tr;
+      const int h = kvh * a.group + (row - tr * a.group);
       if (direct) {
         uint2 pk = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
         *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(b) * a.o_sb +
@@ -901,11 +909,11 @@ __global__ void __launch_bounds__(SplitCfg<NT, STAGES, TPS, F8>::kThreads)
         st_global_hint(a.part_o + pidx * kHeadDim + d, v, l2_evict_last_policy());
       }
     }
-    if (threadIdx.x < a.rows) {
+    if (threadIdx.x < rows) {
       const int row = threadIdx.x;
       const float lse = row_lse(row);
-      const int t = row / a.group;
-      const int h = kvh * a.group + (row - t * a.group);
+      const int tr = row / a.group, t = t0 + tr;
+      const int h = kvh * a.group + (row - tr * a.group);
       const int64_t prow = (static_cast<int64_t>(b) * a.q_len + t) * a.num_q_heads + h;
       if (direct)
         a.lse[prow] = lse;
