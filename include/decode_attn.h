@@ -656,8 +656,9 @@ int decode_attn_tree_mask(int32_t batch, int32_t q_len, int32_t max_seq_len,
  * taken as max_seq_len long, are short and on the GPU together are cut so; the
  * others as decode_attn() plans them.
  * (Hq / Hkv) * q_len may exceed DECODE_ATTN_MAX_ROWS; Hq / Hkv may not, nor q_len
- * DECODE_ATTN_MAX_TREE.  Above that many rows the call cuts its work evenly on the
- * device: num_splits is not used, and the workspace holds 40 MB of partials
+ * DECODE_ATTN_MAX_TREE.  Above that many rows the other calls, and all with
+ * num_splits > 0 (whose value is then not used), cut their work evenly on the
+ * device, and the workspace holds 40 MB of partials
  * whatever the sizes and, for FP8 and 4-bit caches and more than two pairs (one
  * pair) of tiles of 128 rows per KV head, K and V in bf16 (B * max_seq_len * Hkv *
  * 512 bytes) where those are at most 2 GB.

@@ -625,7 +625,8 @@ def decode_attn_tree(q, k_cache, v_cache, block_table, seq_lens, mask, *, max_se
     in its row of `mask` (int32 [B, q_len, ceil(q_len / 32)], or [1, ..] for all
     requests: tree_mask()'s).  Rows from new_lens[b] on are padding: zeros, and an
     lse of -inf.  Any cache type, as decode_attn(); the query rows per KV head may
-    exceed 128 (num_splits is then not used)."""
+    exceed 128 (num_splits then only says, above 0, that a short call is not cut as
+    one of few rows)."""
     return _calls().tree(q, k_cache, v_cache, block_table, seq_lens, mask, new_lens, max_seq_len,
                          scale, num_splits, k_scale, v_scale, k_sf, v_sf, out, lse, workspace,
                          status, stream)
@@ -638,8 +639,7 @@ def cross_attn(q, k_cache, v_cache, block_table, seq_lens, *, max_seq_len: int, 
     """Attention of every token over all seq_lens[b] keys (an encoder's states),
     for one new token or a prompt of any length q_len: (out, lse).  Rows from
     q_lens[b] on are padding: zeros, and an lse of -inf.  Any cache type and
-    layout, as decode_attn(); num_splits is not used above 128 query rows per KV
-    head."""
+    layout, as decode_attn(); num_splits as in decode_attn_tree()."""
     return _calls().cross(q, k_cache, v_cache, block_table, seq_lens, q_lens, max_seq_len, scale,
                           num_splits, k_scale, v_scale, k_sf, v_sf, out, lse, workspace, status,
                           stream)

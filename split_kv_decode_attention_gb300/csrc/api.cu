@@ -830,7 +830,9 @@ int32_t rows_splits(const decode_attn_params* p, int32_t num_splits, const Decod
 // 14.1 / 10.8; of 32 tokens 10.7 / 8.1, 11.9 / 10.6, 15.3 / 12.2, 17.4 / 13.9; 7 of 9
 // tokens, 2 heads, over 2000 13.2 / 10.3.  More and larger clusters are slower (the first
 // over 2000, 512 CTAs in clusters of 16, 14.3 / 16.0), and so are longer chunks (over
-// 4096 14.4 / 22.2).  *gp and *ge become the call as the split kernel sees it, *n its
+// 4096 14.4 / 22.2).  More than 128 rows, on the kernel for them and so: 2 requests of 33
+// tokens, 8 / 2 heads, over 130, 600 and 1000 keys 12.3 / 7.6, 16.2 / 10.2, 19.9 / 10.7;
+// 15 of 35, 8 heads on one, 13.0 / 9.7 over 130.  *gp and *ge become the call as the split kernel sees it, *n its
 // chunks.
 constexpr int kGroupChunk = 160, kGroupCluster = 8, kGroupCtas = 256;
 
@@ -866,21 +868,17 @@ bool grouped_rows(const decode_attn_params* p, const DecodeExt& ext, int32_t num
 
 int rows_workspace_bytes(const decode_attn_params* p, const decode_attn_cache* c, int32_t num_splits,
                          const DecodeExt& ext, size_t* bytes) {
-  if (!is_tall(p)) {
-    const int rc = check_shape(p);
-    if (rc != DA_OK) return rc;
-    decode_attn_params gp;
-    DecodeExt ge;
-    int32_t n = 0;
-    if (bytes != nullptr && grouped_rows(p, ext, num_splits, &gp, &ge, &n)) {
-      *bytes = 0;  // (nothing is merged outside the cluster)
-      return DA_OK;
-    }
-    return workspace_bytes(p, rows_splits(p, num_splits, ext), ext, bytes);
-  }
   const int rc = check_shape(p, false);
   if (rc != DA_OK) return rc;
   if (bytes == nullptr) return DA_ERR_NULL_POINTER;
+  decode_attn_params gp;
+  DecodeExt ge;
+  int32_t n = 0;
+  if (grouped_rows(p, ext, num_splits, &gp, &ge, &n)) {
+    *bytes = 0;  // (nothing is merged outside the cluster)
+    return DA_OK;
+  }
+  if (!is_tall(p)) return workspace_bytes(p, rows_splits(p, num_splits, ext), ext, bytes);
   TallLayout l;
   const int rc2 = tall_layout(p, c, &l);
   if (rc2 == DA_OK) *bytes = l.total;
@@ -891,20 +889,17 @@ int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void
              const int32_t* block_table, const int32_t* seq_lens, void* out, float* lse,
              int32_t num_splits, void* workspace, size_t workspace_bytes, int32_t* status,
              void* stream, const DecodeExt& ext) {
-  if (!is_tall(p)) {
-    const int rc = check_shape(p);
-    if (rc != DA_OK) return rc;
-    decode_attn_params gp;
-    DecodeExt ge;
-    int32_t n = 0;
-    if (grouped_rows(p, ext, num_splits, &gp, &ge, &n))
-      return run_decode(&gp, q, c->k, c->v, block_table, seq_lens, out, lse, n, workspace, workspace_bytes, status, stream,
-                        true, ge);
-    return run_decode(p, q, c->k, c->v, block_table, seq_lens, out, lse, rows_splits(p, num_splits, ext), workspace,
-                      workspace_bytes, status, stream, true, ext);
-  }
   int rc = check_shape(p, false);
   if (rc != DA_OK) return rc;
+  decode_attn_params gp;
+  DecodeExt ge;
+  int32_t n = 0;
+  if (grouped_rows(p, ext, num_splits, &gp, &ge, &n))
+    return run_decode(&gp, q, c->k, c->v, block_table, seq_lens, out, lse, n, workspace, workspace_bytes, status, stream,
+                      true, ge);
+  if (!is_tall(p))
+    return run_decode(p, q, c->k, c->v, block_table, seq_lens, out, lse, rows_splits(p, num_splits, ext), workspace,
+                      workspace_bytes, status, stream, true, ext);
   const bool paged = block_table != nullptr;
   rc = check_paged(p, paged);
   if (rc != DA_OK) return rc;

@@ -617,7 +617,8 @@ def cross_call(da, c, q, **kw):
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
 @pytest.mark.parametrize("seed", range(10))
-def test_many_rows_of_any_shape(da, kind, seed):
+@pytest.mark.parametrize("splits", [0, 1])
+def test_many_rows_of_any_shape(da, kind, seed, splits):
     """Lengths on both sides of a step's 128 keys and of the cuts, empty requests and padding, odd groups."""
     r = random.Random(seed)
     G = [1, 5, 7, 100, 3, 16, 4, 1, 8, 11][seed]
@@ -630,7 +631,7 @@ def test_many_rows_of_any_shape(da, kind, seed):
     c = Paged(kind, lens, heads, r.choice([0, 16, 64, 128]), 400 + seed).gpu()
     q = bf16(gen(seed), B, T, heads * G, D, std=2.0)
     status = status_word()
-    out, lse = cross_call(da, c, q.cuda(), q_lens=ints(own), status=status)
+    out, lse = cross_call(da, c, q.cuda(), q_lens=ints(own), status=status, num_splits=splits)
     check_rows(c, q, out, lse, own, None)
     assert int(status) == 0
 
@@ -656,23 +657,25 @@ def test_many_rows_of_more_heads_than_ctas(da, kind):
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
 @pytest.mark.parametrize("T", [40, 300])
-def test_many_rows_of_nothing_but_padding(da, kind, T):
+@pytest.mark.parametrize("splits", [0, 1])
+def test_many_rows_of_nothing_but_padding(da, kind, T, splits):
     c = Paged(kind, [100, 30], 2, 16, 14).gpu()
     q = torch.full((2, T, 8, D), float("nan"), dtype=torch.bfloat16, device="cuda")
-    out, lse = cross_call(da, c, q, q_lens=ints([0, 0]))
+    out, lse = cross_call(da, c, q, q_lens=ints([0, 0]), num_splits=splits)
     assert bool((out == 0).all()) and bool((lse == -math.inf).all())
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
 @pytest.mark.parametrize("T", [40, 100, 250])
-def test_status_bits_of_many_rows(da, kind, T):
+@pytest.mark.parametrize("splits", [0, 1])
+def test_status_bits_of_many_rows(da, kind, T, splits):
     """As for few rows, also where the cache is read back first."""
     c = Paged(kind, [100, 50], 1, 16, 15).gpu()
     q = bf16(gen(3), 2, T, 4, D).cuda()
 
     def bits(lens=c.dlens, bt=c.dbt, own=None):
         status = status_word()
-        da.cross_attn(q, c.dk, c.dv, bt, lens, max_seq_len=c.max_len, q_lens=own, status=status, **c.scales())
+        da.cross_attn(q, c.dk, c.dv, bt, lens, max_seq_len=c.max_len, q_lens=own, status=status, num_splits=splits, **c.scales())
         return int(status)
 
     bad = c.dbt.clone()
@@ -682,7 +685,8 @@ def test_status_bits_of_many_rows(da, kind, T):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
-def test_many_rows_on_two_streams_and_in_one_workspace(da, kind):
+@pytest.mark.parametrize("splits", [0, 1])
+def test_many_rows_on_two_streams_and_in_one_workspace(da, kind, splits):
     """Calls that overlap on two streams, and calls of different shapes that follow one another in one workspace, give
     the bits of calls alone."""
     shapes = [([700, 90], 2, 4, 50), ([300, 1200, 5], 1, 5, 90), ([90] * 6, 3, 1, 140), ([2500], 1, 8, 17)]
@@ -690,25 +694,26 @@ def test_many_rows_on_two_streams_and_in_one_workspace(da, kind):
     for i, (lens, heads, G, T) in enumerate(shapes):
         c = Paged(kind, lens, heads, 16, 20 + i).gpu()
         q = bf16(gen(i), len(lens), T, heads * G, D, std=2.0).cuda()
-        cases.append((c, q, cross_call(da, c, q)))
+        cases.append((c, q, cross_call(da, c, q, num_splits=splits)))
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in range(2)]
     got = []
     for rep in range(6):
         for i, (c, q, _) in enumerate(cases):
-            got.append((i, cross_call(da, c, q, stream=streams[(i + rep) % 2])))
+            got.append((i, cross_call(da, c, q, num_splits=splits, stream=streams[(i + rep) % 2])))
     torch.cuda.synchronize()
     ws = torch.full((1 << 24,), float("nan"), device="cuda")
     for rep in range(3):
         for i, (c, q, _) in enumerate(cases):
-            got.append((i, cross_call(da, c, q, workspace=ws)))
+            got.append((i, cross_call(da, c, q, num_splits=splits, workspace=ws)))
     torch.cuda.synchronize()
     for i, (out, lse) in got:
         assert torch.equal(out, cases[i][2][0]) and torch.equal(lse, cases[i][2][1]), i
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
-def test_many_rows_replayed_with_other_lengths(da, kind):
+@pytest.mark.parametrize("splits", [0, 1])
+def test_many_rows_replayed_with_other_lengths(da, kind, splits):
     """The plan is made on the device: a captured call follows the lengths, the pages and the rows."""
     c = Paged(kind, [900, 333, 64], 2, 16, 21).gpu()
     T = 60
@@ -718,7 +723,8 @@ def test_many_rows_replayed_with_other_lengths(da, kind):
     lse = torch.empty(3, T, 8, device="cuda")
 
     def call():
-        da.cross_attn(dq, c.dk, c.dv, c.dbt, lens, max_seq_len=900, q_lens=own, out=out, lse=lse, **c.scales())
+        da.cross_attn(dq, c.dk, c.dv, c.dbt, lens, max_seq_len=900, q_lens=own, out=out, lse=lse, num_splits=splits,
+                      **c.scales())
 
     s = torch.cuda.Stream()
     with torch.cuda.stream(s):
@@ -737,8 +743,8 @@ def test_many_rows_replayed_with_other_lengths(da, kind):
         check_rows(c, q, out, lse, rows, None)
 
 
-@pytest.mark.parametrize("T", [4, 50])
-def test_infinite_keys_weigh_nothing_or_everything(da, T):
+@pytest.mark.parametrize("T,splits", [(4, 0), (50, 0), (50, 1)])
+def test_infinite_keys_weigh_nothing_or_everything(da, T, splits):
     """A key whose score is -inf is as if it were not there; one of +inf makes its rows NaN, and those alone."""
     c = Paged("bf16", [300], 1, 16, 22).gpu()
     q = bf16(gen(12), 1, T, 4, D)
@@ -746,7 +752,7 @@ def test_infinite_keys_weigh_nothing_or_everything(da, T):
     q[0, 1, :, 0] = -1.0
     at = (int(c.bt[0, 77 // 16]), 77 % 16)
     c.dk[at[0], at[1], 0, 0] = -math.inf
-    out, lse = cross_call(da, c, q.cuda())
+    out, lse = cross_call(da, c, q.cuda(), num_splits=splits)
     assert bool(out[0, 1].isnan().all()) and bool(lse[0, 1].isnan().all())
     k, v = (R.gather(c.values(w) * 1.0, c.bt, 0, 300)[:, 0] for w in "kv")
     seen = torch.ones(4 * (T - 1), 300, dtype=torch.bool)
@@ -766,7 +772,7 @@ def test_rows_of_any_magnitude(da, kind):
         q[0, t] = (q[0, t].float() * 2.0 ** (-120 + 1.6 * t)).to(torch.bfloat16)
     q[0, 7] = 0
     scale = 2.0 ** -100
-    out, lse = cross_call(da, c, q.cuda(), scale=scale)
+    out, lse = cross_call(da, c, q.cuda(), scale=scale, num_splits=1)
     # Weights of at most 2^-30 of the largest are subnormal in f16, which holds them to 2^-25 (half its last step) of 2^6:
     # 200 of them can be off by 2^-31 each.  (With one key of all the weight that is more than the relative tolerance.)
     lost = 0.0 if kind == "bf16" else 200 * 2.0 ** -31 * float((c.values("v") * c.vs).abs().max())
@@ -783,10 +789,10 @@ def test_far_pages_and_tokens(da):
     k, v = (torch.empty(pages, page, heads, D, dtype=torch.bfloat16, device="cuda") for _ in "kv")
     k[first:], v[first:] = near.dk, near.dv
     bt = near.dbt + first
-    for T in (3, 60):
+    for T, splits in ((3, 0), (60, 0), (60, 1)):
         q = bf16(gen(14), 2, T, 4 * heads, D, std=2.0).cuda()
-        want = cross_call(da, near, q)
-        got = da.cross_attn(q, k, v, bt, near.dlens, max_seq_len=200)
+        want = cross_call(da, near, q, num_splits=splits)
+        got = da.cross_attn(q, k, v, bt, near.dlens, max_seq_len=200, num_splits=splits)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     got = da.cache_read(k, v, bt, near.dlens, max_seq_len=200)
     want = da.cache_read(near.dk, near.dv, near.dbt, near.dlens, max_seq_len=200)
