@@ -823,9 +823,9 @@ int32_t rows_splits(const decode_attn_params* p, int32_t num_splits, const Decod
 }
 
 // Calls of more rows than the split kernel holds, where a CTA for each 16 of them (whole
-// tokens) and for each short chunk is on the GPU at once: the split kernel reads the keys
-// once per 16 rows, from L2, and merges the chunks in a cluster, one launch for two or
-// three.  GB300, bf16, us on the tcgen05 kernel and so: one request of 16 tokens, 32 / 8
+// tokens) and for each short chunk is on the GPU at once: that kernel (or the 4-bit one)
+// reads the keys once per 16 rows, from L2, and merges the chunks in a cluster, one launch
+// for two or three.  GB300, bf16, us on the tcgen05 kernel and so: one request of 16 tokens, 32 / 8
 // heads (64 rows) over 130, 300, 600 and 1000 keys 9.0 / 8.0, 10.4 / 8.2, 13.3 / 10.7,
 // 14.1 / 10.8; of 32 tokens 10.7 / 8.1, 11.9 / 10.6, 15.3 / 12.2, 17.4 / 13.9; 7 of 9
 // tokens, 2 heads, over 2000 13.2 / 10.3.  More and larger clusters are slower (the first
@@ -839,7 +839,7 @@ constexpr int kGroupChunk = 160, kGroupCluster = 8, kGroupCtas = 256;
 bool grouped_rows(const decode_attn_params* p, const DecodeExt& ext, int32_t num_splits, decode_attn_params* gp,
                   DecodeExt* ge, int32_t* n) {
   const int group = p->num_q_heads / p->num_kv_heads;
-  if (num_splits > 0 || ext.fp4 != nullptr || rows_of(p) <= kMaxNarrowRows || group > kMaxNarrowRows || p->batch < 1 ||
+  if (num_splits > 0 || rows_of(p) <= kMaxNarrowRows || group > kMaxNarrowRows || p->batch < 1 ||
       p->max_seq_len < 1)
     return false;
   const int tokens = kMaxNarrowRows / group, groups = (p->q_len + tokens - 1) / tokens;
@@ -852,14 +852,18 @@ bool grouped_rows(const decode_attn_params* p, const DecodeExt& ext, int32_t num
   ge->own.tokens = tokens;
   ge->q_len = p->q_len;
   int64_t slots = 0;
-  if (split_slots(gp, &slots, 0) != DA_OK) return false;
+  const int unit = unit_heads(gp, *ge);
+  if (unit > 1 || split_slots(gp, &slots, unit) != DA_OK) return false;
   const int64_t units = static_cast<int64_t>(gp->batch) * p->num_kv_heads;
   const bool one = p->max_seq_len <= kRowsShort;
   const int64_t chunks = one ? 1 : ceil_div64(p->max_seq_len, kRowsShortChunk);
   for (int64_t i = std::min<int64_t>(std::min<int64_t>(kMaxClusterSplits, chunks), slots / units); i >= 1; --i) {
     if (!one && ceil_div64(p->max_seq_len, i) > kGroupChunk) return false;
+    if (i > kGroupCluster && units * i > kGroupCtas) continue;
+    int32_t chunk = 0, eff = 0;
     *n = static_cast<int32_t>(i);
-    if ((i <= kGroupCluster || units * i <= kGroupCtas) && (i == 1 || use_cluster_merge(gp, *n))) return true;
+    if (chunk_for_splits(gp, *n, &chunk, &eff, unit) != DA_OK) return false;
+    if (eff == 1 || use_cluster_merge(gp, eff, unit)) return true;
   }
   return false;
 }

@@ -234,6 +234,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
   // ---- this CTA's work item: (chunk, KV head group, request)
   int split, unit, b, L, chunk;
   const bool listed = a.items != nullptr;
+  int t0 = 0, rows = a.rows;  // first token of this CTA's rows, and their number (of a head)
   if (listed) {
     const int n_items = a.plan[1];
     const int4 itm = a.items[blockIdx.x];
@@ -247,6 +248,13 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
     split = blockIdx.x;
     unit = blockIdx.y;
     b = blockIdx.z;
+    if constexpr (TR) {
+      if (a.own.groups > 1) {
+        t0 = b % a.own.groups * a.own.tokens;
+        b /= a.own.groups;
+        rows = min(rows, (a.q_len - t0) * a.group);
+      }
+    }
     // (a length per head only with HG = 1)
     L = a.seq_lens[static_cast<int64_t>(b) * a.len_sb + static_cast<int64_t>(unit) * a.len_sh];
     chunk = a.chunk_len;
@@ -267,7 +275,6 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
   const int hh = warp % HG;                              // this (consumer) warp's head of the group
   const int share = warp / HG;                           // and its share of the head's keys
   const int kvh = unit * HG + hh;
-  const int rows = a.rows;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -374,7 +381,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
     for (int i = 0; i < 4; ++i) x[i] = make_uint4(0u, 0u, 0u, 0u);
     if (r < rows) {
       const int t = r / a.group;
-      const uint16_t* qr = a.q + static_cast<int64_t>(b) * a.q_sb + static_cast<int64_t>(t) * a.q_st +
+      const uint16_t* qr = a.q + static_cast<int64_t>(b) * a.q_sb + static_cast<int64_t>(t0 + t) * a.q_st +
                            static_cast<int64_t>(kvh * a.group + (r - t * a.group)) * a.q_sh + 32 * t4;
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint4*>(qr + 8 * i);
@@ -440,7 +447,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
       int lm = t_end;
       if constexpr (TR) {
         // (padding rows are dropped at the end and hold up nothing)
-        if (row / a.group >= own.n) lm = 0;
+        if (t0 + row / a.group >= own.n) lm = 0;
         else lim_all = min(lim_all, lm);
       } else {
         if (a.causal && row < rows) lm = min(lm, L - a.q_len + 1 + row / a.group);
@@ -551,7 +558,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
             for (int j = 0; j < 2; ++j)
               if (tok0 + 16 * h + 8 * j + krow >= lim[nt][rr]) sc[h][nt][2 * j + rr] = -INFINITY;
           if constexpr (TR) {
-            const int t = (nt * 8 + 2 * t4 + rr) / a.group;
+            const int t = t0 + (nt * 8 + 2 * t4 + rr) / a.group;
             if (tok0 + kWarpKeys > own.base && t < own.n) {
               const uint32_t seen = own.bits(t, tok0);
 #pragma unroll
@@ -675,7 +682,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr)
-        if ((nt * 8 + 2 * t4 + rr) / a.group >= own.n || (m[nt][rr] == -INFINITY && l[nt][rr] == 0.f)) {
+        if (t0 + (nt * 8 + 2 * t4 + rr) / a.group >= own.n || (m[nt][rr] == -INFINITY && l[nt][rr] == 0.f)) {
           m[nt][rr] = -INFINITY;
           l[nt][rr] = 0.f;
 #pragma unroll
@@ -697,8 +704,9 @@ __global__ void __launch_bounds__(Fp4Cfg<NT, HG>::kThreads, Fp4Cfg<NT, HG>::kMin
   const int S = a.num_splits;
   // where a row of this head goes: its (token, head), and its partial's index
   auto place = [&](int row, int head, int& t) {
-    t = row / a.group;
-    return (unit * HG + head) * a.group + (row - t * a.group);
+    const int tr = row / a.group;
+    t = t0 + tr;
+    return (unit * HG + head) * a.group + (row - tr * a.group);
   };
   auto part_index = [&](int row, int head, int t, int h) {
     return listed ? (static_cast<int64_t>(blockIdx.x) * HG + head) * a.rows + row
