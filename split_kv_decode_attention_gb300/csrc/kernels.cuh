@@ -25,7 +25,7 @@ struct RowArgs {
   int64_t mask_sb;                     // words between two requests' masks
   int words;                           // words of a row
   const int32_t* own_lens;             // rows of each request (nullptr: q_len); the others are padding
-  // split kernel: a request's tokens go to `groups` CTAs per (chunk, kv head), `tokens`
+  // split and 4-bit kernels: a request's tokens go to `groups` CTAs per (chunk, kv head), `tokens`
   // each (0: all to one)
   int groups, tokens;
 };
