@@ -122,9 +122,12 @@ struct TCfg {
   static constexpr int kSmem = 1024 + kOffExp + (kConv ? 2 * 2 * kTRows * 2 : 0);
   static_assert(kSmem <= 227 * 1024, "shared memory");
   // P = 2^(x - m + kShift) with m the row's maximum when it was last raised; it is
-  // raised when P would pass 2^(kShift + kRaise).  In bf16 nothing is lost below
-  // 2^64; f16 ends at 2^16 and keeps weights down to 2^-24 of 2^kShift.
-  static constexpr float kRaise = kConv ? 8.f : 64.f;      // log2 units
+  // raised when P would pass 2^(kShift + kRaise).  f16 ends at 2^16 and keeps weights
+  // down to 2^-24 of 2^kShift.  bf16 holds far more, but O sums P V in fp32: with P up
+  // to 2^8 (as in the kernels for fewer rows) values of up to 2^119 / keys stay finite,
+  // with 2^64 those above 2^63 did not.  Raised past 8 instead of 64: no call slower
+  // (GB300, 4 x 2048 tokens over 4096 keys 355 us both, 16 x 512 over 1500 107 and 109).
+  static constexpr float kRaise = 8.f;                     // log2 units
   static constexpr float kShift = kConv ? 6.f : 0.f;
 };
 
