@@ -372,6 +372,14 @@ __device__ __forceinline__ float packed_pair_sum(uint32_t v, bool f16) {
   return packed_lo(v, f16) + packed_hi(v, f16);
 }
 
+// sum += the two bf16 values of v, exactly as if unpacked (an add whose operand is bf16)
+__device__ __forceinline__ void add_bf16x2(float2& sum, uint32_t v) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "add.rn.f32.bf16 %0, l, %0;\n\tadd.rn.f32.bf16 %1, h, %1;\n\t}"
+      : "+f"(sum.x), "+f"(sum.y)
+      : "r"(v));
+}
+
 // max(a, b, c) in one instruction (sm_100 and later)
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float r;

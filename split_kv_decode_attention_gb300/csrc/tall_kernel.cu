@@ -26,9 +26,14 @@
 // exponentials of a tile take about 1000 cycles of their unit whoever asks for them.)
 // O is rescaled only when a row's maximum has grown by more than 2^kRaise (the
 // end's division is exact about it), which is rare after the first steps.  P is
-// rounded to 16 bits for the product; the sum that O is divided by is that of the
-// unrounded ones (summing the rounded ones too, as the kernels for fewer rows do,
-// took 9 % longer).
+// rounded to 16 bits for the product.  Over bf16 caches O is divided by the sum of the
+// weights as rounded, as in the kernels for fewer rows, so that those applied sum to
+// one: the error is at most 2^-8 sum_j w_j |v_j - o|, and a row that one key dominates
+// returns that key's value.  (Divided by the unrounded sum, up to 2^-8 |o| of it came
+// on top.)  The second sum costs 5 to 8 % at size, with adds that take a bf16 operand;
+// by unpacking P 11 %, by a warp's mma against a selection of its own lanes 40 %, and
+// behind the release of P, where the warp would wait anyway, no less than before it.
+// In f16 (2^-11) the unrounded sum stays; the LSE has it everywhere.
 //
 // The work is cut evenly, whatever the lengths: all steps of all items stand in
 // one list, by pair of row tiles, request and kv head, and each of kTallCtas CTAs
@@ -54,9 +59,10 @@
 // Values of keys behind a sequence may be anything: they are zeroed in shared
 // memory (0 x NaN is NaN).  Every wait is bounded.
 //
-// GB300, us: 8192 tokens x 8192 keys, 32 / 8 heads: 675 to 705 as the clock goes (1560
-// to 1630 TFLOP/s, 0.83 to 0.86 of a library product's burst); 4 x 2048 x 4096, 32 / 8
-// heads: 356 (1545); 16 requests of 4K to 16K keys, 256 rows per head: 132 (4.8 TB/s; a
+// GB300, us in a replayed graph: 8192 tokens x 8192 keys, 32 / 8 heads: 722 to 738 as
+// the clock goes (1490 to 1520 TFLOP/s, 0.79 to 0.81 of a library product's burst); 4 x
+// 2048 x 4096, 32 / 8 heads: 383 to 390 (1410 to 1440); 16 requests of 4K to 16K keys,
+// 256 rows per head: 137 (4.7 TB/s; a
 // step is bound by HBM, 20 us are the first copies, the last output and the merge); 8
 // requests of up to 448 tokens over up to 1500 FP8 states, 20 heads: 62, half of it the
 // items' begins and ends (7 steps each).
@@ -837,6 +843,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const bool mine = in_tile && t < it.own;
     float m_used = -INFINITY;  // reference maximum of P (log2 domain), raised seldom
     float l = 0.f;             // sum of the weights
+    float lq = 0.f;            // and of the weights as rounded into P (bf16 caches: divides O)
     const bool active = g < it.tiles;
     float sc = a.scale_log2, s_fma = raw ? sc : 1.f;
     if (active) {
@@ -883,7 +890,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         // P of the first quarter as if no maximum grew, while the others' S comes and
         // their maximum is taken
         const float2 s2 = make_float2(s_fma, s_fma);
-        float2 ps;
+        float2 ps, qs;
         uint32_t w0[16];
         auto quarter = [&](const float* x, uint32_t* w, float2 nm2) {
 #pragma unroll
@@ -893,6 +900,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             const float p1 = ex2(y.y);
             ps = __fadd2_rn(ps, make_float2(p0, p1));
             w[e] = C::kConv ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+            if constexpr (!C::kConv) add_bf16x2(qs, w[e]);
           }
         };
         auto shift = [&]() {
@@ -907,7 +915,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; ++e) x[e] = !raw && !edge ? y[0][e] * sc : y[0][e];
-          ps = make_float2(0.f, 0.f);
+          ps = qs = make_float2(0.f, 0.f);
           quarter(x, w0, shift());
 #pragma unroll
           for (int e = 32; e < kTKeys; ++e) x[e] = y[e / 32][e % 32];
@@ -927,6 +935,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           const float alpha = raise ? ex2(m_used - mt) : 1.f;
           if (raise) m_used = mt;
           l *= alpha;
+          lq *= alpha;
           if (i > 0) {  // (S of this step is complete, so is the P V issued before it)
 #pragma unroll 1
             for (int c = 0; c < kHeadDim / 16; ++c) {
@@ -939,7 +948,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
               tmem_st16(o_col + c * 16, w);
             }
           }
-          ps = make_float2(0.f, 0.f);
+          ps = qs = make_float2(0.f, 0.f);
           quarter(x, w0, shift());
         }
         const float2 nm2 = shift();
@@ -980,6 +989,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         }
         p_ready(1);
         l += ps.x + ps.y;
+        lq += qs.x + qs.y;
       }
       if (ok) {
         ok = __all_sync(kFull, mbar_wait_lazy(&o_done[g], o_use & 1)) != 0;
@@ -1000,7 +1010,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const int64_t prow = (static_cast<int64_t>(it.b) * a.q_len + t) * a.num_q_heads + h;
     const int64_t pidx = static_cast<int64_t>(it.slot) * (2 * kTRows) + g * kTRows + r;
     const bool have = ok && active && mine && l != 0.f;
-    const float inv = have ? (1.f / l) * a.v_scale : 0.f;  // (NaN stays NaN)
+    const float inv = have ? (1.f / (C::kConv ? l : lq)) * a.v_scale : 0.f;  // (NaN stays NaN)
     // byte offset of the row, -1 where nothing is written
     const int64_t row_at = !writes ? -1
                            : direct ? 2 * (static_cast<int64_t>(it.b) * a.o_sb + static_cast<int64_t>(t) * a.o_st +
