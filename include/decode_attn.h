@@ -616,6 +616,8 @@ int decode_attn_sparse(const decode_attn_params *p, const decode_attn_cache *c,
  * ------------------------------------------------------------------------ */
 
 #define DECODE_ATTN_MAX_TREE 1024  /* new tokens of a request in a tree */
+#define DECODE_ATTN_ROWS_WORKSPACE 40162048 /* bytes that a call of more than
+                                      DECODE_ATTN_MAX_ROWS rows needs at least */
 #define DA_STATUS_TREE 32u         /* a parent that is no earlier token, or kept tokens
                                       that do not rise */
 
@@ -658,10 +660,13 @@ int decode_attn_tree_mask(int32_t batch, int32_t q_len, int32_t max_seq_len,
  * (Hq / Hkv) * q_len may exceed DECODE_ATTN_MAX_ROWS; Hq / Hkv may not, nor q_len
  * DECODE_ATTN_MAX_TREE.  Above that many rows the other calls, and all with
  * num_splits > 0 (whose value is then not used), cut their work evenly on the
- * device, and the workspace holds 40 MB of partials
- * whatever the sizes and, for FP8 and 4-bit caches and more than two pairs (one
- * pair) of tiles of 128 rows per KV head, K and V in bf16 (B * max_seq_len * Hkv *
- * 512 bytes) where those are at most 2 GB.
+ * device, and the workspace holds 40 MB of partials (DECODE_ATTN_ROWS_WORKSPACE)
+ * whatever the sizes.  For FP8 and 4-bit caches and more than two pairs (one pair) of
+ * tiles of 128 rows per KV head, the sizes below count K and V in bf16 besides (B *
+ * max_seq_len * Hkv * 512 bytes) where those are at most 2 GB.  That copy is the
+ * caller's choice: in a workspace without room for it, these calls convert K and V
+ * as they go (FP8 8 to 28 % slower, 4-bit 3 to 50 %).  For the product with V the
+ * weights are rounded to bf16 with the copy, as over bf16 caches, and to f16 without.
  * Status as decode_attn(); DA_STATUS_SHORT_CAUSAL where L < n_b (the first
  * n_b - L new tokens then have no key).
  */

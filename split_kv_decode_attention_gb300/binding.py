@@ -20,6 +20,7 @@ CALLS_PATH = os.path.join(_PKG, "lib", "_calls.so")
 HEAD_DIM = 128
 MAX_ROWS = 128
 MAX_TREE = 1024
+ROWS_WORKSPACE = 40162048
 TOKEN_TILE = 16
 
 DA_OK = 0
@@ -626,7 +627,9 @@ def decode_attn_tree(q, k_cache, v_cache, block_table, seq_lens, mask, *, max_se
     requests: tree_mask()'s).  Rows from new_lens[b] on are padding: zeros, and an
     lse of -inf.  Any cache type, as decode_attn(); the query rows per KV head may
     exceed 128 (num_splits then only says, above 0, that a short call is not cut as
-    one of few rows)."""
+    one of few rows).  Above 128 rows over FP8 and 4-bit caches the workspace that
+    the call makes may hold K and V in bf16 (up to 2 GB); a `workspace` of at least
+    ROWS_WORKSPACE bytes is used as it is, without that copy where it has no room."""
     return _calls().tree(q, k_cache, v_cache, block_table, seq_lens, mask, new_lens, max_seq_len,
                          scale, num_splits, k_scale, v_scale, k_sf, v_sf, out, lse, workspace,
                          status, stream)
@@ -639,7 +642,7 @@ def cross_attn(q, k_cache, v_cache, block_table, seq_lens, *, max_seq_len: int, 
     """Attention of every token over all seq_lens[b] keys (an encoder's states),
     for one new token or a prompt of any length q_len: (out, lse).  Rows from
     q_lens[b] on are padding: zeros, and an lse of -inf.  Any cache type and
-    layout, as decode_attn(); num_splits as in decode_attn_tree()."""
+    layout, as decode_attn(); num_splits and workspace as in decode_attn_tree()."""
     return _calls().cross(q, k_cache, v_cache, block_table, seq_lens, q_lens, max_seq_len, scale,
                           num_splits, k_scale, v_scale, k_sf, v_sf, out, lse, workspace, status,
                           stream)

@@ -749,7 +749,8 @@ namespace {
 // them itself, once for each.  GB300, 8 requests of 2048 tokens, 32 / 8 heads, us
 // copied and converted: FP8 with 1, 2, 3, 8 pairs 53 / 42, 68 / 65, 82 / 89, 138 /
 // 177; 4-bit 55 / 46, 70 / 72, 84 / 99, 140 / 211.  A copy of more than kTallCopyMost
-// bytes is not made (it would save at most a third of the time).
+// bytes is not made (it would save at most a third of the time), nor one that the
+// workspace given has no room for.
 constexpr int64_t kTallCopyPairsFp8 = 3;
 constexpr int64_t kTallCopyPairsFp4 = 2;
 constexpr size_t kTallCopyMost = size_t{2} << 30;
@@ -767,7 +768,7 @@ struct TallLayout {
   size_t k, v, part_o, part_lse, join, total;
 };
 
-int tall_layout(const decode_attn_params* p, const decode_attn_cache* c, TallLayout* l) {
+int tall_layout(const decode_attn_params* p, const decode_attn_cache* c, TallLayout* l, bool may_copy = true) {
   const int64_t rows = static_cast<int64_t>(p->num_q_heads / p->num_kv_heads) * p->q_len;
   if (p->max_seq_len > (1 << 30) || rows > 0x7fffffff) return DA_ERR_BAD_SHAPE;
   // (the kernel adds up the costs of its steps in 32 bits)
@@ -778,7 +779,7 @@ int tall_layout(const decode_attn_params* p, const decode_attn_cache* c, TallLay
   const size_t part = static_cast<size_t>(kTallSlots) * kTallSlotRows;
   l->tokens = std::max<int64_t>(p->max_seq_len, 1);
   size_t copy = static_cast<size_t>(p->batch) * l->tokens * p->num_kv_heads * kHeadDim * 2;
-  l->copied = c->type != DA_CACHE_BF16 && 2 * copy <= kTallCopyMost &&
+  l->copied = may_copy && c->type != DA_CACHE_BF16 && 2 * copy <= kTallCopyMost &&
               pairs >= (c->type == DA_CACHE_FP4_E2M1 ? kTallCopyPairsFp4 : kTallCopyPairsFp8);
   if (!l->copied) copy = 0;
   l->k = 0;
@@ -929,6 +930,7 @@ int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void
   TallLayout l;
   rc = tall_layout(p, c, &l);
   if (rc != DA_OK) return rc;
+  if (l.copied && workspace_bytes < l.total) tall_layout(p, c, &l, false);
   if (workspace == nullptr || workspace_bytes < l.total || !aligned16(workspace))
     return DA_ERR_WORKSPACE;
   uint8_t* w = static_cast<uint8_t*>(workspace);

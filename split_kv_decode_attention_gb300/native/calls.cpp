@@ -667,19 +667,26 @@ PyObject* rows_attention(PyObject* const* a, const at::Tensor& mask, bool tree) 
   q_strides(p, q, out);
   const int32_t splits = std::max<int32_t>(0, integer32(a[8], "num_splits"));
   const char* where = tree ? "decode_attn_tree" : "decode_attn_cross";
-  size_t need = 0;
-  check(tree ? decode_attn_tree_workspace_bytes(&p, &c.c, splits, &need)
-             : decode_attn_cross_workspace_bytes(&p, &c.c, splits, &need),
-        where);
-  const at::Tensor ws = workspace_or_new(given, need, q);
   const int32_t *own_p = static_cast<const int32_t*>(ptr(own)), *bt_p = static_cast<const int32_t*>(ptr(bt)),
                 *lens_p = static_cast<const int32_t*>(ptr(lens));
-  check(tree ? decode_attn_tree(&p, &c.c, ptr(q), static_cast<const uint32_t*>(ptr(mask)), mask_step, own_p, bt_p,
-                                lens_p, ptr(out), static_cast<float*>(ptr(lse)), splits, ptr(ws), bytes_of(ws),
-                                status_of(status), stream.raw)
-             : decode_attn_cross(&p, &c.c, ptr(q), own_p, bt_p, lens_p, ptr(out), static_cast<float*>(ptr(lse)),
-                                 splits, ptr(ws), bytes_of(ws), status_of(status), stream.raw),
-        where);
+  auto run = [&](const at::Tensor& ws) {
+    return tree ? decode_attn_tree(&p, &c.c, ptr(q), static_cast<const uint32_t*>(ptr(mask)), mask_step, own_p, bt_p,
+                                   lens_p, ptr(out), static_cast<float*>(ptr(lse)), splits, ptr(ws), bytes_of(ws),
+                                   status_of(status), stream.raw)
+                : decode_attn_cross(&p, &c.c, ptr(q), own_p, bt_p, lens_p, ptr(out), static_cast<float*>(ptr(lse)),
+                                    splits, ptr(ws), bytes_of(ws), status_of(status), stream.raw);
+  };
+  // (a call that the workspace given, or none, suffices for runs in it: nothing is
+  // launched where it does not)
+  int rc = run(given.defined() && given.is_contiguous() ? given : undefined());
+  if (rc == DA_ERR_WORKSPACE) {
+    size_t need = 0;
+    check(tree ? decode_attn_tree_workspace_bytes(&p, &c.c, splits, &need)
+               : decode_attn_cross_workspace_bytes(&p, &c.c, splits, &need),
+          where);
+    rc = run(workspace_or_new(undefined(), need, q));
+  }
+  check(rc, where);
   return give({out, lse});
 }
 
