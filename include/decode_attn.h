@@ -667,6 +667,8 @@ int decode_attn_tree_mask(int32_t batch, int32_t q_len, int32_t max_seq_len,
  * caller's choice: in a workspace without room for it, these calls convert K and V
  * as they go (FP8 8 to 28 % slower, 4-bit 3 to 50 %).  For the product with V the
  * weights are rounded to bf16 with the copy, as over bf16 caches, and to f16 without.
+ * A workspace of the bytes below also serves every smaller batch of the same call,
+ * with num_splits <= 0.
  * Status as decode_attn(); DA_STATUS_SHORT_CAUSAL where L < n_b (the first
  * n_b - L new tokens then have no key).
  */

@@ -869,6 +869,41 @@ bool grouped_rows(const decode_attn_params* p, const DecodeExt& ext, int32_t num
   return false;
 }
 
+// Workspace of a call of up to DECODE_ATTN_MAX_ROWS rows, and of every smaller batch:
+// those may be cut into more chunks, or planned on the device where this one is not.
+int few_rows_bytes(const decode_attn_params* p, int32_t num_splits, const DecodeExt& ext, size_t* bytes) {
+  int rc = workspace_bytes(p, rows_splits(p, num_splits, ext), ext, bytes);
+  if (rc != DA_OK || num_splits > 0 || p->batch < 2) return rc;
+  auto also = [&](const decode_attn_params& other) {
+    size_t n = 0;
+    rc = workspace_bytes(&other, rows_splits(&other, num_splits, ext), ext, &n);
+    *bytes = std::max(*bytes, n);
+    return rc;
+  };
+  decode_attn_params other = *p;
+  other.batch = 1;
+  if (also(other) != DA_OK) return rc;
+  if (ext.fp4 != nullptr && !wide4(p)) {
+    // (a plan's partials, of any number of heads to a CTA, are more than one wave's)
+    for (int u = 1; u <= 8; u *= 2) {
+      if (fp4_warps(rows_of(p)) % u != 0 || p->num_kv_heads % u != 0) continue;
+      ListLayout l;
+      rc = list_layout(p, &l, u);
+      if (rc != DA_OK) return rc;
+      *bytes = std::max(*bytes, l.total);
+    }
+    return DA_OK;
+  }
+  // calls that are cut have all their chunks on the GPU at once
+  int64_t slots = 0;
+  rc = split_slots(p, &slots, unit_heads(p, ext));
+  if (rc != DA_OK) return rc;
+  *bytes = std::max(*bytes, static_cast<size_t>(slots) * rows_of(p) * (kHeadDim + 1) * sizeof(float));
+  other.batch = kWideMaxPlannedBatch;  // (no larger batch is planned)
+  if (rows_of(p) > kMaxNarrowRows && p->batch > other.batch) also(other);
+  return rc;
+}
+
 }  // namespace
 
 int rows_workspace_bytes(const decode_attn_params* p, const decode_attn_cache* c, int32_t num_splits,
@@ -883,7 +918,7 @@ int rows_workspace_bytes(const decode_attn_params* p, const decode_attn_cache* c
     *bytes = 0;  // (nothing is merged outside the cluster)
     return DA_OK;
   }
-  if (!is_tall(p)) return workspace_bytes(p, rows_splits(p, num_splits, ext), ext, bytes);
+  if (!is_tall(p)) return few_rows_bytes(p, num_splits, ext, bytes);
   TallLayout l;
   const int rc2 = tall_layout(p, c, &l);
   if (rc2 == DA_OK) *bytes = l.total;

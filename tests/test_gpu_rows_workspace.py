@@ -81,3 +81,49 @@ def test_size_of_the_least_workspace(da):  # noqa: F811
     p = params(fp4=False, q_len=100, max_pages_per_seq=400, block_table_stride=400, max_seq_len=6400)
     assert da.lib().decode_attn_cross_workspace_bytes(ref(p), ref(cache(da.DA_CACHE_BF16)), 0, ctypes.byref(n)) == 0
     assert n.value == da.ROWS_WORKSPACE
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("T,hq,hkv", [(1, 32, 8), (4, 32, 8), (7, 8, 1), (16, 32, 8), (32, 32, 8), (5, 48, 16)])
+def test_a_workspace_serves_smaller_batches(da, kind, T, hq, hkv):  # noqa: F811
+    """Up to 128 rows a smaller batch may be cut into more chunks: sizes that fell from 1 MB for 32 requests to nothing
+    for 64 left a workspace, sized once for the largest batch, too small for most others."""
+    n, kt = ctypes.c_size_t(), {"bf16": 0, "fp8": 1, "fp4": 2}[kind]
+    for L in (40, 300, 640, 1500, 4096, 20000, 100000):
+        pages = -(-L // 16)
+        most = 0
+        for B in (*range(1, 140), 152, 200, 304, 400, 608, 1000, 1024, 1025, 3000):
+            p = da.decode_attn_params_init(B, T, hq, hkv, D, 16, pages, pages, L, False)
+            if kind == "fp4":
+                p.kv_stride_page, p.kv_stride_token, p.kv_stride_head = 16 * hkv * 64, hkv * 64, 64
+            for f in (da.lib().decode_attn_tree_workspace_bytes, da.lib().decode_attn_cross_workspace_bytes):
+                assert f(ref(p), ref(cache(kt)), 0, ctypes.byref(n)) == 0
+                assert n.value >= most, (L, B, n.value, most)
+            most = n.value
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
+def test_one_workspace_for_every_batch(da, kind):  # noqa: F811
+    """Batches of 1 to 64 requests in the workspace of the largest, through the C entry."""
+    T, hq, hkv, L = 1, 32, 8, 640
+    c = Paged(kind, [L - 7 * (b % 9) for b in range(64)], hkv, 16, 32).gpu()
+    q = bf16(gen(32), 64, T, hq, D, std=2.0).cuda()
+    n, kt = ctypes.c_size_t(), {"bf16": 0, "fp8": 1, "fp4": 2}[kind]
+    cc = cache(kt, k=c.dk.data_ptr(), v=c.dv.data_ptr())
+    if kind == "fp4":
+        cc.k_block_scale, cc.v_block_scale = c.dk_sf.data_ptr(), c.dv_sf.data_ptr()
+        cc.bs_stride_page, cc.bs_stride_head = c.dk_sf.stride(0), c.dk_sf.stride(1)
+    ws = None
+    for B in (64, 33, 32, 24, 16, 9, 2, 1):
+        p = da.decode_attn_params_init(B, T, hq, hkv, D, 16, c.dbt.shape[1], c.dk.shape[0], c.max_len, False)
+        p.kv_stride_head, p.kv_stride_token, p.kv_stride_page = c.dk.stride(2), c.dk.stride(1), c.dk.stride(0)
+        p.block_table_stride = c.dbt.stride(0)
+        p.k_scale, p.v_scale = c.ks, c.vs
+        if ws is None:
+            assert da.lib().decode_attn_cross_workspace_bytes(ref(p), ref(cc), 0, ctypes.byref(n)) == 0
+            ws = torch.full((n.value + 16,), 0xff, dtype=torch.uint8, device="cuda")
+        out, lse = torch.empty_like(q[:B]), torch.empty(B, T, hq, device="cuda")
+        assert da.lib().decode_attn_cross(ref(p), ref(cc), q.data_ptr(), None, c.dbt.data_ptr(), c.dlens.data_ptr(), out.data_ptr(),
+                                          lse.data_ptr(), 0, ws.data_ptr(), n.value, None, None) == 0, B
+        want, wlse = da.cross_attn(q[:B], c.dk, c.dv, c.dbt[:B], c.dlens[:B], max_seq_len=c.max_len, **c.scales())
+        assert torch.equal(out, want) and torch.equal(lse, wlse), B
