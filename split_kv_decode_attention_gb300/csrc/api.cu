@@ -1067,7 +1067,7 @@ int run_rows(const decode_attn_params* p, const decode_attn_cache* c, const void
   a.scale_log2 = p->scale * (scaled ? p->k_scale : 1.f) * 1.4426950408889634f;
   a.v_scale = scaled ? p->v_scale : 1.f;
   a.own = ext.own;
-  return launch_tall(type, qmap, maps, a, box, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  return launch_tall(type, qmap, maps, a, box, di.sm_count, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 int plan_uniform(const decode_attn_params* p, const DecodeExt& ext, int32_t* num_splits,

@@ -203,7 +203,7 @@ int fp4_warps(int rows);  // consumer warps of a CTA: its heads divide them
 // group's heads, tall_tile_tokens() tokens.  part_o holds kTallSlots x 256 rows,
 // part_lse as many LSEs, join kTallCtas records; chunk_len and num_splits are not
 // used.
-constexpr int kTallCtas = 152;         // one for each SM
+constexpr int kTallCtas = 152;         // one for each SM, and no more than the device has (of a larger one this many)
 constexpr int kTallSlots = 2 * kTallCtas;
 constexpr int kTallSlotRows = 256;
 constexpr int kTallJoinBytes = 32;
@@ -211,7 +211,7 @@ constexpr int kTallJoinBytes = 32;
 // besides: the total of a call is below 2^32.
 constexpr int kTallCostBoth = 8, kTallCostItem = 24;
 cudaError_t launch_tall(int type, const CUtensorMap& q_map, const Fp4Maps& kv, const SplitArgs& a, int box_tokens,
-                        cudaStream_t stream);
+                        int sm_count, cudaStream_t stream);
 int tall_tile_tokens(int group);
 
 // Launch the combine kernel (one warp per output row, or with by_row and few rows a CTA).

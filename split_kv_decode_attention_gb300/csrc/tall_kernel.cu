@@ -36,7 +36,7 @@
 // In f16 (2^-11) the unrounded sum stays; the LSE has it everywhere.
 //
 // The work is cut evenly, whatever the lengths: all steps of all items stand in
-// one list, by pair of row tiles, request and kv head, and each of kTallCtas CTAs
+// one list, by pair of row tiles, request and kv head, and each CTA (one for each SM)
 // takes the same share of it by measured costs (kTCostBoth).  With the pairs
 // outermost, those of a (request, kv head) are worked on at about the same time and
 // meet its keys in L2 (4 x 2048 tokens x 4096 keys, 32 heads with keys of their own:
@@ -266,7 +266,7 @@ __device__ __forceinline__ TallShares tall_shares(const SplitArgs& a, int tile_t
   }
   TallShares h;
   h.total = tall_cost_below(a, tile_tokens, mine, pairs);
-  h.n = min(static_cast<uint32_t>(kTallCtas), max(h.total / kTCostLeast, 1u));
+  h.n = min(gridDim.x, max(h.total / kTCostLeast, 1u));
   h.each = h.total / h.n;
   h.more = h.total - h.each * h.n;
   return h;
@@ -1173,7 +1173,7 @@ std::mutex g_tall_mu;
 bool g_tall_attr[3][64];
 
 template <int KV>
-cudaError_t launch_tall_t(const TallMaps& maps, const SplitArgs& a, int box_tokens, cudaStream_t stream) {
+cudaError_t launch_tall_t(const TallMaps& maps, const SplitArgs& a, int box_tokens, int ctas, cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1187,7 +1187,7 @@ cudaError_t launch_tall_t(const TallMaps& maps, const SplitArgs& a, int box_toke
     }
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kTallCtas);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kTThreads);
   cfg.dynamicSmemBytes = TCfg<KV>::kSmem;
   cfg.stream = stream;
@@ -1198,7 +1198,7 @@ cudaError_t launch_tall_t(const TallMaps& maps, const SplitArgs& a, int box_toke
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, tall_kernel<KV>, maps, a, box_tokens);
   if (e != cudaSuccess || a.join == nullptr) return e;
-  cfg.gridDim = dim3(kTallCtas, kJoinBlocks);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), kJoinBlocks);
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, tall_join_kernel, a);
@@ -1209,12 +1209,13 @@ cudaError_t launch_tall_t(const TallMaps& maps, const SplitArgs& a, int box_toke
 int tall_tile_tokens(int group) { return kTRows / group; }
 
 cudaError_t launch_tall(int type, const CUtensorMap& q_map, const Fp4Maps& kv, const SplitArgs& a, int box_tokens,
-                        cudaStream_t stream) {
+                        int sm_count, cudaStream_t stream) {
+  const int ctas = sm_count < kTallCtas ? sm_count : kTallCtas;
   const TallMaps maps{q_map, kv.k, kv.v, kv.ks, kv.vs};
   switch (type) {
-    case DA_CACHE_BF16: return launch_tall_t<DA_CACHE_BF16>(maps, a, box_tokens, stream);
-    case DA_CACHE_FP8_E4M3: return launch_tall_t<DA_CACHE_FP8_E4M3>(maps, a, box_tokens, stream);
-    default: return launch_tall_t<DA_CACHE_FP4_E2M1>(maps, a, box_tokens, stream);
+    case DA_CACHE_BF16: return launch_tall_t<DA_CACHE_BF16>(maps, a, box_tokens, ctas, stream);
+    case DA_CACHE_FP8_E4M3: return launch_tall_t<DA_CACHE_FP8_E4M3>(maps, a, box_tokens, ctas, stream);
+    default: return launch_tall_t<DA_CACHE_FP4_E2M1>(maps, a, box_tokens, ctas, stream);
   }
 }
 
