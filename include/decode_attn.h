@@ -744,7 +744,9 @@ typedef struct decode_attn_read {
  *                 c->v then unused).
  * Rows that no token goes to are left as they were.  Status: DA_STATUS_SEQ_LEN
  * where a length or a start is out of range (clamped) or a row of offsets is
- * (not written), DA_STATUS_BAD_PAGE as in decode_attn().
+ * (not written), DA_STATUS_BAD_PAGE as in decode_attn().  A call whose outputs
+ * have no row (max_seq_len, max_tokens or, with offsets, rows 0) launches nothing
+ * and looks at no length: its status stays as it was.
  */
 int decode_attn_cache_read(const decode_attn_params *p, const decode_attn_cache *c,
                            const decode_attn_read *r, const int32_t *starts,
