@@ -631,6 +631,8 @@ int decode_attn_sparse(const decode_attn_params *p, const decode_attn_cache *c,
  *              row t is set for t itself and the tokens on its path
  *   positions  int32 [B, q_len], or NULL: L - n_b + the number of tokens on t's
  *              path before it (what rope_append() takes)
+ * The outputs share no memory with each other or with the inputs, but positions may
+ * be the array of parents itself.
  * Rows t >= n_b get zeros.  Status: DA_STATUS_TREE for a parent that is not
  * allowed (taken as -1), DA_STATUS_SEQ_LEN for a length outside [0, max_seq_len]
  * or [0, q_len] (clamped), DA_STATUS_SHORT_CAUSAL where L < n_b.

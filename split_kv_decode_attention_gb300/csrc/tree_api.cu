@@ -87,6 +87,13 @@ int decode_attn_tree_mask(int32_t batch, int32_t q_len, int32_t max_seq_len, con
   if (!aligned4(parents) || !aligned4(new_lens) || !aligned4(seq_lens) || !aligned4(mask) ||
       !aligned4(positions) || !aligned4(status))
     return DA_ERR_ALIGNMENT;
+  // (a request's rows are written while others' inputs are still to be read; positions
+  // may take the place of parents, which are read first, row by row)
+  const int64_t n = batch, tokens = n * q_len, words = tokens * ((q_len + 31) / 32);
+  if (overlap4(mask, words, parents, tokens) || overlap4(mask, words, new_lens, n) || overlap4(mask, words, seq_lens, n) ||
+      overlap4(mask, words, positions, tokens) || overlap4(positions, tokens, new_lens, n) ||
+      overlap4(positions, tokens, seq_lens, n) || (positions != parents && overlap4(positions, tokens, parents, tokens)))
+    return DA_ERR_BAD_SHAPE;
   const int rc = dattn::check_device(nullptr);
   if (rc != DA_OK) return rc;
   dattn::TreeMaskArgs a;
