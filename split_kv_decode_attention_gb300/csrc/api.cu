@@ -754,10 +754,15 @@ namespace {
 constexpr int64_t kTallCopyPairsFp8 = 3;
 constexpr int64_t kTallCopyPairsFp4 = 2;
 constexpr size_t kTallCopyMost = size_t{2} << 30;
-// Up to this many keys items are not cut, and nothing is merged.  GB300, bf16, us cut
-// and whole: 2 requests of 33 tokens, 8 / 2 heads, over 250, 510, 760 and 1020 keys 13.3 /
-// 11.7, 19.6 / 14.8, 19.5 / 17.0, 19.2 / 19.6; 34 of 34, 32 / 4 heads, 23.3 / 21.7, 35.2 /
-// 29.7, 41.1 / 33.1, 46.0 / 40.5.  (1500 keys, one head, 256 rows: 20.3 / 28.9.)
+// Up to this many keys items are not cut, and nothing is merged: the merge's launch costs
+// as much as the seven steps that a cut may save of an item.  GB300, bf16, us cut and
+// whole, 256 rows, lengths equal: 1 item (one request of 32 heads on one) over 130, 512,
+// 1024 and 1536 keys 13.7 / 12.0, 16.2 / 13.8, 20.2 / 19.8 and 17.0 / 25.7; 16 items 14.6 /
+// 13.2, 22.8 / 15.3, 22.0 / 20.3 and 20.3 / 26.6; 120 items 15.0 / 13.6, 23.8 / 16.2, 34.1 /
+// 22.3 and 42.8 / 30.6; 192 items 22.2 / 20.9, 31.4 / 25.1, 47.1 / 41.6 and 56.7 / 55.3; 456
+// items 32.2 / 30.1, 45.7 / 43.3, 66.1 / 63.7 and 87.0 / 84.0; lengths of an eighth to all of
+// these, and FP8 caches, alike.  (Above, it depends on the number of items: few are
+// faster cut, 64 to 152 whole up to 2048 keys.)
 constexpr int kTallWhole = 1024;
 
 // Workspace of a call of more than DECODE_ATTN_MAX_ROWS rows per KV head: [K and V
