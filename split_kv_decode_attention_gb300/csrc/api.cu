@@ -631,21 +631,24 @@ int run_decode(const decode_attn_params* p, const void* q, const void* k_cache,
   std::memset(&kmap, 0, sizeof(kmap));
   std::memset(&vmap, 0, sizeof(vmap));
   Fp4Maps maps4;
+  // (the maps cover the cache's own requests, also where rows go by groups)
+  decode_attn_params mp = *p;
+  if (ext.own.groups > 1) mp.batch = p->batch / ext.own.groups;
   if (fp4) {
     std::memset(&maps4, 0, sizeof(maps4));
     if (!no_keys) {
       const decode_attn_cache* c = ext.fp4;
       const cuuint32_t box4 = static_cast<cuuint32_t>(16 * fp4_box_halves(p, paged, unit));
-      rc = make_fp4_map(&maps4.k, c->k, p, c, paged, unit, box4, false, ext.per_head);
-      if (rc == DA_OK) rc = make_fp4_map(&maps4.v, c->v, p, c, paged, unit, box4, false, ext.per_head);
-      if (rc == DA_OK) rc = make_fp4_map(&maps4.ks, c->k_block_scale, p, c, paged, unit, box4, true, ext.per_head);
-      if (rc == DA_OK) rc = make_fp4_map(&maps4.vs, c->v_block_scale, p, c, paged, unit, box4, true, ext.per_head);
+      rc = make_fp4_map(&maps4.k, c->k, &mp, c, paged, unit, box4, false, ext.per_head);
+      if (rc == DA_OK) rc = make_fp4_map(&maps4.v, c->v, &mp, c, paged, unit, box4, false, ext.per_head);
+      if (rc == DA_OK) rc = make_fp4_map(&maps4.ks, c->k_block_scale, &mp, c, paged, unit, box4, true, ext.per_head);
+      if (rc == DA_OK) rc = make_fp4_map(&maps4.vs, c->v_block_scale, &mp, c, paged, unit, box4, true, ext.per_head);
       if (rc != DA_OK) return rc;
     }
   } else if (!no_keys) {
-    rc = make_kv_map(&kmap, k_cache, p, paged, box_tokens, ext.per_head);
+    rc = make_kv_map(&kmap, k_cache, &mp, paged, box_tokens, ext.per_head);
     if (rc != DA_OK) return rc;
-    rc = make_kv_map(&vmap, v_cache, p, paged, box_tokens, ext.per_head);
+    rc = make_kv_map(&vmap, v_cache, &mp, paged, box_tokens, ext.per_head);
     if (rc != DA_OK) return rc;
   }
 
