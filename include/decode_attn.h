@@ -651,6 +651,8 @@ int decode_attn_tree_mask(int32_t batch, int32_t q_len, int32_t max_seq_len,
  * for a row that sees no key.  What a hidden key holds does not matter, NaN
  * included; the values of the new tokens have to be finite, though, since a
  * hidden one enters the product with weight 0.
+ * Over bf16 caches a weight may stand at up to 2^8 while the sums run, so values
+ * are to stay below 2^119 / L.
  *   mask                uint32 rows as decode_attn_tree_mask() writes them (any
  *                       other pattern of bits is as good), 4-byte aligned
  *   mask_stride_batch   words from a request's rows to the next one's; 0: one

@@ -776,6 +776,9 @@ struct TallLayout {
   size_t k, v, part_o, part_lse, join, total;
 };
 
+static_assert(DECODE_ATTN_ROWS_WORKSPACE == kTallSlots * kTallSlotRows * (kHeadDim + 1) * 4 + kTallCtas * kTallJoinBytes,
+              "what a call needs without a copy");
+
 int tall_layout(const decode_attn_params* p, const decode_attn_cache* c, TallLayout* l, bool may_copy = true) {
   const int64_t rows = static_cast<int64_t>(p->num_q_heads / p->num_kv_heads) * p->q_len;
   if (p->max_seq_len > (1 << 30) || rows > 0x7fffffff) return DA_ERR_BAD_SHAPE;
