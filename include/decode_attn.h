@@ -665,11 +665,11 @@ int decode_attn_tree_mask(int32_t batch, int32_t q_len, int32_t max_seq_len,
  * DECODE_ATTN_MAX_TREE.  Above that many rows the other calls, and all with
  * num_splits > 0 (whose value is then not used), cut their work evenly on the
  * device, and the workspace holds 40 MB of partials (DECODE_ATTN_ROWS_WORKSPACE)
- * whatever the sizes.  For FP8 and 4-bit caches and more than two pairs (one pair) of
+ * whatever the sizes.  For FP8 and 4-bit caches and more than five pairs (one pair) of
  * tiles of 128 rows per KV head, the sizes below count K and V in bf16 besides (B *
  * max_seq_len * Hkv * 512 bytes) where those are at most 2 GB.  That copy is the
  * caller's choice: in a workspace without room for it, these calls convert K and V
- * as they go (FP8 8 to 28 % slower, 4-bit 3 to 50 %).  For the product with V the
+ * as they go (32 pairs: FP8 17 % slower, 4-bit 36 %).  For the product with V the
  * weights are rounded to bf16 with the copy, as over bf16 caches, and to f16 without.
  * A workspace of the bytes below also serves every smaller batch of the same call,
  * with num_splits <= 0.

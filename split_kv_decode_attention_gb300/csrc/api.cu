@@ -749,12 +749,16 @@ namespace {
 
 // FP8 and 4-bit caches of calls with this many pairs of row tiles per KV head are
 // read back to bf16 in the workspace first; with fewer pairs the kernel converts
-// them itself, once for each.  GB300, 8 requests of 2048 tokens, 32 / 8 heads, us
-// copied and converted: FP8 with 1, 2, 3, 8 pairs 53 / 42, 68 / 65, 82 / 89, 138 /
-// 177; 4-bit 55 / 46, 70 / 72, 84 / 99, 140 / 211.  A copy of more than kTallCopyMost
-// bytes is not made (it would save at most a third of the time), nor one that the
-// workspace given has no room for.
-constexpr int64_t kTallCopyPairsFp8 = 3;
+// them itself, once for each.  GB300, us copied and converted: 8 requests of 2048
+// tokens, 32 / 8 heads, FP8 with 3, 4, 5, 6, 8, 12 pairs 81 / 71, 94 / 88, 103 / 102, 118 /
+// 121, 142 / 152, 184 / 200; 16 of 8192 421 / 366, 495 / 442, 598 / 591, 671 / 670, 834 /
+// 848, 1178 / 1283; one of 1500, 20 heads, 40 / 35, 46 / 41, 50 / 43, 54 / 48, 60 / 52, 74 /
+// 76.  4-bit with 2, 3, 4, 8 pairs 68 / 61, 82 / 81, 95 / 104, 143 / 182; 321 / 302, 420 /
+// 447, 491 / 562, 832 / 1060; 37 / 30, 41 / 38, 48 / 45, 59 / 59 (two pairs are faster
+// converted, but keep the copy that their workspace is sized for).  A copy of more
+// than kTallCopyMost bytes is not made (it would save at most a third of the time), nor one
+// that the workspace given has no room for.
+constexpr int64_t kTallCopyPairsFp8 = 6;
 constexpr int64_t kTallCopyPairsFp4 = 2;
 constexpr size_t kTallCopyMost = size_t{2} << 30;
 // Up to this many keys items are not cut, and nothing is merged: the merge's launch costs

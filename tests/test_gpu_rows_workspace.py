@@ -33,7 +33,7 @@ def check(c, q, out, lse, base):
 
 
 @pytest.mark.parametrize("kind", ["fp8", "fp4"])
-@pytest.mark.parametrize("lens,T,G,page", [([1500, 300, 0, 77], 100, 8, 16), ([2000, 129], 700, 1, 0)])
+@pytest.mark.parametrize("lens,T,G,page", [([1500, 300, 0, 77], 200, 8, 16), ([2000, 129], 1400, 1, 0)])
 def test_many_rows_without_room_for_a_copy(da, kind, lens, T, G, page):  # noqa: F811
     """Calls that would copy K and V to bf16 convert them instead where the workspace holds the partials alone; the C
     entry refuses one byte less."""
