@@ -16,13 +16,13 @@
 // warpgroup per row tile turns S into P.  TMEM holds S (P, in 16 bits, replaces
 // its first half) and O of both tiles, all 512 columns; while one tile's S is in
 // its warpgroup, the tensor core works for the other.  A tile's chain of softmax
-// (about 1300 cycles), P V (514) and S (524) bounds a step at 2900 cycles, where
+// (about 1500 cycles), P V (514) and S (524) bounds a step at 3100 cycles, where
 // the tensor core works 2080.  So: P V of the first 64 keys starts before the rest
 // of P is there; the maximum is taken while the first quarter's exponentials run
 // against the old one; an MMA warp elects one thread per product and folds the
 // commits into it.  (64 keys a step with two buffers of S per tile, so that S is
 // made ahead: slower, the smaller products cost as much as the larger.  Two
-// warpgroups to a tile, half the keys each: 473 us where this takes 356; the
+// warpgroups to a tile, half the keys each: 473 us where this took 356; the
 // exponentials of a tile take about 1000 cycles of their unit whoever asks for them.)
 // O is rescaled only when a row's maximum has grown by more than 2^kRaise (the
 // end's division is exact about it), which is rare after the first steps.  P is
@@ -154,7 +154,7 @@ struct TallItem {
 };
 static_assert(sizeof(TallItem) <= 64, "item slots");
 
-// Costs: of a step of two row tiles (about 2900 cycles) and of one (2650: softmax,
+// Costs: of a step of two row tiles (about 3000 cycles) and of one (2650: softmax,
 // P V and S then follow one another), and of an item besides (Q, the first copies, the
 // masked step, its output).
 constexpr int kTCostBoth = kTallCostBoth, kTCostOne = 7, kTCostItem = kTallCostItem;
