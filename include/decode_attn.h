@@ -616,8 +616,8 @@ int decode_attn_sparse(const decode_attn_params *p, const decode_attn_cache *c,
  * ------------------------------------------------------------------------ */
 
 #define DECODE_ATTN_MAX_TREE 1024  /* new tokens of a request in a tree */
-#define DECODE_ATTN_ROWS_WORKSPACE 40162048 /* bytes that a call of more than
-                                      DECODE_ATTN_MAX_ROWS rows needs at least */
+#define DECODE_ATTN_ROWS_WORKSPACE 40162048 /* bytes of workspace in which any call of more
+                                      than DECODE_ATTN_MAX_ROWS rows runs */
 #define DA_STATUS_TREE 32u         /* a parent that is no earlier token, or kept tokens
                                       that do not rise */
 
